@@ -24,6 +24,8 @@ MOE_F32, MOE_BF16, MOE_FP8_E4M3_B128, MOE_RESPLIT_Q4R4 = 0, 1, 2, 3
 MOE_GATE_SOFTMAX_RENORM, MOE_GATE_SIGMOID_RENORM = 0, 1
 MOE_EVICT_CORE, MOE_EVICT_MRS, MOE_EVICT_LRU = 0, 1, 2
 MOE_MODE_AUTO, MOE_MODE_DECODE, MOE_MODE_PREFILL_STAGED = 0, 1, 2
+MOE_ROTARY_HALF, MOE_ROTARY_PAIRS = 0, 1
+MOE_ATTN_MAX_REQUESTS, MOE_ATTN_MAX_ROWS, MOE_SAMPLE_MAX_VOCAB = 1024, 1 << 20, 327680
 STAGES = ("route", "plan", "copy", "ffn")
 MOE_NUM_STAGES = len(STAGES)
 
@@ -45,6 +47,12 @@ class moe_stats(ctypes.Structure):
                                                "bytes_copied", "near_ties", "staged_layers", "prefetch_issued",
                                                "prefetch_committed", "prefetch_demanded", "prefetch_bytes",
                                                "aes_substitutions", "critical_entries")]
+
+
+class moe_attn_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_q_heads", "num_kv_heads", "head_dim", "page_size", "dtype",
+                                              "rotary_dim", "rotary_style", "window")] + \
+               [("softmax_scale", ctypes.c_float), ("norm_eps", ctypes.c_float)]
 
 
 _vp, _i32, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
@@ -78,6 +86,15 @@ _sig = {
     "moe_launch_count": (ctypes.c_uint64, [_vp]),
     "moe_profile_enable": (_i32, [_vp, _i32]),
     "moe_profile_read": (_i32, [_vp, _i32, _P(ctypes.c_float)]),
+    "moe_attn_create": (_i32, [_P(moe_attn_config), ctypes.c_int, _P(_vp)]),
+    "moe_attn_destroy": (_i32, [_vp]),
+    "moe_attn_get_status": (_i32, [_vp]),
+    "moe_attn_clear_status": (_i32, [_vp]),
+    "moe_attn_tables": (_i32, [_vp, _vp, _vp, _i32, _vp, _i32, _vp, _i32, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp]),
+    "moe_attn_qkv": (_i32, [_vp, _vp, ctypes.c_int64, _i32, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _i32, _vp]),
+    "moe_attn_forward": (_i32, [_vp, _vp, ctypes.c_int64, _i32, _vp, _vp, _i32, _i32, _vp, _vp, _i32, _vp, _i32, _vp,
+                                _vp]),
+    "moe_sample": (_i32, [_vp, _i32, _i32, _i32, ctypes.c_int64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "moe_last_error": (ctypes.c_char_p, []),
     "moe_route_topk_noalloc": (_i32, [_i32, _i32, _i32, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
 }
@@ -334,3 +351,146 @@ class Pool:
 
     def launch_count(self):
         return int(_lib.moe_launch_count(self.h))
+
+
+def make_attn_config(num_q_heads, num_kv_heads, head_dim, page_size, dtype=MOE_BF16, rotary_dim=None,
+                     rotary_style=MOE_ROTARY_HALF, window=0, softmax_scale=None, norm_eps=1e-6):
+    c = moe_attn_config()
+    c.num_q_heads, c.num_kv_heads, c.head_dim, c.page_size, c.dtype = num_q_heads, num_kv_heads, head_dim, page_size, dtype
+    c.rotary_dim = head_dim if rotary_dim is None else rotary_dim
+    c.rotary_style, c.window, c.norm_eps = rotary_style, window, norm_eps
+    c.softmax_scale = head_dim ** -0.5 if softmax_scale is None else softmax_scale
+    return c
+
+
+def _typed(name, t, dtype, shape=None):
+    """The binding passes addresses: a tensor of another type, shape or device must not reach them."""
+    import torch
+    kind = {MOE_F32: torch.float32, MOE_BF16: torch.bfloat16, "i32": torch.int32}[dtype]
+    if t.dtype != kind or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor of {kind}, got {t.dtype} on {t.device}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def _rows(name, t, dtype, width=None):
+    """A 2-d (or head-split 3-d) tensor whose rows are contiguous: its row stride in elements."""
+    _typed(name, t, dtype)
+    inner = 1
+    for n, st in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if n != 1 and st != inner:
+            raise ValueError(f"the rows of {name} must be contiguous")
+        inner *= n
+    if t.dim() < 2 or (width is not None and inner != width):
+        raise ValueError(f"{name} must have rows of {width} elements, got {tuple(t.shape)}")
+    return t.stride(0) if t.shape[0] > 1 else max(inner, t.stride(0))
+
+
+def _flat(name, t, dtype, shape=None):
+    if not _typed(name, t, dtype, shape).is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t
+
+
+class Attention:
+    """The attention of a step over a paged cache (moe_attn_create ... moe_attn_destroy).
+
+    The handle keeps the workspace that every layer and step shares; its calls must be ordered.
+    Cache tensors are [num_pages, num_kv_heads, page_size, head_dim], one pair per layer.
+    """
+
+    def __init__(self, cfg, device=0):
+        self.cfg = cfg
+        self.h = None
+        h = _vp()
+        _check(_lib.moe_attn_create(ctypes.byref(cfg), device, ctypes.byref(h)), "moe_attn_create")
+        self.h = h.value
+
+    def close(self):
+        if self.h:
+            _lib.moe_attn_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def _caches(self, k_cache, v_cache):
+        c = self.cfg
+        shape = (k_cache.shape[0], c.num_kv_heads, c.page_size, c.head_dim)
+        _flat("k_cache", k_cache, c.dtype, shape)
+        _flat("v_cache", v_cache, c.dtype, shape)
+        return k_cache.data_ptr(), v_cache.data_ptr(), shape[0]
+
+    def tables(self, ctx_len, new_len, block_table, free_pages, free_head, free_head_out, row_start, seq_len, positions,
+               slot_map, stream=None):
+        """Fill block_table, free_head_out, row_start, seq_len, positions and slot_map for the step."""
+        R, rows = ctx_len.shape[0], positions.shape[0]
+        for name, t, shape in (("ctx_len", ctx_len, (R,)), ("new_len", new_len, (R,)), ("free_head", free_head, (1,)),
+                               ("free_head_out", free_head_out, (1,)), ("row_start", row_start, (R + 1,)),
+                               ("seq_len", seq_len, (R,)), ("positions", positions, (rows,)),
+                               ("slot_map", slot_map, (rows,)), ("block_table", block_table, (R, block_table.shape[1])),
+                               ("free_pages", free_pages, (free_pages.shape[0],))):
+            _flat(name, t, "i32", shape)
+        _check(_lib.moe_attn_tables(self.h, ctx_len.data_ptr(), new_len.data_ptr(), R, block_table.data_ptr(),
+                                    block_table.shape[1], free_pages.data_ptr(), free_pages.shape[0],
+                                    free_head.data_ptr(), free_head_out.data_ptr(), rows, row_start.data_ptr(),
+                                    seq_len.data_ptr(), positions.data_ptr(), slot_map.data_ptr(), _stream(stream)),
+               "moe_attn_tables")
+
+    def qkv(self, qkv, q_norm, k_norm, rope, positions, slot_map, q, k_cache, v_cache, stream=None):
+        """Norm, rotation and cache write of qkv [rows, (Hq + 2 Hkv) * D]; queries go to q [rows, Hq, D]."""
+        c = self.cfg
+        rows, D = qkv.shape[0], c.head_dim
+        stride = _rows("qkv", qkv, c.dtype, (c.num_q_heads + 2 * c.num_kv_heads) * D)
+        for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
+            if w is not None:
+                _flat(name, w, c.dtype, (D,))
+        if rope is not None:
+            _flat("rope", rope, MOE_F32, (rope.shape[0], c.rotary_dim))
+        _flat("positions", positions, "i32", (rows,))
+        _flat("slot_map", slot_map, "i32", (rows,))
+        _flat("q", q, c.dtype, (rows, c.num_q_heads, D))
+        kp, vp, pages = self._caches(k_cache, v_cache)
+        _check(_lib.moe_attn_qkv(self.h, qkv.data_ptr(), stride, rows, _ptr(q_norm), _ptr(k_norm), _ptr(rope),
+                                 0 if rope is None else rope.shape[0], positions.data_ptr(), slot_map.data_ptr(),
+                                 q.data_ptr(), kp, vp, pages, _stream(stream)), "moe_attn_qkv")
+
+    def forward(self, q, row_start, seq_len, max_new, k_cache, v_cache, block_table, out, stream=None):
+        """Attention of q [rows, Hq, D] over the cache, into out [rows, Hq, D]."""
+        c = self.cfg
+        rows, R = q.shape[0], seq_len.shape[0]
+        stride = _rows("q", q, c.dtype, c.num_q_heads * c.head_dim)
+        _flat("row_start", row_start, "i32", (R + 1,))
+        _flat("seq_len", seq_len, "i32", (R,))
+        _flat("block_table", block_table, "i32", (R, block_table.shape[1]))
+        _flat("out", out, c.dtype, (rows, c.num_q_heads, c.head_dim))
+        kp, vp, pages = self._caches(k_cache, v_cache)
+        _check(_lib.moe_attn_forward(self.h, q.data_ptr(), stride, rows, row_start.data_ptr(), seq_len.data_ptr(), R,
+                                     max_new, kp, vp, pages, block_table.data_ptr(), block_table.shape[1],
+                                     out.data_ptr(), _stream(stream)), "moe_attn_forward")
+
+    def status(self):
+        return _lib.moe_attn_get_status(self.h)
+
+    def clear_status(self):
+        _check(_lib.moe_attn_clear_status(self.h), "moe_attn_clear_status")
+
+
+def moe_sample(logits, u, ids, logp=None, temperature=None, top_k=None, top_p=None, min_p=None, stream=None):
+    """Next token of each row of logits [rows, vocab] into ids (and its log probability into logp)."""
+    import torch
+    rows, vocab = logits.shape
+    dtype = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}.get(logits.dtype)
+    if dtype is None:
+        raise ValueError(f"logits must be float32 or bfloat16, got {logits.dtype}")
+    stride = _rows("logits", logits, dtype, vocab)
+    for name, t, kind in (("u", u, MOE_F32), ("ids", ids, "i32"), ("logp", logp, MOE_F32), ("top_k", top_k, "i32"),
+                          ("temperature", temperature, MOE_F32), ("top_p", top_p, MOE_F32), ("min_p", min_p, MOE_F32)):
+        if t is not None:
+            _flat(name, t, kind, (rows,))
+    _check(_lib.moe_sample(logits.data_ptr(), dtype, rows, vocab, stride, _ptr(temperature), _ptr(top_k), _ptr(top_p),
+                           _ptr(min_p), u.data_ptr(), ids.data_ptr(), _ptr(logp), _stream(stream)), "moe_sample")

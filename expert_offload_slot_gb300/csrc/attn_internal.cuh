@@ -1,0 +1,294 @@
+// Internal declarations of the attention step (moe_attn_*): the handle, the
+// arguments the kernels get, and the division of an attention call's work
+// among its CTAs.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/moeslot.h"
+
+namespace moeslot {
+
+moe_status set_last_error(moe_status st, const char* msg);   // text for moe_last_error()
+
+struct AttnArgs {
+  const void* q;               // [rows][q_stride] elements, heads contiguous
+  void* out;                   // [rows][Hq][D]
+  const void* k_cache;         // [num_pages][Hkv][P][D]
+  const void* v_cache;
+  const int32_t* row_start;    // [R+1]
+  const int32_t* seq_len;      // [R]
+  const int32_t* table;        // [R][table_stride]
+  int64_t q_stride;
+  int32_t R, rows, max_new, table_stride, num_pages;
+  int32_t Hq, Hkv, group, page, page_log2, window;
+  float scale, scale_log2;     // softmax_scale, and times log2(e)
+  // workspace: one CTA owns partial slots 2c (a piece that begins inside an item) and 2c+1
+  float* part_o;               // [2 * grid][rows per slot][D]
+  float2* part_ml;             // [2 * grid][rows per slot]  (running maximum, sum of exponentials)
+  uint32_t* arrived;           // [grid] pieces of the split item that starts in CTA c; self-resetting
+  uint32_t* ticket;            // [2]
+  int32_t* status;             // sticky
+};
+
+__device__ __forceinline__ void attn_status(int32_t* status, int32_t code) { atomicCAS(status, 0, code); }
+
+// ------------------------------------------------------------------ the items
+// An item is (request r, row tile i, kv head h).  Its rows are the query rows
+// of the request's new tokens for the heads that share kv head h, token-major
+// ((token, head in group) flattened), tile i taking rows [i*BM, (i+1)*BM).  Its
+// keys are [lo, hi): all that any of its rows may see, cut into units of
+// `unit` keys aligned to multiples of `unit`.
+struct AttnRequest {
+  int32_t start, n, seq;       // first row, new tokens, cached + new tokens
+};
+
+__device__ __forceinline__ AttnRequest attn_request(const AttnArgs& a, int r) {
+  AttnRequest q;
+  q.start = a.row_start[r];
+  int n = a.row_start[r + 1] - q.start;
+  int seq = a.seq_len[r];
+  const int64_t cap = (int64_t)a.table_stride * a.page;
+  bool bad = q.start < 0 || n < 0 || n > a.max_new || seq < 0 || seq > cap || (int64_t)q.start + n > a.rows;
+  if (q.start < 0 || q.start >= a.rows || n < 0) n = 0;
+  n = min(n, min(a.max_new, a.rows - q.start));
+  if (n <= 0) n = 0;
+  seq = max(0, (int)min((int64_t)seq, cap));
+  if (bad) attn_status(a.status, MOE_ERR_BOUNDS);
+  q.n = n;
+  q.seq = seq;
+  return q;
+}
+
+// Keys of row tile i: first unit and number of units (at least one, so that rows without a
+// key are still written).
+template <int BM>
+__device__ __forceinline__ void attn_units(const AttnArgs& a, const AttnRequest& q, int i, int unit, int& u0, int& nu) {
+  const int first = (i * BM) / a.group;                                   // first and last token of the tile
+  const int last = min(q.n - 1, ((i + 1) * BM - 1) / a.group);
+  const int hi = q.seq - q.n + last + 1;
+  int lo = a.window > 0 ? max(0, q.seq - q.n + first - a.window + 1) : 0;
+  lo = min(lo, max(hi - 1, 0));
+  u0 = lo / unit;
+  nu = hi > 0 ? (hi + unit - 1) / unit - u0 : 1;
+}
+
+template <int BM>
+__device__ __forceinline__ int attn_tiles(const AttnArgs& a, const AttnRequest& q) {
+  return (q.n * a.group + BM - 1) / BM;
+}
+
+template <int BM>
+__device__ __forceinline__ int attn_request_units(const AttnArgs& a, const AttnRequest& q, int unit) {
+  int sum = 0;
+  const int nt = attn_tiles<BM>(a, q);
+  for (int i = 0; i < nt; ++i) {
+    int u0, nu;
+    attn_units<BM>(a, q, i, unit, u0, nu);
+    sum += nu;
+  }
+  return sum * a.Hkv;
+}
+
+// The units of all items, item after item, form one sequence of W units that is cut into
+// `parts` equal ranges, one per CTA.  Every CTA finds its own range by scanning the requests
+// (no schedule is built ahead and nothing waits).  An item that crosses a cut is finished by
+// the last of its CTAs to arrive.
+struct AttnCursor {
+  int32_t r, i, h;             // item
+  int32_t at;                  // unit offset inside the item
+  int32_t left;                // units left in this CTA's range
+  int32_t item_first;          // global index of the item's first unit
+  AttnRequest q;
+  int32_t u0, nu;              // the item's units
+};
+
+struct AttnSplit {
+  int32_t W, parts;
+  __device__ __forceinline__ int begin(int c) const { return (int)((int64_t)c * W / parts); }
+  __device__ __forceinline__ int owner(int x) const { return (int)((((int64_t)x + 1) * parts - 1) / W); }
+};
+
+// Called by all threads of the CTA (NT of them) with at least `min_units` units per part.
+// `sm` holds 3 * 32 + 8 ints.  False when this CTA has no work.
+template <int BM, int NT>
+__device__ __forceinline__ bool attn_find_range(const AttnArgs& a, int unit, int min_units, int32_t* sm, AttnSplit& sp,
+                                                AttnCursor& cur) {
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  constexpr int NW = NT / 32;
+  const int per = (a.R + NT - 1) / NT;
+  const int r0 = min(tid * per, a.R), r1 = min(r0 + per, a.R);
+  int mine = 0;
+  for (int r = r0; r < r1; ++r) mine += attn_request_units<BM>(a, attn_request(a, r), unit);
+  int inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 31) sm[wid] = inc;
+  if (tid == 0) sm[40] = -1;
+  __syncthreads();
+  int base = 0, W = 0;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    const int v = sm[w];
+    base += w < wid ? v : 0;
+    W += v;
+  }
+  sp.W = W;
+  sp.parts = max(1, min((int)gridDim.x, W / min_units));
+  const int c = blockIdx.x;
+  if (W == 0 || c >= sp.parts) return false;
+  const int x0 = sp.begin(c), x1 = sp.begin(c + 1);
+  int lo = base + inc - mine;
+  if (x0 >= lo && x0 < lo + mine) {            // exactly one thread: find the request, then the tile
+    for (int r = r0; r < r1; ++r) {
+      const AttnRequest q = attn_request(a, r);
+      const int w = attn_request_units<BM>(a, q, unit);
+      if (x0 < lo + w) {
+        const int nt = attn_tiles<BM>(a, q);
+        for (int i = 0; i < nt; ++i) {
+          int u0, nu;
+          attn_units<BM>(a, q, i, unit, u0, nu);
+          if (x0 < lo + nu * a.Hkv) {
+            const int h = (x0 - lo) / nu;
+            sm[40] = r; sm[41] = i; sm[42] = h; sm[43] = x0 - lo - h * nu;
+            sm[44] = lo + h * nu;
+            break;
+          }
+          lo += nu * a.Hkv;
+        }
+        break;
+      }
+      lo += w;
+    }
+  }
+  __syncthreads();
+  cur.r = sm[40]; cur.i = sm[41]; cur.h = sm[42]; cur.at = sm[43]; cur.item_first = sm[44];
+  cur.left = x1 - x0;
+  cur.q = attn_request(a, cur.r);
+  attn_units<BM>(a, cur.q, cur.i, unit, cur.u0, cur.nu);
+  return true;
+}
+
+// Units of the current item that fall into this CTA's range.
+__device__ __forceinline__ int attn_piece(const AttnCursor& c) { return min(c.nu - c.at, c.left); }
+
+// Step past the current piece; false at the end of the range.
+template <int BM>
+__device__ __forceinline__ bool attn_next(const AttnArgs& a, int unit, AttnCursor& c) {
+  const int took = attn_piece(c);
+  c.left -= took;
+  if (c.left <= 0) return false;
+  c.item_first += c.nu;
+  c.at = 0;
+  if (++c.h < a.Hkv) return true;
+  c.h = 0;
+  if (++c.i >= attn_tiles<BM>(a, c.q)) {
+    c.i = 0;
+    do {
+      c.q = attn_request(a, ++c.r);
+    } while (c.q.n == 0 && c.r < a.R - 1);
+  }
+  attn_units<BM>(a, c.q, c.i, unit, c.u0, c.nu);
+  return true;
+}
+
+// Partial slot of this CTA's piece of a split item.
+__device__ __forceinline__ int attn_slot(const AttnCursor& c) { return 2 * blockIdx.x + (c.at == 0 ? 1 : 0); }
+
+// All threads, after the piece's partial results are stored: true in the CTA whose piece is the
+// last of the item to arrive, with c0 and n the item's first CTA and number of pieces.
+__device__ __forceinline__ bool attn_arrive(const AttnArgs& a, const AttnSplit& sp, const AttnCursor& c, int32_t* flag,
+                                            int& c0, int& n) {
+  c0 = sp.owner(c.item_first);
+  n = sp.owner(c.item_first + c.nu - 1) - c0 + 1;
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const bool last = atomicAdd(a.arrived + c0, 1u) == (uint32_t)(n - 1);
+    if (last) a.arrived[c0] = 0;
+    *flag = last;
+  }
+  __syncthreads();
+  const bool last = *flag;
+  if (last) __threadfence();
+  return last;
+}
+
+__device__ __forceinline__ void attn_store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void attn_store4(__nv_bfloat16* p, float4 v) {
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+  uint2 u;
+  u.x = *reinterpret_cast<const uint32_t*>(&lo);
+  u.y = *reinterpret_cast<const uint32_t*>(&hi);
+  *reinterpret_cast<uint2*>(p) = u;
+}
+
+// Joins the n pieces of a split item, in piece order (so the sum does not depend on which CTA
+// arrives last), and writes the item's output rows.  LOG2: the maxima are in log2 units.
+template <typename T, int D, int BM, int NT, bool LOG2>
+__device__ __forceinline__ void attn_join(const AttnArgs& a, const AttnCursor& c, int c0, int n) {
+  constexpr int LANES = D / 4;
+  const int rows = min(BM, c.q.n * a.group - c.i * BM);
+  for (int row = threadIdx.x / LANES; row < rows; row += NT / LANES) {
+    const int d = (threadIdx.x % LANES) * 4;
+    float M = -INFINITY;
+    for (int p = 0; p < n; ++p) {
+      const int slot = 2 * (c0 + p) + (p == 0 ? 1 : 0);
+      M = fmaxf(M, __ldcg(a.part_ml + (size_t)slot * BM + row).x);
+    }
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+    if (M > -INFINITY) {
+#pragma unroll 4
+      for (int p = 0; p < n; ++p) {
+        const int slot = 2 * (c0 + p) + (p == 0 ? 1 : 0);
+        const float2 ml = __ldcg(a.part_ml + (size_t)slot * BM + row);
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + ((size_t)slot * BM + row) * D + d));
+        const float f = LOG2 ? exp2f(ml.x - M) : expf(ml.x - M);
+        l += f * ml.y;
+        o.x += f * v.x; o.y += f * v.y; o.z += f * v.z; o.w += f * v.w;
+      }
+      const float inv = 1.f / l;
+      o.x *= inv; o.y *= inv; o.z *= inv; o.w *= inv;
+    }
+    const int fr = c.i * BM + row;
+    const size_t at = ((size_t)(c.q.start + fr / a.group) * a.Hq + c.h * a.group + fr % a.group) * D + d;
+    attn_store4(static_cast<T*>(a.out) + at, o);
+  }
+}
+
+// ------------------------------------------------------------------ launchers
+cudaError_t launch_attn_f32(const AttnArgs& a, int D, int grid, cudaStream_t s);
+cudaError_t launch_attn_rows(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, int D, int grid,
+                             cudaStream_t s);
+constexpr int kAttnRowsTile = 16;     // query rows per item of the row kernel
+constexpr int kAttnF32Tile = 32;
+inline int attn_grid(int sms) { return 2 * sms; }   // CTAs of the largest grid: two per SM
+
+struct TablesArgs {
+  const int32_t *ctx, *fresh, *free_pages, *head_in;
+  int32_t *table, *head_out, *row_start, *seq_len, *positions, *slots, *status;
+  uint32_t* ticket;
+  int32_t R, table_stride, num_free, rows, page, page_log2;
+};
+cudaError_t launch_attn_tables(const TablesArgs& a, cudaStream_t s);
+
+struct QkvArgs {
+  const void *qkv, *q_norm, *k_norm;
+  const float* rope;           // [rope_len][rotary]: cosines, then sines
+  const int32_t *positions, *slots;
+  void *q, *k_cache, *v_cache;
+  int32_t* status;
+  int64_t qkv_stride, num_slots;
+  int32_t rows, Hq, Hkv, page_log2, rotary, pairs, rope_len;
+  float eps;
+};
+cudaError_t launch_attn_qkv(const QkvArgs& a, int dtype, int D, cudaStream_t s);
+
+}  // namespace moeslot

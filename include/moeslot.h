@@ -419,6 +419,139 @@ MOE_API moe_status moe_route_topk_noalloc(int32_t num_experts, int32_t top_k, in
                                           const float* router_b, int32_t* ids, float* w, float* probs, float* gap,
                                           void* stream);
 
+/* ------------------------------------------------------------------------
+ * The attention of a step, around the MoE layers
+ *
+ * Four operators that run with moe_forward in a serving step: the page tables
+ * of the step (once), the query/key norm + rotation + cache write and the
+ * attention over the paged cache (each layer), and the choice of the next
+ * tokens (moe_sample).  Requests bring `new` tokens each (1 in decode, a chunk
+ * of the prompt in prefill, 0 for a request that rests) over `ctx` cached ones;
+ * their rows lie one request after another in every [rows, ...] tensor.
+ *
+ * Cache: k_cache and v_cache, device [num_pages][num_kv_heads][page_size][head_dim]
+ * of dtype, one pair per layer, owned by the caller.  Slot s is row s % page_size
+ * of page s / page_size, in every head.
+ * block_table: device int32 [R][table_stride]; entry j of request r is the page
+ * of its tokens j*page_size .. (j+1)*page_size - 1.
+ *
+ * The handle owns a workspace (partial results of split rows, counters, the
+ * status word) that all layers and steps share: calls on one handle must be
+ * ordered (one stream, or streams joined by events).  Only moe_attn_create
+ * allocates and no call synchronises except the status calls, so a step can
+ * be captured into a CUDA graph; lengths, tables and free list are read on the
+ * device at run time.  Sizes the device finds inconsistent are clamped, never
+ * followed out of range, and reported once in the sticky status:
+ * MOE_ERR_CAPACITY (free list short, table_stride or rows exceeded) or
+ * MOE_ERR_BOUNDS (a negative length, a page, position or slot out of range).
+ * ---------------------------------------------------------------------- */
+enum { MOE_ROTARY_HALF = 0,    /* element i turns with i + rotary_dim/2     */
+       MOE_ROTARY_PAIRS = 1 }; /* element 2i turns with 2i + 1              */
+#define MOE_ATTN_MAX_REQUESTS 1024
+#define MOE_ATTN_MAX_ROWS 1048576
+#define MOE_SAMPLE_MAX_VOCAB 327680
+
+typedef struct {
+  int32_t num_q_heads;     /* multiple of num_kv_heads, at most 1024              */
+  int32_t num_kv_heads;    /* 1..256                                              */
+  int32_t head_dim;        /* 64 or 128                                           */
+  int32_t page_size;       /* tokens per page: 16, 32, 64 or 128                  */
+  int32_t dtype;           /* MOE_F32 or MOE_BF16: qkv, norms, q, caches and out  */
+  int32_t rotary_dim;      /* leading elements of a head that turn: multiple of 16 in 0..head_dim */
+  int32_t rotary_style;    /* MOE_ROTARY_*                                        */
+  int32_t window;          /* a token sees this many keys, itself included; 0: all */
+  float softmax_scale;     /* > 0                                                 */
+  float norm_eps;          /* >= 0                                                */
+} moe_attn_config;
+
+typedef struct moe_attn moe_attn;   /* opaque */
+
+MOE_API moe_status moe_attn_create(const moe_attn_config* cfg, int device, moe_attn** out);
+MOE_API moe_status moe_attn_destroy(moe_attn* attn);      /* synchronises the device */
+
+/* Sticky device status (synchronises the device), and its reset. */
+MOE_API moe_status moe_attn_get_status(moe_attn* attn);
+MOE_API moe_status moe_attn_clear_status(moe_attn* attn);
+
+/* Block tables and row maps of a step from its requests' lengths, in one launch.
+ *   ctx_len, new_len  device int32 [R] cached and new tokens of each request
+ *   block_table       in: the pages of the cached tokens; out: entries
+ *                     ceil(ctx/P) .. ceil((ctx+new)/P) - 1 of each request are
+ *                     filled, request after request, with the free list's pages
+ *                     from *free_head on (-1 where the list is short)
+ *   free_pages        device int32 [num_free]; free_head, free_head_out device
+ *                     int32: how many of them are taken before and after (the two
+ *                     may be the same address).  num_free 0: the tables are
+ *                     complete already and only the maps are wanted
+ *   rows              rows of the step's tensors, at least the sum of new_len
+ *   row_start         out int32 [R+1]: first row of each request, then the sum
+ *   seq_len           out int32 [R]: ctx + new
+ *   positions         out int32 [rows]: position of each row's token in its request
+ *   slot_map          out int32 [rows]: its cache slot; -1 (position 0) for the
+ *                     rows past the last request (the padding of a captured step)
+ * seq_len and row_start must not overlap ctx_len and new_len. */
+MOE_API moe_status moe_attn_tables(moe_attn* attn, const int32_t* ctx_len, const int32_t* new_len, int32_t R,
+                                   int32_t* block_table, int32_t table_stride, const int32_t* free_pages,
+                                   int32_t num_free, const int32_t* free_head, int32_t* free_head_out, int32_t rows,
+                                   int32_t* row_start, int32_t* seq_len, int32_t* positions, int32_t* slot_map,
+                                   void* stream);
+
+/* Norm of each query and key head, rotation, and the cache write, in one pass.
+ *   qkv      device [rows] rows of [num_q_heads | num_kv_heads | num_kv_heads][head_dim]
+ *            (queries, keys, values), qkv_stride elements apart
+ *   q_norm, k_norm  device [head_dim] of dtype: y = x / sqrt(mean(x^2) + norm_eps) * w
+ *            over each head; NULL: that norm is left out
+ *   rope     device fp32 [rope_len][rotary_dim]: for each position the rotary_dim/2
+ *            cosines, then the sines: (a, b) becomes (a cos - b sin, b cos + a sin).
+ *            Not read when rotary_dim is 0
+ *   positions, slot_map  device int32 [rows], as moe_attn_tables writes them; K and V
+ *            of a row with a negative slot are not written
+ *   q        out [rows][num_q_heads][head_dim]
+ * Computed in fp32, rounded once.  A position outside the table is left unrotated and
+ * reported (MOE_ERR_BOUNDS).  qkv, its rows, norms, rope, q and caches 16-byte aligned. */
+MOE_API moe_status moe_attn_qkv(moe_attn* attn, const void* qkv, int64_t qkv_stride, int32_t rows, const void* q_norm,
+                                const void* k_norm, const float* rope, int32_t rope_len, const int32_t* positions,
+                                const int32_t* slot_map, void* q, void* k_cache, void* v_cache, int32_t num_pages,
+                                void* stream);
+
+/* Attention of the new tokens over the cache, which holds their keys and values already.
+ * Token i of request r sits at p = seq_len[r] - new_r + i (new_r = row_start[r+1] -
+ * row_start[r]) and sees the keys max(0, p - window + 1) .. p:
+ *   out[row, head] = sum_j softmax_j(softmax_scale q[row, head] . k[j]) v[j]
+ * with the keys of kv head  head / (num_q_heads / num_kv_heads).  A row that sees no key
+ * (p < 0) gives zeros; rows of no request are not written.  Scores, the softmax's maximum
+ * and sum and the output sums are fp32.  Cache rows that no token of the call sees (the
+ * rest of a last page, pages out of the window) may hold anything, NaN included; the
+ * values of a key that some token of a request's call sees must be finite for the others.
+ *   q         device [rows] rows of [num_q_heads][head_dim], q_stride elements apart
+ *   max_new   bound of new_r over the requests, known to the host (1 in a decode step)
+ *   out       device [rows][num_q_heads][head_dim] of dtype
+ * The result does not depend on the order in which CTAs finish.  q, its rows and out
+ * 16-byte aligned. */
+MOE_API moe_status moe_attn_forward(moe_attn* attn, const void* q, int64_t q_stride, int32_t rows,
+                                    const int32_t* row_start, const int32_t* seq_len, int32_t R, int32_t max_new,
+                                    const void* k_cache, const void* v_cache, int32_t num_pages,
+                                    const int32_t* block_table, int32_t table_stride, void* out, void* stream);
+
+/* The next token of each row: temperature, top-k, top-p, min-p and one given uniform number.
+ *   logits       device [rows] rows of [vocab] of dtype (MOE_F32 or MOE_BF16), row_stride
+ *                elements apart; vocab up to MOE_SAMPLE_MAX_VOCAB
+ *   temperature  device fp32 [rows]: T; 0 or below: the first maximum.  NULL: 1
+ *   top_k        device int32 [rows]; 0 or below: off.  top_p, min_p device fp32 [rows];
+ *                top_p >= 1 and min_p <= 0: off.  Each may be NULL (off)
+ *   u            device fp32 [rows] in [0, 1)
+ *   ids, logp    out int32 and fp32 [rows]; logp may be NULL
+ * With z = (x - max x) / T in fp32 and the integer weight w = floor(exp(z) 2^40): in
+ * descending order of x (equal ones by index) the first top_k are kept; of them, with mass M,
+ * those whose preceding mass is below ceil(top_p M), the first always; of them those with
+ * w >= min_p 2^40.  With kept mass K the token is the lowest index whose inclusive prefix of
+ * kept w, in index order, exceeds floor(u K), and logp = log(w / K).  All sums are integers, so
+ * the token depends on the inputs alone.  NaN counts as -inf; a row without any logit above
+ * -inf gives id -1 and logp -inf.  Runs on the current device; needs no handle or workspace. */
+MOE_API moe_status moe_sample(const void* logits, int32_t dtype, int32_t rows, int32_t vocab, int64_t row_stride,
+                              const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                              const float* u, int32_t* ids, float* logp, void* stream);
+
 /* Number of kernel launches the library issued since the pool was created. */
 MOE_API uint64_t moe_launch_count(const moe_pool* pool);
 

@@ -1,0 +1,356 @@
+"""Page tables, norm + rotation + cache write, and attention over the paged cache against the 64-bit oracle.
+
+Tolerances.  Attention, bf16: the probabilities and the output are each rounded to bf16 (at most
+2^-8 of their size, the probabilities' errors averaging out over the keys) and the fp32 scores are
+off by at most D 2^-24 sum|q k| scale (about 2e-4 here): 2^-7 sum p|v| is allowed.  fp32: the
+scores' error alone, 2e-4 sum p|v|.  Norm + rotation: the reduction and the products keep 1e-6 of
+|a| + |b|; bf16 adds one rounding, 2^-8 |y|.
+"""
+import numpy as np
+import pytest
+import torch
+
+import expert_offload_slot_gb300 as moe
+from oracle import attention as oracle
+
+pytestmark = pytest.mark.gpu
+DT = {"f32": (torch.float32, moe.MOE_F32), "bf16": (torch.bfloat16, moe.MOE_BF16)}
+
+
+def ints(v):
+    return torch.tensor(np.asarray(v), dtype=torch.int32, device="cuda")
+
+
+class Step:
+    """A step's requests with their tables, built by the library."""
+
+    def __init__(self, ctx, new, dtype="bf16", hq=8, hkv=2, dim=128, page=16, window=0, pad=0, spare=3, seed=0, scale=None,
+                 **cfg):
+        self.ctx, self.new, self.page, self.hq, self.hkv, self.dim, self.window = ctx, new, page, hq, hkv, dim, window
+        self.dtype = DT[dtype][0]
+        self.scale = dim ** -0.5 if scale is None else scale
+        rng = np.random.default_rng(seed)
+        have = [-(-c // page) for c in ctx]
+        need = [-(-(c + n) // page) for c, n in zip(ctx, new)]
+        self.pages, self.width, self.rows = sum(need) + spare, max(need + [1]) + 1, sum(new) + pad
+        order = rng.permutation(self.pages)
+        table, at = np.full((len(ctx), self.width), 1 << 30), 0           # entries in no use hold no page
+        for r, h in enumerate(have):
+            table[r, :h] = order[at:at + h]
+            at += h
+        self.free, self.head0, self.table0 = order[at:], 0, table
+        self.handle = moe.Attention(moe.make_attn_config(hq, hkv, dim, page, DT[dtype][1], window=window, softmax_scale=self.scale,
+                                                         **cfg))
+        self.table, self.free_d = ints(table), ints(self.free)
+        self.head = ints([0])
+        self.start, self.seq = ints(np.zeros(len(ctx) + 1)), ints(np.zeros(len(ctx)))
+        self.pos, self.slot = ints(np.zeros(self.rows)), ints(np.zeros(self.rows))
+        self.handle.tables(ints(ctx), ints(new), self.table, self.free_d, self.head, self.head, self.start, self.seq,
+                           self.pos, self.slot)
+
+    def cache(self, gen):
+        shape = (self.pages, self.hkv, self.page, self.dim)
+        return [torch.randn(shape, generator=gen, device="cuda").to(self.dtype) for _ in range(2)]
+
+    def lines(self, cache, r):
+        """Cached rows of request r as [Hkv, seq, D] in 64 bits."""
+        table = self.table.cpu().numpy()[r]
+        n = self.ctx[r] + self.new[r]
+        used = table[:-(-n // self.page)] if n else table[:0]
+        got = cache[torch.tensor(used, dtype=torch.long, device="cuda")]       # [pages, Hkv, P, D]
+        return got.permute(1, 0, 2, 3).reshape(self.hkv, -1, self.dim)[:, :n].double().cpu().numpy()
+
+
+def check_attention(s, seed=1, q_pad=0, poison=True, spike=1.0):
+    gen = torch.Generator("cuda").manual_seed(seed)
+    kc, vc = s.cache(gen)
+    if poison:                      # what no token sees: the rest of last pages, spare pages
+        seen = torch.zeros(s.pages, s.page, dtype=torch.bool)
+        table = s.table.cpu().numpy()
+        for r, (c, n) in enumerate(zip(s.ctx, s.new)):
+            first = max(0, c - s.window + 1) if s.window and n else 0
+            for p in range(first if n else 0, c + n if n else 0):
+                seen[table[r][p // s.page], p % s.page] = True
+        hide = ~seen.cuda()
+        kc.permute(0, 2, 1, 3)[hide] = float("nan")
+        vc.permute(0, 2, 1, 3)[hide] = float("inf")
+    wide = torch.randn(s.rows, s.hq * s.dim + q_pad, generator=gen, device="cuda").mul_(2 * spike).to(s.dtype)
+    q = wide[:, :s.hq * s.dim].view(s.rows, s.hq, s.dim) if not q_pad else wide[:, :s.hq * s.dim].unflatten(1, (s.hq, s.dim))
+    out = torch.full((s.rows, s.hq, s.dim), 7.0, device="cuda", dtype=s.dtype)
+    args = (q, s.start, s.seq, max(s.new), kc, vc, s.table)
+    s.handle.forward(*args, out)
+    again = torch.full_like(out, 7.0)
+    s.handle.forward(*args, again)
+    assert torch.equal(out, again)                         # the same bits whatever the CTAs' order
+    assert s.handle.status() == moe.MOE_OK
+    got, qh, row = out.double().cpu().numpy(), q.double().cpu().numpy(), 0
+    tol = 2.0 ** -7 if s.dtype is torch.bfloat16 else 2e-4
+    rng = np.random.default_rng(seed)
+    for r, (c, n) in enumerate(zip(s.ctx, s.new)):
+        if n:
+            k, v = s.lines(kc, r), s.lines(vc, r)
+            if s.window:                                   # keys before every window may be anything
+                k[:, :max(0, c - s.window + 1)], v[:, :max(0, c - s.window + 1)] = 0, 0
+        some = range(n) if n <= 40 else sorted({0, 1, n - 2, n - 1, *rng.integers(0, n, 24).tolist()})
+        for i in some:
+            for h in range(s.hq):
+                ref, size = oracle.attend(qh[row + i, h], k[h // (s.hq // s.hkv)], v[h // (s.hq // s.hkv)], c + i, s.scale,
+                                          s.window)
+                err = np.abs(got[row + i, h] - ref)
+                assert (err <= tol * size + 1e-30).all(), (r, i, h, float((err / (size + 1e-30)).max()))
+        row += n
+    assert (out[row:] == 7.0).all()                        # rows of no request are not written
+
+
+# ------------------------------------------------------------------------------------------ tables
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("ctx,new,pad", [
+    ([0], [1], 0), ([15], [1], 0), ([16], [1], 3), ([0], [0], 2), ([5, 8, 0, 128, 127], [4, 0, 3, 1, 2], 5),
+    (list(range(300)), [1 + i % 3 for i in range(300)], 1), ([0, 7000, 3], [5000, 1, 700], 0),
+    ([i * 7 for i in range(1024)], [i % 2 for i in range(1024)], 16)])
+def test_tables(ctx, new, pad, page):
+    s = Step(ctx, new, page=page, pad=pad)
+    table, start, seq, pos, slot, head = oracle.tables(ctx, new, s.table0, s.free.tolist(), 0, page, s.rows)
+    assert s.table.cpu().tolist() == table.tolist()
+    assert s.start.cpu().tolist() == start.tolist() and s.seq.cpu().tolist() == seq.tolist()
+    assert s.pos.cpu().tolist() == pos.tolist() and s.slot.cpu().tolist() == slot.tolist()
+    assert int(s.head) == head                             # free_head_out is free_head here
+    assert s.handle.status() == moe.MOE_OK
+
+
+def test_tables_without_a_free_list_only_map():
+    s = Step([30, 5], [2, 7])
+    table, pos, slot = s.table.clone(), s.pos.clone(), s.slot.clone()
+    h2 = ints([9])
+    full = ints([-(-32 // 16) * 16 - 0, 16])
+    # the same rows with every page in the tables already: lengths whose pages are all there
+    s.handle.tables(ints([30, 5]), ints([2, 7]), s.table, s.free_d, ints([0]), h2, s.start, s.seq, s.pos, s.slot)
+    assert torch.equal(table, s.table) and torch.equal(pos, s.pos) and torch.equal(slot, s.slot)
+    s.handle.tables(full, ints([0, 0]), s.table, s.free_d[:0], ints([4]), h2, s.start, s.seq, s.pos, s.slot)
+    assert int(h2) == 4 and s.handle.status() == moe.MOE_OK
+
+
+@pytest.mark.parametrize("what", ["free", "width", "rows", "negative"])
+def test_tables_report_what_does_not_fit(what):
+    s = Step([10, 3], [30, 5])
+    table, slot, rows = s.table.clone(), s.slot, s.rows
+    new, free, want = [30, 5], s.free_d, moe.MOE_ERR_CAPACITY
+    if what == "free":
+        free = free[:1]
+    elif what == "width":
+        table = table[:, :2].contiguous()
+    elif what == "rows":
+        rows -= 1
+    else:
+        new, want = [-4, 5], moe.MOE_ERR_BOUNDS
+    pos, slot = ints(np.zeros(rows)), ints(np.full(rows, 99))
+    s.handle.tables(ints([10, 3]), ints(new), table, free, ints([0]), s.head, s.start, s.seq, pos, slot)
+    assert s.handle.status() == want
+    assert slot.max() < s.pages * s.page
+    s.handle.clear_status()
+    assert s.handle.status() == moe.MOE_OK
+
+
+# --------------------------------------------------------------------------------------------- qkv
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dim,rotary,pairs,norm,heads", [
+    (128, 128, False, True, (8, 2)), (128, 64, False, True, (3, 1)), (64, 64, True, True, (4, 4)), (64, 32, True, False, (6, 2)),
+    (128, 0, False, True, (2, 2)), (128, 16, False, False, (5, 1)), (64, 48, False, True, (1, 1))])
+def test_qkv(dtype, dim, rotary, pairs, norm, heads):
+    hq, hkv = heads
+    s = Step([0, 20, 3], [1, 5, 30], dtype, hq, hkv, dim, pad=3, rotary_dim=rotary,
+             rotary_style=moe.MOE_ROTARY_PAIRS if pairs else moe.MOE_ROTARY_HALF, norm_eps=1e-5)
+    gen = torch.Generator("cuda").manual_seed(3)
+    width = (hq + 2 * hkv) * dim
+    wide = torch.randn(s.rows, width + 16, generator=gen, device="cuda").to(s.dtype)
+    qkv = wide[:, 8:8 + width] if dtype == "bf16" else wide[:, 4:4 + width]       # strided rows
+    wq, wk = [(1 + 0.3 * torch.randn(dim, generator=gen, device="cuda")).to(s.dtype) if norm else None for _ in range(2)]
+    rope = torch.randn(40, rotary, generator=gen, device="cuda") if rotary else None
+    kc, vc = s.cache(gen)
+    k0, v0 = kc.clone(), vc.clone()
+    q = torch.empty(s.rows, hq, dim, device="cuda", dtype=s.dtype)
+    s.handle.qkv(qkv, wq, wk, rope, s.pos, s.slot, q, kc, vc)
+    assert s.handle.status() == moe.MOE_OK
+    x = qkv.double().cpu().numpy().reshape(s.rows, hq + 2 * hkv, dim)
+    pos, slot = s.pos.cpu().numpy(), s.slot.cpu().numpy()
+    table = rope.double().cpu().numpy() if rotary else np.zeros((40, 0))
+    weights = [None if w is None else w.double().cpu().numpy() for w in (wq, wk)]
+    one = 2.0 ** -8 if dtype == "bf16" else 0.0
+    half = rotary // 2
+    written = np.zeros((s.pages, s.page), bool)
+    for t in range(s.rows):
+        for h in range(hq + 2 * hkv):
+            if h >= hq and slot[t] < 0:
+                continue
+            w = weights[0 if h < hq else 1]
+            plain = oracle.norm_rotate(x[t, h], w, 1e-5, np.ones(0), np.ones(0), pairs)
+            ref = oracle.norm_rotate(x[t, h], w, 1e-5, table[pos[t], :half], table[pos[t], half:], pairs)
+            if h >= hq + hkv:
+                ref = plain = x[t, h]
+            if h < hq:
+                got = q[t, h]
+            else:
+                c = kc if h < hq + hkv else vc
+                got = c[slot[t] // s.page, (h - hq) % hkv, slot[t] % s.page]
+                written[slot[t] // s.page, slot[t] % s.page] = True
+            size = 4 * np.abs(plain).max()
+            err = np.abs(got.double().cpu().numpy() - ref)
+            assert (err <= one * np.abs(ref) + 1e-6 * size).all(), (t, h, err.max())
+    keep = torch.tensor(~written).cuda()
+    for c, c0 in ((kc, k0), (vc, v0)):
+        assert torch.equal(c.permute(0, 2, 1, 3)[keep], c0.permute(0, 2, 1, 3)[keep])
+
+
+def test_qkv_reports_positions_and_slots_out_of_range():
+    s = Step([0], [4], hq=2, hkv=1)
+    gen = torch.Generator("cuda").manual_seed(3)
+    qkv = torch.randn(4, 4 * 128, generator=gen, device="cuda").bfloat16()
+    rope = torch.randn(3, 128, generator=gen, device="cuda")              # position 3 is outside
+    kc, vc = s.cache(gen)
+    q = torch.empty(4, 2, 128, device="cuda", dtype=torch.bfloat16)
+    s.handle.qkv(qkv, None, None, rope, s.pos, s.slot, q, kc, vc)
+    assert s.handle.status() == moe.MOE_ERR_BOUNDS
+    s.handle.clear_status()
+    before = kc.clone()
+    s.handle.qkv(qkv, None, None, torch.cat([rope, rope]), s.pos, ints([s.pages * s.page, 1 << 30, -1, -7]), q, kc, vc)
+    assert s.handle.status() == moe.MOE_ERR_BOUNDS and torch.equal(before, kc)
+
+
+# --------------------------------------------------------------------------------------- attention
+LENGTHS = [
+    ([0], [1]), ([15], [1]), ([16], [1]), ([1], [1]), ([127], [1]), ([128], [1]), ([0], [17]), ([3], [33]), ([200], [2]),
+    ([0, 31, 300, 5, 64], [1, 1, 1, 1, 1]), ([40, 0, 129, 7], [0, 5, 1, 130]), ([2000], [1]), ([513, 1], [70, 0]),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("ctx,new", LENGTHS)
+def test_attention_lengths(dtype, ctx, new):
+    check_attention(Step(ctx, new, dtype, pad=2))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("heads", [(1, 1), (3, 1), (8, 1), (16, 1), (6, 2), (20, 4), (8, 8), (40, 2)])
+def test_attention_heads(dtype, dim, heads):
+    check_attention(Step([70, 0, 17], [1, 20, 3], dtype, *heads, dim))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("window", [0, 1, 16, 50, 129])
+def test_attention_pages_and_windows(dtype, page, window):
+    check_attention(Step([300, 0, 64, 10], [1, 40, 1, 150], dtype, page=page, window=window))
+    check_attention(Step([700, 3], [1, 1], dtype, page=page, window=window))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attention_strided_queries_and_sharp_scores(dtype):
+    check_attention(Step([90, 4], [3, 65], dtype), q_pad=8)
+    check_attention(Step([500], [1], dtype, scale=0.02), spike=20.0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attention_long_rows_are_split(dtype):
+    check_attention(Step([9000, 17, 4000], [1, 1, 1], dtype, 8, 1, page=64), poison=False)
+    check_attention(Step([30011], [1], dtype, 4, 1, page=32), poison=False)
+    check_attention(Step([6000], [9], dtype, 8, 2), poison=False)
+
+
+def test_attention_prefill_of_many_rows():
+    check_attention(Step([0, 100], [700, 333], "bf16", 8, 2), poison=True)
+    check_attention(Step([1500], [600], "bf16", 16, 2, page=64), poison=True)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_before_the_first_key_are_zero(dtype):
+    s = Step([0], [6], dtype)
+    gen = torch.Generator("cuda").manual_seed(1)
+    kc, vc = s.cache(gen)
+    q = torch.randn(6, s.hq, s.dim, generator=gen, device="cuda").to(s.dtype)
+    out = torch.full_like(q, 7.0)
+    s.handle.forward(q, s.start, ints([2]), 6, kc, vc, s.table, out)      # six rows, two keys: four rows see none
+    assert (out[:4] == 0).all() and torch.isfinite(out).all() and (out[4:] != 0).any()
+    out.fill_(7.0)
+    s.handle.forward(q, s.start, ints([0]), 6, kc, vc, s.table, out)
+    assert (out == 0).all() and s.handle.status() == moe.MOE_OK
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attention_reports_bad_tables_and_lengths(dtype):
+    s = Step([40], [1], dtype)
+    gen = torch.Generator("cuda").manual_seed(1)
+    kc, vc = s.cache(gen)
+    q = torch.randn(1, s.hq, s.dim, generator=gen, device="cuda").to(s.dtype)
+    out = torch.empty_like(q)
+    for table, seq, start in ((ints([[0, s.pages, 1, 0]]), [41], [0, 1]), (ints([[0, -1, 1, 0]]), [41], [0, 1]),
+                              (s.table, [1 << 30], [0, 1]), (s.table, [-5], [0, 1]), (s.table, [41], [0, 9]),
+                              (s.table, [41], [-1, 1]), (s.table, [41], [1, 0])):
+        s.handle.forward(q, ints(start), ints(seq), 1, kc, vc, table, out)
+        assert s.handle.status() == moe.MOE_ERR_BOUNDS, (seq, start)
+        s.handle.clear_status()
+    s.handle.forward(q, s.start, s.seq, 1, kc, vc, s.table, out)
+    assert s.handle.status() == moe.MOE_OK
+
+
+def test_attention_on_another_stream_and_in_a_graph():
+    s = Step([300, 20], [1, 1])
+    gen = torch.Generator("cuda").manual_seed(1)
+    kc, vc = s.cache(gen)
+    q = torch.randn(2, s.hq, s.dim, generator=gen, device="cuda").to(s.dtype)
+    out, ref = torch.empty_like(q), torch.empty_like(q)
+    s.handle.forward(q, s.start, s.seq, 1, kc, vc, s.table, ref)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    s.handle.forward(q, s.start, s.seq, 1, kc, vc, s.table, out, stream=side)
+    side.synchronize()
+    assert torch.equal(out, ref)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        s.handle.forward(q, s.start, s.seq, 1, kc, vc, s.table, out)
+    out.zero_()
+    q.mul_(0.5)
+    graph.replay()
+    s.handle.forward(q, s.start, s.seq, 1, kc, vc, s.table, ref)
+    assert torch.equal(out, ref)
+
+
+def test_refusals():
+    good = dict(num_q_heads=8, num_kv_heads=2, head_dim=128, page_size=16)
+    for bad in (dict(num_q_heads=7), dict(num_kv_heads=0), dict(head_dim=96), dict(page_size=8), dict(page_size=48),
+                dict(rotary_dim=24), dict(rotary_dim=256), dict(rotary_style=2), dict(window=-1), dict(softmax_scale=0.0),
+                dict(softmax_scale=float("nan")), dict(norm_eps=-1.0), dict(dtype=moe.MOE_FP8_E4M3_B128)):
+        with pytest.raises(moe.MoeError) as e:
+            moe.Attention(moe.make_attn_config(**{**good, **bad}))
+        assert e.value.status == moe.MOE_ERR_INVALID, bad
+    s = Step([40], [2])
+    gen = torch.Generator("cuda").manual_seed(1)
+    kc, vc = s.cache(gen)
+    q = torch.zeros(2, s.hq, s.dim, device="cuda", dtype=s.dtype)
+    out = torch.empty_like(q)
+    with pytest.raises(ValueError):
+        s.handle.forward(q.float(), s.start, s.seq, 2, kc, vc, s.table, out)
+    with pytest.raises(ValueError):
+        s.handle.forward(q, s.start, s.seq.long(), 2, kc, vc, s.table, out)
+    with pytest.raises(ValueError):
+        s.handle.forward(q, s.start, s.seq, 2, kc, vc[:, :1], s.table, out)
+    with pytest.raises(ValueError):
+        s.handle.forward(q.transpose(1, 2).contiguous().transpose(1, 2), s.start, s.seq, 2, kc, vc, s.table, out)
+    lib, h, st = moe._lib, s.handle.h, torch.cuda.current_stream().cuda_stream
+
+    def raw(**kw):
+        a = dict(q=q.data_ptr(), stride=s.hq * s.dim, rows=2, start=s.start.data_ptr(), seq=s.seq.data_ptr(), R=1, new=2,
+                 k=kc.data_ptr(), v=vc.data_ptr(), pages=s.pages, table=s.table.data_ptr(), width=s.width, out=out.data_ptr())
+        a.update(kw)
+        return lib.moe_attn_forward(h, a["q"], a["stride"], a["rows"], a["start"], a["seq"], a["R"], a["new"], a["k"], a["v"],
+                                    a["pages"], a["table"], a["width"], a["out"], st)
+    assert raw() == moe.MOE_OK
+    for kw in (dict(q=None), dict(q=q.data_ptr() + 2), dict(stride=8), dict(stride=s.hq * s.dim + 1), dict(rows=-1), dict(R=1025),
+               dict(new=3), dict(new=-1), dict(k=None), dict(v=vc.data_ptr() + 4), dict(pages=0), dict(pages=1 << 30),
+               dict(table=None), dict(width=0), dict(out=None), dict(out=out.data_ptr() + 8), dict(start=s.start.data_ptr() + 1)):
+        assert raw(**kw) == moe.MOE_ERR_INVALID, kw
+    assert raw(R=0) == moe.MOE_OK and raw(rows=0, new=0) == moe.MOE_OK
+    # seq_len must not be the lengths it is computed from
+    assert lib.moe_attn_tables(h, s.seq.data_ptr(), s.seq.data_ptr(), 1, s.table.data_ptr(), s.width, s.free_d.data_ptr(), 1,
+                               s.head.data_ptr(), s.head.data_ptr(), 2, s.start.data_ptr(), s.seq.data_ptr(),
+                               s.pos.data_ptr(), s.slot.data_ptr(), st) == moe.MOE_ERR_INVALID
