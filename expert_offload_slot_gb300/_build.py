@@ -17,7 +17,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoeslot.so")
 
 SOURCES = ["api.cu", "pack.cu", "quota.cu", "k_route.cu", "k_plan.cu", "k_copy.cu", "k_ffn.cu", "k_noalloc.cu", "k_tc.cu",
-           "attn_api.cu", "k_attn_step.cu", "k_attn_f32.cu", "k_attn_rows.cu", "k_sample.cu"]
+           "attn_api.cu", "k_attn_step.cu", "k_attn_f32.cu", "k_attn_rows.cu", "k_attn_tiles.cu", "k_sample.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden,-ffp-contract=off", f"-I{INCLUDE}"]
 

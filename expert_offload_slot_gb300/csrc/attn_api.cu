@@ -63,8 +63,8 @@ moe_status check_config(const moe_attn_config* c) {
 }
 
 // A cache [num_pages][Hkv][P][D] as [D / 64][num_pages * Hkv * P][64] bf16: a box of `rows`
-// consecutive keys of one head comes as D / 64 tiles of 128-byte rows, 128-byte swizzled.
-bool cache_map(CUtensorMap* m, const void* base, int64_t keys, int D, int rows) {
+// consecutive keys of one head comes as `halves` tiles of 128-byte rows, 128-byte swizzled.
+bool cache_map(CUtensorMap* m, const void* base, int64_t keys, int D, int rows, int halves) {
   static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
     void* p = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -76,7 +76,7 @@ bool cache_map(CUtensorMap* m, const void* base, int64_t keys, int D, int rows) 
   if (!encode) return false;
   const cuuint64_t dims[3] = {64, (cuuint64_t)keys, (cuuint64_t)(D / 64)};
   const cuuint64_t strides[2] = {(cuuint64_t)D * 2, 128};
-  const cuuint32_t box[3] = {64, (cuuint32_t)rows, (cuuint32_t)(D / 64)}, one[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {64, (cuuint32_t)rows, (cuuint32_t)halves}, one[3] = {1, 1, 1};
   return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, one,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -111,10 +111,10 @@ MOE_API moe_status moe_attn_create(const moe_attn_config* cfg, int device, moe_a
   while ((1 << A->page_log2) < cfg->page_size) ++A->page_log2;
   cudaDeviceGetAttribute(&A->sms, cudaDevAttrMultiProcessorCount, device);
   if (A->sms < 1) A->sms = 1;
-  // two partial slots of a row tile per CTA, two CTAs per SM at most
-  const int tile = cfg->dtype == MOE_F32 ? kAttnF32Tile : kAttnRowsTile;
+  // two partial slots of a row tile per CTA: the fp32 kernel has two CTAs per SM, the others one
   const size_t slots = (size_t)2 * attn_grid(A->sms);
-  const size_t o_bytes = slots * tile * cfg->head_dim * sizeof(float), ml_bytes = slots * tile * sizeof(float2);
+  const size_t part_rows = cfg->dtype == MOE_F32 ? slots * kAttnF32Tile : (size_t)2 * A->sms * kAttnTile;
+  const size_t o_bytes = part_rows * cfg->head_dim * sizeof(float), ml_bytes = part_rows * sizeof(float2);
   A->zero_bytes = (slots + 8) * sizeof(uint32_t);
   e = cudaMalloc(&A->work, o_bytes + ml_bytes + A->zero_bytes);
   if (e != cudaSuccess) {
@@ -254,9 +254,12 @@ MOE_API moe_status moe_attn_forward(moe_attn* A, const void* q, int64_t q_stride
   if (c.dtype == MOE_F32) return launched(launch_attn_f32(a, c.head_dim, attn_grid(A->sms), s), "moe_attn_forward");
   CUtensorMap mk, mv;
   const int64_t keys = (int64_t)num_pages * c.num_kv_heads * c.page_size;
-  if (!cache_map(&mk, k_cache, keys, c.head_dim, 16) || !cache_map(&mv, v_cache, keys, c.head_dim, 16))
+  const bool few = (int64_t)max_new * a.group <= kAttnRowsTile;
+  const int box = few ? 16 : c.page_size, halves = few ? c.head_dim / 64 : 1;
+  if (!cache_map(&mk, k_cache, keys, c.head_dim, box, halves) || !cache_map(&mv, v_cache, keys, c.head_dim, box, halves))
     return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for the caches");
-  return launched(launch_attn_rows(a, mk, mv, c.head_dim, A->sms, s), "moe_attn_forward");
+  return launched(few ? launch_attn_rows(a, mk, mv, c.head_dim, A->sms, s) : launch_attn_tiles(a, mk, mv, c.head_dim, A->sms, s),
+                  "moe_attn_forward");
 }
 
 MOE_API moe_status moe_sample(const void* logits, int32_t dtype, int32_t rows, int32_t vocab, int64_t row_stride,

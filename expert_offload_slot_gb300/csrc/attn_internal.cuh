@@ -14,6 +14,10 @@ namespace moeslot {
 
 moe_status set_last_error(moe_status st, const char* msg);   // text for moe_last_error()
 
+constexpr int kAttnRowsTile = 16;     // query rows per item of the row kernel
+constexpr int kAttnTile = 256;        // and of the tile kernel
+constexpr int kAttnF32Tile = 32;
+
 struct AttnArgs {
   const void* q;               // [rows][q_stride] elements, heads contiguous
   void* out;                   // [rows][Hq][D]
@@ -267,8 +271,8 @@ __device__ __forceinline__ void attn_join(const AttnArgs& a, const AttnCursor& c
 cudaError_t launch_attn_f32(const AttnArgs& a, int D, int grid, cudaStream_t s);
 cudaError_t launch_attn_rows(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, int D, int grid,
                              cudaStream_t s);
-constexpr int kAttnRowsTile = 16;     // query rows per item of the row kernel
-constexpr int kAttnF32Tile = 32;
+cudaError_t launch_attn_tiles(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, int D, int grid,
+                              cudaStream_t s);
 inline int attn_grid(int sms) { return 2 * sms; }   // CTAs of the largest grid: two per SM
 
 struct TablesArgs {

@@ -1,0 +1,407 @@
+// Attention of new tokens over the paged cache, bf16, for chunks of tokens: both
+// products on the tensor cores (tcgen05, accumulators in tensor memory).
+//
+//   out[t, head] = sum_j softmax_j(scale q[t, head] . k[j]) v[j],
+//   j in (pos - window, pos], pos = seq_len - new + t
+//
+// An item is 256 query rows (all heads of one kv head's group, token-major, so
+// that a key tile serves the whole group) as two M = 128 tiles A and B.  Per 128
+// keys and tile: S = Q K^T (128 x 128, K-major operands from shared memory), the
+// softmax in registers, one thread per row, P in bf16 back into tensor memory over
+// S, and O += P V with P as the tensor-memory operand and V as an MN-major
+// operand, straight from its [key][d] layout.  While one tile is in the softmax
+// the tensor cores work on the other.
+//
+// The running maximum m is only raised (and O, l rescaled by 2^(m - m')) when a
+// score exceeds it by more than 2^8: P stays below 256, which bf16 and fp32 hold
+// with the same relative precision, and the rescaling of O through tensor memory
+// becomes rare.  O and l are divided once at the end, so the choice of m cancels.
+//
+// Roles (three warpgroups): warps 0..3 and 4..7 softmax and output of tiles A and B;
+// warp 8 loads K and V tiles by TMA, one box per page and 64-column half; warp 9
+// issues the MMAs.  A softmax thread holds its row's 128 scores, so the third
+// warpgroup gives registers up: launched with 168 each (384 x 168 = 64512), 216 for
+// the first two and 72 for the third (256 x 216 + 128 x 72 = 64512).  Tensor memory
+// (512 columns): S/P of A, S/P of B, O of A, O of B.
+#include "attn_internal.cuh"
+#include "sm103.cuh"
+
+namespace moeslot {
+namespace {
+using namespace sm103;
+
+constexpr int NT = 384, BM = kAttnTile, UNIT = 128;
+constexpr float kRaise = 8.f;                  // log2 of the growth of P that m lets pass
+
+template <int D>
+struct TileCfg {
+  static constexpr int kHalf = UNIT * 128;               // bytes of a 64-column half of a 128-row tile
+  static constexpr int kTile = kHalf * (D / 64);
+  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kBytes = (2 + kStages) * kTile + 1024;
+};
+
+template <int D>
+__global__ __launch_bounds__(NT, 1) void attn_tiles_kernel(const __grid_constant__ CUtensorMap mk,
+                                                           const __grid_constant__ CUtensorMap mv, const AttnArgs a) {
+  using C = TileCfg<D>;
+  extern __shared__ uint8_t raw[];
+  __shared__ int32_t sched[64];
+  __shared__ __align__(8) uint64_t full[C::kStages], empty[C::kStages], edge, drain, q_full[2], s_full[2], p_full[2], o_full[2];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int32_t last_flag[2];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sq = smem_addr(smem), ring = sq + 2 * C::kTile;
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  if (tid == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      bar_init(full + s, 1);
+      bar_init(empty + s, 1);
+    }
+    bar_init(&edge, 1);
+    bar_init(&drain, 1);
+    for (int t = 0; t < 2; ++t) {
+      bar_init(q_full + t, 128);
+      bar_init(s_full + t, 1);
+      bar_init(p_full + t, 128);
+      bar_init(o_full + t, 1);
+    }
+    bar_init_done();
+  }
+  AttnSplit sp;
+  AttnCursor c;
+  if (!attn_find_range<BM, NT>(a, UNIT, 1, sched, sp, c)) return;      // the same answer in every thread
+  if (wid == 9) tmem_alloc(&tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+
+  bool alive = true;
+  auto wait = [&](uint64_t* b, uint32_t parity) {                      // bounded; after a timeout nothing waits any more
+    if (alive && !bar_wait(b, parity)) {
+      alive = false;
+      attn_status(a.status, MOE_ERR_TIMEOUT);
+    }
+  };
+
+  if (wid >= 8) {
+  regs_give<72>();
+  if (wid == 8) {
+    // ---------------------------------------------------------------- loads
+    const int row_limit = (int)((int64_t)a.num_pages * a.Hkv * a.page);   // out of range: zeros arrive
+    const int box = min(a.page, UNIT), boxes = UNIT / box;
+    const bool mine = lane < boxes * (D / 64);
+    const int my_box = lane % boxes, my_half = lane / boxes;
+    uint32_t n = 0, edges = 0;
+    do {
+      const int first = (c.i * BM) / a.group, last = min(c.q.n - 1, ((c.i + 1) * BM - 1) / a.group);
+      const int hi = c.q.seq - c.q.n + last + 1;
+      const int lo = a.window > 0 ? max(0, c.q.seq - c.q.n + first - a.window + 1) : 0;
+      const int units = attn_piece(c);
+      for (int j = 0; j < units; ++j) {
+        const int key0 = (c.u0 + c.at + j) * UNIT, key = key0 + my_box * box;
+        int at = row_limit;
+        if (mine && key < c.q.seq) {
+          const int page = a.table[(size_t)c.r * a.table_stride + (key >> a.page_log2)];
+          if ((uint32_t)page < (uint32_t)a.num_pages) at = ((page * a.Hkv + c.h) << a.page_log2) + (key & (a.page - 1));
+          else attn_status(a.status, MOE_ERR_BOUNDS);
+        }
+        for (int kv = 0; kv < 2; ++kv, ++n) {
+          const int st = n % C::kStages;
+          const uint32_t stage = ring + st * C::kTile;
+          wait(empty + st, ((n / C::kStages) & 1) ^ 1);
+          __syncwarp();
+          // values of keys that no row of the item sees may be anything (0 x NaN is NaN): they are
+          // zeroed here, in the first and last unit of an item
+          const bool clean = kv == 1 && (key0 < lo || key0 + UNIT > hi);
+          uint64_t* bar = clean ? &edge : full + st;
+          if (lane == 0) bar_expect(bar, C::kTile);
+          __syncwarp();
+          if (mine) tma_3d(stage + my_half * C::kHalf + my_box * box * 128, kv ? &mv : &mk, bar, 0, at, my_half);
+          if (clean) {
+            wait(&edge, edges & 1);
+            ++edges;
+            __syncwarp();
+            for (int r = lane; r < UNIT; r += 32) {
+              if (key0 + r >= lo && key0 + r < hi) continue;
+              for (int h = 0; h < D / 64; ++h)
+                for (int ch = 0; ch < 8; ++ch)
+                  *reinterpret_cast<uint4*>(smem + (stage - sq) + h * C::kHalf + r * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) bar_arrive(full + st);
+          }
+        }
+      }
+    } while (attn_next<BM>(a, UNIT, c));
+    if (!alive)                                          // bounded: copies in flight land before the memory is given up
+      for (uint32_t k = n > C::kStages ? n - C::kStages : 0; k < n; ++k) bar_wait(full + k % C::kStages, (k / C::kStages) & 1);
+  } else if (wid == 9) {
+    // ----------------------------------------------------------------- MMAs
+    if (lane == 0) {
+      constexpr uint32_t kS = tc_idesc(UNIT, false), kO = tc_idesc(D, true);
+      uint32_t n = 0;                                    // ring position
+      uint32_t np[2] = {0, 0}, pieces[2] = {0, 0};       // P tiles and Q tiles taken
+      auto scores = [&](int t, uint32_t stage) {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = (k >> 2) * C::kHalf + (k & 3) * 32;
+          tc_mma_ss(tmem + t * UNIT, tc_desc(sq + t * C::kTile + off, 16), tc_desc(stage + off, 16), kS, k > 0);
+        }
+        tc_commit(s_full + t);
+      };
+      do {
+        const int rows = min(BM, c.q.n * a.group - c.i * BM), tiles = rows > 128 ? 2 : 1;
+        const int units = attn_piece(c);
+        wait(full + n % C::kStages, (n / C::kStages) & 1);
+        for (int t = 0; t < tiles; ++t) {
+          wait(q_full + t, pieces[t]++ & 1);
+          tc_fence_after();
+          scores(t, ring + n % C::kStages * C::kTile);
+        }
+        tc_commit(empty + n % C::kStages);
+        ++n;
+        for (int j = 0; j < units; ++j) {
+          const uint32_t vs = n % C::kStages, ks = (n + 1) % C::kStages;
+          const bool more = j + 1 < units;
+          wait(full + vs, (n / C::kStages) & 1);
+          for (int t = 0; t < tiles; ++t) {
+            wait(p_full + t, np[t]++ & 1);
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < UNIT / 16; ++k)
+              tc_mma_ts(tmem + 256 + t * 128, tmem + t * UNIT + k * 8,
+                        tc_desc(ring + vs * C::kTile + k * 2048, C::kHalf), kO, (j > 0 || k > 0));
+            if (more) {
+              if (t == 0) wait(full + ks, ((n + 1) / C::kStages) & 1);
+              scores(t, ring + ks * C::kTile);
+            } else {
+              tc_commit(o_full + t);
+            }
+          }
+          tc_commit(empty + vs);
+          if (more) tc_commit(empty + ks);
+          n += more ? 2 : 1;
+        }
+      } while (attn_next<BM>(a, UNIT, c));
+      if (!alive) {                                      // bounded: products in flight end before the memory is given up
+        tc_commit(&drain);
+        bar_wait(&drain, 0);
+      }
+    }
+    __syncwarp();
+  }
+  } else {
+    regs_take<216>();
+    // ------------------------------------------------- softmax and output of tile t
+    const int t = wid >> 2, row = (wid & 3) * 32 + lane;
+    const uint32_t lanes = tmem + ((uint32_t)(wid & 3) << 21);        // this warp's 32 lanes of tensor memory
+    const uint32_t s_addr = lanes + t * UNIT, o_addr = lanes + 256 + t * 128;
+    uint32_t ns = 0, no = 0;
+    auto load_q = [&](const AttnCursor& x) {             // this thread's row of tile t, 128-byte swizzled
+      const int f = x.i * BM + t * 128 + row;
+      const bool live = f < x.q.n * a.group;
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q);
+      if (live) src += (size_t)(x.q.start + f / a.group) * a.q_stride + (size_t)(x.h * a.group + f % a.group) * D;
+      const uint32_t dst = sq + t * C::kTile + row * 128;
+#pragma unroll
+      for (int ch = 0; ch < D / 8; ++ch)
+        cp_async16(dst + (ch >> 3) * C::kHalf + (((ch & 7) ^ (row & 7)) << 4), src + ch * 8, live ? 16 : 0);
+    };
+    auto has_tile = [&](const AttnCursor& x) { return x.q.n * a.group - x.i * BM > t * 128; };
+    bool mine = has_tile(c);
+    if (mine) {
+      load_q(c);
+      cp_async_wait();
+      fence_async_smem();
+      bar_arrive(q_full + t);
+    }
+    bool more;
+    do {
+      AttnCursor nx = c;
+      more = attn_next<BM>(a, UNIT, nx);
+      const bool next_mine = more && has_tile(nx);
+      if (!mine) {                                       // an item of 128 rows or fewer has no tile B
+        if (next_mine) {
+          load_q(nx);
+          cp_async_wait();
+          fence_async_smem();
+          bar_arrive(q_full + t);
+        }
+        c = nx;
+        mine = next_mine;
+        continue;
+      }
+      const int rows = min(BM, c.q.n * a.group - c.i * BM) - t * 128;     // of this tile (may exceed 128)
+      const int f = c.i * BM + t * 128 + row, base_pos = c.q.seq - c.q.n;
+      const int pos = row < rows ? base_pos + f / a.group : -1;
+      const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+      // keys that every row of this tile sees need no mask
+      const int f0 = c.i * BM + t * 128, f1 = f0 + min(rows, 128) - 1;
+      const int all_hi = base_pos + f0 / a.group + 1;
+      const int all_lo = a.window > 0 ? max(0, base_pos + f1 / a.group - a.window + 1) : 0;
+      float m = -INFINITY, l = 0.f;
+      const int units = attn_piece(c);
+      for (int j = 0; j < units; ++j) {
+        const int key0 = (c.u0 + c.at + j) * UNIT;
+        wait(s_full + t, ns++ & 1);
+        __syncwarp();
+        tc_fence_after();
+        float s[UNIT];
+        tmem_ld64(s_addr, s);
+        tmem_ld64(s_addr + 64, s + 64);
+        if (j == units - 1 && next_mine) load_q(nx);     // every product that reads this tile's Q has ended
+        if (key0 < all_lo || key0 + UNIT > all_hi) {
+#pragma unroll
+          for (int i = 0; i < UNIT; ++i)
+            if (key0 + i < lo || key0 + i > pos) s[i] = -INFINITY;
+        }
+        float top[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int i = 4; i < UNIT; ++i) top[i & 3] = fmaxf(top[i & 3], s[i]);
+        const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
+        const bool raise = mx > m + kRaise || (m == -INFINITY && mx > m);
+        float fac = 1.f;
+        if (raise) {
+          fac = ex2(m - mx);                             // 0 from -inf
+          m = mx;
+          l *= fac;
+        }
+        if (j > 0 && __any_sync(0xffffffffu, raise)) {
+#pragma unroll 1
+          for (int d = 0; d < D; d += 32) {
+            float o[32];
+            tmem_ld32(o_addr + d, o);
+            uint32_t w[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(o[i] * fac);
+            tmem_st32(o_addr + d, w);
+          }
+        }
+        const float neg = m == -INFINITY ? 0.f : -m;     // no key yet: every exponential is 0, not NaN
+        const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2), neg2 = pack2(neg, neg);
+        uint64_t sum2[2] = {0, 0};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t w[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            float x, y;
+            unpack2(fma2(pack2(s[64 * h + 2 * i], s[64 * h + 2 * i + 1]), scale2, neg2), x, y);
+            x = ex2(x);
+            y = ex2(y);
+            sum2[i & 1] = add2(sum2[i & 1], pack2(x, y));
+            w[i] = pack_bf16(x, y);
+          }
+          tmem_st32(s_addr + 32 * h, w);
+        }
+        float x, y;
+        unpack2(add2(sum2[0], sum2[1]), x, y);
+        l += x + y;
+        tc_wait_st();
+        tc_fence_before();
+        bar_arrive(p_full + t);
+      }
+      if (next_mine) {
+        cp_async_wait();
+        fence_async_smem();
+        bar_arrive(q_full + t);
+      }
+      wait(o_full + t, no++ & 1);
+      __syncwarp();
+      tc_fence_after();
+      const bool whole = units == c.nu;
+      const size_t part = ((size_t)attn_slot(c) * BM + t * 128 + row);
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out);
+      if (row < rows) dst += ((size_t)(c.q.start + f / a.group) * a.Hq + c.h * a.group + f % a.group) * D;
+#pragma unroll 1
+      for (int d = 0; d < D; d += 32) {
+        float o[32];
+        __syncwarp();
+        tmem_ld32(o_addr + d, o);
+        if (row >= rows) continue;
+        if (whole) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 8) {
+            uint4 w;
+            w.x = pack_bf16(o[i] * inv, o[i + 1] * inv);
+            w.y = pack_bf16(o[i + 2] * inv, o[i + 3] * inv);
+            w.z = pack_bf16(o[i + 4] * inv, o[i + 5] * inv);
+            w.w = pack_bf16(o[i + 6] * inv, o[i + 7] * inv);
+            *reinterpret_cast<uint4*>(dst + d + i) = w;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            attn_store4(a.part_o + part * D + d + i, make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]));
+        }
+      }
+      if (!whole) {
+        if (row < rows) a.part_ml[part] = make_float2(m, l);
+        const int c0 = sp.owner(c.item_first), n = sp.owner(c.item_first + c.nu - 1) - c0 + 1;
+        __threadfence();
+        named_sync(1 + t, 128);
+        if (tid == t * 128) {
+          const bool last = atomicAdd(a.arrived + 2 * c0 + t, 1u) == (uint32_t)(n - 1);
+          if (last) a.arrived[2 * c0 + t] = 0;
+          last_flag[t] = last;
+        }
+        named_sync(1 + t, 128);
+        if (last_flag[t]) {                              // the item's last piece to arrive joins tile t, in piece order
+          __threadfence();
+          constexpr int LANES = D / 4, STEP = 128 / LANES;
+          const int d = (tid % LANES) * 4;
+          for (int r = (tid & 127) / LANES; r < min(rows, 128); r += STEP) {
+            float M = -INFINITY;
+            for (int p = 0; p < n; ++p)
+              M = fmaxf(M, __ldcg(a.part_ml + (size_t)(2 * (c0 + p) + (p == 0)) * BM + t * 128 + r).x);
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            float sum = 0.f;
+            if (M > -INFINITY) {
+              for (int p = 0; p < n; ++p) {
+                const size_t at = (size_t)(2 * (c0 + p) + (p == 0)) * BM + t * 128 + r;
+                const float2 ml = __ldcg(a.part_ml + at);
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D + d));
+                const float g = ex2(ml.x - M);
+                sum += g * ml.y;
+                o.x += g * v.x; o.y += g * v.y; o.z += g * v.z; o.w += g * v.w;
+              }
+              const float in = 1.f / sum;
+              o.x *= in; o.y *= in; o.z *= in; o.w *= in;
+            }
+            const int fr = c.i * BM + t * 128 + r;
+            attn_store4(static_cast<__nv_bfloat16*>(a.out) +
+                            ((size_t)(c.q.start + fr / a.group) * a.Hq + c.h * a.group + fr % a.group) * D + d, o);
+          }
+        }
+      }
+      c = nx;
+      mine = next_mine;
+    } while (more);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (wid == 9) tmem_free(tmem, 512);
+}
+
+template <int D>
+cudaError_t launch(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, int grid, cudaStream_t s) {
+  const cudaError_t e =
+      cudaFuncSetAttribute(attn_tiles_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, TileCfg<D>::kBytes);
+  if (e != cudaSuccess) return e;
+  attn_tiles_kernel<D><<<grid, NT, TileCfg<D>::kBytes, s>>>(mk, mv, a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attn_tiles(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, int D, int grid,
+                              cudaStream_t s) {
+  return D == 64 ? launch<64>(a, mk, mv, grid, s) : launch<128>(a, mk, mv, grid, s);
+}
+
+}  // namespace moeslot
