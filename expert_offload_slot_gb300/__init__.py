@@ -363,34 +363,43 @@ def make_attn_config(num_q_heads, num_kv_heads, head_dim, page_size, dtype=MOE_B
     return c
 
 
-def _typed(name, t, dtype, shape=None):
-    """The binding passes addresses: a tensor of another type, shape or device must not reach them."""
-    import torch
-    kind = {MOE_F32: torch.float32, MOE_BF16: torch.bfloat16, "i32": torch.int32}[dtype]
-    if t.dtype != kind or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor of {kind}, got {t.dtype} on {t.device}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    return t
+# The calls below run once per layer and step, beside kernels of a few microseconds, so their checks
+# are written flat: type, device, shape and layout of each tensor, since the library sees addresses only.
+_kinds = {}
 
 
-def _rows(name, t, dtype, width=None):
-    """A 2-d (or head-split 3-d) tensor whose rows are contiguous: its row stride in elements."""
-    _typed(name, t, dtype)
-    inner = 1
-    for n, st in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
-        if n != 1 and st != inner:
-            raise ValueError(f"the rows of {name} must be contiguous")
-        inner *= n
-    if t.dim() < 2 or (width is not None and inner != width):
-        raise ValueError(f"{name} must have rows of {width} elements, got {tuple(t.shape)}")
-    return t.stride(0) if t.shape[0] > 1 else max(inner, t.stride(0))
+def _torch_kinds():
+    """(float32, bfloat16, int32) and the raw-stream getter, looked up once."""
+    if not _kinds:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _kinds["stream"] = raw or (lambda device: torch.cuda.current_stream(device).cuda_stream)
+        _kinds[MOE_F32], _kinds[MOE_BF16], _kinds["i32"] = torch.float32, torch.bfloat16, torch.int32
+    return _kinds
 
 
-def _flat(name, t, dtype, shape=None):
-    if not _typed(name, t, dtype, shape).is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t
+def _refuse(name, t, kind, shape):
+    raise ValueError(f"{name} must be a contiguous CUDA tensor of {kind} and shape {tuple(shape)}, "
+                     f"got {t.dtype}, {tuple(t.shape)}, strides {t.stride()}, on {t.device}")
+
+
+def _flat(name, t, kind, shape):
+    """Address of a contiguous CUDA tensor of exactly this type and shape."""
+    if t.dtype is not kind or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        _refuse(name, t, kind, shape)
+    return t.data_ptr()
+
+
+def _rows(name, t, kind, rows, inner):
+    """Address and row stride in elements of a CUDA tensor [rows, *inner] whose rows are contiguous."""
+    if t.dtype is not kind or t.shape != (rows, *inner) or not t.is_cuda:
+        _refuse(name, t, kind, (rows, *inner))
+    width = 1
+    for n, st in zip(reversed(inner), reversed(t.stride())):
+        if n != 1 and st != width:
+            _refuse(name, t, kind, (rows, *inner))
+        width *= n
+    return t.data_ptr(), (t.stride(0) if rows > 1 else width)
 
 
 class Attention:
@@ -406,6 +415,13 @@ class Attention:
         h = _vp()
         _check(_lib.moe_attn_create(ctypes.byref(cfg), device, ctypes.byref(h)), "moe_attn_create")
         self.h = h.value
+        kinds = _torch_kinds()
+        self._kind, self._i32, self._f32 = kinds[cfg.dtype], kinds["i32"], kinds[MOE_F32]
+        self._current, self._device = kinds["stream"], device
+        self._q_shape = (cfg.num_q_heads, cfg.head_dim)
+        self._qkv_shape = ((cfg.num_q_heads + 2 * cfg.num_kv_heads) * cfg.head_dim,)
+        self._page_shape = (cfg.num_kv_heads, cfg.page_size, cfg.head_dim)
+        self._norm_shape, self._rotary = (cfg.head_dim,), cfg.rotary_dim
 
     def close(self):
         if self.h:
@@ -418,60 +434,51 @@ class Attention:
         except Exception:
             pass
 
-    def _caches(self, k_cache, v_cache):
-        c = self.cfg
-        shape = (k_cache.shape[0], c.num_kv_heads, c.page_size, c.head_dim)
-        _flat("k_cache", k_cache, c.dtype, shape)
-        _flat("v_cache", v_cache, c.dtype, shape)
-        return k_cache.data_ptr(), v_cache.data_ptr(), shape[0]
+    def _on(self, stream):
+        return self._current(self._device) if stream is None else _stream(stream)
 
     def tables(self, ctx_len, new_len, block_table, free_pages, free_head, free_head_out, row_start, seq_len, positions,
                slot_map, stream=None):
         """Fill block_table, free_head_out, row_start, seq_len, positions and slot_map for the step."""
-        R, rows = ctx_len.shape[0], positions.shape[0]
-        for name, t, shape in (("ctx_len", ctx_len, (R,)), ("new_len", new_len, (R,)), ("free_head", free_head, (1,)),
-                               ("free_head_out", free_head_out, (1,)), ("row_start", row_start, (R + 1,)),
-                               ("seq_len", seq_len, (R,)), ("positions", positions, (rows,)),
-                               ("slot_map", slot_map, (rows,)), ("block_table", block_table, (R, block_table.shape[1])),
-                               ("free_pages", free_pages, (free_pages.shape[0],))):
-            _flat(name, t, "i32", shape)
-        _check(_lib.moe_attn_tables(self.h, ctx_len.data_ptr(), new_len.data_ptr(), R, block_table.data_ptr(),
-                                    block_table.shape[1], free_pages.data_ptr(), free_pages.shape[0],
-                                    free_head.data_ptr(), free_head_out.data_ptr(), rows, row_start.data_ptr(),
-                                    seq_len.data_ptr(), positions.data_ptr(), slot_map.data_ptr(), _stream(stream)),
-               "moe_attn_tables")
+        i32, n, rows, free, width = self._i32, len(ctx_len), len(positions), len(free_pages), block_table.shape[1]
+        one, per = (1,), (n,)
+        st = _lib.moe_attn_tables(
+            self.h, _flat("ctx_len", ctx_len, i32, per), _flat("new_len", new_len, i32, per), n,
+            _flat("block_table", block_table, i32, (n, width)), width, _flat("free_pages", free_pages, i32, (free,)), free,
+            _flat("free_head", free_head, i32, one), _flat("free_head_out", free_head_out, i32, one), rows,
+            _flat("row_start", row_start, i32, (n + 1,)), _flat("seq_len", seq_len, i32, per),
+            _flat("positions", positions, i32, (rows,)), _flat("slot_map", slot_map, i32, (rows,)), self._on(stream))
+        if st:
+            _check(st, "moe_attn_tables")
 
     def qkv(self, qkv, q_norm, k_norm, rope, positions, slot_map, q, k_cache, v_cache, stream=None):
         """Norm, rotation and cache write of qkv [rows, (Hq + 2 Hkv) * D]; queries go to q [rows, Hq, D]."""
-        c = self.cfg
-        rows, D = qkv.shape[0], c.head_dim
-        stride = _rows("qkv", qkv, c.dtype, (c.num_q_heads + 2 * c.num_kv_heads) * D)
-        for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
-            if w is not None:
-                _flat(name, w, c.dtype, (D,))
-        if rope is not None:
-            _flat("rope", rope, MOE_F32, (rope.shape[0], c.rotary_dim))
-        _flat("positions", positions, "i32", (rows,))
-        _flat("slot_map", slot_map, "i32", (rows,))
-        _flat("q", q, c.dtype, (rows, c.num_q_heads, D))
-        kp, vp, pages = self._caches(k_cache, v_cache)
-        _check(_lib.moe_attn_qkv(self.h, qkv.data_ptr(), stride, rows, _ptr(q_norm), _ptr(k_norm), _ptr(rope),
-                                 0 if rope is None else rope.shape[0], positions.data_ptr(), slot_map.data_ptr(),
-                                 q.data_ptr(), kp, vp, pages, _stream(stream)), "moe_attn_qkv")
+        kind, i32, rows, pages = self._kind, self._i32, len(qkv), len(k_cache)
+        length = 0 if rope is None else len(rope)
+        at, stride = _rows("qkv", qkv, kind, rows, self._qkv_shape)
+        st = _lib.moe_attn_qkv(
+            self.h, at, stride, rows, None if q_norm is None else _flat("q_norm", q_norm, kind, self._norm_shape),
+            None if k_norm is None else _flat("k_norm", k_norm, kind, self._norm_shape),
+            None if rope is None else _flat("rope", rope, self._f32, (length, self._rotary)), length,
+            _flat("positions", positions, i32, (rows,)), _flat("slot_map", slot_map, i32, (rows,)),
+            _flat("q", q, kind, (rows, *self._q_shape)), _flat("k_cache", k_cache, kind, (pages, *self._page_shape)),
+            _flat("v_cache", v_cache, kind, (pages, *self._page_shape)), pages, self._on(stream))
+        if st:
+            _check(st, "moe_attn_qkv")
 
     def forward(self, q, row_start, seq_len, max_new, k_cache, v_cache, block_table, out, stream=None):
         """Attention of q [rows, Hq, D] over the cache, into out [rows, Hq, D]."""
-        c = self.cfg
-        rows, R = q.shape[0], seq_len.shape[0]
-        stride = _rows("q", q, c.dtype, c.num_q_heads * c.head_dim)
-        _flat("row_start", row_start, "i32", (R + 1,))
-        _flat("seq_len", seq_len, "i32", (R,))
-        _flat("block_table", block_table, "i32", (R, block_table.shape[1]))
-        _flat("out", out, c.dtype, (rows, c.num_q_heads, c.head_dim))
-        kp, vp, pages = self._caches(k_cache, v_cache)
-        _check(_lib.moe_attn_forward(self.h, q.data_ptr(), stride, rows, row_start.data_ptr(), seq_len.data_ptr(), R,
-                                     max_new, kp, vp, pages, block_table.data_ptr(), block_table.shape[1],
-                                     out.data_ptr(), _stream(stream)), "moe_attn_forward")
+        kind, i32, rows, n, pages, width = (self._kind, self._i32, len(q), len(seq_len), len(k_cache),
+                                            block_table.shape[1])
+        at, stride = _rows("q", q, kind, rows, self._q_shape)
+        st = _lib.moe_attn_forward(
+            self.h, at, stride, rows, _flat("row_start", row_start, i32, (n + 1,)), _flat("seq_len", seq_len, i32, (n,)), n,
+            max_new, _flat("k_cache", k_cache, kind, (pages, *self._page_shape)),
+            _flat("v_cache", v_cache, kind, (pages, *self._page_shape)), pages,
+            _flat("block_table", block_table, i32, (n, width)), width, _flat("out", out, kind, (rows, *self._q_shape)),
+            self._on(stream))
+        if st:
+            _check(st, "moe_attn_forward")
 
     def status(self):
         return _lib.moe_attn_get_status(self.h)
@@ -482,15 +489,17 @@ class Attention:
 
 def moe_sample(logits, u, ids, logp=None, temperature=None, top_k=None, top_p=None, min_p=None, stream=None):
     """Next token of each row of logits [rows, vocab] into ids (and its log probability into logp)."""
-    import torch
+    kinds = _torch_kinds()
+    f32, i32 = kinds[MOE_F32], kinds["i32"]
     rows, vocab = logits.shape
-    dtype = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}.get(logits.dtype)
-    if dtype is None:
-        raise ValueError(f"logits must be float32 or bfloat16, got {logits.dtype}")
-    stride = _rows("logits", logits, dtype, vocab)
-    for name, t, kind in (("u", u, MOE_F32), ("ids", ids, "i32"), ("logp", logp, MOE_F32), ("top_k", top_k, "i32"),
-                          ("temperature", temperature, MOE_F32), ("top_p", top_p, MOE_F32), ("min_p", min_p, MOE_F32)):
-        if t is not None:
-            _flat(name, t, kind, (rows,))
-    _check(_lib.moe_sample(logits.data_ptr(), dtype, rows, vocab, stride, _ptr(temperature), _ptr(top_k), _ptr(top_p),
-                           _ptr(min_p), u.data_ptr(), ids.data_ptr(), _ptr(logp), _stream(stream)), "moe_sample")
+    per = (rows,)
+    dtype = MOE_F32 if logits.dtype is f32 else MOE_BF16
+    at, stride = _rows("logits", logits, f32 if dtype == MOE_F32 else kinds[MOE_BF16], rows, (vocab,))
+    st = _lib.moe_sample(
+        at, dtype, rows, vocab, stride, None if temperature is None else _flat("temperature", temperature, f32, per),
+        None if top_k is None else _flat("top_k", top_k, i32, per), None if top_p is None else _flat("top_p", top_p, f32, per),
+        None if min_p is None else _flat("min_p", min_p, f32, per), _flat("u", u, f32, per), _flat("ids", ids, i32, per),
+        None if logp is None else _flat("logp", logp, f32, per),
+        kinds["stream"](logits.device.index) if stream is None else _stream(stream))
+    if st:
+        _check(st, "moe_sample")

@@ -104,6 +104,9 @@ MOE_API moe_status moe_attn_create(const moe_attn_config* cfg, int device, moe_a
   if (device < 0 || device >= ndev) return fail(MOE_ERR_INVALID, "device %d out of range", device);
   e = cudaSetDevice(device);
   if (e != cudaSuccess) return launched(e, "cudaSetDevice");
+  e = cfg->dtype == MOE_F32 ? prepare_attn_f32(cfg->head_dim) : prepare_attn_rows(cfg->head_dim);
+  if (e == cudaSuccess && cfg->dtype == MOE_BF16) e = prepare_attn_tiles(cfg->head_dim);
+  if (e != cudaSuccess) return launched(e, "preparing the attention kernels");
   moe_attn* A = new (std::nothrow) moe_attn;
   if (!A) return fail(MOE_ERR_OOM, "host allocation failed");
   A->cfg = *cfg;

@@ -268,6 +268,10 @@ __device__ __forceinline__ void attn_join(const AttnArgs& a, const AttnCursor& c
 }
 
 // ------------------------------------------------------------------ launchers
+// prepare_*: once per device, before the first launch
+cudaError_t prepare_attn_f32(int D);
+cudaError_t prepare_attn_rows(int D);
+cudaError_t prepare_attn_tiles(int D);
 cudaError_t launch_attn_f32(const AttnArgs& a, int D, int grid, cudaStream_t s);
 cudaError_t launch_attn_rows(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, int D, int grid,
                              cudaStream_t s);

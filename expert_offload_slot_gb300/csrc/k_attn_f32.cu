@@ -142,16 +142,24 @@ __global__ __launch_bounds__(NT) void attn_f32_kernel(const AttnArgs a) {
 }
 
 template <int D>
+constexpr int f32_bytes() {
+  return ((BM + 2 * BN) * (D + 4) + BM * (BN + 1)) * 4;
+}
+
+template <int D>
 cudaError_t launch(const AttnArgs& a, int grid, cudaStream_t s) {
-  constexpr int bytes = ((BM + 2 * BN) * (D + 4) + BM * (BN + 1)) * 4;
-  const cudaError_t e =
-      cudaFuncSetAttribute(attn_f32_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != cudaSuccess) return e;
-  attn_f32_kernel<D><<<grid, NT, bytes, s>>>(a);
+  attn_f32_kernel<D><<<grid, NT, f32_bytes<D>(), s>>>(a);
   return cudaGetLastError();
 }
 
+template <int D>
+cudaError_t prepare() {
+  return cudaFuncSetAttribute(attn_f32_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, f32_bytes<D>());
+}
+
 }  // namespace
+
+cudaError_t prepare_attn_f32(int D) { return D == 64 ? prepare<64>() : prepare<128>(); }
 
 cudaError_t launch_attn_f32(const AttnArgs& a, int D, int grid, cudaStream_t s) {
   return D == 64 ? launch<64>(a, grid, s) : launch<128>(a, grid, s);

@@ -308,14 +308,18 @@ __global__ __launch_bounds__(NT, 1) void attn_rows_kernel(const __grid_constant_
 
 template <int D>
 cudaError_t launch(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, int grid, cudaStream_t s) {
-  const cudaError_t e =
-      cudaFuncSetAttribute(attn_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, RowsCfg<D>::kBytes);
-  if (e != cudaSuccess) return e;
   attn_rows_kernel<D><<<grid, NT, RowsCfg<D>::kBytes, s>>>(mk, mv, a);
   return cudaGetLastError();
 }
 
+template <int D>
+cudaError_t prepare() {
+  return cudaFuncSetAttribute(attn_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, RowsCfg<D>::kBytes);
+}
+
 }  // namespace
+
+cudaError_t prepare_attn_rows(int D) { return D == 64 ? prepare<64>() : prepare<128>(); }
 
 cudaError_t launch_attn_rows(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, int D, int grid,
                              cudaStream_t s) {

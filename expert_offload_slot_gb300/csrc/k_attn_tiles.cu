@@ -390,14 +390,18 @@ __global__ __launch_bounds__(NT, 1) void attn_tiles_kernel(const __grid_constant
 
 template <int D>
 cudaError_t launch(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, int grid, cudaStream_t s) {
-  const cudaError_t e =
-      cudaFuncSetAttribute(attn_tiles_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, TileCfg<D>::kBytes);
-  if (e != cudaSuccess) return e;
   attn_tiles_kernel<D><<<grid, NT, TileCfg<D>::kBytes, s>>>(mk, mv, a);
   return cudaGetLastError();
 }
 
+template <int D>
+cudaError_t prepare() {
+  return cudaFuncSetAttribute(attn_tiles_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, TileCfg<D>::kBytes);
+}
+
 }  // namespace
+
+cudaError_t prepare_attn_tiles(int D) { return D == 64 ? prepare<64>() : prepare<128>(); }
 
 cudaError_t launch_attn_tiles(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, int D, int grid,
                               cudaStream_t s) {
