@@ -12,11 +12,15 @@
 // to e^-27.7 of the largest.
 //
 // A cluster of CTAs holds a row: each CTA keeps its share of the logits in shared
-// memory, so HBM is read once, and the cut of top-k and that of top-p are each
-// found by a radix descent over the ordered bits of x (four bits a pass; a bf16
-// logit has 16, an fp32 one 32).  In a pass every thread adds (count, mass) of its
-// own logits to its own 16 counters in shared memory — no atomics — and the
-// cluster adds up the counters over distributed shared memory.
+// memory, so HBM is read once.  A cut (of top-k by count, of top-p by mass) is found
+// over the distance d = max x - x in [0, 28 T), beyond which no token has weight:
+// one pass adds the tokens up in 2048 bins of count or 1024 of mass with shared-memory
+// atomics on integers, the cluster adds its CTAs' bins over distributed shared memory,
+// and the tokens of the bin that holds the cut are collected and sorted by (x, index).
+// Where top-k leaves 2048 tokens or fewer down to the end of that bin, all of them are
+// collected instead and the first CTA does the rest on its sorted list.  A bin with
+// more tokens than the list holds (equal logits) is resolved by a radix descent over
+// the ordered bits of x and a count of the ties in index order.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -25,12 +29,18 @@
 #include "sample_internal.cuh"
 
 namespace moeslot {
+int sm_count();
+
 namespace {
 namespace cg = cooperative_groups;
 typedef unsigned long long u64;
 
-constexpr int NT = 512, NWARP = NT / 32, BINS = 16;
+constexpr int NT = 512, NWARP = NT / 32, BINS = 16, PAR = 4;
 constexpr int kMaxCluster = 8;
+constexpr int kShared = 230400;                // dynamic shared memory of a CTA, beside about 1 KB of static
+static_assert(((int64_t)kShared - 8 * 16 * 512) / 4 / 8 * 8 * kMaxCluster >= MOE_SAMPLE_MAX_VOCAB, "the largest row must fit");
+constexpr int kList = 2048;                    // tokens that are collected and sorted
+constexpr int kCountBins = 2048, kMassBins = 1024, kCountShift = 13, kMassShift = 14;
 constexpr u64 kMassMask = (1ull << 48) - 1;    // a thread's counter: count in the top 16 bits, mass below
 
 struct Exchange {                              // what a CTA shows its cluster; two of them take turns
@@ -40,24 +50,77 @@ struct Exchange {                              // what a CTA shows its cluster; 
   int32_t first;
 };
 
-// Order-preserving key; -0 counts as +0, NaN as -inf.
+struct Cut {                                   // kept: key above it, or equal and index not above it
+  uint32_t key;
+  int32_t index;
+};
+
+template <typename T>
+__device__ __forceinline__ float value(T x) {  // NaN counts as -inf, -0 as +0
+  const float f = (float)x + 0.f;
+  return f == f ? f : -INFINITY;
+}
+// Order-preserving key.
 __device__ __forceinline__ uint32_t key_of(float x) {
-  const uint32_t u = __float_as_uint(x + 0.f);
+  const uint32_t u = __float_as_uint(x);
   return (u >> 31) ? ~u : u | 0x80000000u;
 }
-__device__ __forceinline__ float value_of(uint32_t key) {
-  return __uint_as_float((key >> 31) ? key & 0x7fffffffu : ~key);
-}
-__device__ __forceinline__ u64 weight_of(float x, float best, float temp) {
-  if (x == best) return 1ull << 40;
-  const float e = expf((x - best) / temp) * 1099511627776.f;
-  return e >= 1.f ? (u64)e : 0ull;             // NaN (inf temperature against -inf) compares false
-}
-
+// z / T and the weight.  The quotient is the correctly rounded one: with r = 1/T correctly
+// rounded, a quotient within one unit in the last place becomes the rounded one by one more step
+// q + (z - q T) r in fused arithmetic (Markstein), and the first step makes it that close.  T in
+// [1e-30, 1e30], so that r has all its bits.
+struct Softener {
+  float best, temp, inv;
+  __device__ __forceinline__ Softener(float b, float t) : best(b), temp(t), inv(1.f / t) {}
+  __device__ __forceinline__ u64 weight(float x) const {
+    if (x == best) return 1ull << 40;
+    const float d = x - best;
+    float z = d * inv;
+    z = fmaf(fmaf(-z, temp, d), inv, z);
+    z = fmaf(fmaf(-z, temp, d), inv, z);
+    const float e = expf(z) * 1099511627776.f;
+    if (!(e >= 1.f)) return 0;                 // also the NaN of an infinite d
+    // the integer part from the bits: 64-bit conversions run at a small part of the integer rate
+    const uint32_t bits = __float_as_uint(e), m = (bits & 0x7fffffu) | 0x800000u;
+    const int up = (int)(bits >> 23) - 150;    // e = m 2^up, up in [-23, 17]
+    return up >= 0 ? (u64)m << up : (u64)(m >> -up);
+  }
+};
 __device__ __forceinline__ u64 warp_add(u64 v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
+}
+
+// 16 bytes at a time where the row allows it.
+template <typename T>
+__device__ __forceinline__ float load_share(const T* src, T* xs, int n) {
+  constexpr int PER = 16 / sizeof(T);
+  float best = -INFINITY;
+  if ((reinterpret_cast<uintptr_t>(src) & 15) == 0) {
+    const int nv = n / PER;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < nv; i += NT) {
+      const uint4 v = __ldcs(reinterpret_cast<const uint4*>(src) + i);
+      reinterpret_cast<uint4*>(xs)[i] = v;
+      T e[PER];
+      *reinterpret_cast<uint4*>(e) = v;
+#pragma unroll
+      for (int j = 0; j < PER; ++j) best = fmaxf(best, (float)e[j]);
+    }
+    for (int i = nv * PER + threadIdx.x; i < n; i += NT) {
+      xs[i] = src[i];
+      best = fmaxf(best, (float)xs[i]);
+    }
+  } else {
+#pragma unroll 8
+    for (int i = threadIdx.x; i < n; i += NT) {
+      const T e = src[i];
+      xs[i] = e;
+      best = fmaxf(best, (float)e);
+    }
+  }
+  return best + 0.f;
 }
 
 template <typename T>
@@ -67,46 +130,57 @@ __global__ __launch_bounds__(NT) void sample_kernel(const SampleArgs a) {
   const int row = blockIdx.x / CS, tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   extern __shared__ __align__(16) uint8_t raw[];
   u64* bins = reinterpret_cast<u64*>(raw);                       // [BINS][NT]
-  float* xs = reinterpret_cast<float*>(raw + sizeof(u64) * BINS * NT);
+  T* xs = reinterpret_cast<T*>(raw + sizeof(u64) * BINS * NT);
   __shared__ Exchange ex[2];
   __shared__ u64 s_mass[NWARP];
   __shared__ uint32_t s_count[NWARP];
   __shared__ float s_best[NWARP];
   __shared__ u64 t_mass[BINS];                                   // the cluster's sums of a pass
   __shared__ uint32_t t_count[BINS];
+  // in the counters' place: the bins of the first pass, this CTA's list, the cluster's, its prefix sums
+  uint32_t* hist = reinterpret_cast<uint32_t*>(raw);             // [kCountBins], or low and high words [2][kMassBins]
+  u64* own = bins + kCountBins / 2;                              // [kList] ~key << 32 | index: ascending in (-x, index)
+  u64* all = own + kList;                                        // [kList]
+  u64* sums = all + kList;                                       // [kList]
+  static_assert(kCountBins / 2 + 3 * kList <= BINS * NT && 2 * kMassBins <= kCountBins, "the lists share the counters' memory");
+  __shared__ int32_t list_n;
+  __shared__ Cut s_cut;
+  __shared__ u64 s_kept, s_goal, s_above;
+  __shared__ int32_t s_bin, s_in;
   int turn = 0;
 
-  const int chunk = (a.vocab + CS - 1) / CS;
+  const int chunk = a.chunk;
   const int i0 = min(rank * chunk, a.vocab), n = min(i0 + chunk, a.vocab) - i0;
-  const T* src = static_cast<const T*>(a.logits) + (size_t)row * a.row_stride + i0;
-  float best = -INFINITY;
-  for (int i = tid; i < n; i += NT) {
-    float x = (float)src[i];
-    if (x != x) x = -INFINITY;
-    xs[i] = x;
-    best = fmaxf(best, x);
-  }
+  float temp = a.temperature ? a.temperature[row] : 1.f;
+  const int top_k = a.top_k ? a.top_k[row] : 0;
+  const float top_p = a.top_p ? a.top_p[row] : 1.f;
+  const float min_p = a.min_p ? a.min_p[row] : 0.f;
+  const float u = a.u[row];
+  float best = load_share(static_cast<const T*>(a.logits) + (size_t)row * a.row_stride + i0, xs, n);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
   if (lane == 0) s_best[wid] = best;
+  if (tid == 0) list_n = 0;
   __syncthreads();
   best = s_best[0];
 #pragma unroll
   for (int w = 1; w < NWARP; ++w) best = fmaxf(best, s_best[w]);
   if (tid == 0) ex[0].best = best;
   cluster.sync();
-  for (int c = 0; c < CS; ++c) best = fmaxf(best, cluster.map_shared_rank(&ex[0], c)->best);
+  best = lane < CS ? cluster.map_shared_rank(&ex[0], lane)->best : -INFINITY;
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
+  best = __shfl_sync(0xffffffffu, best, 0);
   turn = 1;
 
-  const float temp = a.temperature ? a.temperature[row] : 1.f;
   const bool greedy = !(temp > 0.f);
+  temp = fminf(fmaxf(temp, 1e-30f), 1e30f);
   const bool none = best == -INFINITY;                           // no token has any weight
   if (greedy || none) {
     int first = 0x7fffffff;
     for (int i = tid; i < n; i += NT)
-      if (xs[i] == best) { first = i0 + i; break; }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) first = min(first, __shfl_xor_sync(0xffffffffu, first, o));
+      if (value(xs[i]) == best) { first = i0 + i; break; }
+    first = __reduce_min_sync(0xffffffffu, first);
     if (lane == 0) s_count[wid] = (uint32_t)first;
     __syncthreads();
     if (tid == 0) {
@@ -123,21 +197,15 @@ __global__ __launch_bounds__(NT) void sample_kernel(const SampleArgs a) {
     return;
   }
 
-  // The cluster's (count, mass) of every 4-bit digit of the keys whose upper bits equal `prefix`.
-  auto histogram = [&](uint32_t prefix, int shift) {
-#pragma unroll
-    for (int b = 0; b < BINS; ++b) bins[b * NT + tid] = 0;
-    for (int i = tid; i < n; i += NT) {
-      const float x = xs[i];
-      const uint32_t key = key_of(x);
-      if (shift == 28 || (key >> (shift + 4)) == prefix)
-        bins[((key >> shift) & 15) * NT + tid] += (1ull << 48) + weight_of(x, best, temp);
-    }
+  const Softener soft(best, temp);
+  // The cluster's sums over the threads' counters, into t_mass and t_count.
+  auto add_up = [&]() {
     __syncthreads();
     u64 mass = 0;
     uint32_t count = 0;
-    for (int t = lane; t < NT; t += 32) {                        // one warp per digit
-      const u64 v = bins[wid * NT + t];
+#pragma unroll
+    for (int t = 0; t < NT; t += 32) {                           // one warp per bin
+      const u64 v = bins[wid * NT + t + lane];
       mass += v & kMassMask;
       count += (uint32_t)(v >> 48);
     }
@@ -148,106 +216,384 @@ __global__ __launch_bounds__(NT) void sample_kernel(const SampleArgs a) {
       ex[turn].count[wid] = count;
     }
     cluster.sync();
-    if (tid < BINS) {
-      u64 m = 0;
-      uint32_t k = 0;
-      for (int c = 0; c < CS; ++c) {
-        const Exchange* e = cluster.map_shared_rank(&ex[turn], c);
-        m += e->mass[tid];
-        k += e->count[tid];
+    if (tid < BINS * kMaxCluster) {
+      const int b = tid / kMaxCluster, c = tid % kMaxCluster;
+      const Exchange* e = cluster.map_shared_rank(&ex[turn], c < CS ? c : 0);
+      u64 m = c < CS ? e->mass[b] : 0;
+      uint32_t k = c < CS ? e->count[b] : 0;
+#pragma unroll
+      for (int o = 1; o < kMaxCluster; o <<= 1) {
+        m += __shfl_xor_sync(0xffffffffu, m, o);
+        k += __shfl_xor_sync(0xffffffffu, k, o);
       }
-      t_mass[tid] = m;
-      t_count[tid] = k;
+      if (c == 0) {
+        t_mass[b] = m;
+        t_count[b] = k;
+      }
     }
     turn ^= 1;
     __syncthreads();
   };
-  constexpr int kLastShift = sizeof(T) == 2 ? 16 : 0;            // a bf16's lower key bits say nothing more
-  constexpr uint32_t kLowMask = sizeof(T) == 2 ? 0xffffu : 0u;
+  auto clear = [&]() {
+#pragma unroll
+    for (int b = 0; b < BINS; ++b) bins[b * NT + tid] = 0;
+  };
+  // First digit from the top at which the running sum reaches `limit`; `above` moves past the
+  // digits before it.  Every warp finds the same.
+  auto find = [&](bool by_mass, u64 limit, u64& above) -> int {
+    const int b = BINS - 1 - lane;
+    const u64 v = lane < BINS ? by_mass ? t_mass[b] : (u64)t_count[b] : 0;
+    u64 run = v;
+#pragma unroll
+    for (int o = 1; o < BINS; o <<= 1) {
+      const u64 x = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += x;
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, lane < BINS && above + run >= limit);
+    const int at = hit ? __ffs(hit) - 1 : BINS - 1;
+    above += __shfl_sync(0xffffffffu, run - v, at);
+    return BINS - 1 - at;
+  };
 
-  // cut: keys above cut_key are kept, and the first `ties` (by index) of those equal to it
-  bool cut = false;
-  uint32_t cut_key = 0;
-  u64 ties = 0, kept_mass = 0;
-  bool have_mass = false;
-  const int top_k = a.top_k ? a.top_k[row] : 0;
-  const float top_p = a.top_p ? a.top_p[row] : 1.f;
+  // Walks this CTA's logits, PAR a thread at a time so that their arithmetic overlaps; those past the
+  // end come as -inf, which has no weight.
+  auto each = [&](auto&& f) {
+    for (int base = tid; base < n; base += NT * PAR) {
+      float x[PAR];
+      int i[PAR];
+#pragma unroll
+      for (int j = 0; j < PAR; ++j) {
+        i[j] = base + j * NT;
+        x[j] = i[j] < n ? value(xs[i[j]]) : -INFINITY;
+      }
+      f(x, i);
+    }
+  };
+  const float to_q = 16777216.f / 28.f / temp;                   // d in [0, 28 T) to [0, 2^24)
+  auto q_of = [&](float x) -> uint32_t {                          // a NaN (infinities) goes to the end
+    return x == best ? 0u : (uint32_t)fminf((best - x) * to_q, 16777216.f);
+  };
+
+  // Inclusive sum over the threads; every thread gets the total.
+  auto scan = [&](u64 v, u64& total) -> u64 {
+    u64 inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const u64 x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    __syncthreads();
+    if (lane == 31) s_mass[wid] = inc;
+    __syncthreads();
+    const u64 w = lane < NWARP ? s_mass[lane] : 0;
+    total = warp_add(w);
+    return inc + warp_add(lane < wid ? w : 0);
+  };
+  // The first bin at which the cluster's running sum reaches `limit`: s_bin, the sum before it s_above,
+  // the tokens in it s_in (by count).  False when the total stays below the limit.
+  auto find_bin = [&](bool by_mass, u64 limit, u64& total, bool only_total) -> bool {
+    u64 v[4] = {0, 0, 0, 0}, sum = 0;
+    if (by_mass) {
+      for (int c = 0; c < CS; ++c) {
+        const uint32_t* h = cluster.map_shared_rank(hist, c);
+        const uint2 lo = *reinterpret_cast<const uint2*>(h + 2 * tid);
+        const uint2 hi = *reinterpret_cast<const uint2*>(h + kMassBins + 2 * tid);
+        v[0] += (u64)hi.x << 32 | lo.x;
+        v[1] += (u64)hi.y << 32 | lo.y;
+      }
+    } else {
+      for (int c = 0; c < CS; ++c) {
+        const uint4 k = *reinterpret_cast<const uint4*>(cluster.map_shared_rank(hist, c) + 4 * tid);
+        v[0] += k.x; v[1] += k.y; v[2] += k.z; v[3] += k.w;
+      }
+    }
+    sum = v[0] + v[1] + v[2] + v[3];
+    const u64 inc = scan(sum, total);
+    if (only_total) return true;
+    u64 run = inc - sum;
+    if (run < limit && inc >= limit) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (run < limit && run + v[j] >= limit) {
+          s_bin = (by_mass ? 2 : 4) * tid + j;
+          s_above = run;
+          s_in = (int)v[j];
+        }
+        run += v[j];
+      }
+    }
+    __syncthreads();
+    return total >= limit;
+  };
+  // Sorts the first m (a power of two) of list, ascending.
+  auto sort = [&](u64* list, int m) {
+    for (int size = 2; size <= m; size <<= 1) {
+      for (int stride = size >> 1; stride > 0; stride >>= 1) {
+        __syncthreads();
+        for (int p = tid; p < m / 2; p += NT) {
+          const int i = 2 * p - (p & (stride - 1)), j = i + stride;
+          const u64 x = list[i], y = list[j];
+          if ((x > y) == ((i & size) == 0)) {
+            list[i] = y;
+            list[j] = x;
+          }
+        }
+      }
+    }
+    __syncthreads();
+  };
+  auto key_in = [](u64 item) -> uint32_t { return ~(uint32_t)(item >> 32); };
+  auto x_of = [](uint32_t key) -> float { return __uint_as_float((key >> 31) ? key & 0x7fffffffu : ~key); };
+
+  Cut cut = {0, 0x7fffffff};                                     // everything
+  auto passes = [&](uint32_t key, int i) { return key > cut.key || (key == cut.key && i <= cut.index); };
+  // Collects the tokens of bins [from, to], those that pass the cut, and sorts them into `all` (in the
+  // first CTA only, or in every one): their number, or -1 when they are too many.
+  auto collect = [&](int shift, uint32_t from, uint32_t to, bool leader) -> int {
+    if (tid == 0) list_n = 0;
+    __syncthreads();
+    each([&](const float (&x)[PAR], const int (&i)[PAR]) {
+#pragma unroll
+      for (int j = 0; j < PAR; ++j) {
+        const uint32_t q = q_of(x[j]), bin = q >> shift;
+        if (bin >= from && bin <= to && q < 16777216u && passes(key_of(x[j]), i0 + i[j])) {
+          const int at = atomicAdd(&list_n, 1);
+          if (at < kList) own[at] = (u64)(~key_of(x[j])) << 32 | (uint32_t)(i0 + i[j]);
+        }
+      }
+    });
+    __syncthreads();
+    if (tid == 0) ex[turn].first = list_n;
+    cluster.sync();
+    const int mine = lane < CS ? cluster.map_shared_rank(&ex[turn], lane)->first : 0;
+    turn ^= 1;
+    int inc = mine;
+#pragma unroll
+    for (int o = 1; o < kMaxCluster; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    const int total = __shfl_sync(0xffffffffu, inc, kMaxCluster - 1);
+    if (total > kList) return -1;                                // the same in every CTA
+    if (!leader || rank == 0) {
+      for (int c = 0; c < CS; ++c) {
+        const int m = __shfl_sync(0xffffffffu, mine, c), at = __shfl_sync(0xffffffffu, inc - mine, c);
+        const u64* r = cluster.map_shared_rank(own, c);
+        for (int i = tid; i < m; i += NT) all[at + i] = r[i];
+      }
+      int m = 32;
+      while (m < total) m <<= 1;
+      for (int i = total + tid; i < m; i += NT) all[i] = ~0ull;
+      sort(all, m);
+    }
+    cluster.sync();                                              // every list has been read
+    return total;
+  };
+  auto clear_hist = [&]() {
+    for (int b = tid; b < kCountBins; b += NT) hist[b] = 0;
+    __syncthreads();
+  };
+
+  const bool cut_p = top_p < 1.f;
+  const u64 least = min_p > 0.f ? (u64)ceilf(fminf(min_p, 1.f) * 1099511627776.f) : 0ull;   // exact: a scaling by 2^40
+  u64 kept_mass = 0;
   for (int what = 0; what < 2; ++what) {                         // 0: top-k by count, 1: top-p by mass
-    if (what == 0 ? top_k <= 0 || top_k >= a.vocab : !(top_p < 1.f)) continue;
-    u64 limit = (u64)top_k, above = 0, above_mass = 0;
+    u64 limit = 0, above = 0, above_mass = 0, total;
+    if (what == 0 ? !(top_k > 0 && top_k < a.vocab) : !cut_p) continue;
+    clear_hist();
+    if (what == 0) {
+      each([&](const float (&x)[PAR], const int (&)[PAR]) {
+#pragma unroll
+        for (int j = 0; j < PAR; ++j) {
+          const uint32_t q = q_of(x[j]);
+          if (q < 16777216u) atomicAdd(hist + (q >> kCountShift), 1u);
+        }
+      });
+      cluster.sync();
+      limit = (u64)top_k;
+      const bool cuts = find_bin(false, limit, total, false);
+      cluster.sync();                                            // the bins have been read
+      if (!cuts) continue;                                       // every token that has weight is among the first
+      above = s_above;
+      const int bin = s_bin, in = s_in;
+      if (above + in <= kList) {
+        // all that may be kept, in one list
+        const int count = min(collect(kCountShift, 0, bin, true), top_k);
+        if (rank != 0) return;
+        u64 w[4], sum = 0;                                       // four consecutive tokens a thread
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          w[j] = 4 * tid + j < count ? soft.weight(x_of(key_in(all[4 * tid + j]))) : 0;
+          sum += w[j];
+        }
+        u64 run = scan(sum, total) - sum;
+        if (tid == 0) {
+          s_kept = ~0ull;
+          if (cut_p) {
+            const double goal = ceil((double)fmaxf(top_p, 0.f) * (double)total);
+            s_kept = goal > 1.0 ? (u64)goal : 1ull;
+          }
+          list_n = 0;
+        }
+        __syncthreads();
+        limit = s_kept;
+        int kept = 0;                                            // the kept ones are the first of the list
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (w[j] && w[j] >= least && run < limit) ++kept;
+          run += w[j];
+          sums[4 * tid + j] = run;
+        }
+        kept = __reduce_add_sync(0xffffffffu, kept);
+        if (lane == 0 && kept) atomicAdd(&list_n, kept);
+        __syncthreads();
+        kept = list_n;
+        total = sums[kept - 1];
+        if (tid == 0) s_goal = u > 0.f ? (u64)((double)u * (double)total) : 0ull;
+        int m = 32;
+        while (m < kept) m <<= 1;
+        for (int i = tid; i < m; i += NT) own[i] = i < kept ? (u64)(uint32_t)all[i] << 32 | (uint32_t)i : ~0ull;
+        sort(own, m);                                            // by index
+        const u64 goal = min(s_goal, total - 1);
+        sum = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int i = 4 * tid + j < kept ? (int)(uint32_t)own[4 * tid + j] : -1;
+          w[j] = i < 0 ? 0 : sums[i] - (i ? sums[i - 1] : 0);
+          sum += w[j];
+        }
+        u64 all_mass;
+        run = scan(sum, all_mass) - sum;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (run <= goal && goal < run + w[j]) {
+            a.ids[row] = (int32_t)(own[4 * tid + j] >> 32);
+            if (a.logp) a.logp[row] = logf((float)w[j] / (float)total);
+          }
+          run += w[j];
+        }
+        return;
+      }
+    } else {
+      uint32_t* hi = hist + kMassBins;
+      each([&](const float (&x)[PAR], const int (&i)[PAR]) {
+        u64 w[PAR];
+#pragma unroll
+        for (int j = 0; j < PAR; ++j) w[j] = passes(key_of(x[j]), i0 + i[j]) ? soft.weight(x[j]) : 0;
+#pragma unroll
+        for (int j = 0; j < PAR; ++j) {
+          if (!w[j]) continue;
+          const uint32_t b = min(q_of(x[j]), 16777215u) >> kMassShift, low = (uint32_t)w[j];
+          const uint32_t old = atomicAdd(hist + b, low);         // a 64-bit sum in two words: the carry is seen here
+          const uint32_t up = (uint32_t)(w[j] >> 32) + (old + low < old ? 1u : 0u);
+          if (up) atomicAdd(hi + b, up);
+        }
+      });
+      cluster.sync();
+      find_bin(true, 0, kept_mass, true);
+      if (tid == 0) {                                            // one thread: fp64 is slow here
+        const double goal = ceil((double)fmaxf(top_p, 0.f) * (double)kept_mass);
+        s_kept = goal > 1.0 ? (u64)goal : 1ull;
+      }
+      __syncthreads();
+      limit = s_kept;
+      find_bin(true, limit, total, false);
+      cluster.sync();                                            // the bins have been read
+      above_mass = s_above;
+    }
+    const int bin = s_bin, count = collect(what == 0 ? kCountShift : kMassShift, bin, bin, false);
+    if (count >= 0) {
+      u64 v[4], sum = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[j] = 4 * tid + j < count ? what == 0 ? 1ull : soft.weight(x_of(key_in(all[4 * tid + j]))) : 0ull;
+        sum += v[j];
+      }
+      u64 run = (what == 0 ? above : above_mass) + scan(sum, total) - sum;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (run < limit && run + v[j] >= limit) s_cut = Cut{key_in(all[4 * tid + j]), (int32_t)(uint32_t)all[4 * tid + j]};
+        run += v[j];
+      }
+      __syncthreads();
+      cut = s_cut;                                               // never above an earlier cut: its tokens alone were counted
+      __syncthreads();
+      continue;
+    }
+    // crowded: radix descent over the keys, then the index of the last tie that is kept
+    constexpr int kLastShift = sizeof(T) == 2 ? 16 : 0;        // a bf16's lower key bits say nothing more
+    above = 0;
     uint32_t prefix = 0;
     for (int shift = 28; shift >= kLastShift; shift -= 4) {
-      histogram(prefix, shift);
-      if (what == 1 && shift == 28) {
-        if (!have_mass) {
-          kept_mass = 0;
-          for (int b = 0; b < BINS; ++b) kept_mass += t_mass[b];
-        }
-        const double goal = ceil((double)fmaxf(top_p, 0.f) * (double)kept_mass);
-        limit = goal > 1.0 ? (u64)goal : 1ull;
+      clear();
+      for (int i = tid; i < n; i += NT) {
+        const float x = value(xs[i]);
+        const uint32_t key = key_of(x);
+        if (shift == 28 || (key >> (shift + 4)) == prefix)
+          bins[((key >> shift) & 15) * NT + tid] += (1ull << 48) + soft.weight(x);
       }
-      int digit = 0;
-      for (int b = BINS - 1; b >= 0; --b) {
-        const u64 v = what == 0 ? (u64)t_count[b] : t_mass[b];
-        if (above + v >= limit) { digit = b; break; }
-        above += v;
-        above_mass += t_mass[b];
-      }
-      prefix = (prefix << 4) | digit;
-      __syncthreads();                                           // the sums are read: the next pass may write them
+      add_up();
+      prefix = prefix << 4 | find(what == 1, limit, above);
+      __syncthreads();
     }
     uint32_t key = prefix << kLastShift;
-    if (kLowMask && !(key >> 31)) key |= kLowMask;               // a negative bf16's low key bits are ones
-    const u64 w = weight_of(value_of(key), best, temp);
-    if (what == 0) {
-      cut_key = key;
-      ties = limit - above;
-      kept_mass = above_mass + ties * w;
-      have_mass = true;
-    } else {                                                     // never below the cut of top-k: limit <= its mass
-      const u64 t = w ? (limit - above + w - 1) / w : 1;
-      ties = cut && key == cut_key && ties < t ? ties : t;
-      cut_key = key;
-    }
-    cut = true;
-  }
-
-  // kept mass of every warp's span of indices
-  const float min_p = a.min_p ? a.min_p[row] : 0.f;
-  const double least = min_p > 0.f ? (double)fminf(min_p, 1.f) * 1099511627776.0 : 0.0;
-  const int span = ((n + NWARP - 1) / NWARP + 31) / 32 * 32;
-  const int w0 = min(wid * span, n), w1 = min(w0 + span, n);
-  u64 tie_base = 0;
-  if (cut) {
+    if (sizeof(T) == 2 && !(key >> 31)) key |= 0xffffu;        // a negative bf16's low key bits are ones
+    const u64 w = soft.weight(__uint_as_float((key >> 31) ? key & 0x7fffffffu : ~key));
+    const u64 ties = what == 0 ? limit - above : w ? (limit - above + w - 1) / w : 1;   // kept of the equal ones
+    const int span = ((n + NWARP - 1) / NWARP + 31) / 32 * 32;
+    const int w0 = min(wid * span, n), w1 = min(w0 + span, n);
     uint32_t mine = 0;
-    for (int i = w0 + lane; i < w1; i += 32) mine += key_of(xs[i]) == cut_key;
+    for (int i = w0 + lane; i < w1; i += 32) mine += key_of(value(xs[i])) == key;
     mine = __reduce_add_sync(0xffffffffu, mine);
     if (lane == 0) s_count[wid] = mine;
     __syncthreads();
     if (tid == 0) {
       uint32_t sum = 0;
-      for (int w = 0; w < NWARP; ++w) sum += s_count[w];
+      for (int v = 0; v < NWARP; ++v) sum += s_count[v];
       ex[turn].count[0] = sum;
+      ex[turn].first = 0x7fffffff;
     }
     cluster.sync();
-    for (int c = 0; c < rank; ++c) tie_base += cluster.map_shared_rank(&ex[turn], c)->count[0];
-    for (int w = 0; w < wid; ++w) tie_base += s_count[w];
-    turn ^= 1;
+    u64 before = 0;
+    for (int c = 0; c < rank; ++c) before += cluster.map_shared_rank(&ex[turn], c)->count[0];
+    for (int v = 0; v < wid; ++v) before += s_count[v];
+    if (before < ties && before + mine >= ties) {              // one warp of the cluster
+      for (int i = w0; i < w1; i += 32) {
+        const bool tie = i + lane < w1 && key_of(value(xs[min(i + lane, w1 - 1)])) == key;
+        const uint32_t votes = __ballot_sync(0xffffffffu, tie);
+        if (before + __popc(votes) >= ties) {
+          if (tie && before + __popc(votes & ((2u << lane) - 1)) == ties) ex[turn].first = i0 + i + lane;
+          break;
+        }
+        before += __popc(votes);
+      }
+    }
+    cluster.sync();
+    Cut found = {key, 0x7fffffff};
+    for (int c = 0; c < CS; ++c) found.index = min(found.index, cluster.map_shared_rank(&ex[turn], c)->first);
+    if (found.key > cut.key || (found.key == cut.key && found.index < cut.index)) cut = found;
+    cluster.sync();                                            // read by all before it is written again
   }
-  // weight of index i if it is kept, walking a warp's span 32 indices at a time
-  auto kept = [&](int i, u64& tie_rank) -> u64 {
-    const float x = i < w1 ? xs[i] : -INFINITY;
+
+  // kept mass of every warp's span of indices
+  const int span = ((n + NWARP - 1) / NWARP + 31) / 32 * 32;
+  const int w0 = min(wid * span, n), w1 = min(w0 + span, n);
+  auto kept = [&](int i, int end) -> u64 {                       // weight of the token if it is kept
+    if (i >= end) return 0;
+    const float x = value(xs[i]);
     const uint32_t key = key_of(x);
-    const bool tie = cut && i < w1 && key == cut_key;
-    const uint32_t votes = __ballot_sync(0xffffffffu, tie);
-    const u64 rank_here = tie_rank + __popc(votes & ((1u << lane) - 1));
-    tie_rank += __popc(votes);
-    if (i >= w1 || (cut && (key < cut_key || (tie && rank_here >= ties)))) return 0;
-    const u64 w = weight_of(x, best, temp);
-    return (double)w >= least ? w : 0;
+    if (key < cut.key || (key == cut.key && i0 + i > cut.index)) return 0;
+    const u64 w = soft.weight(x);
+    return w >= least ? w : 0;
   };
-  u64 mass = 0, tr = tie_base;
-  for (int i = w0; i < w1; i += 32) mass += kept(i + lane, tr);
+  u64 mass = 0;
+  for (int i = w0 + lane; i < w1; i += 32 * PAR) {
+    u64 w[PAR];
+#pragma unroll
+    for (int j = 0; j < PAR; ++j) w[j] = kept(i + 32 * j, w1);
+#pragma unroll
+    for (int j = 0; j < PAR; ++j) mass += w[j];
+  }
   mass = warp_add(mass);
   if (lane == 0) s_mass[wid] = mass;
   __syncthreads();
@@ -258,46 +604,67 @@ __global__ __launch_bounds__(NT) void sample_kernel(const SampleArgs a) {
   }
   cluster.sync();
   u64 before = 0, total = 0;
-  for (int c = 0; c < CS; ++c) {
-    const u64 v = cluster.map_shared_rank(&ex[turn], c)->mass[0];
-    before += c < rank ? v : 0;
-    total += v;
+  {
+    const u64 v = lane < CS ? cluster.map_shared_rank(&ex[turn], lane)->mass[0] : 0;
+    before = warp_add(lane < rank ? v : 0);
+    total = warp_add(v);
+    before += warp_add(lane < wid ? s_mass[lane & (NWARP - 1)] : 0);
   }
-  for (int w = 0; w < wid; ++w) before += s_mass[w];
-  const float u = a.u[row];
-  u64 goal = u > 0.f ? (u64)((double)u * (double)total) : 0ull;
+  if (tid == 0) s_goal = u > 0.f ? (u64)((double)u * (double)total) : 0ull;
+  __syncthreads();
+  u64 goal = s_goal;
   if (goal >= total) goal = total - 1;
-  if (goal >= before && goal < before + mass) {                  // one warp of the cluster
-    u64 run = before;
-    tr = tie_base;
-    for (int i = w0; i < w1; i += 32) {
-      const u64 w = kept(i + lane, tr);
-      u64 inc = w;
+  if (tid == 0) list_n = -1;
+  __syncthreads();
+  if (lane == 0 && goal >= before && goal < before + mass) {     // one warp of the cluster
+    list_n = wid;
+    s_kept = before;
+  }
+  __syncthreads();
+  if (list_n >= 0) {                                             // its span, by all warps of its CTA
+    const int sub = (span / NWARP + 31) / 32 * 32;
+    const int end = min(list_n * span + span, n), v0 = min(list_n * span + wid * sub, end), v1 = min(v0 + sub, end);
+    u64 part = 0;
+    for (int i = v0 + lane; i < v1; i += 32) part += kept(i, v1);
+    part = warp_add(part);
+    if (lane == 0) s_mass[wid] = part;
+    __syncthreads();
+    u64 run = s_kept + warp_add(lane < wid ? s_mass[lane & (NWARP - 1)] : 0);
+    if (goal >= run && goal < run + part) {
+      for (int i = v0; i < v1; i += 32) {
+        const u64 w = kept(i + lane, v1);
+        u64 inc = w;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const u64 v = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += v;
-      }
-      const uint32_t past = __ballot_sync(0xffffffffu, run + inc > goal);
-      if (past) {
-        if (lane == __ffs(past) - 1) {
-          a.ids[row] = i0 + i + lane;
-          if (a.logp) a.logp[row] = logf((float)w / (float)total);
+        for (int o = 1; o < 32; o <<= 1) {
+          const u64 v = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += v;
         }
-        break;
+        const uint32_t past = __ballot_sync(0xffffffffu, run + inc > goal);
+        if (past) {
+          if (lane == __ffs(past) - 1) {
+            a.ids[row] = i0 + i + lane;
+            if (a.logp) a.logp[row] = logf((float)w / (float)total);
+          }
+          break;
+        }
+        run += __shfl_sync(0xffffffffu, inc, 31);
       }
-      run += __shfl_sync(0xffffffffu, inc, 31);
     }
   }
   cluster.sync();                                                // no CTA leaves while its memory is read
 }
 
 template <typename T>
-cudaError_t launch(const SampleArgs& a, cudaStream_t s) {
-  int cs = kMaxCluster;
-  while (cs > 1 && (a.vocab + cs / 2 - 1) / (cs / 2) <= 4096) cs /= 2;
-  const int chunk = (a.vocab + cs - 1) / cs;
-  const size_t bytes = sizeof(u64) * BINS * NT + (size_t)chunk * 4;
+cudaError_t launch(SampleArgs a, cudaStream_t s) {
+  // CTAs per row: as many as fill the GPU once (a second round costs more than longer shares), each
+  // with 2048 logits or more, and no fewer than hold the row in shared memory
+  const int64_t fit = (kShared - (int64_t)sizeof(u64) * BINS * NT) / sizeof(T) / 8 * 8;
+  const int least = (int)((a.vocab + fit - 1) / fit);
+  int cs = sm_count() / a.rows;
+  cs = cs < (a.vocab + 2047) / 2048 ? cs : (a.vocab + 2047) / 2048;
+  cs = cs < least ? least : cs > kMaxCluster ? kMaxCluster : cs;
+  a.chunk = ((a.vocab + cs - 1) / cs + 7) / 8 * 8;               // every share is aligned as the row is
+  const size_t bytes = sizeof(u64) * BINS * NT + (size_t)a.chunk * sizeof(T);
   cudaError_t e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};

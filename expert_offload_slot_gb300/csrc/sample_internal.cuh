@@ -13,7 +13,7 @@ struct SampleArgs {
   const int32_t* top_k;
   int32_t* ids;
   float* logp;
-  int32_t rows, vocab;
+  int32_t rows, vocab, chunk;  // chunk: logits per CTA of the row's cluster
 };
 cudaError_t launch_sample(const SampleArgs& a, int dtype, cudaStream_t s);
 

@@ -536,7 +536,8 @@ MOE_API moe_status moe_attn_forward(moe_attn* attn, const void* q, int64_t q_str
 /* The next token of each row: temperature, top-k, top-p, min-p and one given uniform number.
  *   logits       device [rows] rows of [vocab] of dtype (MOE_F32 or MOE_BF16), row_stride
  *                elements apart; vocab up to MOE_SAMPLE_MAX_VOCAB
- *   temperature  device fp32 [rows]: T; 0 or below: the first maximum.  NULL: 1
+ *   temperature  device fp32 [rows]: T (taken within 1e-30 .. 1e30); 0 or below: the first
+ *                maximum.  NULL: 1
  *   top_k        device int32 [rows]; 0 or below: off.  top_p, min_p device fp32 [rows];
  *                top_p >= 1 and min_p <= 0: off.  Each may be NULL (off)
  *   u            device fp32 [rows] in [0, 1)
