@@ -41,6 +41,108 @@ struct TileCfg {
   static constexpr int kBytes = (2 + kStages) * kTile + 1024;
 };
 
+// A call's work is divided in one of two ways, chosen from the lengths by every CTA alike.
+// Whole: the items, longest first within a request, are dealt out to the CTAs to and fro, so that
+// long and short ones meet in each; nothing is split.  Ranges: the keys of all items are cut into
+// equal ranges (attn_find_range), which balances any lengths but has split items join their
+// pieces through memory; that takes about as long as kJoin units.  So items stay whole unless
+// the longest takes kJoin units more than an even share.
+struct TileCursor : AttnCursor {
+  int32_t next;                                // whole items: place of the next one in the CTA's list
+};
+constexpr int kListMax = 32, kJoin = 6;
+
+struct TileWork {
+  AttnSplit sp;
+  bool whole;
+  int count;                                   // whole: items of this CTA
+  int2* list;                                  // [kListMax] (request | head << 16, tile)
+};
+
+__device__ __forceinline__ void tile_take(const AttnArgs& a, const TileWork& w, TileCursor& c) {
+  const int2 e = w.list[c.next++];
+  c.r = e.x & 0xffff;
+  c.h = e.x >> 16;
+  c.i = e.y;
+  c.q = attn_request(a, c.r);
+  attn_units<BM>(a, c.q, c.i, UNIT, c.u0, c.nu);
+  c.at = 0;
+  c.left = c.nu;
+  c.item_first = 0;
+}
+
+__device__ __forceinline__ bool tile_next(const AttnArgs& a, const TileWork& w, TileCursor& c) {
+  if (!w.whole) return attn_next<BM>(a, UNIT, c);
+  if (c.next >= w.count) return false;
+  tile_take(a, w, c);
+  return true;
+}
+
+// All threads; sm: 64 ints.
+__device__ __forceinline__ bool tile_work(const AttnArgs& a, int32_t* sm, TileWork& w, TileCursor& c) {
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, G = gridDim.x;
+  const int per = (a.R + NT - 1) / NT;
+  const int r0 = min(tid * per, a.R), r1 = min(r0 + per, a.R);
+  int units = 0, items = 0, longest = 0;
+  for (int r = r0; r < r1; ++r) {
+    const AttnRequest q = attn_request(a, r);
+    const int nt = attn_tiles<BM>(a, q);
+    items += nt * a.Hkv;
+    for (int i = 0; i < nt; ++i) {
+      int u0, nu;
+      attn_units<BM>(a, q, i, UNIT, u0, nu);
+      units += nu * a.Hkv;
+      longest = max(longest, nu);
+    }
+  }
+  int inc = items;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  units = __reduce_add_sync(0xffffffffu, units);
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  if (lane == 31) sm[wid] = inc;
+  if (lane == 0) {
+    sm[16 + wid] = units;
+    sm[32 + wid] = longest;
+  }
+  __syncthreads();
+  int base = 0, all = 0, W = 0, top = 0;
+#pragma unroll
+  for (int k = 0; k < NT / 32; ++k) {
+    base += k < wid ? sm[k] : 0;
+    all += sm[k];
+    W += sm[16 + k];
+    top = max(top, sm[32 + k]);
+  }
+  if (W == 0) return false;
+  w.whole = top <= (W + G - 1) / G + kJoin && all <= G * kListMax;
+  w.count = 0;
+  if (!w.whole) {
+    __syncthreads();
+    return attn_find_range<BM, NT>(a, UNIT, 1, sm, w.sp, c);
+  }
+  int lo = base + inc - items;
+  for (int r = r0; r < r1; ++r) {
+    const int nt = attn_tiles<BM>(a, attn_request(a, r)), hi = lo + nt * a.Hkv;
+    for (int j = lo / G; j * G < hi; ++j) {
+      const int k = (j & 1) ? (j + 1) * G - 1 - (int)blockIdx.x : j * G + (int)blockIdx.x;
+      if (k >= lo && k < hi) w.list[j] = make_int2(r | ((k - lo) % a.Hkv) << 16, nt - 1 - (k - lo) / a.Hkv);
+    }
+    lo = hi;
+  }
+  const int last = (all - 1) / G;              // round of the last item; only that round may lack one
+  const int k = (last & 1) ? (last + 1) * G - 1 - (int)blockIdx.x : last * G + (int)blockIdx.x;
+  w.count = last + (k < all);
+  __syncthreads();
+  if (w.count == 0) return false;
+  c.next = 0;
+  tile_take(a, w, c);
+  return true;
+}
+
 template <int D>
 __global__ __launch_bounds__(NT, 1) void attn_tiles_kernel(const __grid_constant__ CUtensorMap mk,
                                                            const __grid_constant__ CUtensorMap mv, const AttnArgs a) {
@@ -68,9 +170,11 @@ __global__ __launch_bounds__(NT, 1) void attn_tiles_kernel(const __grid_constant
     }
     bar_init_done();
   }
-  AttnSplit sp;
-  AttnCursor c;
-  if (!attn_find_range<BM, NT>(a, UNIT, 1, sched, sp, c)) return;      // the same answer in every thread
+  __shared__ int2 items[kListMax];
+  TileWork work;
+  TileCursor c;
+  work.list = items;
+  if (!tile_work(a, sched, work, c)) return;           // the same answer in every thread
   if (wid == 9) tmem_alloc(&tmem_slot, 512);
   tc_fence_before();
   __syncthreads();
@@ -135,59 +239,69 @@ __global__ __launch_bounds__(NT, 1) void attn_tiles_kernel(const __grid_constant
           }
         }
       }
-    } while (attn_next<BM>(a, UNIT, c));
+    } while (tile_next(a, work, c));
     if (!alive)                                          // bounded: copies in flight land before the memory is given up
       for (uint32_t k = n > C::kStages ? n - C::kStages : 0; k < n; ++k) bar_wait(full + k % C::kStages, (k / C::kStages) & 1);
   } else if (wid == 9) {
     // ----------------------------------------------------------------- MMAs
-    if (lane == 0) {
+    {
+      const uint32_t lead = elect_lead();
       constexpr uint32_t kS = tc_idesc(UNIT, false), kO = tc_idesc(D, true);
       uint32_t n = 0;                                    // ring position
       uint32_t np[2] = {0, 0}, pieces[2] = {0, 0};       // P tiles and Q tiles taken
+      // Descriptors are made once; a step in K or to another stage adds to their address field (units
+      // of 16 bytes).
+      const uint64_t q_desc = tc_desc(sq, 16), k_desc = tc_desc(ring, 16), v_desc = tc_desc(ring, C::kHalf);
       auto scores = [&](int t, uint32_t stage) {
+        const uint64_t qd = q_desc + t * (C::kTile >> 4), kd = k_desc + stage * (C::kTile >> 4);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (k >> 2) * C::kHalf + (k & 3) * 32;
-          tc_mma_ss(tmem + t * UNIT, tc_desc(sq + t * C::kTile + off, 16), tc_desc(stage + off, 16), kS, k > 0);
+          const uint32_t off = ((k >> 2) * C::kHalf + (k & 3) * 32) >> 4;
+          tc_mma_ss(lead, tmem + t * UNIT, qd + off, kd + off, kS, k > 0);
         }
-        tc_commit(s_full + t);
+        tc_commit(lead, s_full + t);
       };
       do {
         const int rows = min(BM, c.q.n * a.group - c.i * BM), tiles = rows > 128 ? 2 : 1;
         const int units = attn_piece(c);
         wait(full + n % C::kStages, (n / C::kStages) & 1);
+        __syncwarp();
         for (int t = 0; t < tiles; ++t) {
           wait(q_full + t, pieces[t]++ & 1);
+          __syncwarp();
           tc_fence_after();
-          scores(t, ring + n % C::kStages * C::kTile);
+          scores(t, n % C::kStages);
         }
-        tc_commit(empty + n % C::kStages);
+        tc_commit(lead, empty + n % C::kStages);
         ++n;
         for (int j = 0; j < units; ++j) {
           const uint32_t vs = n % C::kStages, ks = (n + 1) % C::kStages;
           const bool more = j + 1 < units;
           wait(full + vs, (n / C::kStages) & 1);
+          __syncwarp();
           for (int t = 0; t < tiles; ++t) {
+            const uint64_t vd = v_desc + vs * (C::kTile >> 4);
             wait(p_full + t, np[t]++ & 1);
+            __syncwarp();
             tc_fence_after();
 #pragma unroll
             for (int k = 0; k < UNIT / 16; ++k)
-              tc_mma_ts(tmem + 256 + t * 128, tmem + t * UNIT + k * 8,
-                        tc_desc(ring + vs * C::kTile + k * 2048, C::kHalf), kO, (j > 0 || k > 0));
+              tc_mma_ts(lead, tmem + 256 + t * 128, tmem + t * UNIT + k * 8, vd + k * (2048 >> 4), kO, k > 0 || j > 0);
             if (more) {
               if (t == 0) wait(full + ks, ((n + 1) / C::kStages) & 1);
-              scores(t, ring + ks * C::kTile);
+              __syncwarp();
+              scores(t, ks);
             } else {
-              tc_commit(o_full + t);
+              tc_commit(lead, o_full + t);
             }
           }
-          tc_commit(empty + vs);
-          if (more) tc_commit(empty + ks);
+          tc_commit(lead, empty + vs);
+          if (more) tc_commit(lead, empty + ks);
           n += more ? 2 : 1;
         }
-      } while (attn_next<BM>(a, UNIT, c));
+      } while (tile_next(a, work, c));
       if (!alive) {                                      // bounded: products in flight end before the memory is given up
-        tc_commit(&drain);
+        tc_commit(lead, &drain);
         bar_wait(&drain, 0);
       }
     }
@@ -220,8 +334,8 @@ __global__ __launch_bounds__(NT, 1) void attn_tiles_kernel(const __grid_constant
     }
     bool more;
     do {
-      AttnCursor nx = c;
-      more = attn_next<BM>(a, UNIT, nx);
+      TileCursor nx = c;
+      more = tile_next(a, work, nx);
       const bool next_mine = more && has_tile(nx);
       if (!mine) {                                       // an item of 128 rows or fewer has no tile B
         if (next_mine) {
@@ -341,7 +455,7 @@ __global__ __launch_bounds__(NT, 1) void attn_tiles_kernel(const __grid_constant
       }
       if (!whole) {
         if (row < rows) a.part_ml[part] = make_float2(m, l);
-        const int c0 = sp.owner(c.item_first), n = sp.owner(c.item_first + c.nu - 1) - c0 + 1;
+        const int c0 = work.sp.owner(c.item_first), n = work.sp.owner(c.item_first + c.nu - 1) - c0 + 1;
         __threadfence();
         named_sync(1 + t, 128);
         if (tid == t * 128) {
@@ -352,29 +466,46 @@ __global__ __launch_bounds__(NT, 1) void attn_tiles_kernel(const __grid_constant
         named_sync(1 + t, 128);
         if (last_flag[t]) {                              // the item's last piece to arrive joins tile t, in piece order
           __threadfence();
-          constexpr int LANES = D / 4, STEP = 128 / LANES;
-          const int d = (tid % LANES) * 4;
-          for (int r = (tid & 127) / LANES; r < min(rows, 128); r += STEP) {
-            float M = -INFINITY;
-            for (int p = 0; p < n; ++p)
-              M = fmaxf(M, __ldcg(a.part_ml + (size_t)(2 * (c0 + p) + (p == 0)) * BM + t * 128 + r).x);
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            float sum = 0.f;
-            if (M > -INFINITY) {
-              for (int p = 0; p < n; ++p) {
-                const size_t at = (size_t)(2 * (c0 + p) + (p == 0)) * BM + t * 128 + r;
-                const float2 ml = __ldcg(a.part_ml + at);
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D + d));
-                const float g = ex2(ml.x - M);
-                sum += g * ml.y;
-                o.x += g * v.x; o.y += g * v.y; o.z += g * v.z; o.w += g * v.w;
+          // a warp joins its 32 rows, 16 loads of a piece in flight per lane
+          constexpr int LANES = D / 4, PER = 32 / LANES, B = 16;
+          const int r0 = (wid & 3) * 32;
+          const float2* ml = a.part_ml + t * 128 + row;
+          auto slot = [&](int p) { return (size_t)(2 * (c0 + p) + (p == 0)) * BM; };
+          float M = -INFINITY, sum = 0.f;
+          for (int p = 0; p < n; ++p) M = fmaxf(M, __ldcg(ml + slot(p)).x);
+          const float top = M == -INFINITY ? 0.f : M;
+          for (int p = 0; p < n; ++p) {
+            const float2 v = __ldcg(ml + slot(p));
+            sum += ex2(v.x - top) * v.y;
+          }
+          const float in = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll 1
+          for (int b = 0; b < 32; b += B * PER) {
+            float4 o[B];
+#pragma unroll
+            for (int k = 0; k < B; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+            for (int p = 0; p < n; ++p) {
+              const float g = ex2(__ldcg(ml + slot(p)).x - top) * in;
+              float4 v[B];
+#pragma unroll
+              for (int k = 0; k < B; ++k)
+                v[k] = __ldcg(reinterpret_cast<const float4*>(
+                    a.part_o + (slot(p) + t * 128 + r0 + b + k * PER + lane / LANES) * D + lane % LANES * 4));
+#pragma unroll
+              for (int k = 0; k < B; ++k) {
+                const float w = __shfl_sync(0xffffffffu, g, b + k * PER + lane / LANES);
+                o[k].x += w * v[k].x; o[k].y += w * v[k].y; o[k].z += w * v[k].z; o[k].w += w * v[k].w;
               }
-              const float in = 1.f / sum;
-              o.x *= in; o.y *= in; o.z *= in; o.w *= in;
             }
-            const int fr = c.i * BM + t * 128 + r;
-            attn_store4(static_cast<__nv_bfloat16*>(a.out) +
-                            ((size_t)(c.q.start + fr / a.group) * a.Hq + c.h * a.group + fr % a.group) * D + d, o);
+#pragma unroll
+            for (int k = 0; k < B; ++k) {
+              const int r = r0 + b + k * PER + lane / LANES, fr = c.i * BM + t * 128 + r;
+              if (r < rows)
+                attn_store4(static_cast<__nv_bfloat16*>(a.out) +
+                                ((size_t)(c.q.start + fr / a.group) * a.Hq + c.h * a.group + fr % a.group) * D +
+                                lane % LANES * 4, o[k]);
+            }
           }
         }
       }
