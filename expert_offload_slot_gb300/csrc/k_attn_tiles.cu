@@ -56,25 +56,28 @@ struct TileWork {
   AttnSplit sp;
   bool whole;
   int count;                                   // whole: items of this CTA
-  int2* list;                                  // [kListMax] (request | head << 16, tile)
+  int4* list;                                  // [2 * kListMax] (request, head, tile, units), (first row, new, seq, first unit)
 };
 
-__device__ __forceinline__ void tile_take(const AttnArgs& a, const TileWork& w, TileCursor& c) {
-  const int2 e = w.list[c.next++];
-  c.r = e.x & 0xffff;
-  c.h = e.x >> 16;
-  c.i = e.y;
-  c.q = attn_request(a, c.r);
-  attn_units<BM>(a, c.q, c.i, UNIT, c.u0, c.nu);
+__device__ __forceinline__ void tile_take(const TileWork& w, TileCursor& c) {
+  const int4 x = w.list[2 * c.next], y = w.list[2 * c.next + 1];
+  ++c.next;
+  c.r = x.x;
+  c.h = x.y;
+  c.i = x.z;
+  c.nu = c.left = x.w;
+  c.q.start = y.x;
+  c.q.n = y.y;
+  c.q.seq = y.z;
+  c.u0 = y.w;
   c.at = 0;
-  c.left = c.nu;
   c.item_first = 0;
 }
 
 __device__ __forceinline__ bool tile_next(const AttnArgs& a, const TileWork& w, TileCursor& c) {
   if (!w.whole) return attn_next<BM>(a, UNIT, c);
   if (c.next >= w.count) return false;
-  tile_take(a, w, c);
+  tile_take(w, c);
   return true;
 }
 
@@ -126,10 +129,16 @@ __device__ __forceinline__ bool tile_work(const AttnArgs& a, int32_t* sm, TileWo
   }
   int lo = base + inc - items;
   for (int r = r0; r < r1; ++r) {
-    const int nt = attn_tiles<BM>(a, attn_request(a, r)), hi = lo + nt * a.Hkv;
+    const AttnRequest q = attn_request(a, r);
+    const int nt = attn_tiles<BM>(a, q), hi = lo + nt * a.Hkv;
     for (int j = lo / G; j * G < hi; ++j) {
       const int k = (j & 1) ? (j + 1) * G - 1 - (int)blockIdx.x : j * G + (int)blockIdx.x;
-      if (k >= lo && k < hi) w.list[j] = make_int2(r | ((k - lo) % a.Hkv) << 16, nt - 1 - (k - lo) / a.Hkv);
+      if (k < lo || k >= hi) continue;
+      const int i = nt - 1 - (k - lo) / a.Hkv;
+      int u0, nu;
+      attn_units<BM>(a, q, i, UNIT, u0, nu);
+      w.list[2 * j] = make_int4(r, (k - lo) % a.Hkv, i, nu);
+      w.list[2 * j + 1] = make_int4(q.start, q.n, q.seq, u0);
     }
     lo = hi;
   }
@@ -139,7 +148,7 @@ __device__ __forceinline__ bool tile_work(const AttnArgs& a, int32_t* sm, TileWo
   __syncthreads();
   if (w.count == 0) return false;
   c.next = 0;
-  tile_take(a, w, c);
+  tile_take(w, c);
   return true;
 }
 
@@ -170,7 +179,7 @@ __global__ __launch_bounds__(NT, 1) void attn_tiles_kernel(const __grid_constant
     }
     bar_init_done();
   }
-  __shared__ int2 items[kListMax];
+  __shared__ int4 items[2 * kListMax];
   TileWork work;
   TileCursor c;
   work.list = items;
