@@ -253,6 +253,12 @@ MOE_API moe_status moe_attn_forward(moe_attn* A, const void* q, int64_t q_stride
   a.page = c.page_size; a.page_log2 = A->page_log2; a.window = c.window; a.scale = c.softmax_scale;
   a.scale_log2 = c.softmax_scale * 1.44269504088896340736f;
   a.part_o = A->part_o; a.part_ml = A->part_ml; a.arrived = A->arrived; a.ticket = A->ticket; a.status = A->status;
+  // ceil(2^(31 + l) / group) with 2^l >= group: row * mul / 2^(31 + l) has the quotient's floor for
+  // every row below 2^31 (the excess, below row * group / 2^(31 + l) < 1, never reaches the next one)
+  int l = 0;
+  while ((1 << l) < a.group) ++l;
+  a.group_shift = 31 + l;
+  a.group_mul = (uint32_t)(((1ull << a.group_shift) + a.group - 1) / a.group);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (c.dtype == MOE_F32) return launched(launch_attn_f32(a, c.head_dim, attn_grid(A->sms), s), "moe_attn_forward");
   CUtensorMap mk, mv;

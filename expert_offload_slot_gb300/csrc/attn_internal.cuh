@@ -36,6 +36,10 @@ struct AttnArgs {
   uint32_t* arrived;           // [grid] pieces of the split item that starts in CTA c; self-resetting
   uint32_t* ticket;            // [2]
   int32_t* status;             // sticky
+  uint32_t group_mul;          // token of a row without a division: (row * group_mul) >> group_shift,
+  int32_t group_shift;         // exact below 2^31 (group_mul = ceil(2^group_shift / group))
+  __device__ __forceinline__ int token(int row) const { return (int)(((uint64_t)(uint32_t)row * group_mul) >> group_shift); }
+  __device__ __forceinline__ int head_of(int row) const { return row - token(row) * group; }
 };
 
 __device__ __forceinline__ void attn_status(int32_t* status, int32_t code) { atomicCAS(status, 0, code); }
@@ -71,8 +75,8 @@ __device__ __forceinline__ AttnRequest attn_request(const AttnArgs& a, int r) {
 // key are still written).
 template <int BM>
 __device__ __forceinline__ void attn_units(const AttnArgs& a, const AttnRequest& q, int i, int unit, int& u0, int& nu) {
-  const int first = (i * BM) / a.group;                                   // first and last token of the tile
-  const int last = min(q.n - 1, ((i + 1) * BM - 1) / a.group);
+  const int first = a.token(i * BM);                                   // first and last token of the tile
+  const int last = min(q.n - 1, a.token((i + 1) * BM - 1));
   const int hi = q.seq - q.n + last + 1;
   int lo = a.window > 0 ? max(0, q.seq - q.n + first - a.window + 1) : 0;
   lo = min(lo, max(hi - 1, 0));
@@ -85,16 +89,39 @@ __device__ __forceinline__ int attn_tiles(const AttnArgs& a, const AttnRequest& 
   return (q.n * a.group + BM - 1) / BM;
 }
 
+// Units of a request's row tiles for one kv head, and the most of one tile: its lane by itself where
+// there are few tiles, else the whole warp for one lane after another.
 template <int BM>
-__device__ __forceinline__ int attn_request_units(const AttnArgs& a, const AttnRequest& q, int unit) {
-  int sum = 0;
-  const int nt = attn_tiles<BM>(a, q);
-  for (int i = 0; i < nt; ++i) {
-    int u0, nu;
+__device__ __forceinline__ void attn_count_units(const AttnArgs& a, const AttnRequest& q, int nt, int unit, int& sum,
+                                                 int& longest) {
+  const int lane = threadIdx.x & 31;
+  sum = longest = 0;
+  int u0, nu;
+  for (int i = 0; i < min(nt, 2); ++i) {
     attn_units<BM>(a, q, i, unit, u0, nu);
     sum += nu;
+    longest = max(longest, nu);
   }
-  return sum * a.Hkv;
+  for (uint32_t todo = __ballot_sync(0xffffffffu, nt > 2); todo; todo &= todo - 1) {
+    const int src = __ffs(todo) - 1;
+    AttnRequest x;
+    x.start = 0;
+    x.n = __shfl_sync(0xffffffffu, q.n, src);
+    x.seq = __shfl_sync(0xffffffffu, q.seq, src);
+    const int xt = __shfl_sync(0xffffffffu, nt, src);
+    int total = 0, top = 0;
+    for (int i = lane; i < xt; i += 32) {
+      attn_units<BM>(a, x, i, unit, u0, nu);
+      total += nu;
+      top = max(top, nu);
+    }
+    total = __reduce_add_sync(0xffffffffu, total);
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == src) {
+      sum = total;
+      longest = top;
+    }
+  }
 }
 
 // The units of all items, item after item, form one sequence of W units that is cut into
@@ -117,7 +144,7 @@ struct AttnSplit {
 };
 
 // Called by all threads of the CTA (NT of them) with at least `min_units` units per part.
-// `sm` holds 3 * 32 + 8 ints.  False when this CTA has no work.
+// `sm` holds 64 ints.  False when this CTA has no work.
 template <int BM, int NT>
 __device__ __forceinline__ bool attn_find_range(const AttnArgs& a, int unit, int min_units, int32_t* sm, AttnSplit& sp,
                                                 AttnCursor& cur) {
@@ -125,8 +152,15 @@ __device__ __forceinline__ bool attn_find_range(const AttnArgs& a, int unit, int
   constexpr int NW = NT / 32;
   const int per = (a.R + NT - 1) / NT;
   const int r0 = min(tid * per, a.R), r1 = min(r0 + per, a.R);
+  AttnRequest q = {0, 0, 0};                   // of the last request looked at: the only one when per is 1
   int mine = 0;
-  for (int r = r0; r < r1; ++r) mine += attn_request_units<BM>(a, attn_request(a, r), unit);
+  for (int k = 0; k < per; ++k) {
+    if (r0 + k < r1) q = attn_request(a, r0 + k);
+    else q.n = 0;
+    int sum, longest;
+    attn_count_units<BM>(a, q, attn_tiles<BM>(a, q), unit, sum, longest);
+    mine += sum * a.Hkv;
+  }
   int inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -134,7 +168,6 @@ __device__ __forceinline__ bool attn_find_range(const AttnArgs& a, int unit, int
     if (lane >= o) inc += v;
   }
   if (lane == 31) sm[wid] = inc;
-  if (tid == 0) sm[40] = -1;
   __syncthreads();
   int base = 0, W = 0;
 #pragma unroll
@@ -149,33 +182,44 @@ __device__ __forceinline__ bool attn_find_range(const AttnArgs& a, int unit, int
   if (W == 0 || c >= sp.parts) return false;
   const int x0 = sp.begin(c), x1 = sp.begin(c + 1);
   int lo = base + inc - mine;
-  if (x0 >= lo && x0 < lo + mine) {            // exactly one thread: find the request, then the tile
-    for (int r = r0; r < r1; ++r) {
-      const AttnRequest q = attn_request(a, r);
-      const int w = attn_request_units<BM>(a, q, unit);
-      if (x0 < lo + w) {
-        const int nt = attn_tiles<BM>(a, q);
-        for (int i = 0; i < nt; ++i) {
-          int u0, nu;
-          attn_units<BM>(a, q, i, unit, u0, nu);
-          if (x0 < lo + nu * a.Hkv) {
-            const int h = (x0 - lo) / nu;
-            sm[40] = r; sm[41] = i; sm[42] = h; sm[43] = x0 - lo - h * nu;
-            sm[44] = lo + h * nu;
-            break;
-          }
-          lo += nu * a.Hkv;
+  const uint32_t has = __ballot_sync(0xffffffffu, x0 >= lo && x0 < lo + mine);
+  if (has) {                                   // one warp, whose lane `src` has the request
+    const int src = __ffs(has) - 1;
+    int r = __shfl_sync(0xffffffffu, r0, src);
+    lo = __shfl_sync(0xffffffffu, lo, src);
+    q.start = __shfl_sync(0xffffffffu, q.start, src);
+    q.n = __shfl_sync(0xffffffffu, q.n, src);
+    q.seq = __shfl_sync(0xffffffffu, q.seq, src);
+    for (;; ++r) {                             // the whole warp, over the lane's requests and 32 tiles at a time
+      if (per > 1) q = attn_request(a, r);
+      const int nt = attn_tiles<BM>(a, q);
+      bool found = false;
+      for (int i0 = 0; i0 < nt && !found; i0 += 32) {
+        int u0 = 0, nu = 0;
+        if (i0 + lane < nt) attn_units<BM>(a, q, i0 + lane, unit, u0, nu);
+        int run = nu * a.Hkv;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, run, o);
+          if (lane >= o) run += v;
         }
-        break;
+        const int before = lo + run - nu * a.Hkv;
+        const bool here = nu > 0 && x0 >= before && x0 < before + nu * a.Hkv;
+        if (here) {
+          const int h = (x0 - before) / nu;
+          sm[40] = r; sm[41] = i0 + lane; sm[42] = h; sm[43] = x0 - before - h * nu; sm[44] = before + h * nu;
+          sm[45] = q.start; sm[46] = q.n; sm[47] = q.seq; sm[48] = u0; sm[49] = nu;
+        }
+        found = __any_sync(0xffffffffu, here);
+        lo += __shfl_sync(0xffffffffu, run, 31);
       }
-      lo += w;
+      if (found || r + 1 >= a.R) break;
     }
   }
   __syncthreads();
   cur.r = sm[40]; cur.i = sm[41]; cur.h = sm[42]; cur.at = sm[43]; cur.item_first = sm[44];
+  cur.q.start = sm[45]; cur.q.n = sm[46]; cur.q.seq = sm[47]; cur.u0 = sm[48]; cur.nu = sm[49];
   cur.left = x1 - x0;
-  cur.q = attn_request(a, cur.r);
-  attn_units<BM>(a, cur.q, cur.i, unit, cur.u0, cur.nu);
   return true;
 }
 
@@ -262,7 +306,7 @@ __device__ __forceinline__ void attn_join(const AttnArgs& a, const AttnCursor& c
       o.x *= inv; o.y *= inv; o.z *= inv; o.w *= inv;
     }
     const int fr = c.i * BM + row;
-    const size_t at = ((size_t)(c.q.start + fr / a.group) * a.Hq + c.h * a.group + fr % a.group) * D + d;
+    const size_t at = ((size_t)(c.q.start + a.token(fr)) * a.Hq + c.h * a.group + a.head_of(fr)) * D + d;
     attn_store4(static_cast<T*>(a.out) + at, o);
   }
 }

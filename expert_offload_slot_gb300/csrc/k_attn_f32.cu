@@ -32,9 +32,9 @@ __global__ __launch_bounds__(NT) void attn_f32_kernel(const AttnArgs a) {
   do {
     const int rows = min(BM, c.q.n * a.group - c.i * BM);
     const int fr = c.i * BM + row;
-    const int pos = row < rows ? c.q.seq - c.q.n + fr / a.group : -1;
+    const int pos = row < rows ? c.q.seq - c.q.n + a.token(fr) : -1;
     const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
-    const int first = (c.i * BM) / a.group, last = min(c.q.n - 1, ((c.i + 1) * BM - 1) / a.group);
+    const int first = a.token(c.i * BM), last = min(c.q.n - 1, a.token((c.i + 1) * BM - 1));
     const int tile_hi = c.q.seq - c.q.n + last + 1;
     const int tile_lo = a.window > 0 ? max(0, c.q.seq - c.q.n + first - a.window + 1) : 0;
     __syncthreads();
@@ -44,8 +44,8 @@ __global__ __launch_bounds__(NT) void attn_f32_kernel(const AttnArgs a) {
       if (rr < rows) {
         const int f = c.i * BM + rr;
         v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) +
-                                             (size_t)(c.q.start + f / a.group) * a.q_stride +
-                                             (size_t)(c.h * a.group + f % a.group) * D + d);
+                                             (size_t)(c.q.start + a.token(f)) * a.q_stride +
+                                             (size_t)(c.h * a.group + a.head_of(f)) * D + d);
       }
       *reinterpret_cast<float4*>(sq + rr * LD + d) = v;
     }
@@ -124,7 +124,7 @@ __global__ __launch_bounds__(NT) void attn_f32_kernel(const AttnArgs a) {
       if (row < rows) {
         const float inv = l > 0.f ? 1.f / l : 0.f;
         float* dst = static_cast<float*>(a.out) +
-                     ((size_t)(c.q.start + fr / a.group) * a.Hq + c.h * a.group + fr % a.group) * D + sub * 4;
+                     ((size_t)(c.q.start + a.token(fr)) * a.Hq + c.h * a.group + a.head_of(fr)) * D + sub * 4;
 #pragma unroll
         for (int k = 0; k < D / 32; ++k)
           attn_store4(dst + 32 * k, make_float4(o[4 * k] * inv, o[4 * k + 1] * inv, o[4 * k + 2] * inv, o[4 * k + 3] * inv));

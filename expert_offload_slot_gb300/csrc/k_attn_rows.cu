@@ -113,11 +113,11 @@ __global__ __launch_bounds__(NT, 1) void attn_rows_kernel(const __grid_constant_
 #pragma unroll
     for (int hh = 0; hh < 2; ++hh) {
       const int row = g + 8 * hh, f = c.i * BM + row;
-      pos[hh] = row < rows ? c.q.seq - c.q.n + f / a.group : -1;
+      pos[hh] = row < rows ? c.q.seq - c.q.n + a.token(f) : -1;
       lo[hh] = a.window > 0 ? max(0, pos[hh] - a.window + 1) : 0;
       const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) +
-                                 (size_t)(c.q.start + f / a.group) * a.q_stride +
-                                 (size_t)(c.h * a.group + f % a.group) * D + t4 * 2;
+                                 (size_t)(c.q.start + a.token(f)) * a.q_stride +
+                                 (size_t)(c.h * a.group + a.head_of(f)) * D + t4 * 2;
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         qf[k][hh] = row < rows ? *reinterpret_cast<const uint32_t*>(src + 16 * k) : 0u;
@@ -131,7 +131,7 @@ __global__ __launch_bounds__(NT, 1) void attn_rows_kernel(const __grid_constant_
       for (int k = 0; k < 4; ++k) o[d][k] = 0.f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     // keys that every row of the tile sees need no mask: [all_lo, all_hi)
-    const int first = (c.i * BM) / a.group, last = min(c.q.n - 1, ((c.i + 1) * BM - 1) / a.group);
+    const int first = a.token(c.i * BM), last = min(c.q.n - 1, a.token((c.i + 1) * BM - 1));
     const int tile_hi = c.q.seq - c.q.n + last + 1;
     const int tile_lo = a.window > 0 ? max(0, c.q.seq - c.q.n + first - a.window + 1) : 0;
     const int all_hi = c.q.seq - c.q.n + first + 1;
@@ -283,7 +283,7 @@ __global__ __launch_bounds__(NT, 1) void attn_rows_kernel(const __grid_constant_
         if (whole) {
           const float inv = l[hh] > 0.f ? 1.f / l[hh] : 0.f;
           __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) +
-                               ((size_t)(c.q.start + f / a.group) * a.Hq + c.h * a.group + f % a.group) * D + 2 * t4;
+                               ((size_t)(c.q.start + a.token(f)) * a.Hq + c.h * a.group + a.head_of(f)) * D + 2 * t4;
 #pragma unroll
           for (int d = 0; d < ND; ++d)
             *reinterpret_cast<uint32_t*>(dst + 8 * d) = pack_bf16(o[d][2 * hh] * inv, o[d][2 * hh + 1] * inv);

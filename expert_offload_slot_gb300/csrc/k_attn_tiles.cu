@@ -86,17 +86,17 @@ __device__ __forceinline__ bool tile_work(const AttnArgs& a, int32_t* sm, TileWo
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, G = gridDim.x;
   const int per = (a.R + NT - 1) / NT;
   const int r0 = min(tid * per, a.R), r1 = min(r0 + per, a.R);
+  AttnRequest q = {0, 0, 0};
   int units = 0, items = 0, longest = 0;
-  for (int r = r0; r < r1; ++r) {
-    const AttnRequest q = attn_request(a, r);
+  for (int k = 0; k < per; ++k) {
+    if (r0 + k < r1) q = attn_request(a, r0 + k);
+    else q.n = 0;
     const int nt = attn_tiles<BM>(a, q);
+    int sum, top;
+    attn_count_units<BM>(a, q, nt, UNIT, sum, top);
+    units += sum * a.Hkv;
     items += nt * a.Hkv;
-    for (int i = 0; i < nt; ++i) {
-      int u0, nu;
-      attn_units<BM>(a, q, i, UNIT, u0, nu);
-      units += nu * a.Hkv;
-      longest = max(longest, nu);
-    }
+    longest = max(longest, top);
   }
   int inc = items;
 #pragma unroll
@@ -129,7 +129,7 @@ __device__ __forceinline__ bool tile_work(const AttnArgs& a, int32_t* sm, TileWo
   }
   int lo = base + inc - items;
   for (int r = r0; r < r1; ++r) {
-    const AttnRequest q = attn_request(a, r);
+    if (per > 1) q = attn_request(a, r);
     const int nt = attn_tiles<BM>(a, q), hi = lo + nt * a.Hkv;
     for (int j = lo / G; j * G < hi; ++j) {
       const int k = (j & 1) ? (j + 1) * G - 1 - (int)blockIdx.x : j * G + (int)blockIdx.x;
@@ -208,7 +208,7 @@ __global__ __launch_bounds__(NT, 1) void attn_tiles_kernel(const __grid_constant
     const int my_box = lane % boxes, my_half = lane / boxes;
     uint32_t n = 0, edges = 0;
     do {
-      const int first = (c.i * BM) / a.group, last = min(c.q.n - 1, ((c.i + 1) * BM - 1) / a.group);
+      const int first = a.token(c.i * BM), last = min(c.q.n - 1, a.token((c.i + 1) * BM - 1));
       const int hi = c.q.seq - c.q.n + last + 1;
       const int lo = a.window > 0 ? max(0, c.q.seq - c.q.n + first - a.window + 1) : 0;
       const int units = attn_piece(c);
@@ -323,15 +323,19 @@ __global__ __launch_bounds__(NT, 1) void attn_tiles_kernel(const __grid_constant
     const uint32_t lanes = tmem + ((uint32_t)(wid & 3) << 21);        // this warp's 32 lanes of tensor memory
     const uint32_t s_addr = lanes + t * UNIT, o_addr = lanes + 256 + t * 128;
     uint32_t ns = 0, no = 0;
-    auto load_q = [&](const AttnCursor& x) {             // this thread's row of tile t, 128-byte swizzled
-      const int f = x.i * BM + t * 128 + row;
-      const bool live = f < x.q.n * a.group;
-      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q);
-      if (live) src += (size_t)(x.q.start + f / a.group) * a.q_stride + (size_t)(x.h * a.group + f % a.group) * D;
-      const uint32_t dst = sq + t * C::kTile + row * 128;
+    // This warp's 32 rows of tile t, 128-byte swizzled: D / 8 lanes read a row together.
+    auto load_q = [&](const AttnCursor& x) {
+      constexpr int PER = 32 / (D / 8);
+      const int limit = x.q.n * a.group, ch = lane % (D / 8);
+      const uint32_t dst = sq + t * C::kTile + (ch >> 3) * C::kHalf;
 #pragma unroll
-      for (int ch = 0; ch < D / 8; ++ch)
-        cp_async16(dst + (ch >> 3) * C::kHalf + (((ch & 7) ^ (row & 7)) << 4), src + ch * 8, live ? 16 : 0);
+      for (int k = 0; k < 32; k += PER) {
+        const int r = (wid & 3) * 32 + k + lane / (D / 8), f = x.i * BM + t * 128 + r, token = a.token(f);
+        const bool live = f < limit;
+        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q);
+        if (live) src += (size_t)(x.q.start + token) * a.q_stride + (size_t)(x.h * a.group + f - token * a.group) * D;
+        cp_async16(dst + r * 128 + (((ch & 7) ^ (r & 7)) << 4), src + ch * 8, live ? 16 : 0);
+      }
     };
     auto has_tile = [&](const AttnCursor& x) { return x.q.n * a.group - x.i * BM > t * 128; };
     bool mine = has_tile(c);
@@ -359,12 +363,12 @@ __global__ __launch_bounds__(NT, 1) void attn_tiles_kernel(const __grid_constant
       }
       const int rows = min(BM, c.q.n * a.group - c.i * BM) - t * 128;     // of this tile (may exceed 128)
       const int f = c.i * BM + t * 128 + row, base_pos = c.q.seq - c.q.n;
-      const int pos = row < rows ? base_pos + f / a.group : -1;
+      const int pos = row < rows ? base_pos + a.token(f) : -1;
       const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
       // keys that every row of this tile sees need no mask
       const int f0 = c.i * BM + t * 128, f1 = f0 + min(rows, 128) - 1;
-      const int all_hi = base_pos + f0 / a.group + 1;
-      const int all_lo = a.window > 0 ? max(0, base_pos + f1 / a.group - a.window + 1) : 0;
+      const int all_hi = base_pos + a.token(f0) + 1;
+      const int all_lo = a.window > 0 ? max(0, base_pos + a.token(f1) - a.window + 1) : 0;
       float m = -INFINITY, l = 0.f;
       const int units = attn_piece(c);
       for (int j = 0; j < units; ++j) {
@@ -439,7 +443,7 @@ __global__ __launch_bounds__(NT, 1) void attn_tiles_kernel(const __grid_constant
       const size_t part = ((size_t)attn_slot(c) * BM + t * 128 + row);
       const float inv = l > 0.f ? 1.f / l : 0.f;
       __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out);
-      if (row < rows) dst += ((size_t)(c.q.start + f / a.group) * a.Hq + c.h * a.group + f % a.group) * D;
+      if (row < rows) dst += ((size_t)(c.q.start + a.token(f)) * a.Hq + c.h * a.group + a.head_of(f)) * D;
 #pragma unroll 1
       for (int d = 0; d < D; d += 32) {
         float o[32];
@@ -512,7 +516,7 @@ __global__ __launch_bounds__(NT, 1) void attn_tiles_kernel(const __grid_constant
               const int r = r0 + b + k * PER + lane / LANES, fr = c.i * BM + t * 128 + r;
               if (r < rows)
                 attn_store4(static_cast<__nv_bfloat16*>(a.out) +
-                                ((size_t)(c.q.start + fr / a.group) * a.Hq + c.h * a.group + fr % a.group) * D +
+                                ((size_t)(c.q.start + a.token(fr)) * a.Hq + c.h * a.group + a.head_of(fr)) * D +
                                 lane % LANES * 4, o[k]);
             }
           }
