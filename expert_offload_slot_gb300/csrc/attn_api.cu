@@ -62,9 +62,10 @@ moe_status check_config(const moe_attn_config* c) {
   return MOE_OK;
 }
 
-// A cache [num_pages][Hkv][P][D] as [D / 64][num_pages * Hkv * P][64] bf16: a box of `rows`
-// consecutive keys of one head comes as `halves` tiles of 128-byte rows, 128-byte swizzled.
-bool cache_map(CUtensorMap* m, const void* base, int64_t keys, int D, int rows, int halves) {
+// A cache [num_pages][Hkv][P][D] as [D / cols][num_pages * Hkv * P][cols] bf16, cols 64 or 32: a box
+// of `rows` consecutive keys of one head comes as `blocks` tiles of rows of 2 cols bytes, swizzled
+// over as many.
+bool cache_map(CUtensorMap* m, const void* base, int64_t keys, int D, int rows, int cols, int blocks) {
   static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
     void* p = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -74,11 +75,12 @@ bool cache_map(CUtensorMap* m, const void* base, int64_t keys, int D, int rows, 
     return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
   }();
   if (!encode) return false;
-  const cuuint64_t dims[3] = {64, (cuuint64_t)keys, (cuuint64_t)(D / 64)};
-  const cuuint64_t strides[2] = {(cuuint64_t)D * 2, 128};
-  const cuuint32_t box[3] = {64, (cuuint32_t)rows, (cuuint32_t)halves}, one[3] = {1, 1, 1};
+  const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)keys, (cuuint64_t)(D / cols)};
+  const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)cols * 2};
+  const cuuint32_t box[3] = {(cuuint32_t)cols, (cuuint32_t)rows, (cuuint32_t)blocks}, one[3] = {1, 1, 1};
   return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, one,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -116,7 +118,7 @@ MOE_API moe_status moe_attn_create(const moe_attn_config* cfg, int device, moe_a
   if (A->sms < 1) A->sms = 1;
   // two partial slots of a row tile per CTA: the fp32 kernel has two CTAs per SM, the others one
   const size_t slots = (size_t)2 * attn_grid(A->sms);
-  const size_t part_rows = cfg->dtype == MOE_F32 ? slots * kAttnF32Tile : (size_t)2 * A->sms * kAttnTile;
+  const size_t part_rows = cfg->dtype == MOE_F32 ? slots * kAttnF32Tile : (size_t)A->sms * kAttnTile;
   const size_t o_bytes = part_rows * cfg->head_dim * sizeof(float), ml_bytes = part_rows * sizeof(float2);
   A->zero_bytes = (slots + 8) * sizeof(uint32_t);
   e = cudaMalloc(&A->work, o_bytes + ml_bytes + A->zero_bytes);
@@ -264,10 +266,16 @@ MOE_API moe_status moe_attn_forward(moe_attn* A, const void* q, int64_t q_stride
   CUtensorMap mk, mv;
   const int64_t keys = (int64_t)num_pages * c.num_kv_heads * c.page_size;
   const bool few = (int64_t)max_new * a.group <= kAttnRowsTile;
-  const int box = few ? 16 : c.page_size, halves = few ? c.head_dim / 64 : 1;
-  if (!cache_map(&mk, k_cache, keys, c.head_dim, box, halves) || !cache_map(&mv, v_cache, keys, c.head_dim, box, halves))
-    return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for the caches");
-  return launched(few ? launch_attn_rows(a, mk, mv, c.head_dim, A->sms, s) : launch_attn_tiles(a, mk, mv, c.head_dim, A->sms, s),
+  const int D = c.head_dim;
+  bool ok;
+  if (few) {                   // 16 keys of a head at a time, all columns
+    ok = cache_map(&mk, k_cache, keys, D, 16, 64, D / 64) && cache_map(&mv, v_cache, keys, D, 16, 64, D / 64);
+  } else {                     // half a K tile is 64 keys, half a V tile half the columns: a CTA's share of a pair
+    ok = cache_map(&mk, k_cache, keys, D, c.page_size < 64 ? c.page_size : 64, 64, 1) &&
+         cache_map(&mv, v_cache, keys, D, c.page_size, D / 2, 1);
+  }
+  if (!ok) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for the caches");
+  return launched(few ? launch_attn_rows(a, mk, mv, D, A->sms, s) : launch_attn_tiles(a, mk, mv, D, A->sms / 2 * 2, s),
                   "moe_attn_forward");
 }
 

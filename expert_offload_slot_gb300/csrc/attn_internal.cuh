@@ -15,7 +15,7 @@ namespace moeslot {
 moe_status set_last_error(moe_status st, const char* msg);   // text for moe_last_error()
 
 constexpr int kAttnRowsTile = 16;     // query rows per item of the row kernel
-constexpr int kAttnTile = 256;        // and of the tile kernel
+constexpr int kAttnTile = 512;        // and of the tile kernel, by a pair of CTAs
 constexpr int kAttnF32Tile = 32;
 
 struct AttnArgs {
@@ -143,10 +143,10 @@ struct AttnSplit {
   __device__ __forceinline__ int owner(int x) const { return (int)((((int64_t)x + 1) * parts - 1) / W); }
 };
 
-// Called by all threads of the CTA (NT of them) with at least `min_units` units per part.
-// `sm` holds 64 ints.  False when this CTA has no work.
+// Called by all threads of the CTA (NT of them) for part c of at most `most`.  `sm` holds 64 ints.
+// False when the part has no work.
 template <int BM, int NT>
-__device__ __forceinline__ bool attn_find_range(const AttnArgs& a, int unit, int min_units, int32_t* sm, AttnSplit& sp,
+__device__ __forceinline__ bool attn_find_range(const AttnArgs& a, int unit, int c, int most, int32_t* sm, AttnSplit& sp,
                                                 AttnCursor& cur) {
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   constexpr int NW = NT / 32;
@@ -177,8 +177,7 @@ __device__ __forceinline__ bool attn_find_range(const AttnArgs& a, int unit, int
     W += v;
   }
   sp.W = W;
-  sp.parts = max(1, min((int)gridDim.x, W / min_units));
-  const int c = blockIdx.x;
+  sp.parts = max(1, min(most, W));
   if (W == 0 || c >= sp.parts) return false;
   const int x0 = sp.begin(c), x1 = sp.begin(c + 1);
   int lo = base + inc - mine;
@@ -246,8 +245,8 @@ __device__ __forceinline__ bool attn_next(const AttnArgs& a, int unit, AttnCurso
   return true;
 }
 
-// Partial slot of this CTA's piece of a split item.
-__device__ __forceinline__ int attn_slot(const AttnCursor& c) { return 2 * blockIdx.x + (c.at == 0 ? 1 : 0); }
+// Partial slot of part `part`'s piece of a split item.
+__device__ __forceinline__ int attn_slot(const AttnCursor& c, int part) { return 2 * part + (c.at == 0 ? 1 : 0); }
 
 // All threads, after the piece's partial results are stored: true in the CTA whose piece is the
 // last of the item to arrive, with c0 and n the item's first CTA and number of pieces.

@@ -27,7 +27,7 @@ __global__ __launch_bounds__(NT) void attn_f32_kernel(const AttnArgs a) {
   __shared__ int32_t sched[128];
   AttnSplit sp;
   AttnCursor c;
-  if (!attn_find_range<BM, NT>(a, BN, 2, sched, sp, c)) return;
+  if (!attn_find_range<BM, NT>(a, BN, blockIdx.x, gridDim.x, sched, sp, c)) return;
   const int tid = threadIdx.x, row = tid / 8, sub = tid % 8;
   do {
     const int rows = min(BM, c.q.n * a.group - c.i * BM);
@@ -130,7 +130,7 @@ __global__ __launch_bounds__(NT) void attn_f32_kernel(const AttnArgs a) {
           attn_store4(dst + 32 * k, make_float4(o[4 * k] * inv, o[4 * k + 1] * inv, o[4 * k + 2] * inv, o[4 * k + 3] * inv));
       }
     } else {
-      const size_t at = (size_t)attn_slot(c) * BM + row;
+      const size_t at = (size_t)attn_slot(c, blockIdx.x) * BM + row;
       if (sub == 0) a.part_ml[at] = make_float2(m, l);
 #pragma unroll
       for (int k = 0; k < D / 32; ++k)

@@ -56,7 +56,7 @@ __global__ __launch_bounds__(NT, 1) void attn_rows_kernel(const __grid_constant_
   }
   AttnSplit sp;
   AttnCursor c;
-  if (!attn_find_range<BM, NT>(a, UNIT, 1, sched, sp, c)) return;
+  if (!attn_find_range<BM, NT>(a, UNIT, blockIdx.x, gridDim.x, sched, sp, c)) return;
 
   uint64_t* bar = bars + wid * C::kStages;
   const uint32_t ring = smem_addr(smem) + wid * C::kStages * 2 * C::kTile;
@@ -288,7 +288,7 @@ __global__ __launch_bounds__(NT, 1) void attn_rows_kernel(const __grid_constant_
           for (int d = 0; d < ND; ++d)
             *reinterpret_cast<uint32_t*>(dst + 8 * d) = pack_bf16(o[d][2 * hh] * inv, o[d][2 * hh + 1] * inv);
         } else {
-          const size_t at = (size_t)attn_slot(c) * BM + row;
+          const size_t at = (size_t)attn_slot(c, blockIdx.x) * BM + row;
           if (t4 == 0) a.part_ml[at] = make_float2(m[hh], l[hh]);
 #pragma unroll
           for (int d = 0; d < ND; ++d)

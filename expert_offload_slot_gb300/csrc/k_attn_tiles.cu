@@ -4,25 +4,31 @@
 //   out[t, head] = sum_j softmax_j(scale q[t, head] . k[j]) v[j],
 //   j in (pos - window, pos], pos = seq_len - new + t
 //
-// An item is 256 query rows (all heads of one kv head's group, token-major, so
-// that a key tile serves the whole group) as two M = 128 tiles A and B.  Per 128
-// keys and tile: S = Q K^T (128 x 128, K-major operands from shared memory), the
-// softmax in registers, one thread per row, P in bf16 back into tensor memory over
-// S, and O += P V with P as the tensor-memory operand and V as an MN-major
-// operand, straight from its [key][d] layout.  While one tile is in the softmax
-// the tensor cores work on the other.
+// Two CTAs work as a pair (cluster of two, tcgen05 cta_group::2).  An item is 512 query
+// rows (all heads of one kv head's group, token-major, so that a key tile serves the
+// whole group) as two M = 256 tiles A and B, half of each in either CTA.  Per 128 keys
+// and tile: S = Q K^T (K-major operands from shared memory), the softmax in registers,
+// one thread per row, P in bf16 back into tensor memory over S, and O += P V with P as
+// the tensor-memory operand and V as an MN-major operand, straight from its [key][d]
+// layout.  While one tile is in the softmax the tensor cores work on the other.
+//
+// Why pairs: each CTA keeps and loads only half of every K tile (64 of the keys) and V
+// tile (half of the columns).  An SM's TMA unit brings swizzled boxes of 16, 64 and 128
+// rows in at 20, 31 and 35 bytes a cycle (measured, L2 hits), and one CTA alone would want
+// 64 KB every 2048 cycles that its products take; its shared memory would be busy with
+// operands in all of them (128 bytes a cycle).
 //
 // The running maximum m is only raised (and O, l rescaled by 2^(m - m')) when a
 // score exceeds it by more than 2^8: P stays below 256, which bf16 and fp32 hold
 // with the same relative precision, and the rescaling of O through tensor memory
 // becomes rare.  O and l are divided once at the end, so the choice of m cancels.
 //
-// Roles (three warpgroups): warps 0..3 and 4..7 softmax and output of tiles A and B;
-// warp 8 loads K and V tiles by TMA, one box per page and 64-column half; warp 9
-// issues the MMAs.  A softmax thread holds its row's 128 scores, so the third
-// warpgroup gives registers up: launched with 168 each (384 x 168 = 64512), 216 for
-// the first two and 72 for the third (256 x 216 + 128 x 72 = 64512).  Tensor memory
-// (512 columns): S/P of A, S/P of B, O of A, O of B.
+// Roles (three warpgroups in each CTA): warps 0..3 and 4..7 softmax and output of this
+// CTA's rows of tiles A and B; warp 8 loads K and V by TMA, one box per page and 64-column
+// half; warp 9 of the first CTA issues the MMAs.  A softmax thread holds its row's 128
+// scores, so the third warpgroup gives registers up: launched with 168 each (384 x 168 =
+// 64512), 216 for the first two and 72 for the third (256 x 216 + 128 x 72 = 64512).
+// Tensor memory (512 columns): S/P of A, S/P of B, O of A, O of B.
 #include "attn_internal.cuh"
 #include "sm103.cuh"
 
@@ -35,27 +41,28 @@ constexpr float kRaise = 8.f;                  // log2 of the growth of P that m
 
 template <int D>
 struct TileCfg {
-  static constexpr int kHalf = UNIT * 128;               // bytes of a 64-column half of a 128-row tile
-  static constexpr int kTile = kHalf * (D / 64);
-  static constexpr int kStages = D == 128 ? 5 : 8;
-  static constexpr int kBytes = (2 + kStages) * kTile + 1024;
+  static constexpr int kQ = 128 * D * 2;                 // this CTA's rows of a Q tile: [D / 64][128][128 bytes]
+  static constexpr int kTile = 64 * D * 2;               // its half of a K tile [D / 64][64 keys][128 bytes]
+                                                         // or of a V tile [128 keys][D bytes]
+  static constexpr int kStages = D == 128 ? 10 : 16;
+  static constexpr int kBytes = 2 * kQ + kStages * kTile + 1024;
 };
 
 // A call's work is divided in one of two ways, chosen from the lengths by every CTA alike.
-// Whole: the items, longest first within a request, are dealt out to the CTAs to and fro, so that
+// Whole: the items, longest first within a request, are dealt out to the pairs to and fro, so that
 // long and short ones meet in each; nothing is split.  Ranges: the keys of all items are cut into
 // equal ranges (attn_find_range), which balances any lengths but has split items join their
 // pieces through memory; that takes about as long as kJoin units.  So items stay whole unless
 // the longest takes kJoin units more than an even share.
 struct TileCursor : AttnCursor {
-  int32_t next;                                // whole items: place of the next one in the CTA's list
+  int32_t next;                                // whole items: place of the next one in the pair's list
 };
 constexpr int kListMax = 32, kJoin = 6;
 
 struct TileWork {
   AttnSplit sp;
   bool whole;
-  int count;                                   // whole: items of this CTA
+  int count;                                   // whole: items of this pair
   int4* list;                                  // [2 * kListMax] (request, head, tile, units), (first row, new, seq, first unit)
 };
 
@@ -83,7 +90,7 @@ __device__ __forceinline__ bool tile_next(const AttnArgs& a, const TileWork& w, 
 
 // All threads; sm: 64 ints.
 __device__ __forceinline__ bool tile_work(const AttnArgs& a, int32_t* sm, TileWork& w, TileCursor& c) {
-  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, G = gridDim.x;
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, G = (int)gridDim.x / 2, pair = (int)blockIdx.x / 2;
   const int per = (a.R + NT - 1) / NT;
   const int r0 = min(tid * per, a.R), r1 = min(r0 + per, a.R);
   AttnRequest q = {0, 0, 0};
@@ -125,14 +132,14 @@ __device__ __forceinline__ bool tile_work(const AttnArgs& a, int32_t* sm, TileWo
   w.count = 0;
   if (!w.whole) {
     __syncthreads();
-    return attn_find_range<BM, NT>(a, UNIT, 1, sm, w.sp, c);
+    return attn_find_range<BM, NT>(a, UNIT, pair, G, sm, w.sp, c);
   }
   int lo = base + inc - items;
   for (int r = r0; r < r1; ++r) {
     if (per > 1) q = attn_request(a, r);
     const int nt = attn_tiles<BM>(a, q), hi = lo + nt * a.Hkv;
     for (int j = lo / G; j * G < hi; ++j) {
-      const int k = (j & 1) ? (j + 1) * G - 1 - (int)blockIdx.x : j * G + (int)blockIdx.x;
+      const int k = (j & 1) ? (j + 1) * G - 1 - pair : j * G + pair;
       if (k < lo || k >= hi) continue;
       const int i = nt - 1 - (k - lo) / a.Hkv;
       int u0, nu;
@@ -143,7 +150,7 @@ __device__ __forceinline__ bool tile_work(const AttnArgs& a, int32_t* sm, TileWo
     lo = hi;
   }
   const int last = (all - 1) / G;              // round of the last item; only that round may lack one
-  const int k = (last & 1) ? (last + 1) * G - 1 - (int)blockIdx.x : last * G + (int)blockIdx.x;
+  const int k = (last & 1) ? (last + 1) * G - 1 - pair : last * G + pair;
   w.count = last + (k < all);
   __syncthreads();
   if (w.count == 0) return false;
@@ -153,45 +160,49 @@ __device__ __forceinline__ bool tile_work(const AttnArgs& a, int32_t* sm, TileWo
 }
 
 template <int D>
-__global__ __launch_bounds__(NT, 1) void attn_tiles_kernel(const __grid_constant__ CUtensorMap mk,
-                                                           const __grid_constant__ CUtensorMap mv, const AttnArgs a) {
+__global__ __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
+void attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const AttnArgs a) {
   using C = TileCfg<D>;
   extern __shared__ uint8_t raw[];
   __shared__ int32_t sched[64];
-  __shared__ __align__(8) uint64_t full[C::kStages], empty[C::kStages], edge, drain, q_full[2], s_full[2], p_full[2], o_full[2];
+  // full, q_full and p_full are the first CTA's, who issues the products, for both; the others are of each its own
+  __shared__ __align__(8) uint64_t full[C::kStages], empty[C::kStages], edge[C::kStages], drain, q_full[2], s_full[2],
+      p_full[2], o_full[2];
   __shared__ uint32_t tmem_slot;
   __shared__ int32_t last_flag[2];
+  __shared__ int4 items[2 * kListMax];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  const uint32_t sq = smem_addr(smem), ring = sq + 2 * C::kTile;
+  const uint32_t sq = smem_addr(smem), ring = sq + 2 * C::kQ;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const int rank = (int)pair_rank(), part = (int)blockIdx.x / 2;
+  TileWork work;
+  TileCursor c;
+  work.list = items;
+  if (!tile_work(a, sched, work, c)) return;             // the same answer in every thread of the pair
   if (tid == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      bar_init(full + s, 1);
+      bar_init(full + s, 2);
       bar_init(empty + s, 1);
+      bar_init(edge + s, 1);
     }
-    bar_init(&edge, 1);
     bar_init(&drain, 1);
     for (int t = 0; t < 2; ++t) {
-      bar_init(q_full + t, 128);
+      bar_init(q_full + t, 8);
       bar_init(s_full + t, 1);
-      bar_init(p_full + t, 128);
+      bar_init(p_full + t, 8);
       bar_init(o_full + t, 1);
     }
     bar_init_done();
   }
-  __shared__ int4 items[2 * kListMax];
-  TileWork work;
-  TileCursor c;
-  work.list = items;
-  if (!tile_work(a, sched, work, c)) return;           // the same answer in every thread
   if (wid == 9) tmem_alloc(&tmem_slot, 512);
   tc_fence_before();
   __syncthreads();
+  pair_sync();                                           // the other CTA's barriers are ready, too
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
 
   bool alive = true;
-  auto wait = [&](uint64_t* b, uint32_t parity) {                      // bounded; after a timeout nothing waits any more
+  auto wait = [&](uint64_t* b, uint32_t parity) {        // bounded; after a timeout nothing waits any more
     if (alive && !bar_wait(b, parity)) {
       alive = false;
       attn_status(a.status, MOE_ERR_TIMEOUT);
@@ -199,82 +210,94 @@ __global__ __launch_bounds__(NT, 1) void attn_tiles_kernel(const __grid_constant
   };
 
   if (wid >= 8) {
-  regs_give<72>();
-  if (wid == 8) {
-    // ---------------------------------------------------------------- loads
-    const int row_limit = (int)((int64_t)a.num_pages * a.Hkv * a.page);   // out of range: zeros arrive
-    const int box = min(a.page, UNIT), boxes = UNIT / box;
-    const bool mine = lane < boxes * (D / 64);
-    const int my_box = lane % boxes, my_half = lane / boxes;
-    uint32_t n = 0, edges = 0;
-    do {
-      const int first = a.token(c.i * BM), last = min(c.q.n - 1, a.token((c.i + 1) * BM - 1));
-      const int hi = c.q.seq - c.q.n + last + 1;
-      const int lo = a.window > 0 ? max(0, c.q.seq - c.q.n + first - a.window + 1) : 0;
-      const int units = attn_piece(c);
-      for (int j = 0; j < units; ++j) {
-        const int key0 = (c.u0 + c.at + j) * UNIT, key = key0 + my_box * box;
-        int at = row_limit;
-        if (mine && key < c.q.seq) {
-          const int page = a.table[(size_t)c.r * a.table_stride + (key >> a.page_log2)];
-          if ((uint32_t)page < (uint32_t)a.num_pages) at = ((page * a.Hkv + c.h) << a.page_log2) + (key & (a.page - 1));
-          else attn_status(a.status, MOE_ERR_BOUNDS);
-        }
-        for (int kv = 0; kv < 2; ++kv, ++n) {
-          const int st = n % C::kStages;
-          const uint32_t stage = ring + st * C::kTile;
-          wait(empty + st, ((n / C::kStages) & 1) ^ 1);
-          __syncwarp();
-          // values of keys that no row of the item sees may be anything (0 x NaN is NaN): they are
-          // zeroed here, in the first and last unit of an item
-          const bool clean = kv == 1 && (key0 < lo || key0 + UNIT > hi);
-          uint64_t* bar = clean ? &edge : full + st;
-          if (lane == 0) bar_expect(bar, C::kTile);
-          __syncwarp();
-          if (mine) tma_3d(stage + my_half * C::kHalf + my_box * box * 128, kv ? &mv : &mk, bar, 0, at, my_half);
-          if (clean) {
-            wait(&edge, edges & 1);
-            ++edges;
+    regs_give<72>();
+    if (wid == 8) {
+      // ---------------------------------------------------------------- loads
+      // A K tile as 64 keys x D (one box per page and 64 columns), a V tile as 128 keys x D / 2.
+      const int row_limit = (int)((int64_t)a.num_pages * a.Hkv * a.page);   // out of range: zeros arrive
+      const int k_box = min(a.page, 64), k_boxes = 64 / k_box, v_box = min(a.page, UNIT), v_boxes = UNIT / v_box;
+      const bool my_k = lane < k_boxes * (D / 64), my_v = lane < v_boxes;
+      const int k_col = lane / k_boxes;
+      const uint32_t k_dst = k_col * (64 * 128) + lane % k_boxes * k_box * 128, v_dst = lane * v_box * D;
+      uint32_t n = 0, edge_phase = 0;
+      auto row_of = [&](int key) -> int {                // row of the cache map that holds the key
+        if (key >= c.q.seq) return row_limit;
+        const int page = a.table[(size_t)c.r * a.table_stride + (key >> a.page_log2)];
+        if ((uint32_t)page < (uint32_t)a.num_pages) return ((page * a.Hkv + c.h) << a.page_log2) + (key & (a.page - 1));
+        attn_status(a.status, MOE_ERR_BOUNDS);
+        return row_limit;
+      };
+      do {
+        const int first = a.token(c.i * BM), last = min(c.q.n - 1, a.token((c.i + 1) * BM - 1));
+        const int hi = c.q.seq - c.q.n + last + 1;
+        const int lo = a.window > 0 ? max(0, c.q.seq - c.q.n + first - a.window + 1) : 0;
+        const int units = attn_piece(c);
+        for (int j = 0; j < units; ++j) {
+          const int key0 = (c.u0 + c.at + j) * UNIT;
+          const int k_at = my_k ? row_of(key0 + rank * 64 + lane % k_boxes * k_box) : 0;
+          const int v_at = my_v ? row_of(key0 + lane * v_box) : 0;
+          for (int kv = 0; kv < 2; ++kv, ++n) {
+            const int st = n % C::kStages;
+            const uint32_t stage = ring + st * C::kTile, lead_full = lead_addr(full + st);
+            wait(empty + st, ((n / C::kStages) & 1) ^ 1);
             __syncwarp();
-            for (int r = lane; r < UNIT; r += 32) {
-              if (key0 + r >= lo && key0 + r < hi) continue;
-              for (int h = 0; h < D / 64; ++h)
-                for (int ch = 0; ch < 8; ++ch)
-                  *reinterpret_cast<uint4*>(smem + (stage - sq) + h * C::kHalf + r * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
+            // Values of keys that no row of the item sees may be anything (0 x NaN is NaN): they are
+            // zeroed here, in the first and last unit of an item, once they have landed.
+            const bool clean = kv == 1 && (key0 < lo || key0 + UNIT > hi);
+            if (clean) {
+              if (lane == 0) bar_expect(edge + st, C::kTile);
+              __syncwarp();
+              if (my_v) tma_3d(stage + v_dst, &mv, edge + st, 0, v_at, rank);
+              // the barrier's phase is that of its uses, not of the ring: one bit per stage
+              wait(edge + st, (edge_phase >> st) & 1);
+              edge_phase ^= 1u << st;
+              __syncwarp();
+              for (int r = lane; r < UNIT; r += 32) {
+                if (key0 + r >= lo && key0 + r < hi) continue;
+                for (int ch = 0; ch < D / 16; ++ch)
+                  *reinterpret_cast<uint4*>(smem + (stage - sq) + r * D + ch * 16) = make_uint4(0, 0, 0, 0);
+              }
+              fence_async_smem();
+              __syncwarp();
+              if (lane == 0) bar_arrive_at(lead_full);
+              continue;
             }
-            fence_async_smem();
+            if (lane == 0) {
+              if (rank == 0) bar_expect(full + st, 2 * C::kTile);      // of both CTAs
+              else bar_arrive_at(lead_full);
+            }
             __syncwarp();
-            if (lane == 0) bar_arrive(full + st);
+            if (kv == 0 ? my_k : my_v)
+              tma_3d_pair(stage + (kv == 0 ? k_dst : v_dst), kv == 0 ? &mk : &mv, lead_full, 0, kv == 0 ? k_at : v_at,
+                          kv == 0 ? k_col : rank);
           }
         }
+      } while (tile_next(a, work, c));
+      if (!alive) {                                      // bounded: copies in flight land (on the first CTA's barriers,
+        const uint64_t t0 = now_ns();                    // which this one cannot test) before the memory is given up
+        while (now_ns() - t0 < 1000000ull) __nanosleep(1000);
       }
-    } while (tile_next(a, work, c));
-    if (!alive)                                          // bounded: copies in flight land before the memory is given up
-      for (uint32_t k = n > C::kStages ? n - C::kStages : 0; k < n; ++k) bar_wait(full + k % C::kStages, (k / C::kStages) & 1);
-  } else if (wid == 9) {
-    // ----------------------------------------------------------------- MMAs
-    {
+    } else if (wid == 9 && rank == 0) {
+      // ----------------------------------------------------------------- MMAs
       const uint32_t lead = elect_lead();
       constexpr uint32_t kS = tc_idesc(UNIT, false), kO = tc_idesc(D, true);
       uint32_t n = 0;                                    // ring position
       uint32_t np[2] = {0, 0}, pieces[2] = {0, 0};       // P tiles and Q tiles taken
       // Descriptors are made once; a step in K or to another stage adds to their address field (units
       // of 16 bytes).
-      const uint64_t q_desc = tc_desc(sq, 16), k_desc = tc_desc(ring, 16), v_desc = tc_desc(ring, C::kHalf);
+      const uint64_t q_desc = tc_desc<128>(sq), k_desc = tc_desc<128>(ring), v_desc = tc_desc<D>(ring);
       auto scores = [&](int t, uint32_t stage) {
-        const uint64_t qd = q_desc + t * (C::kTile >> 4), kd = k_desc + stage * (C::kTile >> 4);
+        const uint64_t qd = q_desc + t * (C::kQ >> 4), kd = k_desc + stage * (C::kTile >> 4);
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = ((k >> 2) * C::kHalf + (k & 3) * 32) >> 4;
-          tc_mma_ss(lead, tmem + t * UNIT, qd + off, kd + off, kS, k > 0);
-        }
+        for (int k = 0; k < D / 16; ++k)
+          tc_mma_ss(lead, tmem + t * UNIT, qd + (((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4),
+                    kd + (((k >> 2) * (64 * 128) + (k & 3) * 32) >> 4), kS, k > 0);
         tc_commit(lead, s_full + t);
       };
       do {
-        const int rows = min(BM, c.q.n * a.group - c.i * BM), tiles = rows > 128 ? 2 : 1;
+        const int tiles = c.q.n * a.group - c.i * BM > 256 ? 2 : 1;
         const int units = attn_piece(c);
         wait(full + n % C::kStages, (n / C::kStages) & 1);
-        __syncwarp();
         for (int t = 0; t < tiles; ++t) {
           wait(q_full + t, pieces[t]++ & 1);
           __syncwarp();
@@ -287,15 +310,14 @@ __global__ __launch_bounds__(NT, 1) void attn_tiles_kernel(const __grid_constant
           const uint32_t vs = n % C::kStages, ks = (n + 1) % C::kStages;
           const bool more = j + 1 < units;
           wait(full + vs, (n / C::kStages) & 1);
-          __syncwarp();
+          const uint64_t vd = v_desc + vs * (C::kTile >> 4);
           for (int t = 0; t < tiles; ++t) {
-            const uint64_t vd = v_desc + vs * (C::kTile >> 4);
             wait(p_full + t, np[t]++ & 1);
             __syncwarp();
             tc_fence_after();
 #pragma unroll
             for (int k = 0; k < UNIT / 16; ++k)
-              tc_mma_ts(lead, tmem + 256 + t * 128, tmem + t * UNIT + k * 8, vd + k * (2048 >> 4), kO, k > 0 || j > 0);
+              tc_mma_ts(lead, tmem + 256 + t * 128, tmem + t * UNIT + k * 8, vd + k * (16 * D >> 4), kO, k > 0 || j > 0);
             if (more) {
               if (t == 0) wait(full + ks, ((n + 1) / C::kStages) & 1);
               __syncwarp();
@@ -314,61 +336,63 @@ __global__ __launch_bounds__(NT, 1) void attn_tiles_kernel(const __grid_constant
         bar_wait(&drain, 0);
       }
     }
-    __syncwarp();
-  }
   } else {
     regs_take<216>();
     // ------------------------------------------------- softmax and output of tile t
     const int t = wid >> 2, row = (wid & 3) * 32 + lane;
+    const int f_off = t * 256 + rank * 128;                           // this CTA's first row of the tile
     const uint32_t lanes = tmem + ((uint32_t)(wid & 3) << 21);        // this warp's 32 lanes of tensor memory
     const uint32_t s_addr = lanes + t * UNIT, o_addr = lanes + 256 + t * 128;
+    const uint32_t lead_p = lead_addr(p_full + t), lead_q = lead_addr(q_full + t);
     uint32_t ns = 0, no = 0;
     // This warp's 32 rows of tile t, 128-byte swizzled: D / 8 lanes read a row together.
     auto load_q = [&](const AttnCursor& x) {
       constexpr int PER = 32 / (D / 8);
       const int limit = x.q.n * a.group, ch = lane % (D / 8);
-      const uint32_t dst = sq + t * C::kTile + (ch >> 3) * C::kHalf;
+      const uint32_t dst = sq + t * C::kQ + (ch >> 3) * (128 * 128);
 #pragma unroll
       for (int k = 0; k < 32; k += PER) {
-        const int r = (wid & 3) * 32 + k + lane / (D / 8), f = x.i * BM + t * 128 + r, token = a.token(f);
+        const int r = (wid & 3) * 32 + k + lane / (D / 8), f = x.i * BM + f_off + r, token = a.token(f);
         const bool live = f < limit;
         const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q);
         if (live) src += (size_t)(x.q.start + token) * a.q_stride + (size_t)(x.h * a.group + f - token * a.group) * D;
         cp_async16(dst + r * 128 + (((ch & 7) ^ (r & 7)) << 4), src + ch * 8, live ? 16 : 0);
       }
     };
-    auto has_tile = [&](const AttnCursor& x) { return x.q.n * a.group - x.i * BM > t * 128; };
+    auto q_loaded = [&]() {
+      cp_async_wait();
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) bar_arrive_at(lead_q);
+    };
+    auto has_tile = [&](const AttnCursor& x) { return x.q.n * a.group - x.i * BM > t * 256; };
     bool mine = has_tile(c);
     if (mine) {
       load_q(c);
-      cp_async_wait();
-      fence_async_smem();
-      bar_arrive(q_full + t);
+      q_loaded();
     }
     bool more;
     do {
       TileCursor nx = c;
       more = tile_next(a, work, nx);
       const bool next_mine = more && has_tile(nx);
-      if (!mine) {                                       // an item of 128 rows or fewer has no tile B
+      if (!mine) {                                       // an item of 256 rows or fewer has no tile B
         if (next_mine) {
           load_q(nx);
-          cp_async_wait();
-          fence_async_smem();
-          bar_arrive(q_full + t);
+          q_loaded();
         }
         c = nx;
         mine = next_mine;
         continue;
       }
-      const int rows = min(BM, c.q.n * a.group - c.i * BM) - t * 128;     // of this tile (may exceed 128)
-      const int f = c.i * BM + t * 128 + row, base_pos = c.q.seq - c.q.n;
+      const int f0 = c.i * BM + f_off, f = f0 + row;
+      const int rows = c.q.n * a.group - f0;             // of this CTA's part of the tile: may exceed 128, or be none
+      const int base_pos = c.q.seq - c.q.n;
       const int pos = row < rows ? base_pos + a.token(f) : -1;
       const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
-      // keys that every row of this tile sees need no mask
-      const int f0 = c.i * BM + t * 128, f1 = f0 + min(rows, 128) - 1;
+      // keys that every row of this part of the tile sees need no mask
       const int all_hi = base_pos + a.token(f0) + 1;
-      const int all_lo = a.window > 0 ? max(0, base_pos + a.token(f1) - a.window + 1) : 0;
+      const int all_lo = a.window > 0 ? max(0, base_pos + a.token(f0 + max(0, min(rows, 128) - 1)) - a.window + 1) : 0;
       float m = -INFINITY, l = 0.f;
       const int units = attn_piece(c);
       for (int j = 0; j < units; ++j) {
@@ -429,18 +453,15 @@ __global__ __launch_bounds__(NT, 1) void attn_tiles_kernel(const __grid_constant
         l += x + y;
         tc_wait_st();
         tc_fence_before();
-        bar_arrive(p_full + t);
+        __syncwarp();
+        if (lane == 0) bar_arrive_at(lead_p);
       }
-      if (next_mine) {
-        cp_async_wait();
-        fence_async_smem();
-        bar_arrive(q_full + t);
-      }
+      if (next_mine) q_loaded();
       wait(o_full + t, no++ & 1);
       __syncwarp();
       tc_fence_after();
       const bool whole = units == c.nu;
-      const size_t part = ((size_t)attn_slot(c) * BM + t * 128 + row);
+      const size_t at = (size_t)attn_slot(c, part) * BM + f_off + row;
       const float inv = l > 0.f ? 1.f / l : 0.f;
       __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out);
       if (row < rows) dst += ((size_t)(c.q.start + a.token(f)) * a.Hq + c.h * a.group + a.head_of(f)) * D;
@@ -463,26 +484,26 @@ __global__ __launch_bounds__(NT, 1) void attn_tiles_kernel(const __grid_constant
         } else {
 #pragma unroll
           for (int i = 0; i < 32; i += 4)
-            attn_store4(a.part_o + part * D + d + i, make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]));
+            attn_store4(a.part_o + at * D + d + i, make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]));
         }
       }
-      if (!whole) {
-        if (row < rows) a.part_ml[part] = make_float2(m, l);
+      if (!whole && rows > 0) {
+        if (row < rows) a.part_ml[at] = make_float2(m, l);
         const int c0 = work.sp.owner(c.item_first), n = work.sp.owner(c.item_first + c.nu - 1) - c0 + 1;
+        uint32_t* counter = a.arrived + 4 * c0 + 2 * t + rank;
         __threadfence();
         named_sync(1 + t, 128);
         if (tid == t * 128) {
-          const bool last = atomicAdd(a.arrived + 2 * c0 + t, 1u) == (uint32_t)(n - 1);
-          if (last) a.arrived[2 * c0 + t] = 0;
+          const bool last = atomicAdd(counter, 1u) == (uint32_t)(n - 1);
+          if (last) *counter = 0;
           last_flag[t] = last;
         }
         named_sync(1 + t, 128);
-        if (last_flag[t]) {                              // the item's last piece to arrive joins tile t, in piece order
-          __threadfence();
-          // a warp joins its 32 rows, 16 loads of a piece in flight per lane
+        if (last_flag[t]) {                              // the last of the item's pieces to arrive joins these rows, in
+          __threadfence();                               // piece order: a warp its 32 rows, 16 loads in flight per lane
           constexpr int LANES = D / 4, PER = 32 / LANES, B = 16;
           const int r0 = (wid & 3) * 32;
-          const float2* ml = a.part_ml + t * 128 + row;
+          const float2* ml = a.part_ml + f_off + row;
           auto slot = [&](int p) { return (size_t)(2 * (c0 + p) + (p == 0)) * BM; };
           float M = -INFINITY, sum = 0.f;
           for (int p = 0; p < n; ++p) M = fmaxf(M, __ldcg(ml + slot(p)).x);
@@ -504,7 +525,7 @@ __global__ __launch_bounds__(NT, 1) void attn_tiles_kernel(const __grid_constant
 #pragma unroll
               for (int k = 0; k < B; ++k)
                 v[k] = __ldcg(reinterpret_cast<const float4*>(
-                    a.part_o + (slot(p) + t * 128 + r0 + b + k * PER + lane / LANES) * D + lane % LANES * 4));
+                    a.part_o + (slot(p) + f_off + r0 + b + k * PER + lane / LANES) * D + lane % LANES * 4));
 #pragma unroll
               for (int k = 0; k < B; ++k) {
                 const float w = __shfl_sync(0xffffffffu, g, b + k * PER + lane / LANES);
@@ -513,7 +534,7 @@ __global__ __launch_bounds__(NT, 1) void attn_tiles_kernel(const __grid_constant
             }
 #pragma unroll
             for (int k = 0; k < B; ++k) {
-              const int r = r0 + b + k * PER + lane / LANES, fr = c.i * BM + t * 128 + r;
+              const int r = r0 + b + k * PER + lane / LANES, fr = f0 + r;
               if (r < rows)
                 attn_store4(static_cast<__nv_bfloat16*>(a.out) +
                                 ((size_t)(c.q.start + a.token(fr)) * a.Hq + c.h * a.group + a.head_of(fr)) * D +
@@ -528,6 +549,7 @@ __global__ __launch_bounds__(NT, 1) void attn_tiles_kernel(const __grid_constant
   }
   tc_fence_before();
   __syncthreads();
+  pair_sync();                                           // neither CTA's memory or barriers are used any more
   tc_fence_after();
   if (wid == 9) tmem_free(tmem, 512);
 }

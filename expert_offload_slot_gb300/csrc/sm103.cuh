@@ -98,14 +98,43 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// ------------------------------------------------------- pairs of CTAs (cluster of two)
+__device__ __forceinline__ uint32_t pair_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void pair_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Cluster address of the same shared-memory variable in the pair's first CTA.
+__device__ __forceinline__ uint32_t lead_addr(const void* p) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_addr(p)));
+  return r;
+}
+__device__ __forceinline__ void bar_arrive_at(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+// A tile into this CTA's memory, counted on a barrier of either CTA of the pair.
+__device__ __forceinline__ void tma_3d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, "
+      "%5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
 // ------------------------------------------------------------------- tcgen05
+// All of it in its two-CTA form: a product has M = 256, rows 0..127 from and to the first CTA of
+// the pair and 128..255 the second; each holds half of B's N, and one thread of the first issues.
 __device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t cols) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(dst)), "r"(cols)
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(dst)), "r"(cols)
                : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -119,19 +148,20 @@ __device__ __forceinline__ uint32_t elect_lead() {
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
   return r;
 }
-// Arrive on `bar` once every MMA this thread has issued so far has completed.
+// Arrive on `bar` in both CTAs once every MMA this thread has issued so far has completed.
 __device__ __forceinline__ void tc_commit(uint32_t lead, uint64_t* bar) {
   asm volatile(
       "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
-      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_addr(bar)),
-      "r"(lead)
+      " @q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;\n}\n" ::"r"(
+          smem_addr(bar)),
+      "r"(lead), "h"((uint16_t)3)
       : "memory");
 }
 // D[tmem] (+)= A B, bf16 in, fp32 out; A and B by shared-memory descriptors.
 __device__ __forceinline__ void tc_mma_ss(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n .reg .pred p, q;\n setp.ne.b32 q, %5, 0;\n setp.ne.b32 p, %4, 0;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      " @q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
       : "memory");
 }
@@ -139,20 +169,22 @@ __device__ __forceinline__ void tc_mma_ss(uint32_t lead, uint32_t d, uint64_t a,
 __device__ __forceinline__ void tc_mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n .reg .pred p, q;\n setp.ne.b32 q, %5, 0;\n setp.ne.b32 p, %4, 0;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      " @q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
       : "memory");
 }
-// Shared-memory operand of 128-byte rows, 128-byte swizzled, 8-row groups 1024 bytes apart.
-// K-major: a row is 64 elements of K.  MN-major: a row is 64 elements of M or N of one K index,
-// and `block` is the distance in bytes to the next 64 elements.
-__device__ __forceinline__ uint64_t tc_desc(uint32_t saddr, uint32_t block) {
-  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(block >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+// Shared-memory operand of rows of ROW bytes (128 or 64), swizzled over as many, 8-row groups apart
+// by 8 ROW bytes.  K-major: a row is ROW bytes of K of one row of A or B.  MN-major: a row is the N
+// (at most ROW bytes of it) of one K index.
+template <int ROW>
+__device__ __forceinline__ uint64_t tc_desc(uint32_t saddr) {
+  static_assert(ROW == 128 || ROW == 64, "128- or 64-byte swizzle");
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)1 << 16) | ((uint64_t)(8 * ROW >> 4) << 32) | ((uint64_t)1 << 46) |
+         ((uint64_t)(ROW == 128 ? 2 : 4) << 61);
 }
-// kind::f16, A = B = bf16, D = fp32, M = 128; bit 16: B is MN-major.
+// kind::f16, A = B = bf16, D = fp32, M = 256; bit 16: B is MN-major.
 __device__ __forceinline__ constexpr uint32_t tc_idesc(int n, bool b_mn_major) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | (16u << 24);
 }
 // 32 consecutive fp32 columns of this thread's lane; the load is complete on return.
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, float* v) {
