@@ -49,8 +49,8 @@ struct TileCfg {
 };
 
 // A call's work is divided in one of two ways, chosen from the lengths by every CTA alike.
-// Whole: the items, longest first within a request, are dealt out to the pairs to and fro, so that
-// long and short ones meet in each; nothing is split.  Ranges: the keys of all items are cut into
+// Whole: the items, longest first, are dealt out to the pairs to and fro, so that long and
+// short ones meet in each; nothing is split.  Ranges: the keys of all items are cut into
 // equal ranges (attn_find_range), which balances any lengths but has split items join their
 // pieces through memory; that takes about as long as kJoin units.  So items stay whole unless
 // the longest takes kJoin units more than an even share.
@@ -88,24 +88,31 @@ __device__ __forceinline__ bool tile_next(const AttnArgs& a, const TileWork& w, 
   return true;
 }
 
-// All threads; sm: 64 ints.
-__device__ __forceinline__ bool tile_work(const AttnArgs& a, int32_t* sm, TileWork& w, TileCursor& c) {
+// All threads; sm: 64 ints, scratch: 24 KB of shared memory that nothing else uses yet.
+__device__ __forceinline__ bool tile_work(const AttnArgs& a, int32_t* sm, uint8_t* scratch, TileWork& w, TileCursor& c) {
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, G = (int)gridDim.x / 2, pair = (int)blockIdx.x / 2;
+  int32_t* s_nu = reinterpret_cast<int32_t*>(scratch);                   // [NT] units of each row tile
+  int32_t* s_tile = s_nu + NT;                                           // [R + 1] first row tile of each request
+  int4* s_req = reinterpret_cast<int4*>(scratch + 6144);                 // [R] (first row, new, seq)
+  static_assert((NT + MOE_ATTN_MAX_REQUESTS + 1) * 4 <= 6144 && 6144 + MOE_ATTN_MAX_REQUESTS * 16 <= 24 * 1024, "scratch");
   const int per = (a.R + NT - 1) / NT;
   const int r0 = min(tid * per, a.R), r1 = min(r0 + per, a.R);
   AttnRequest q = {0, 0, 0};
-  int units = 0, items = 0, longest = 0;
+  int units = 0, tiles = 0, longest = 0;
   for (int k = 0; k < per; ++k) {
-    if (r0 + k < r1) q = attn_request(a, r0 + k);
-    else q.n = 0;
+    q.n = 0;
+    if (r0 + k < r1) {
+      q = attn_request(a, r0 + k);
+      s_req[r0 + k] = make_int4(q.start, q.n, q.seq, 0);
+    }
     const int nt = attn_tiles<BM>(a, q);
     int sum, top;
     attn_count_units<BM>(a, q, nt, UNIT, sum, top);
-    units += sum * a.Hkv;
-    items += nt * a.Hkv;
+    units += sum;
+    tiles += nt;
     longest = max(longest, top);
   }
-  int inc = items;
+  int inc = tiles;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int v = __shfl_up_sync(0xffffffffu, inc, o);
@@ -119,35 +126,61 @@ __device__ __forceinline__ bool tile_work(const AttnArgs& a, int32_t* sm, TileWo
     sm[32 + wid] = longest;
   }
   __syncthreads();
-  int base = 0, all = 0, W = 0, top = 0;
+  int base = 0, T = 0, W = 0, top = 0;                       // row tiles, units and the most of one tile
 #pragma unroll
   for (int k = 0; k < NT / 32; ++k) {
     base += k < wid ? sm[k] : 0;
-    all += sm[k];
-    W += sm[16 + k];
+    T += sm[k];
+    W += sm[16 + k] * a.Hkv;
     top = max(top, sm[32 + k]);
   }
   if (W == 0) return false;
+  const int all = T * a.Hkv;
   w.whole = top <= (W + G - 1) / G + kJoin && all <= G * kListMax;
   w.count = 0;
   if (!w.whole) {
     __syncthreads();
     return attn_find_range<BM, NT>(a, UNIT, pair, G, sm, w.sp, c);
   }
-  int lo = base + inc - items;
+  int at = base + inc - tiles;
   for (int r = r0; r < r1; ++r) {
-    if (per > 1) q = attn_request(a, r);
-    const int nt = attn_tiles<BM>(a, q), hi = lo + nt * a.Hkv;
-    for (int j = lo / G; j * G < hi; ++j) {
-      const int k = (j & 1) ? (j + 1) * G - 1 - pair : j * G + pair;
-      if (k < lo || k >= hi) continue;
-      const int i = nt - 1 - (k - lo) / a.Hkv;
-      int u0, nu;
-      attn_units<BM>(a, q, i, UNIT, u0, nu);
-      w.list[2 * j] = make_int4(r, (k - lo) % a.Hkv, i, nu);
-      w.list[2 * j + 1] = make_int4(q.start, q.n, q.seq, u0);
+    s_tile[r] = at;
+    at += (s_req[r].y * a.group + BM - 1) / BM;
+  }
+  if (tid == 0) s_tile[a.R] = T;
+  __syncthreads();
+  const bool sort = a.R > 1 && T <= NT;
+  for (int x0 = 0; x0 < T; x0 += NT) {                       // one row tile a thread
+    const int x = min(x0 + tid, T - 1);
+    int lo = 0, hi = a.R - 1;
+    while (lo < hi) {                                        // last request that starts at or before tile x
+      const int mid = (lo + hi + 1) >> 1;
+      if (s_tile[mid] <= x) lo = mid;
+      else hi = mid - 1;
     }
-    lo = hi;
+    const int4 e = s_req[lo];
+    const AttnRequest y = {e.x, e.y, e.z};
+    const int i = x - s_tile[lo];
+    int u0, nu, place = T - 1 - x;                           // the tiles of one request grow with i
+    attn_units<BM>(a, y, i, UNIT, u0, nu);
+    // Of several requests: the place by length.  More tiles than threads go as they come: then a pair
+    // has so many items that they even out.
+    if (sort) {
+      s_nu[x] = nu;
+      __syncthreads();
+      place = 0;
+      for (int z = 0; z < T; ++z) {
+        const int v = s_nu[z];
+        place += v > nu || (v == nu && z < x) ? 1 : 0;
+      }
+    }
+    if (x0 + tid >= T) continue;
+    for (int h = 0; h < a.Hkv; ++h) {
+      const int k = place * a.Hkv + h, j = k / G, pos = k - j * G;
+      if (pos != ((j & 1) ? G - 1 - pair : pair)) continue;
+      w.list[2 * j] = make_int4(lo, h, i, nu);
+      w.list[2 * j + 1] = make_int4(y.start, y.n, y.seq, u0);
+    }
   }
   const int last = (all - 1) / G;              // round of the last item; only that round may lack one
   const int k = (last & 1) ? (last + 1) * G - 1 - pair : last * G + pair;
@@ -167,7 +200,7 @@ void attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_cons
   __shared__ int32_t sched[64];
   // full, q_full and p_full are the first CTA's, who issues the products, for both; the others are of each its own
   __shared__ __align__(8) uint64_t full[C::kStages], empty[C::kStages], edge[C::kStages], drain, q_full[2], s_full[2],
-      p_full[2], o_full[2];
+      p_full[2][2], o_full[2];
   __shared__ uint32_t tmem_slot;
   __shared__ int32_t last_flag[2];
   __shared__ int4 items[2 * kListMax];
@@ -178,7 +211,7 @@ void attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_cons
   TileWork work;
   TileCursor c;
   work.list = items;
-  if (!tile_work(a, sched, work, c)) return;             // the same answer in every thread of the pair
+  if (!tile_work(a, sched, smem, work, c)) return;             // the same answer in every thread of the pair
   if (tid == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       bar_init(full + s, 2);
@@ -189,13 +222,15 @@ void attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_cons
     for (int t = 0; t < 2; ++t) {
       bar_init(q_full + t, 8);
       bar_init(s_full + t, 1);
-      bar_init(p_full + t, 8);
+      bar_init(&p_full[t][0], 8);
+      bar_init(&p_full[t][1], 8);
       bar_init(o_full + t, 1);
     }
     bar_init_done();
   }
   if (wid == 9) tmem_alloc(&tmem_slot, 512);
   tc_fence_before();
+  fence_async_smem();                                    // the scratch of tile_work becomes the loads' memory
   __syncthreads();
   pair_sync();                                           // the other CTA's barriers are ready, too
   tc_fence_after();
@@ -312,12 +347,16 @@ void attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_cons
           wait(full + vs, (n / C::kStages) & 1);
           const uint64_t vd = v_desc + vs * (C::kTile >> 4);
           for (int t = 0; t < tiles; ++t) {
-            wait(p_full + t, np[t]++ & 1);
-            __syncwarp();
-            tc_fence_after();
 #pragma unroll
-            for (int k = 0; k < UNIT / 16; ++k)
-              tc_mma_ts(lead, tmem + 256 + t * 128, tmem + t * UNIT + k * 8, vd + k * (16 * D >> 4), kO, k > 0 || j > 0);
+            for (int h = 0; h < 2; ++h) {                // P comes in halves of 64 keys
+              wait(&p_full[t][h], np[t] & 1);
+              __syncwarp();
+              tc_fence_after();
+#pragma unroll
+              for (int k = 4 * h; k < 4 * h + 4; ++k)
+                tc_mma_ts(lead, tmem + 256 + t * 128, tmem + t * UNIT + k * 8, vd + k * (16 * D >> 4), kO, k > 0 || j > 0);
+            }
+            ++np[t];
             if (more) {
               if (t == 0) wait(full + ks, ((n + 1) / C::kStages) & 1);
               __syncwarp();
@@ -343,7 +382,7 @@ void attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_cons
     const int f_off = t * 256 + rank * 128;                           // this CTA's first row of the tile
     const uint32_t lanes = tmem + ((uint32_t)(wid & 3) << 21);        // this warp's 32 lanes of tensor memory
     const uint32_t s_addr = lanes + t * UNIT, o_addr = lanes + 256 + t * 128;
-    const uint32_t lead_p = lead_addr(p_full + t), lead_q = lead_addr(q_full + t);
+    const uint32_t lead_p[2] = {lead_addr(&p_full[t][0]), lead_addr(&p_full[t][1])}, lead_q = lead_addr(q_full + t);
     uint32_t ns = 0, no = 0;
     // This warp's 32 rows of tile t, 128-byte swizzled: D / 8 lanes read a row together.
     auto load_q = [&](const AttnCursor& x) {
@@ -447,14 +486,14 @@ void attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_cons
             w[i] = pack_bf16(x, y);
           }
           tmem_st32(s_addr + 32 * h, w);
+          tc_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive_at(lead_p[h]);       // its product may start
         }
         float x, y;
         unpack2(add2(sum2[0], sum2[1]), x, y);
         l += x + y;
-        tc_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) bar_arrive_at(lead_p);
       }
       if (next_mine) q_loaded();
       wait(o_full + t, no++ & 1);
@@ -473,13 +512,16 @@ void attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_cons
         if (row >= rows) continue;
         if (whole) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            uint4 w;
-            w.x = pack_bf16(o[i] * inv, o[i + 1] * inv);
-            w.y = pack_bf16(o[i + 2] * inv, o[i + 3] * inv);
-            w.z = pack_bf16(o[i + 4] * inv, o[i + 5] * inv);
-            w.w = pack_bf16(o[i + 6] * inv, o[i + 7] * inv);
-            *reinterpret_cast<uint4*>(dst + d + i) = w;
+          for (int i = 0; i < 32; i += 16) {
+            uint32_t w[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) w[k] = pack_bf16(o[i + 2 * k] * inv, o[i + 2 * k + 1] * inv);
+            if (a.out_32) {                              // a row per thread: whole 32-byte sectors, where aligned
+              store_32(dst + d + i, w);
+            } else {
+              *reinterpret_cast<uint4*>(dst + d + i) = make_uint4(w[0], w[1], w[2], w[3]);
+              *reinterpret_cast<uint4*>(dst + d + i + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+            }
           }
         } else {
 #pragma unroll
