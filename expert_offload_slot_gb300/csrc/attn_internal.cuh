@@ -278,36 +278,57 @@ __device__ __forceinline__ void attn_store4(__nv_bfloat16* p, float4 v) {
 }
 
 // Joins the n pieces of a split item, in piece order (so the sum does not depend on which CTA
-// arrives last), and writes the item's output rows.  LOG2: the maxima are in log2 units.
+// arrives last), and writes the item's output rows: a warp per row, whose lanes take the pieces'
+// maxima and sums at once and then D / 32 columns each.  LOG2: the maxima are in log2 units.
 template <typename T, int D, int BM, int NT, bool LOG2>
 __device__ __forceinline__ void attn_join(const AttnArgs& a, const AttnCursor& c, int c0, int n) {
-  constexpr int LANES = D / 4;
-  const int rows = min(BM, c.q.n * a.group - c.i * BM);
-  for (int row = threadIdx.x / LANES; row < rows; row += NT / LANES) {
-    const int d = (threadIdx.x % LANES) * 4;
-    float M = -INFINITY;
-    for (int p = 0; p < n; ++p) {
-      const int slot = 2 * (c0 + p) + (p == 0 ? 1 : 0);
-      M = fmaxf(M, __ldcg(a.part_ml + (size_t)slot * BM + row).x);
-    }
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-    if (M > -INFINITY) {
-#pragma unroll 4
-      for (int p = 0; p < n; ++p) {
-        const int slot = 2 * (c0 + p) + (p == 0 ? 1 : 0);
-        const float2 ml = __ldcg(a.part_ml + (size_t)slot * BM + row);
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + ((size_t)slot * BM + row) * D + d));
-        const float f = LOG2 ? exp2f(ml.x - M) : expf(ml.x - M);
-        l += f * ml.y;
-        o.x += f * v.x; o.y += f * v.y; o.z += f * v.z; o.w += f * v.w;
+  constexpr int COLS = D / 32, U = 8;
+  const int lane = threadIdx.x & 31, rows = min(BM, c.q.n * a.group - c.i * BM);
+  auto slot = [&](int p) { return (size_t)(2 * (c0 + p) + (p == 0 ? 1 : 0)) * BM; };
+  for (int row = threadIdx.x / 32; row < rows; row += NT / 32) {
+    float M = -INFINITY, l = 0.f, o[COLS];
+    for (int p = lane; p < n; p += 32) M = fmaxf(M, __ldcg(a.part_ml + slot(p) + row).x);
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
+    const float top = M == -INFINITY ? 0.f : M;
+#pragma unroll
+    for (int k = 0; k < COLS; ++k) o[k] = 0.f;
+    for (int p0 = 0; p0 < n; p0 += 32) {
+      float g = 0.f, gl = 0.f;
+      if (p0 + lane < n) {
+        const float2 ml = __ldcg(a.part_ml + slot(p0 + lane) + row);
+        g = LOG2 ? exp2f(ml.x - top) : expf(ml.x - top);
+        gl = g * ml.y;
       }
-      const float inv = 1.f / l;
-      o.x *= inv; o.y *= inv; o.z *= inv; o.w *= inv;
+      const int m = min(32, n - p0);
+      for (int p = 0; p < m; p += U) {
+        float v[U][COLS];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const float* src = a.part_o + (slot(p0 + min(p + u, m - 1)) + row) * D + lane * COLS;
+          if constexpr (COLS == 4) *reinterpret_cast<float4*>(v[u]) = __ldcg(reinterpret_cast<const float4*>(src));
+          else *reinterpret_cast<float2*>(v[u]) = __ldcg(reinterpret_cast<const float2*>(src));
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const float w = __shfl_sync(0xffffffffu, g, (p + u) & 31), x = __shfl_sync(0xffffffffu, gl, (p + u) & 31);
+          if (p + u < m) {
+            l += x;
+#pragma unroll
+            for (int k = 0; k < COLS; ++k) o[k] += w * v[u][k];
+          }
+        }
+      }
     }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
     const int fr = c.i * BM + row;
-    const size_t at = ((size_t)(c.q.start + a.token(fr)) * a.Hq + c.h * a.group + a.head_of(fr)) * D + d;
-    attn_store4(static_cast<T*>(a.out) + at, o);
+    T* dst = static_cast<T*>(a.out) + ((size_t)(c.q.start + a.token(fr)) * a.Hq + c.h * a.group + a.head_of(fr)) * D + lane * COLS;
+    if constexpr (COLS == 4) {
+      attn_store4(dst, make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv));
+    } else {
+#pragma unroll
+      for (int k = 0; k < COLS; ++k) dst[k] = (T)(o[k] * inv);
+    }
   }
 }
 

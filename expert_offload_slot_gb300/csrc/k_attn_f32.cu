@@ -10,6 +10,7 @@
 // A CTA holds 32 query rows (all heads of a kv head's group together, so a key
 // read once serves the whole group) and walks its units of 32 keys.
 #include "attn_internal.cuh"
+#include "sm103.cuh"
 
 namespace moeslot {
 namespace {
@@ -25,6 +26,7 @@ __global__ __launch_bounds__(NT) void attn_f32_kernel(const AttnArgs a) {
   float* sv = sk + BN * LD;                 // [BN][LD]
   float* spr = sv + BN * LD;                // [BM][BN + 1]
   __shared__ int32_t sched[128];
+  sm103::grid_wait();
   AttnSplit sp;
   AttnCursor c;
   if (!attn_find_range<BM, NT>(a, BN, blockIdx.x, gridDim.x, sched, sp, c)) return;
@@ -148,8 +150,7 @@ constexpr int f32_bytes() {
 
 template <int D>
 cudaError_t launch(const AttnArgs& a, int grid, cudaStream_t s) {
-  attn_f32_kernel<D><<<grid, NT, f32_bytes<D>(), s>>>(a);
-  return cudaGetLastError();
+  return sm103::launch(attn_f32_kernel<D>, grid, NT, f32_bytes<D>(), s, a);
 }
 
 template <int D>

@@ -54,6 +54,7 @@ __global__ __launch_bounds__(NT, 1) void attn_rows_kernel(const __grid_constant_
     for (int s = 0; s < C::kStages; ++s) bar_init(bars + wid * C::kStages + s, 1);
     bar_init_done();
   }
+  grid_wait();
   AttnSplit sp;
   AttnCursor c;
   if (!attn_find_range<BM, NT>(a, UNIT, blockIdx.x, gridDim.x, sched, sp, c)) return;
@@ -236,13 +237,15 @@ __global__ __launch_bounds__(NT, 1) void attn_rows_kernel(const __grid_constant_
       l[hh] += __shfl_xor_sync(0xffffffffu, l[hh], 1);
       l[hh] += __shfl_xor_sync(0xffffffffu, l[hh], 2);
     }
-    // join the warps in a fixed tree: 4..7 into 0..3, 2..3 into 0..1, 1 into 0
+    // join the warps in a fixed tree: 4..7 into 0..3, 2..3 into 0..1, 1 into 0; rows 8..15 only if there are any
+    const int used = rows > 8 ? 2 : 1;
 #pragma unroll
     for (int half = NW / 2; half > 0; half >>= 1) {
       if (wid >= half && wid < 2 * half) {
         float* dst = join + (wid - half) * BM * D;
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
+          if (hh >= used) break;
           const int row = g + 8 * hh;
           if (t4 == 0) {
             sm_m[wid - half][row] = m[hh];
@@ -258,6 +261,7 @@ __global__ __launch_bounds__(NT, 1) void attn_rows_kernel(const __grid_constant_
         const float* src = join + wid * BM * D;
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
+          if (hh >= used) break;
           const int row = g + 8 * hh;
           const float m2 = sm_m[wid][row], l2 = sm_l[wid][row];
           const float top = fmaxf(m[hh], m2), base = top == -INFINITY ? 0.f : top;
@@ -272,7 +276,7 @@ __global__ __launch_bounds__(NT, 1) void attn_rows_kernel(const __grid_constant_
           }
         }
       }
-      __syncthreads();
+      if (half > 1) __syncthreads();
     }
     const bool whole = attn_piece(c) == c.nu;
     if (wid == 0) {
@@ -296,6 +300,7 @@ __global__ __launch_bounds__(NT, 1) void attn_rows_kernel(const __grid_constant_
         }
       }
     }
+    __syncthreads();                         // the join's memory is read: the next piece may write it
     if (!whole) {
       int c0, n;
       if (attn_arrive(a, sp, c, sched, c0, n)) attn_join<__nv_bfloat16, D, BM, NT, true>(a, c, c0, n);
@@ -308,8 +313,7 @@ __global__ __launch_bounds__(NT, 1) void attn_rows_kernel(const __grid_constant_
 
 template <int D>
 cudaError_t launch(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, int grid, cudaStream_t s) {
-  attn_rows_kernel<D><<<grid, NT, RowsCfg<D>::kBytes, s>>>(mk, mv, a);
-  return cudaGetLastError();
+  return sm103::launch(attn_rows_kernel<D>, grid, NT, RowsCfg<D>::kBytes, s, mk, mv, a);
 }
 
 template <int D>

@@ -13,6 +13,7 @@
 // `rotary` elements, and K and V into their cache slots, in one pass: each head
 // is read once and written once.
 #include "attn_internal.cuh"
+#include "sm103.cuh"
 
 namespace moeslot {
 namespace {
@@ -46,6 +47,7 @@ __global__ __launch_bounds__(TT) void attn_tables_kernel(const TablesArgs a) {
   __shared__ int32_t s_warp[2][TT / 32];
   __shared__ int32_t s_carry[2];
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  sm103::grid_wait();
   const int head = *a.head_in;
   bool bad = false, full = false;
   if (tid < 2) s_carry[tid] = 0;
@@ -168,87 +170,92 @@ struct Vec<__nv_bfloat16> {
   }
 };
 
-// One group of D * sizeof(T) / 16 lanes per head.
+// A CTA per row: a group of D * sizeof(T) / 16 lanes takes a head at a time, its cosines, sines and
+// norm weights in registers for all of the row's heads, U heads in flight.
 template <typename T, int D>
-__global__ __launch_bounds__(QT) void attn_qkv_kernel(const QkvArgs a) {
-  constexpr int N = Vec<T>::N, G = D / N;
-  const int heads = a.Hq + 2 * a.Hkv;
-  const int64_t unit = (int64_t)blockIdx.x * (QT / G) + threadIdx.x / G;
-  const int sub = threadIdx.x % G;
-  const bool live = unit < (int64_t)a.rows * heads;
-  const int t = live ? (int)(unit / heads) : 0, head = live ? (int)(unit % heads) : 0;
-  const int e0 = sub * N;
-  float x[N];
-  Vec<T>::load(static_cast<const T*>(a.qkv) + (size_t)t * a.qkv_stride + (size_t)head * D + e0, x);
-  const bool is_q = head < a.Hq, is_v = head >= a.Hq + a.Hkv;
-  const void* w = is_q ? a.q_norm : a.k_norm;
-  float ss = 0.f;
+__global__ __launch_bounds__(QT, 4) void attn_qkv_kernel(const QkvArgs a) {
+  constexpr int N = Vec<T>::N, G = D / N, GROUPS = QT / G, U = 2;
+  const int heads = a.Hq + 2 * a.Hkv, t = blockIdx.x, group = threadIdx.x / G, sub = threadIdx.x % G, e0 = sub * N;
+  const int lane = threadIdx.x & 31, half = a.rotary / 2;
+  sm103::grid_wait();
+  const int64_t slot = a.slots[t];
+  const int64_t pos = a.rotary > 0 ? a.positions[t] : 0;
+  const T* src = static_cast<const T*>(a.qkv) + (size_t)t * a.qkv_stride + e0;
+  float x[U][N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) ss += x[i] * x[i];
+  for (int u = 0; u < U; ++u)
+    if (group + u * GROUPS < heads) Vec<T>::load(src + (size_t)(group + u * GROUPS) * D, x[u]);
+  const bool in_table = pos >= 0 && pos < a.rope_len, turn = e0 < a.rotary && in_table;
+  const bool first = e0 < half;
+  float cs[N], sn[N];                         // of this lane's elements (MOE_ROTARY_PAIRS: the first N / 2)
+  if (turn) {
+    const float* row = a.rope + pos * a.rotary;
+    const int i0 = a.pairs ? e0 / 2 : first ? e0 : e0 - half;
 #pragma unroll
-  for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  if (!is_v && w) {
-    float g[N];
-    Vec<T>::load(static_cast<const T*>(w) + e0, g);
-    const float inv = 1.f / sqrtf(ss * (1.f / D) + a.eps);
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = x[i] * inv * g[i];
+    for (int i = 0; i < N; ++i) {
+      if (a.pairs && i >= N / 2) break;
+      cs[i] = row[i0 + i];
+      sn[i] = row[half + i0 + i];
+    }
   }
-  if (a.rotary > 0) {                         // uniform: every lane takes part in the exchange
-    const int half = a.rotary / 2;
-    const int64_t pos = a.positions[t];
-    const bool ok = pos >= 0 && pos < a.rope_len;
-    if (!ok && live) atomicCAS(a.status, 0, MOE_ERR_BOUNDS);
-    const float* row = a.rope + (ok ? pos : 0) * a.rotary;
-    const bool turn = e0 < a.rotary && !is_v && ok;
-    if (a.pairs) {
-      if (turn) {
+  if (a.rotary > 0 && !in_table && threadIdx.x == 0) atomicCAS(a.status, 0, MOE_ERR_BOUNDS);
+  if (slot >= a.num_slots && threadIdx.x == 0) atomicCAS(a.status, 0, MOE_ERR_BOUNDS);
+  const bool cached = slot >= 0 && slot < a.num_slots;
+  const int64_t page = slot >> a.page_log2, in = slot & ((1 << a.page_log2) - 1);
+  const int peer = e0 < a.rotary ? (first ? lane + half / N : lane - half / N) : lane;
+  for (int h0 = group; h0 - group < heads; h0 += U * GROUPS) {       // the same number of rounds in every group
 #pragma unroll
-        for (int i = 0; i < N; i += 2) {
-          const float c = row[(e0 + i) / 2], s = row[half + (e0 + i) / 2];
-          const float p = x[i], q = x[i + 1];
-          x[i] = p * c - q * s;
-          x[i + 1] = q * c + p * s;
-        }
-      }
-    } else {
-      const int lane = threadIdx.x & 31;
-      const bool first = e0 < half;
-      const int peer = e0 < a.rotary ? (first ? lane + half / N : lane - half / N) : lane;
-      const int i0 = first ? e0 : e0 - half;
+    for (int u = 0; u < U; ++u) {
+      const int head = h0 + u * GROUPS;
+      const bool is_q = head < a.Hq, is_v = head >= a.Hq + a.Hkv;
+      float y[N], ss = 0.f;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const float y = __shfl_sync(0xffffffffu, x[i], peer);
-        if (turn) {
-          const float c = row[i0 + i], s = row[half + i0 + i];
-          x[i] = first ? x[i] * c - y * s : x[i] * c + y * s;
+        y[i] = x[u][i];
+        ss += y[i] * y[i];
+      }
+      if (head + U * GROUPS < heads) Vec<T>::load(src + (size_t)(head + U * GROUPS) * D, x[u]);   // of the next round
+#pragma unroll
+      for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      const void* w = is_q ? a.q_norm : a.k_norm;
+      if (!is_v && w) {
+        float g[N];
+        Vec<T>::load(static_cast<const T*>(w) + e0, g);
+        const float inv = 1.f / sqrtf(ss * (1.f / D) + a.eps);
+#pragma unroll
+        for (int i = 0; i < N; ++i) y[i] = y[i] * inv * g[i];
+      }
+      if (a.pairs) {
+        if (turn && !is_v) {
+#pragma unroll
+          for (int i = 0; i < N; i += 2) {
+            const float p = y[i], q = y[i + 1];
+            y[i] = p * cs[i / 2] - q * sn[i / 2];
+            y[i + 1] = q * cs[i / 2] + p * sn[i / 2];
+          }
+        }
+      } else if (a.rotary > 0) {              // uniform: every lane takes part in the exchange
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const float z = __shfl_sync(0xffffffffu, y[i], peer);
+          if (turn && !is_v) y[i] = first ? y[i] * cs[i] - z * sn[i] : y[i] * cs[i] + z * sn[i];
         }
       }
+      if (head >= heads) continue;
+      if (is_q) {
+        Vec<T>::store(static_cast<T*>(a.q) + ((size_t)t * a.Hq + head) * D + e0, y);
+      } else if (cached) {
+        const int h = head - a.Hq - (is_v ? a.Hkv : 0);
+        T* dst = static_cast<T*>(is_v ? a.v_cache : a.k_cache);
+        Vec<T>::store(dst + ((((page * a.Hkv + h) << a.page_log2) + in) * D + e0), y);
+      }
     }
-  }
-  if (!live) return;
-  if (is_q) {
-    Vec<T>::store(static_cast<T*>(a.q) + ((size_t)t * a.Hq + head) * D + e0, x);
-  } else {
-    const int64_t slot = a.slots[t];
-    if (slot < 0) return;                     // a padding row
-    if (slot >= a.num_slots) {
-      atomicCAS(a.status, 0, MOE_ERR_BOUNDS);
-      return;
-    }
-    const int h = head - a.Hq - (is_v ? a.Hkv : 0);
-    const int64_t page = slot >> a.page_log2, in = slot & ((1 << a.page_log2) - 1);
-    T* dst = static_cast<T*>(is_v ? a.v_cache : a.k_cache) + ((((page * a.Hkv + h) << a.page_log2) + in) * D + e0);
-    Vec<T>::store(dst, x);
   }
 }
 
 template <typename T, int D>
 cudaError_t qkv(const QkvArgs& a, cudaStream_t s) {
-  constexpr int per = QT / (D / Vec<T>::N);
-  const int64_t units = (int64_t)a.rows * (a.Hq + 2 * a.Hkv);
-  attn_qkv_kernel<T, D><<<(unsigned)((units + per - 1) / per), QT, 0, s>>>(a);
-  return cudaGetLastError();
+  return sm103::launch(attn_qkv_kernel<T, D>, a.rows, QT, 0, s, a);
 }
 
 }  // namespace
@@ -257,8 +264,7 @@ cudaError_t launch_attn_tables(const TablesArgs& a, cudaStream_t s) {
   const int work = a.rows > a.R * 32 ? a.rows : a.R * 32;
   int grid = (work + TT - 1) / TT;
   grid = grid < 1 ? 1 : grid > 152 ? 152 : grid;
-  attn_tables_kernel<<<grid, TT, (2 * a.R + 1) * sizeof(int32_t), s>>>(a);
-  return cudaGetLastError();
+  return sm103::launch(attn_tables_kernel, grid, TT, (2 * a.R + 1) * sizeof(int32_t), s, a);
 }
 
 cudaError_t launch_attn_qkv(const QkvArgs& a, int dtype, int D, cudaStream_t s) {

@@ -208,6 +208,7 @@ void attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_cons
   const uint32_t sq = smem_addr(smem), ring = sq + 2 * C::kQ;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int rank = (int)pair_rank(), part = (int)blockIdx.x / 2;
+  grid_wait();
   TileWork work;
   TileCursor c;
   work.list = items;
@@ -598,8 +599,7 @@ void attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_cons
 
 template <int D>
 cudaError_t launch(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, int grid, cudaStream_t s) {
-  attn_tiles_kernel<D><<<grid, NT, TileCfg<D>::kBytes, s>>>(mk, mv, a);
-  return cudaGetLastError();
+  return sm103::launch(attn_tiles_kernel<D>, grid, NT, TileCfg<D>::kBytes, s, mk, mv, a);
 }
 
 template <int D>

@@ -25,8 +25,11 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "../../include/moeslot.h"
 #include "sample_internal.cuh"
+#include "sm103.cuh"
 
 namespace moeslot {
 int sm_count();
@@ -149,6 +152,7 @@ __global__ __launch_bounds__(NT) void sample_kernel(const SampleArgs a) {
   __shared__ int32_t s_bin, s_in;
   int turn = 0;
 
+  sm103::grid_wait();
   const int chunk = a.chunk;
   const int i0 = min(rank * chunk, a.vocab), n = min(i0 + chunk, a.vocab) - i0;
   float temp = a.temperature ? a.temperature[row] : 1.f;
@@ -665,19 +669,29 @@ cudaError_t launch(SampleArgs a, cudaStream_t s) {
   cs = cs < least ? least : cs > kMaxCluster ? kMaxCluster : cs;
   a.chunk = ((a.vocab + cs - 1) / cs + 7) / 8 * 8;               // every share is aligned as the row is
   const size_t bytes = sizeof(u64) * BINS * NT + (size_t)a.chunk * sizeof(T);
-  cudaError_t e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  static std::atomic<uint64_t> ready{0};                         // devices whose kernel has the attribute
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev > 63 || !(ready.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kShared);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_relaxed);
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.rows * cs);
   cfg.blockDim = dim3(NT);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = s;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = cs;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, sample_kernel<T>, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
