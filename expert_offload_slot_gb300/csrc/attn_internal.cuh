@@ -125,10 +125,14 @@ __device__ __forceinline__ void attn_count_units(const AttnArgs& a, const AttnRe
   }
 }
 
-// The units of all items, item after item, form one sequence of W units that is cut into
-// `parts` equal ranges, one per CTA.  Every CTA finds its own range by scanning the requests
-// (no schedule is built ahead and nothing waits).  An item that crosses a cut is finished by
-// the last of its CTAs to arrive.
+// How a call's units are divided among its parts (a part: a CTA, or a pair of them).  Every CTA
+// finds its share by scanning the requests itself: no schedule is built ahead and nothing waits.
+// Pieces: each item is cut into equal pieces, one part each, of at most L units, L the smallest
+// for which the parts suffice.  Ranges: the units of all items, item after item, are cut into
+// equal ranges; that balances any lengths, but a part whose range crosses an item's end has to
+// finish one piece before it goes on with the next, which costs it `overhead` units.  So pieces
+// are taken where L is at most that much above an even share.  An item of several pieces is
+// finished by the last of its parts to arrive.
 struct AttnCursor {
   int32_t r, i, h;             // item
   int32_t at;                  // unit offset inside the item
@@ -139,26 +143,31 @@ struct AttnCursor {
 };
 
 struct AttnSplit {
-  int32_t W, parts;
+  int32_t W, parts;            // ranges
+  int32_t first, count;        // pieces: first part and number of parts of this part's item (count 0: ranges)
   __device__ __forceinline__ int begin(int c) const { return (int)((int64_t)c * W / parts); }
   __device__ __forceinline__ int owner(int x) const { return (int)((((int64_t)x + 1) * parts - 1) / W); }
+  __device__ __forceinline__ void pieces(const AttnCursor& c, int& c0, int& n) const {
+    c0 = count ? first : owner(c.item_first);
+    n = count ? count : owner(c.item_first + c.nu - 1) - c0 + 1;
+  }
 };
 
 // Called by all threads of the CTA (NT of them) for part c of at most `most`.  `sm` holds 64 ints.
 // False when the part has no work.
 template <int BM, int NT>
-__device__ __forceinline__ bool attn_find_range(const AttnArgs& a, int unit, int c, int most, int32_t* sm, AttnSplit& sp,
-                                                AttnCursor& cur) {
+__device__ __forceinline__ bool attn_find_range(const AttnArgs& a, int unit, int overhead, int c, int most, int32_t* sm,
+                                                AttnSplit& sp, AttnCursor& cur) {
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   constexpr int NW = NT / 32;
   const int per = (a.R + NT - 1) / NT;
   const int r0 = min(tid * per, a.R), r1 = min(r0 + per, a.R);
   AttnRequest q = {0, 0, 0};                   // of the last request looked at: the only one when per is 1
-  int mine = 0;
+  int mine = 0, longest = 0;
   for (int k = 0; k < per; ++k) {
     if (r0 + k < r1) q = attn_request(a, r0 + k);
     else q.n = 0;
-    int sum, longest;
+    int sum;
     attn_count_units<BM>(a, q, attn_tiles<BM>(a, q), unit, sum, longest);
     mine += sum * a.Hkv;
   }
@@ -179,6 +188,63 @@ __device__ __forceinline__ bool attn_find_range(const AttnArgs& a, int unit, int
   }
   sp.W = W;
   sp.parts = max(1, min(most, W));
+  sp.count = 0;
+  if (W > 0 && per == 1) {
+    const int items = attn_tiles<BM>(a, q) * a.Hkv;                    // of this thread's request
+    // pieces of at most L units: the parts that takes, and with `mine` those of the requests before
+    auto parts_for = [&](int L, int& before, int& own) -> int {
+      own = items > 0 ? items * ((longest + L - 1) / L) : 0;
+      int run = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += v;
+      }
+      __syncthreads();
+      if (lane == 31) sm[wid] = run;
+      __syncthreads();
+      int total = 0, ahead = 0;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        ahead += w < wid ? sm[w] : 0;
+        total += sm[w];
+      }
+      before = ahead + run - own;
+      return total;
+    };
+    int lo = (W + most - 1) / most, hi = lo + overhead, before, own;
+    if (parts_for(hi, before, own) <= most) {
+      while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (parts_for(mid, before, own) <= most) hi = mid;
+        else lo = mid + 1;
+      }
+      parts_for(lo, before, own);
+      if (tid == 0) sm[40] = -1;
+      __syncthreads();
+      if (c >= before && c < before + own) {                           // one thread
+        const int per_item = own / items, local = c - before, item = local / per_item, p = local - item * per_item;
+        const int i = item / a.Hkv;
+        int u0, nu;
+        attn_units<BM>(a, q, i, unit, u0, nu);
+        const int n = min(per_item, nu);                               // a short tile has fewer pieces
+        if (p < n) {
+          sm[40] = r0; sm[41] = i; sm[42] = item - i * a.Hkv;
+          sm[43] = (int)((int64_t)p * nu / n); sm[44] = (int)((int64_t)(p + 1) * nu / n);
+          sm[45] = q.start; sm[46] = q.n; sm[47] = q.seq; sm[48] = u0; sm[49] = nu;
+          sm[50] = c - p; sm[51] = n;
+        }
+      }
+      __syncthreads();
+      if (sm[40] < 0) return false;
+      cur.r = sm[40]; cur.i = sm[41]; cur.h = sm[42]; cur.at = sm[43]; cur.left = sm[44] - sm[43];
+      cur.q.start = sm[45]; cur.q.n = sm[46]; cur.q.seq = sm[47]; cur.u0 = sm[48]; cur.nu = sm[49];
+      cur.item_first = 0;
+      sp.first = sm[50];
+      sp.count = sm[51];
+      return true;
+    }
+  }
   if (W == 0 || c >= sp.parts) return false;
   const int x0 = sp.begin(c), x1 = sp.begin(c + 1);
   int lo = base + inc - mine;
@@ -253,8 +319,7 @@ __device__ __forceinline__ int attn_slot(const AttnCursor& c, int part) { return
 // last of the item to arrive, with c0 and n the item's first CTA and number of pieces.
 __device__ __forceinline__ bool attn_arrive(const AttnArgs& a, const AttnSplit& sp, const AttnCursor& c, int32_t* flag,
                                             int& c0, int& n) {
-  c0 = sp.owner(c.item_first);
-  n = sp.owner(c.item_first + c.nu - 1) - c0 + 1;
+  sp.pieces(c, c0, n);
   __threadfence();
   __syncthreads();
   if (threadIdx.x == 0) {

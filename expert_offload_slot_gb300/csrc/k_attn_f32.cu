@@ -29,7 +29,7 @@ __global__ __launch_bounds__(NT) void attn_f32_kernel(const AttnArgs a) {
   sm103::grid_wait();
   AttnSplit sp;
   AttnCursor c;
-  if (!attn_find_range<BM, NT>(a, BN, blockIdx.x, gridDim.x, sched, sp, c)) return;
+  if (!attn_find_range<BM, NT>(a, BN, 4, blockIdx.x, gridDim.x, sched, sp, c)) return;
   const int tid = threadIdx.x, row = tid / 8, sub = tid % 8;
   do {
     const int rows = min(BM, c.q.n * a.group - c.i * BM);

@@ -57,7 +57,7 @@ __global__ __launch_bounds__(NT, 1) void attn_rows_kernel(const __grid_constant_
   grid_wait();
   AttnSplit sp;
   AttnCursor c;
-  if (!attn_find_range<BM, NT>(a, UNIT, blockIdx.x, gridDim.x, sched, sp, c)) return;
+  if (!attn_find_range<BM, NT>(a, UNIT, 5, blockIdx.x, gridDim.x, sched, sp, c)) return;
 
   uint64_t* bar = bars + wid * C::kStages;
   const uint32_t ring = smem_addr(smem) + wid * C::kStages * 2 * C::kTile;

@@ -140,7 +140,7 @@ __device__ __forceinline__ bool tile_work(const AttnArgs& a, int32_t* sm, uint8_
   w.count = 0;
   if (!w.whole) {
     __syncthreads();
-    return attn_find_range<BM, NT>(a, UNIT, pair, G, sm, w.sp, c);
+    return attn_find_range<BM, NT>(a, UNIT, kJoin, pair, G, sm, w.sp, c);
   }
   int at = base + inc - tiles;
   for (int r = r0; r < r1; ++r) {
@@ -532,7 +532,8 @@ void attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_cons
       }
       if (!whole && rows > 0) {
         if (row < rows) a.part_ml[at] = make_float2(m, l);
-        const int c0 = work.sp.owner(c.item_first), n = work.sp.owner(c.item_first + c.nu - 1) - c0 + 1;
+        int c0, n;
+        work.sp.pieces(c, c0, n);
         uint32_t* counter = a.arrived + 4 * c0 + 2 * t + rank;
         __threadfence();
         named_sync(1 + t, 128);
