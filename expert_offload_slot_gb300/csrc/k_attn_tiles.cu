@@ -413,16 +413,13 @@ void attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_cons
     }
     bool more;
     do {
-      TileCursor nx = c;
-      more = tile_next(a, work, nx);
-      const bool next_mine = more && has_tile(nx);
       if (!mine) {                                       // an item of 256 rows or fewer has no tile B
-        if (next_mine) {
-          load_q(nx);
+        more = tile_next(a, work, c);
+        mine = more && has_tile(c);
+        if (mine) {
+          load_q(c);
           q_loaded();
         }
-        c = nx;
-        mine = next_mine;
         continue;
       }
       const int f0 = c.i * BM + f_off, f = f0 + row;
@@ -435,6 +432,7 @@ void attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_cons
       const int all_lo = a.window > 0 ? max(0, base_pos + a.token(f0 + max(0, min(rows, 128) - 1)) - a.window + 1) : 0;
       float m = -INFINITY, l = 0.f;
       const int units = attn_piece(c);
+      bool next_mine = false;
       for (int j = 0; j < units; ++j) {
         const int key0 = (c.u0 + c.at + j) * UNIT;
         wait(s_full + t, ns++ & 1);
@@ -443,7 +441,12 @@ void attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_cons
         float s[UNIT];
         tmem_ld64(s_addr, s);
         tmem_ld64(s_addr + 64, s + 64);
-        if (j == units - 1 && next_mine) load_q(nx);     // every product that reads this tile's Q has ended
+        if (j == units - 1) {                            // every product that reads this tile's Q has ended
+          TileCursor nx = c;
+          more = tile_next(a, work, nx);
+          next_mine = more && has_tile(nx);
+          if (next_mine) load_q(nx);
+        }
         if (key0 < all_lo || key0 + UNIT > all_hi) {
 #pragma unroll
           for (int i = 0; i < UNIT; ++i)
@@ -587,7 +590,7 @@ void attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_cons
           }
         }
       }
-      c = nx;
+      more = tile_next(a, work, c);
       mine = next_mine;
     } while (more);
   }
