@@ -504,7 +504,11 @@ void attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_cons
       __syncwarp();
       tc_fence_after();
       const bool whole = units == c.nu;
-      const size_t at = (size_t)attn_slot(c, part) * BM + f_off + row;
+      // Partial results lie a warp's 32 rows together, [D / 4][32 rows][4]: a warp stores and loads 512
+      // contiguous bytes at a time, a row staying in its thread.
+      const size_t warp_rows = f_off + (wid & 3) * 32;
+      const size_t part_slot = (size_t)attn_slot(c, part) * BM;
+      float* part_dst = a.part_o + (part_slot + warp_rows) * D + lane * 4;
       const float inv = l > 0.f ? 1.f / l : 0.f;
       __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out);
       if (row < rows) dst += ((size_t)(c.q.start + a.token(f)) * a.Hq + c.h * a.group + a.head_of(f)) * D;
@@ -530,11 +534,11 @@ void attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_cons
         } else {
 #pragma unroll
           for (int i = 0; i < 32; i += 4)
-            attn_store4(a.part_o + at * D + d + i, make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]));
+            attn_store4(part_dst + (d + i) * 32, make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]));
         }
       }
       if (!whole && rows > 0) {
-        if (row < rows) a.part_ml[at] = make_float2(m, l);
+        if (row < rows) a.part_ml[part_slot + f_off + row] = make_float2(m, l);
         int c0, n;
         work.sp.pieces(c, c0, n);
         uint32_t* counter = a.arrived + 4 * c0 + 2 * t + rank;
@@ -546,47 +550,45 @@ void attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_cons
           last_flag[t] = last;
         }
         named_sync(1 + t, 128);
-        if (last_flag[t]) {                              // the last of the item's pieces to arrive joins these rows, in
-          __threadfence();                               // piece order: a warp its 32 rows, 16 loads in flight per lane
-          constexpr int LANES = D / 4, PER = 32 / LANES, B = 16;
-          const int r0 = (wid & 3) * 32;
-          const float2* ml = a.part_ml + f_off + row;
+        if (last_flag[t] && row < rows) {                // the last of the item's pieces to arrive joins these rows, in
+          __threadfence();                               // piece order
           auto slot = [&](int p) { return (size_t)(2 * (c0 + p) + (p == 0)) * BM; };
+          const float2* ml = a.part_ml + f_off + row;
           float M = -INFINITY, sum = 0.f;
+#pragma unroll 4
           for (int p = 0; p < n; ++p) M = fmaxf(M, __ldcg(ml + slot(p)).x);
           const float top = M == -INFINITY ? 0.f : M;
+#pragma unroll 4
           for (int p = 0; p < n; ++p) {
             const float2 v = __ldcg(ml + slot(p));
             sum += ex2(v.x - top) * v.y;
           }
           const float in = sum > 0.f ? 1.f / sum : 0.f;
+          const float* src = a.part_o + warp_rows * D + lane * 4;
 #pragma unroll 1
-          for (int b = 0; b < 32; b += B * PER) {
-            float4 o[B];
+          for (int d = 0; d < D; d += 64) {
+            float o[64];
 #pragma unroll
-            for (int k = 0; k < B; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int i = 0; i < 64; ++i) o[i] = 0.f;
 #pragma unroll 1
             for (int p = 0; p < n; ++p) {
               const float g = ex2(__ldcg(ml + slot(p)).x - top) * in;
-              float4 v[B];
+              float4 v[16];
 #pragma unroll
-              for (int k = 0; k < B; ++k)
-                v[k] = __ldcg(reinterpret_cast<const float4*>(
-                    a.part_o + (slot(p) + f_off + r0 + b + k * PER + lane / LANES) * D + lane % LANES * 4));
+              for (int i = 0; i < 16; ++i)
+                v[i] = __ldcg(reinterpret_cast<const float4*>(src + slot(p) * D + (d + 4 * i) * 32));
 #pragma unroll
-              for (int k = 0; k < B; ++k) {
-                const float w = __shfl_sync(0xffffffffu, g, b + k * PER + lane / LANES);
-                o[k].x += w * v[k].x; o[k].y += w * v[k].y; o[k].z += w * v[k].z; o[k].w += w * v[k].w;
+              for (int i = 0; i < 16; ++i) {
+                o[4 * i] += g * v[i].x;
+                o[4 * i + 1] += g * v[i].y;
+                o[4 * i + 2] += g * v[i].z;
+                o[4 * i + 3] += g * v[i].w;
               }
             }
 #pragma unroll
-            for (int k = 0; k < B; ++k) {
-              const int r = r0 + b + k * PER + lane / LANES, fr = f0 + r;
-              if (r < rows)
-                attn_store4(static_cast<__nv_bfloat16*>(a.out) +
-                                ((size_t)(c.q.start + a.token(fr)) * a.Hq + c.h * a.group + a.head_of(fr)) * D +
-                                lane % LANES * 4, o[k]);
-            }
+            for (int i = 0; i < 64; i += 8)
+              *reinterpret_cast<uint4*>(dst + d + i) = make_uint4(pack_bf16(o[i], o[i + 1]), pack_bf16(o[i + 2], o[i + 3]),
+                                                                  pack_bf16(o[i + 4], o[i + 5]), pack_bf16(o[i + 6], o[i + 7]));
           }
         }
       }
