@@ -253,7 +253,7 @@ void attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_cons
       const int row_limit = (int)((int64_t)a.num_pages * a.Hkv * a.page);   // out of range: zeros arrive
       const int k_box = min(a.page, 64), k_boxes = 64 / k_box, v_box = min(a.page, UNIT), v_boxes = UNIT / v_box;
       const bool my_k = lane < k_boxes * (D / 64), my_v = lane < v_boxes;
-      const int k_col = lane / k_boxes;
+      const int k_col = lane / k_boxes, my_key = rank * 64 + lane % k_boxes * k_box;
       const uint32_t k_dst = k_col * (64 * 128) + lane % k_boxes * k_box * 128, v_dst = lane * v_box * D;
       uint32_t n = 0, edge_phase = 0;
       auto row_of = [&](int key) -> int {                // row of the cache map that holds the key
@@ -268,10 +268,15 @@ void attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_cons
         const int hi = c.q.seq - c.q.n + last + 1;
         const int lo = a.window > 0 ? max(0, c.q.seq - c.q.n + first - a.window + 1) : 0;
         const int units = attn_piece(c);
+        // a unit's pages are looked up while the one before it is issued: a lookup takes about half as long
+        // as the boxes of a unit of small pages
+        const int piece0 = (c.u0 + c.at) * UNIT;
+        int k_at = my_k ? row_of(piece0 + my_key) : 0, v_at = my_v ? row_of(piece0 + lane * v_box) : 0;
         for (int j = 0; j < units; ++j) {
-          const int key0 = (c.u0 + c.at + j) * UNIT;
-          const int k_at = my_k ? row_of(key0 + rank * 64 + lane % k_boxes * k_box) : 0;
-          const int v_at = my_v ? row_of(key0 + lane * v_box) : 0;
+          const int key0 = piece0 + j * UNIT;
+          const bool ahead = j + 1 < units;
+          const int k_next = my_k && ahead ? row_of(key0 + UNIT + my_key) : 0;
+          const int v_next = my_v && ahead ? row_of(key0 + UNIT + lane * v_box) : 0;
           for (int kv = 0; kv < 2; ++kv, ++n) {
             const int st = n % C::kStages;
             const uint32_t stage = ring + st * C::kTile, lead_full = lead_addr(full + st);
@@ -307,6 +312,8 @@ void attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_cons
               tma_3d_pair(stage + (kv == 0 ? k_dst : v_dst), kv == 0 ? &mk : &mv, lead_full, 0, kv == 0 ? k_at : v_at,
                           kv == 0 ? k_col : rank);
           }
+          k_at = k_next;
+          v_at = v_next;
         }
       } while (tile_next(a, work, c));
       if (!alive) {                                      // bounded: copies in flight land (on the first CTA's barriers,
