@@ -40,6 +40,15 @@ moe_status launched(cudaError_t e, const char* what) {
   return e == cudaSuccess ? MOE_OK : fail(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
+// floor(n / d) as (n * mul) >> shift for n below 2^31: mul = ceil(2^(31 + l) / d) with 2^l >= d; what
+// that adds to n / d is below n / 2^(31 + l) <= 1 / d, too little to reach the next integer.
+void divider(uint32_t d, uint32_t& mul, int32_t& shift) {
+  int l = 0;
+  while ((1u << l) < d) ++l;
+  shift = 31 + l;
+  mul = (uint32_t)(((1ull << shift) + d - 1) / d);
+}
+
 bool misaligned(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
 
 moe_status check_config(const moe_attn_config* c) {
@@ -225,6 +234,8 @@ MOE_API moe_status moe_attn_qkv(moe_attn* A, const void* qkv, int64_t qkv_stride
   a.num_slots = (int64_t)num_pages * c.page_size; a.rows = rows; a.Hq = c.num_q_heads; a.Hkv = c.num_kv_heads;
   a.page_log2 = A->page_log2; a.rotary = c.rotary_dim; a.pairs = c.rotary_style == MOE_ROTARY_PAIRS; a.rope_len = rope_len;
   a.eps = c.norm_eps;
+  a.heads = a.Hq + 2 * a.Hkv;
+  divider(a.heads, a.heads_mul, a.heads_shift);
   return launched(launch_attn_qkv(a, c.dtype, c.head_dim, static_cast<cudaStream_t>(stream)), "moe_attn_qkv");
 }
 
@@ -256,12 +267,7 @@ MOE_API moe_status moe_attn_forward(moe_attn* A, const void* q, int64_t q_stride
   a.scale_log2 = c.softmax_scale * 1.44269504088896340736f;
   a.out_32 = !misaligned(out, 32);
   a.part_o = A->part_o; a.part_ml = A->part_ml; a.arrived = A->arrived; a.ticket = A->ticket; a.status = A->status;
-  // ceil(2^(31 + l) / group) with 2^l >= group: row * mul / 2^(31 + l) has the quotient's floor for
-  // every row below 2^31 (the excess, below row * group / 2^(31 + l) < 1, never reaches the next one)
-  int l = 0;
-  while ((1 << l) < a.group) ++l;
-  a.group_shift = 31 + l;
-  a.group_mul = (uint32_t)(((1ull << a.group_shift) + a.group - 1) / a.group);
+  divider(a.group, a.group_mul, a.group_shift);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (c.dtype == MOE_F32) return launched(launch_attn_f32(a, c.head_dim, attn_grid(A->sms), s), "moe_attn_forward");
   CUtensorMap mk, mv;

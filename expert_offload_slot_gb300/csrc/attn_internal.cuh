@@ -424,7 +424,9 @@ struct QkvArgs {
   void *q, *k_cache, *v_cache;
   int32_t* status;
   int64_t qkv_stride, num_slots;
-  int32_t rows, Hq, Hkv, page_log2, rotary, pairs, rope_len;
+  int32_t rows, heads, Hq, Hkv, page_log2, rotary, pairs, rope_len;
+  uint32_t heads_mul;          // row of a (row, head) unit without a division, as AttnArgs::group_mul
+  int32_t heads_shift;
   float eps;
 };
 cudaError_t launch_attn_qkv(const QkvArgs& a, int dtype, int D, cudaStream_t s);

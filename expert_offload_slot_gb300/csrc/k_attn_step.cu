@@ -134,128 +134,111 @@ __global__ __launch_bounds__(TT) void attn_tables_kernel(const TablesArgs a) {
 // ---------------------------------------------------------------------- qkv
 constexpr int QT = 256;
 
-template <typename T>
-struct Vec;                                   // 16 bytes of a head
-template <>
-struct Vec<float> {
-  static constexpr int N = 4;
-  static __device__ __forceinline__ void load(const void* p, float* v) {
-    const float4 x = *static_cast<const float4*>(p);
-    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-  }
-  static __device__ __forceinline__ void store(void* p, const float* v) {
-    *static_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-  }
-};
-template <>
-struct Vec<__nv_bfloat16> {
-  static constexpr int N = 8;
-  static __device__ __forceinline__ void load(const void* p, float* v) {
-    const uint4 x = *static_cast<const uint4*>(p);
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+// Eight consecutive elements.
+__device__ __forceinline__ void load8(const float* p, float* v) {
+  const float4 x = *reinterpret_cast<const float4*>(p), y = *reinterpret_cast<const float4*>(p + 4);
+  v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+  v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* v) {
+  const uint4 x = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
-  static __device__ __forceinline__ void store(void* p, const float* v) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&b);
-    }
-    *static_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-  }
-};
+}
+__device__ __forceinline__ void store8(float* p, const float* v) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* v) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(sm103::pack_bf16(v[0], v[1]), sm103::pack_bf16(v[2], v[3]),
+                                            sm103::pack_bf16(v[4], v[5]), sm103::pack_bf16(v[6], v[7]));
+}
 
-// A CTA per row: a group of D * sizeof(T) / 16 lanes takes a head at a time, its cosines, sines and
-// norm weights in registers for all of the row's heads, U heads in flight.
+// D / 16 lanes a head, 16 elements a lane in two chunks of eight.  With MOE_ROTARY_HALF a lane of the
+// turning part has elements i .. i+7 and their partners i + half .. i + half + 7, so the rotation
+// needs no exchange; the lanes after it have the rest in order (rotary_dim is a multiple of 16, so
+// the two parts fill whole lanes).  Every (row, head) is independent: a group of lanes each.
 template <typename T, int D>
-__global__ __launch_bounds__(QT, 4) void attn_qkv_kernel(const QkvArgs a) {
-  constexpr int N = Vec<T>::N, G = D / N, GROUPS = QT / G, U = 2;
-  const int heads = a.Hq + 2 * a.Hkv, t = blockIdx.x, group = threadIdx.x / G, sub = threadIdx.x % G, e0 = sub * N;
-  const int lane = threadIdx.x & 31, half = a.rotary / 2;
+__global__ __launch_bounds__(QT) void attn_qkv_kernel(const QkvArgs a) {
+  constexpr int G = D / 16;
+  const int half = a.rotary / 2, sub = threadIdx.x % G;
+  const uint32_t unit = blockIdx.x * (QT / G) + threadIdx.x / G;
   sm103::grid_wait();
-  const int64_t slot = a.slots[t];
-  const int64_t pos = a.rotary > 0 ? a.positions[t] : 0;
-  const T* src = static_cast<const T*>(a.qkv) + (size_t)t * a.qkv_stride + e0;
-  float x[U][N];
+  if (unit >= (uint32_t)a.rows * a.heads) return;            // whole groups of lanes
+  const int t = (int)(((uint64_t)unit * a.heads_mul) >> a.heads_shift), head = (int)(unit - (uint32_t)t * a.heads);
+  const bool is_q = head < a.Hq, is_v = head >= a.Hq + a.Hkv;
+  const bool split = !a.pairs && 8 * sub < half;
+  const int e0 = split ? 8 * sub : a.pairs ? 16 * sub : a.rotary + 16 * (sub - half / 8);
+  const int e1 = split ? half + 8 * sub : e0 + 8;
+  float x[16];
+  const T* src = static_cast<const T*>(a.qkv) + (size_t)t * a.qkv_stride + (size_t)head * D;
+  load8(src + e0, x);
+  load8(src + e1, x + 8);
+  const int64_t slot = is_q ? 0 : a.slots[t];
+  if (!is_v) {
+    const T* w = static_cast<const T*>(is_q ? a.q_norm : a.k_norm);
+    const bool turn = split || (a.pairs && 16 * sub < a.rotary);
+    const int64_t pos = a.rotary > 0 ? a.positions[t] : 0;
+    const bool in_table = pos >= 0 && pos < a.rope_len;
+    if (a.rotary > 0 && !in_table && sub == 0) atomicCAS(a.status, 0, MOE_ERR_BOUNDS);
+    if (w) {
+      float ss = 0.f, g[16];
 #pragma unroll
-  for (int u = 0; u < U; ++u)
-    if (group + u * GROUPS < heads) Vec<T>::load(src + (size_t)(group + u * GROUPS) * D, x[u]);
-  const bool in_table = pos >= 0 && pos < a.rope_len, turn = e0 < a.rotary && in_table;
-  const bool first = e0 < half;
-  float cs[N], sn[N];                         // of this lane's elements (MOE_ROTARY_PAIRS: the first N / 2)
-  if (turn) {
-    const float* row = a.rope + pos * a.rotary;
-    const int i0 = a.pairs ? e0 / 2 : first ? e0 : e0 - half;
+      for (int i = 0; i < 16; ++i) ss += x[i] * x[i];
+      const uint32_t lanes = (G == 32 ? 0xffffffffu : ((1u << G) - 1) << ((threadIdx.x & 31) / G * G));
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if (a.pairs && i >= N / 2) break;
-      cs[i] = row[i0 + i];
-      sn[i] = row[half + i0 + i];
+      for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(lanes, ss, o);
+      load8(w + e0, g);
+      load8(w + e1, g + 8);
+      const float inv = rsqrtf(ss * (1.f / D) + a.eps);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = x[i] * inv * g[i];
     }
-  }
-  if (a.rotary > 0 && !in_table && threadIdx.x == 0) atomicCAS(a.status, 0, MOE_ERR_BOUNDS);
-  if (slot >= a.num_slots && threadIdx.x == 0) atomicCAS(a.status, 0, MOE_ERR_BOUNDS);
-  const bool cached = slot >= 0 && slot < a.num_slots;
-  const int64_t page = slot >> a.page_log2, in = slot & ((1 << a.page_log2) - 1);
-  const int peer = e0 < a.rotary ? (first ? lane + half / N : lane - half / N) : lane;
-  for (int h0 = group; h0 - group < heads; h0 += U * GROUPS) {       // the same number of rounds in every group
+    if (turn && in_table) {
+      const float* row = a.rope + pos * a.rotary + 8 * sub;
+      float cs[8], sn[8];
+      load8(row, cs);
+      load8(row + half, sn);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int head = h0 + u * GROUPS;
-      const bool is_q = head < a.Hq, is_v = head >= a.Hq + a.Hkv;
-      float y[N], ss = 0.f;
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        y[i] = x[u][i];
-        ss += y[i] * y[i];
-      }
-      if (head + U * GROUPS < heads) Vec<T>::load(src + (size_t)(head + U * GROUPS) * D, x[u]);   // of the next round
-#pragma unroll
-      for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      const void* w = is_q ? a.q_norm : a.k_norm;
-      if (!is_v && w) {
-        float g[N];
-        Vec<T>::load(static_cast<const T*>(w) + e0, g);
-        const float inv = 1.f / sqrtf(ss * (1.f / D) + a.eps);
-#pragma unroll
-        for (int i = 0; i < N; ++i) y[i] = y[i] * inv * g[i];
-      }
-      if (a.pairs) {
-        if (turn && !is_v) {
-#pragma unroll
-          for (int i = 0; i < N; i += 2) {
-            const float p = y[i], q = y[i + 1];
-            y[i] = p * cs[i / 2] - q * sn[i / 2];
-            y[i + 1] = q * cs[i / 2] + p * sn[i / 2];
-          }
+      for (int i = 0; i < 8; ++i) {
+        const float u = a.pairs ? x[2 * i] : x[i], v = a.pairs ? x[2 * i + 1] : x[i + 8];
+        const float y = u * cs[i] - v * sn[i], z = v * cs[i] + u * sn[i];
+        if (a.pairs) {
+          x[2 * i] = y;
+          x[2 * i + 1] = z;
+        } else {
+          x[i] = y;
+          x[i + 8] = z;
         }
-      } else if (a.rotary > 0) {              // uniform: every lane takes part in the exchange
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const float z = __shfl_sync(0xffffffffu, y[i], peer);
-          if (turn && !is_v) y[i] = first ? y[i] * cs[i] - z * sn[i] : y[i] * cs[i] + z * sn[i];
-        }
-      }
-      if (head >= heads) continue;
-      if (is_q) {
-        Vec<T>::store(static_cast<T*>(a.q) + ((size_t)t * a.Hq + head) * D + e0, y);
-      } else if (cached) {
-        const int h = head - a.Hq - (is_v ? a.Hkv : 0);
-        T* dst = static_cast<T*>(is_v ? a.v_cache : a.k_cache);
-        Vec<T>::store(dst + ((((page * a.Hkv + h) << a.page_log2) + in) * D + e0), y);
       }
     }
   }
+  T* dst;
+  if (is_q) {
+    dst = static_cast<T*>(a.q) + ((size_t)t * a.Hq + head) * D;
+  } else {
+    if (slot < 0) return;                                    // a padding row
+    if (slot >= a.num_slots) {
+      atomicCAS(a.status, 0, MOE_ERR_BOUNDS);
+      return;
+    }
+    const int64_t page = slot >> a.page_log2, in = slot & ((1 << a.page_log2) - 1);
+    const int h = head - a.Hq - (is_v ? a.Hkv : 0);
+    dst = static_cast<T*>(is_v ? a.v_cache : a.k_cache) + (((page * a.Hkv + h) << a.page_log2) + in) * D;
+  }
+  store8(dst + e0, x);
+  store8(dst + e1, x + 8);
 }
 
 template <typename T, int D>
 cudaError_t qkv(const QkvArgs& a, cudaStream_t s) {
-  return sm103::launch(attn_qkv_kernel<T, D>, a.rows, QT, 0, s, a);
+  constexpr int per = QT / (D / 16);
+  const int64_t units = (int64_t)a.rows * a.heads;
+  return sm103::launch(attn_qkv_kernel<T, D>, (int)((units + per - 1) / per), QT, 0, s, a);
 }
 
 }  // namespace
