@@ -38,11 +38,12 @@ namespace {
 namespace cg = cooperative_groups;
 typedef unsigned long long u64;
 
-constexpr int NT = 512, NWARP = NT / 32, BINS = 16, PAR = 4;
+constexpr int NT = 512, NWARP = NT / 32, BINS = 16, PAR = 4;                 // PAR: logits a thread weighs at once
 constexpr int kMaxCluster = 8;
 constexpr int kShared = 230400;                // dynamic shared memory of a CTA, beside about 1 KB of static
 static_assert(((int64_t)kShared - 8 * 16 * 512) / 4 / 8 * 8 * kMaxCluster >= MOE_SAMPLE_MAX_VOCAB, "the largest row must fit");
 constexpr int kList = 2048;                    // tokens that are collected and sorted
+constexpr float kHead = 10.f;
 constexpr int kCountBins = 2048, kMassBins = 1024, kCountShift = 13, kMassShift = 14;
 constexpr u64 kMassMask = (1ull << 48) - 1;    // a thread's counter: count in the top 16 bits, mass below
 
@@ -58,10 +59,9 @@ struct Cut {                                   // kept: key above it, or equal a
   int32_t index;
 };
 
-template <typename T>
-__device__ __forceinline__ float value(T x) {  // NaN counts as -inf, -0 as +0
-  const float f = (float)x + 0.f;
-  return f == f ? f : -INFINITY;
+__device__ __forceinline__ float value(float x) {  // NaN counts as -inf, -0 as +0
+  x += 0.f;
+  return x == x ? x : -INFINITY;
 }
 // Order-preserving key.
 __device__ __forceinline__ uint32_t key_of(float x) {
@@ -85,8 +85,7 @@ struct Softener {
     if (!(e >= 1.f)) return 0;                 // also the NaN of an infinite d
     // the integer part from the bits: 64-bit conversions run at a small part of the integer rate
     const uint32_t bits = __float_as_uint(e), m = (bits & 0x7fffffu) | 0x800000u;
-    const int up = (int)(bits >> 23) - 150;    // e = m 2^up, up in [-23, 17]
-    return up >= 0 ? (u64)m << up : (u64)(m >> -up);
+    return ((u64)m << 17) >> (167 - (int)(bits >> 23));      // e = m 2^(exponent - 150), at most 2^40
   }
 };
 __device__ __forceinline__ u64 warp_add(u64 v) {
@@ -95,39 +94,60 @@ __device__ __forceinline__ u64 warp_add(u64 v) {
   return v;
 }
 
-// 16 bytes at a time where the row allows it.
+template <typename T>
+constexpr int kVec = 16 / sizeof(T);           // logits per 16 bytes
+__device__ __forceinline__ void unpack(uint4 v, float (&x)[4]) {
+  x[0] = __uint_as_float(v.x); x[1] = __uint_as_float(v.y); x[2] = __uint_as_float(v.z); x[3] = __uint_as_float(v.w);
+}
+__device__ __forceinline__ void unpack(uint4 v, float (&x)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ uint4 pack(const float (&x)[4]) {
+  return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+}
+__device__ __forceinline__ uint4 pack(const float (&x)[8]) {   // of values that are bf16 already
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = __byte_perm(__float_as_uint(x[2 * i]), __float_as_uint(x[2 * i + 1]), 0x7632);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// This CTA's share into shared memory, NaN as -inf and -0 as +0, padded with -inf to whole vectors.
+// Returns the thread's maximum.
 template <typename T>
 __device__ __forceinline__ float load_share(const T* src, T* xs, int n) {
-  constexpr int PER = 16 / sizeof(T);
+  constexpr int V = kVec<T>;
   float best = -INFINITY;
-  if ((reinterpret_cast<uintptr_t>(src) & 15) == 0) {
-    const int nv = n / PER;
+  const bool aligned = (reinterpret_cast<uintptr_t>(src) & 15) == 0;
+  const int nv = aligned ? n / V : 0;
 #pragma unroll 4
-    for (int i = threadIdx.x; i < nv; i += NT) {
-      const uint4 v = __ldcs(reinterpret_cast<const uint4*>(src) + i);
-      reinterpret_cast<uint4*>(xs)[i] = v;
-      T e[PER];
-      *reinterpret_cast<uint4*>(e) = v;
+  for (int i = threadIdx.x; i < nv; i += NT) {
+    float x[V];
+    unpack(__ldcs(reinterpret_cast<const uint4*>(src) + i), x);
 #pragma unroll
-      for (int j = 0; j < PER; ++j) best = fmaxf(best, (float)e[j]);
+    for (int j = 0; j < V; ++j) {
+      x[j] = value(x[j]);
+      best = fmaxf(best, x[j]);
     }
-    for (int i = nv * PER + threadIdx.x; i < n; i += NT) {
-      xs[i] = src[i];
-      best = fmaxf(best, (float)xs[i]);
-    }
-  } else {
-#pragma unroll 8
-    for (int i = threadIdx.x; i < n; i += NT) {
-      const T e = src[i];
-      xs[i] = e;
-      best = fmaxf(best, (float)e);
-    }
+    reinterpret_cast<uint4*>(xs)[i] = pack(x);
   }
-  return best + 0.f;
+#pragma unroll 8
+  for (int i = nv * V + threadIdx.x; i < n; i += NT) {
+    const float x = value((float)src[i]);
+    xs[i] = (T)x;
+    best = fmaxf(best, x);
+  }
+  for (int i = n + threadIdx.x; i < (n + V - 1) / V * V; i += NT) xs[i] = (T)-INFINITY;
+  return best;
 }
 
 template <typename T>
-__global__ __launch_bounds__(NT) void sample_kernel(const SampleArgs a) {
+__global__ __launch_bounds__(NT, 2) void sample_kernel(const SampleArgs a) {
   cg::cluster_group cluster = cg::this_cluster();
   const int CS = cluster.num_blocks(), rank = cluster.block_rank();
   const int row = blockIdx.x / CS, tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
@@ -160,7 +180,8 @@ __global__ __launch_bounds__(NT) void sample_kernel(const SampleArgs a) {
   const float top_p = a.top_p ? a.top_p[row] : 1.f;
   const float min_p = a.min_p ? a.min_p[row] : 0.f;
   const float u = a.u[row];
-  float best = load_share(static_cast<const T*>(a.logits) + (size_t)row * a.row_stride + i0, xs, n);
+  const float mine_best = load_share(static_cast<const T*>(a.logits) + (size_t)row * a.row_stride + i0, xs, n);
+  float best = mine_best;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
   if (lane == 0) s_best[wid] = best;
@@ -183,7 +204,7 @@ __global__ __launch_bounds__(NT) void sample_kernel(const SampleArgs a) {
   if (greedy || none) {
     int first = 0x7fffffff;
     for (int i = tid; i < n; i += NT)
-      if (value(xs[i]) == best) { first = i0 + i; break; }
+      if ((float)(xs[i]) == best) { first = i0 + i; break; }
     first = __reduce_min_sync(0xffffffffu, first);
     if (lane == 0) s_count[wid] = (uint32_t)first;
     __syncthreads();
@@ -259,18 +280,13 @@ __global__ __launch_bounds__(NT) void sample_kernel(const SampleArgs a) {
     return BINS - 1 - at;
   };
 
-  // Walks this CTA's logits, PAR a thread at a time so that their arithmetic overlaps; those past the
-  // end come as -inf, which has no weight.
+  // Walks this CTA's logits, a vector at a time: f(values, index of the first).
+  constexpr int V = kVec<T>;
   auto each = [&](auto&& f) {
-    for (int base = tid; base < n; base += NT * PAR) {
-      float x[PAR];
-      int i[PAR];
-#pragma unroll
-      for (int j = 0; j < PAR; ++j) {
-        i[j] = base + j * NT;
-        x[j] = i[j] < n ? value(xs[i[j]]) : -INFINITY;
-      }
-      f(x, i);
+    for (int v = tid; v < (n + V - 1) / V; v += NT) {
+      float x[V];
+      unpack(reinterpret_cast<const uint4*>(xs)[v], x);
+      f(x, i0 + v * V);
     }
   };
   const float to_q = 16777216.f / 28.f / temp;                   // d in [0, 28 T) to [0, 2^24)
@@ -298,17 +314,33 @@ __global__ __launch_bounds__(NT) void sample_kernel(const SampleArgs a) {
   auto find_bin = [&](bool by_mass, u64 limit, u64& total, bool only_total) -> bool {
     u64 v[4] = {0, 0, 0, 0}, sum = 0;
     if (by_mass) {
-      for (int c = 0; c < CS; ++c) {
-        const uint32_t* h = cluster.map_shared_rank(hist, c);
-        const uint2 lo = *reinterpret_cast<const uint2*>(h + 2 * tid);
-        const uint2 hi = *reinterpret_cast<const uint2*>(h + kMassBins + 2 * tid);
-        v[0] += (u64)hi.x << 32 | lo.x;
-        v[1] += (u64)hi.y << 32 | lo.y;
+#pragma unroll 1
+      for (int c0 = 0; c0 < CS; c0 += 4) {                       // four CTAs' loads in flight together
+        uint2 lo[4], hi[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t* h = cluster.map_shared_rank(hist, min(c0 + c, CS - 1));
+          lo[c] = *reinterpret_cast<const uint2*>(h + 2 * tid);
+          hi[c] = *reinterpret_cast<const uint2*>(h + kMassBins + 2 * tid);
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          v[0] += c0 + c < CS ? (u64)hi[c].x << 32 | lo[c].x : 0;
+          v[1] += c0 + c < CS ? (u64)hi[c].y << 32 | lo[c].y : 0;
+        }
       }
     } else {
-      for (int c = 0; c < CS; ++c) {
-        const uint4 k = *reinterpret_cast<const uint4*>(cluster.map_shared_rank(hist, c) + 4 * tid);
-        v[0] += k.x; v[1] += k.y; v[2] += k.z; v[3] += k.w;
+#pragma unroll 1
+      for (int c0 = 0; c0 < CS; c0 += 4) {
+        uint4 k[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          k[c] = *reinterpret_cast<const uint4*>(cluster.map_shared_rank(hist, min(c0 + c, CS - 1)) + 4 * tid);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (c0 + c >= CS) break;
+          v[0] += k[c].x; v[1] += k[c].y; v[2] += k[c].z; v[3] += k[c].w;
+        }
       }
     }
     sum = v[0] + v[1] + v[2] + v[3];
@@ -329,17 +361,33 @@ __global__ __launch_bounds__(NT) void sample_kernel(const SampleArgs a) {
     __syncthreads();
     return total >= limit;
   };
-  // Sorts the first m (a power of two) of list, ascending.
+  // Sorts the first m of list (at most kList, all different), ascending: few by counting the smaller
+  // ones, more in a bitonic network over the next power of two.
   auto sort = [&](u64* list, int m) {
-    for (int size = 2; size <= m; size <<= 1) {
-      for (int stride = size >> 1; stride > 0; stride >>= 1) {
-        __syncthreads();
-        for (int p = tid; p < m / 2; p += NT) {
-          const int i = 2 * p - (p & (stride - 1)), j = i + stride;
-          const u64 x = list[i], y = list[j];
-          if ((x > y) == ((i & size) == 0)) {
-            list[i] = y;
-            list[j] = x;
+    __syncthreads();
+    if (m <= 128) {
+      const u64 x = tid < m ? list[tid] : 0;
+      int place = 0;
+      if (tid < m) {
+#pragma unroll 8
+        for (int j = 0; j < m; ++j) place += list[j] < x;
+      }
+      __syncthreads();
+      if (tid < m) list[place] = x;
+    } else {
+      int top = 256;
+      while (top < m) top <<= 1;
+      for (int i = m + tid; i < top; i += NT) list[i] = ~0ull;
+      for (int size = 2; size <= top; size <<= 1) {
+        for (int stride = size >> 1; stride > 0; stride >>= 1) {
+          __syncthreads();
+          for (int p = tid; p < top / 2; p += NT) {
+            const int i = 2 * p - (p & (stride - 1)), j = i + stride;
+            const u64 x = list[i], y = list[j];
+            if ((x > y) == ((i & size) == 0)) {
+              list[i] = y;
+              list[j] = x;
+            }
           }
         }
       }
@@ -356,13 +404,21 @@ __global__ __launch_bounds__(NT) void sample_kernel(const SampleArgs a) {
   auto collect = [&](int shift, uint32_t from, uint32_t to, bool leader) -> int {
     if (tid == 0) list_n = 0;
     __syncthreads();
-    each([&](const float (&x)[PAR], const int (&i)[PAR]) {
+    // below `floor` nothing can be in the bins: most vectors are passed over by their maximum
+    const float reach = (float)((to + 1) << shift) / to_q;
+    const float floor = best - reach * 1.0001f - 1e-6f * fabsf(best);
+    each([&](const float (&x)[V], int i) {
+      float top = x[0];
 #pragma unroll
-      for (int j = 0; j < PAR; ++j) {
-        const uint32_t q = q_of(x[j]), bin = q >> shift;
-        if (bin >= from && bin <= to && q < 16777216u && passes(key_of(x[j]), i0 + i[j])) {
+      for (int j = 1; j < V; ++j) top = fmaxf(top, x[j]);
+      if (top < floor) return;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        if (x[j] < floor) continue;
+        const uint32_t q = q_of(x[j]), bin = q >> shift, key = key_of(x[j]);
+        if (bin >= from && bin <= to && q < 16777216u && passes(key, i + j)) {
           const int at = atomicAdd(&list_n, 1);
-          if (at < kList) own[at] = (u64)(~key_of(x[j])) << 32 | (uint32_t)(i0 + i[j]);
+          if (at < kList) own[at] = (u64)(~key) << 32 | (uint32_t)(i + j);
         }
       }
     });
@@ -380,15 +436,11 @@ __global__ __launch_bounds__(NT) void sample_kernel(const SampleArgs a) {
     const int total = __shfl_sync(0xffffffffu, inc, kMaxCluster - 1);
     if (total > kList) return -1;                                // the same in every CTA
     if (!leader || rank == 0) {
-      for (int c = 0; c < CS; ++c) {
-        const int m = __shfl_sync(0xffffffffu, mine, c), at = __shfl_sync(0xffffffffu, inc - mine, c);
-        const u64* r = cluster.map_shared_rank(own, c);
-        for (int i = tid; i < m; i += NT) all[at + i] = r[i];
-      }
-      int m = 32;
-      while (m < total) m <<= 1;
-      for (int i = total + tid; i < m; i += NT) all[i] = ~0ull;
-      sort(all, m);
+      const int c = wid % kMaxCluster;                           // two warps per CTA of the cluster
+      const int m = __shfl_sync(0xffffffffu, mine, c), at = __shfl_sync(0xffffffffu, inc - mine, c);
+      const u64* r = cluster.map_shared_rank(own, min(c, CS - 1));
+      for (int i = lane + 32 * (wid / kMaxCluster); i < m; i += 32 * (NWARP / kMaxCluster)) all[at + i] = r[i];
+      sort(all, total);
     }
     cluster.sync();                                              // every list has been read
     return total;
@@ -406,24 +458,42 @@ __global__ __launch_bounds__(NT) void sample_kernel(const SampleArgs a) {
     if (what == 0 ? !(top_k > 0 && top_k < a.vocab) : !cut_p) continue;
     clear_hist();
     if (what == 0) {
-      each([&](const float (&x)[PAR], const int (&)[PAR]) {
-#pragma unroll
-        for (int j = 0; j < PAR; ++j) {
-          const uint32_t q = q_of(x[j]);
-          if (q < 16777216u) atomicAdd(hist + (q >> kCountShift), 1u);
-        }
-      });
-      cluster.sync();
       limit = (u64)top_k;
-      const bool cuts = find_bin(false, limit, total, false);
-      cluster.sync();                                            // the bins have been read
-      if (!cuts) continue;                                       // every token that has weight is among the first
-      above = s_above;
-      const int bin = s_bin, in = s_in;
-      if (above + in <= kList) {
+      // The k-th largest of the threads' maxima is no larger than the k-th largest logit, and few more than
+      // k logits reach it: its bin bounds the list without a pass over all logits.  Failing that
+      // (many equal ones, few threads) all logits are counted.
+      int count = -1;
+      if (2 * top_k <= CS * NT) {
+        const uint32_t q = q_of(mine_best);
+        if (q < 16777216u) atomicAdd(hist + (q >> kCountShift), 1u);
+        cluster.sync();
+        const bool cuts = find_bin(false, limit, total, false);
+        const int bin = s_bin;
+        cluster.sync();                                          // the bins have been read
+        if (cuts) count = collect(kCountShift, 0, bin, true);
+        clear_hist();
+      }
+      int bin = 0;
+      if (count < 0) {
+        each([&](const float (&x)[V], int) {
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            const uint32_t q = q_of(x[j]);
+            if (q < 16777216u) atomicAdd(hist + (q >> kCountShift), 1u);
+          }
+        });
+        cluster.sync();
+        const bool cuts = find_bin(false, limit, total, false);
+        cluster.sync();                                          // the bins have been read
+        if (!cuts) continue;                                     // every token that has weight is among the first
+        above = s_above;
+        bin = s_bin;
+        if (above + s_in <= kList) count = collect(kCountShift, 0, bin, true);
+      }
+      if (count >= 0) {
         // all that may be kept, in one list
-        const int count = min(collect(kCountShift, 0, bin, true), top_k);
         if (rank != 0) return;
+        count = min(count, top_k);
         u64 w[4], sum = 0;                                       // four consecutive tokens a thread
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -454,10 +524,8 @@ __global__ __launch_bounds__(NT) void sample_kernel(const SampleArgs a) {
         kept = list_n;
         total = sums[kept - 1];
         if (tid == 0) s_goal = u > 0.f ? (u64)((double)u * (double)total) : 0ull;
-        int m = 32;
-        while (m < kept) m <<= 1;
-        for (int i = tid; i < m; i += NT) own[i] = i < kept ? (u64)(uint32_t)all[i] << 32 | (uint32_t)i : ~0ull;
-        sort(own, m);                                            // by index
+        for (int i = tid; i < kept; i += NT) own[i] = (u64)(uint32_t)all[i] << 32 | (uint32_t)i;
+        sort(own, kept);                                         // by index
         const u64 goal = min(s_goal, total - 1);
         sum = 0;
 #pragma unroll
@@ -479,28 +547,47 @@ __global__ __launch_bounds__(NT) void sample_kernel(const SampleArgs a) {
         return;
       }
     } else {
+      // Bins for the tokens up to kHead T below the maximum; the mass of the others in one sum, unless
+      // the cut turns out to lie among them.
       uint32_t* hi = hist + kMassBins;
-      each([&](const float (&x)[PAR], const int (&i)[PAR]) {
-        u64 w[PAR];
+      uint32_t reach = (uint32_t)(16777216.f / 28.f * kHead);
+      for (;;) {
+        u64 rest = 0;
+        each([&](const float (&x)[V], int i) {
 #pragma unroll
-        for (int j = 0; j < PAR; ++j) w[j] = passes(key_of(x[j]), i0 + i[j]) ? soft.weight(x[j]) : 0;
-#pragma unroll
-        for (int j = 0; j < PAR; ++j) {
-          if (!w[j]) continue;
-          const uint32_t b = min(q_of(x[j]), 16777215u) >> kMassShift, low = (uint32_t)w[j];
-          const uint32_t old = atomicAdd(hist + b, low);         // a 64-bit sum in two words: the carry is seen here
-          const uint32_t up = (uint32_t)(w[j] >> 32) + (old + low < old ? 1u : 0u);
-          if (up) atomicAdd(hi + b, up);
+          for (int j = 0; j < V; ++j) {
+            const u64 w = passes(key_of(x[j]), i + j) ? soft.weight(x[j]) : 0;
+            const uint32_t q = min(q_of(x[j]), 16777215u);
+            if (q >= reach) {
+              rest += w;
+            } else if (w) {
+              const uint32_t b = q >> kMassShift, low = (uint32_t)w;
+              const uint32_t old = atomicAdd(hist + b, low);     // a 64-bit sum in two words: the carry is seen here
+              const uint32_t up = (uint32_t)(w >> 32) + (old + low < old ? 1u : 0u);
+              if (up) atomicAdd(hi + b, up);
+            }
+          }
+        });
+        u64 sum;
+        scan(rest, sum);
+        if (tid == 0) ex[turn].mass[0] = sum;
+        cluster.sync();
+        const u64 others = warp_add(lane < CS ? cluster.map_shared_rank(&ex[turn], lane)->mass[0] : 0);
+        turn ^= 1;
+        find_bin(true, 0, kept_mass, true);
+        const u64 head = kept_mass;
+        kept_mass += others;
+        if (tid == 0) {                                          // one thread: fp64 is slow here
+          const double goal = ceil((double)fmaxf(top_p, 0.f) * (double)kept_mass);
+          s_kept = goal > 1.0 ? (u64)goal : 1ull;
         }
-      });
-      cluster.sync();
-      find_bin(true, 0, kept_mass, true);
-      if (tid == 0) {                                            // one thread: fp64 is slow here
-        const double goal = ceil((double)fmaxf(top_p, 0.f) * (double)kept_mass);
-        s_kept = goal > 1.0 ? (u64)goal : 1ull;
+        __syncthreads();
+        limit = s_kept;
+        if (limit <= head) break;
+        cluster.sync();                                          // the bins have been read
+        reach = 16777216u;
+        clear_hist();
       }
-      __syncthreads();
-      limit = s_kept;
       find_bin(true, limit, total, false);
       cluster.sync();                                            // the bins have been read
       above_mass = s_above;
@@ -531,7 +618,7 @@ __global__ __launch_bounds__(NT) void sample_kernel(const SampleArgs a) {
     for (int shift = 28; shift >= kLastShift; shift -= 4) {
       clear();
       for (int i = tid; i < n; i += NT) {
-        const float x = value(xs[i]);
+        const float x = (float)(xs[i]);
         const uint32_t key = key_of(x);
         if (shift == 28 || (key >> (shift + 4)) == prefix)
           bins[((key >> shift) & 15) * NT + tid] += (1ull << 48) + soft.weight(x);
@@ -547,7 +634,7 @@ __global__ __launch_bounds__(NT) void sample_kernel(const SampleArgs a) {
     const int span = ((n + NWARP - 1) / NWARP + 31) / 32 * 32;
     const int w0 = min(wid * span, n), w1 = min(w0 + span, n);
     uint32_t mine = 0;
-    for (int i = w0 + lane; i < w1; i += 32) mine += key_of(value(xs[i])) == key;
+    for (int i = w0 + lane; i < w1; i += 32) mine += key_of((float)(xs[i])) == key;
     mine = __reduce_add_sync(0xffffffffu, mine);
     if (lane == 0) s_count[wid] = mine;
     __syncthreads();
@@ -563,7 +650,7 @@ __global__ __launch_bounds__(NT) void sample_kernel(const SampleArgs a) {
     for (int v = 0; v < wid; ++v) before += s_count[v];
     if (before < ties && before + mine >= ties) {              // one warp of the cluster
       for (int i = w0; i < w1; i += 32) {
-        const bool tie = i + lane < w1 && key_of(value(xs[min(i + lane, w1 - 1)])) == key;
+        const bool tie = i + lane < w1 && key_of((float)(xs[min(i + lane, w1 - 1)])) == key;
         const uint32_t votes = __ballot_sync(0xffffffffu, tie);
         if (before + __popc(votes) >= ties) {
           if (tie && before + __popc(votes & ((2u << lane) - 1)) == ties) ex[turn].first = i0 + i + lane;
@@ -584,7 +671,7 @@ __global__ __launch_bounds__(NT) void sample_kernel(const SampleArgs a) {
   const int w0 = min(wid * span, n), w1 = min(w0 + span, n);
   auto kept = [&](int i, int end) -> u64 {                       // weight of the token if it is kept
     if (i >= end) return 0;
-    const float x = value(xs[i]);
+    const float x = (float)(xs[i]);
     const uint32_t key = key_of(x);
     if (key < cut.key || (key == cut.key && i0 + i > cut.index)) return 0;
     const u64 w = soft.weight(x);
