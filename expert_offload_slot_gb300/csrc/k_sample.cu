@@ -17,7 +17,7 @@
 // one pass adds the tokens up in 2048 bins of count or 1024 of mass with shared-memory
 // atomics on integers, the cluster adds its CTAs' bins over distributed shared memory,
 // and the tokens of the bin that holds the cut are collected and sorted by (x, index).
-// Where top-k leaves 2048 tokens or fewer down to the end of that bin, all of them are
+// Where top-k leaves 256 tokens or fewer down to the end of that bin, all of them are
 // collected instead and the first CTA does the rest on its sorted list.  A bin with
 // more tokens than the list holds (equal logits) is resolved by a radix descent over
 // the ordered bits of x and a count of the ties in index order.
@@ -38,13 +38,17 @@ namespace {
 namespace cg = cooperative_groups;
 typedef unsigned long long u64;
 
-constexpr int NT = 512, NWARP = NT / 32, BINS = 16, PAR = 4;                 // PAR: logits a thread weighs at once
+constexpr int NT = 512, NWARP = NT / 32, PAR = 4;   // PAR: logits a thread weighs at once
+constexpr int DIGIT = 2, BINS = 1 << DIGIT;    // bits a pass of the radix descent
 constexpr int kMaxCluster = 8;
-constexpr int kShared = 230400;                // dynamic shared memory of a CTA, beside about 1 KB of static
-static_assert(((int64_t)kShared - 8 * 16 * 512) / 4 / 8 * 8 * kMaxCluster >= MOE_SAMPLE_MAX_VOCAB, "the largest row must fit");
-constexpr int kList = 2048;                    // tokens that are collected and sorted
+constexpr int kList = 1024;                    // tokens that are collected and sorted
+constexpr int kFinish = 256;                   // of top-k, so many that one CTA does the rest on the list
 constexpr float kHead = 10.f;
 constexpr int kCountBins = 2048, kMassBins = 1024, kCountShift = 13, kMassShift = 14;
+constexpr int kScratch = kCountBins * 4 + 3 * kList * 8;       // bins and three lists, or the descent's counters
+static_assert(BINS * NT * 8 <= kScratch, "the counters share the lists' memory");
+constexpr int kShared = 230400;                // dynamic shared memory of a CTA, beside about 1 KB of static
+static_assert((kShared - kScratch) / 4 / 8 * 8 * kMaxCluster >= MOE_SAMPLE_MAX_VOCAB, "the largest row must fit");
 constexpr u64 kMassMask = (1ull << 48) - 1;    // a thread's counter: count in the top 16 bits, mass below
 
 struct Exchange {                              // what a CTA shows its cluster; two of them take turns
@@ -153,7 +157,7 @@ __global__ __launch_bounds__(NT, 2) void sample_kernel(const SampleArgs a) {
   const int row = blockIdx.x / CS, tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   extern __shared__ __align__(16) uint8_t raw[];
   u64* bins = reinterpret_cast<u64*>(raw);                       // [BINS][NT]
-  T* xs = reinterpret_cast<T*>(raw + sizeof(u64) * BINS * NT);
+  T* xs = reinterpret_cast<T*>(raw + kScratch);
   __shared__ Exchange ex[2];
   __shared__ u64 s_mass[NWARP];
   __shared__ uint32_t s_count[NWARP];
@@ -165,7 +169,6 @@ __global__ __launch_bounds__(NT, 2) void sample_kernel(const SampleArgs a) {
   u64* own = bins + kCountBins / 2;                              // [kList] ~key << 32 | index: ascending in (-x, index)
   u64* all = own + kList;                                        // [kList]
   u64* sums = all + kList;                                       // [kList]
-  static_assert(kCountBins / 2 + 3 * kList <= BINS * NT && 2 * kMassBins <= kCountBins, "the lists share the counters' memory");
   __shared__ int32_t list_n;
   __shared__ Cut s_cut;
   __shared__ u64 s_kept, s_goal, s_above;
@@ -226,19 +229,21 @@ __global__ __launch_bounds__(NT, 2) void sample_kernel(const SampleArgs a) {
   // The cluster's sums over the threads' counters, into t_mass and t_count.
   auto add_up = [&]() {
     __syncthreads();
-    u64 mass = 0;
-    uint32_t count = 0;
+    if (wid < BINS) {                                            // one warp per bin
+      u64 mass = 0;
+      uint32_t count = 0;
 #pragma unroll
-    for (int t = 0; t < NT; t += 32) {                           // one warp per bin
-      const u64 v = bins[wid * NT + t + lane];
-      mass += v & kMassMask;
-      count += (uint32_t)(v >> 48);
-    }
-    mass = warp_add(mass);
-    count = __reduce_add_sync(0xffffffffu, count);
-    if (lane == 0) {
-      ex[turn].mass[wid] = mass;
-      ex[turn].count[wid] = count;
+      for (int t = 0; t < NT; t += 32) {
+        const u64 v = bins[wid * NT + t + lane];
+        mass += v & kMassMask;
+        count += (uint32_t)(v >> 48);
+      }
+      mass = warp_add(mass);
+      count = __reduce_add_sync(0xffffffffu, count);
+      if (lane == 0) {
+        ex[turn].mass[wid] = mass;
+        ex[turn].count[wid] = count;
+      }
     }
     cluster.sync();
     if (tid < BINS * kMaxCluster) {
@@ -309,63 +314,75 @@ __global__ __launch_bounds__(NT, 2) void sample_kernel(const SampleArgs a) {
     total = warp_add(w);
     return inc + warp_add(lane < wid ? w : 0);
   };
-  // The first bin at which the cluster's running sum reaches `limit`: s_bin, the sum before it s_above,
-  // the tokens in it s_in (by count).  False when the total stays below the limit.
-  auto find_bin = [&](bool by_mass, u64 limit, u64& total, bool only_total) -> bool {
-    u64 v[4] = {0, 0, 0, 0}, sum = 0;
-    if (by_mass) {
+  // The first bin at which the cluster's running sum reaches a limit: s_bin, the sum before it s_above,
+  // the tokens in it s_in (by count), in every CTA.  The limit follows from the total, to which each
+  // CTA adds `rest`.  Each CTA adds up a share of the bins only: reading all bins of all CTAs took most of
+  // a top-p call.  False when the bins' sum stays below the limit.
+  auto find_bin = [&](bool by_mass, u64 rest, u64& total, auto&& limit_of) -> bool {
+    const int nb = by_mass ? kMassBins : kCountBins, Q = by_mass ? 2 : 4, per = ((nb + CS - 1) / CS + 3) / 4 * 4;
+    const int b0 = min(rank * per, nb), b1 = min(b0 + per, nb), b = b0 + Q * tid;
+    cluster.sync();                                              // the bins are complete
+    u64 v[4] = {0, 0, 0, 0};
+    if (b < b1) {
 #pragma unroll 1
       for (int c0 = 0; c0 < CS; c0 += 4) {                       // four CTAs' loads in flight together
-        uint2 lo[4], hi[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint32_t* h = cluster.map_shared_rank(hist, min(c0 + c, CS - 1));
-          lo[c] = *reinterpret_cast<const uint2*>(h + 2 * tid);
-          hi[c] = *reinterpret_cast<const uint2*>(h + kMassBins + 2 * tid);
-        }
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          v[0] += c0 + c < CS ? (u64)hi[c].x << 32 | lo[c].x : 0;
-          v[1] += c0 + c < CS ? (u64)hi[c].y << 32 | lo[c].y : 0;
-        }
-      }
-    } else {
-#pragma unroll 1
-      for (int c0 = 0; c0 < CS; c0 += 4) {
         uint4 k[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          k[c] = *reinterpret_cast<const uint4*>(cluster.map_shared_rank(hist, min(c0 + c, CS - 1)) + 4 * tid);
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t* h = cluster.map_shared_rank(hist, min(c0 + c, CS - 1)) + b;
+          if (by_mass) {
+            const uint2 lo = *reinterpret_cast<const uint2*>(h), hi = *reinterpret_cast<const uint2*>(h + kMassBins);
+            k[c] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+          } else {
+            k[c] = *reinterpret_cast<const uint4*>(h);
+          }
+        }
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           if (c0 + c >= CS) break;
-          v[0] += k[c].x; v[1] += k[c].y; v[2] += k[c].z; v[3] += k[c].w;
+          v[0] += by_mass ? (u64)k[c].z << 32 | k[c].x : (u64)k[c].x;
+          v[1] += by_mass ? (u64)k[c].w << 32 | k[c].y : (u64)k[c].y;
+          v[2] += by_mass ? 0 : k[c].z;
+          v[3] += by_mass ? 0 : k[c].w;
         }
       }
     }
-    sum = v[0] + v[1] + v[2] + v[3];
-    const u64 inc = scan(sum, total);
-    if (only_total) return true;
-    u64 run = inc - sum;
-    if (run < limit && inc >= limit) {
+    const u64 sum = v[0] + v[1] + v[2] + v[3];
+    u64 share;
+    const u64 inc = scan(sum, share);
+    if (tid == 0) {
+      ex[turn].mass[0] = share;
+      ex[turn].mass[1] = rest;
+    }
+    cluster.sync();
+    const Exchange* e = cluster.map_shared_rank(&ex[turn], lane < CS ? lane : 0);
+    const u64 shares = lane < CS ? e->mass[0] : 0, rests = lane < CS ? e->mass[1] : 0;
+    turn ^= 1;
+    const u64 before = warp_add(lane < rank ? shares : 0), all = warp_add(shares);
+    total = all + warp_add(rests);
+    const u64 limit = limit_of(total);
+    u64 run = before + inc - sum;
+    if (run < limit && run + sum >= limit) {                     // one thread of the cluster tells all CTAs
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if (run < limit && run + v[j] >= limit) {
-          s_bin = (by_mass ? 2 : 4) * tid + j;
-          s_above = run;
-          s_in = (int)v[j];
+          for (int c = 0; c < CS; ++c) {
+            *cluster.map_shared_rank(&s_bin, c) = b0 + Q * tid + j;
+            *cluster.map_shared_rank(&s_above, c) = run;
+            *cluster.map_shared_rank(&s_in, c) = (int)v[j];
+          }
         }
         run += v[j];
       }
     }
-    __syncthreads();
-    return total >= limit;
+    cluster.sync();
+    return all >= limit;
   };
-  // Sorts the first m of list (at most kList, all different), ascending: few by counting the smaller
-  // ones, more in a bitonic network over the next power of two.
+  // Sorts the first m of list (at most kList, all different), ascending: one a thread by counting the
+  // smaller ones, more in a bitonic network over the next power of two (0.2 us for each of its passes).
   auto sort = [&](u64* list, int m) {
     __syncthreads();
-    if (m <= 128) {
+    if (m <= NT) {
       const u64 x = tid < m ? list[tid] : 0;
       int place = 0;
       if (tid < m) {
@@ -375,7 +392,7 @@ __global__ __launch_bounds__(NT, 2) void sample_kernel(const SampleArgs a) {
       __syncthreads();
       if (tid < m) list[place] = x;
     } else {
-      int top = 256;
+      int top = 2 * NT;
       while (top < m) top <<= 1;
       for (int i = m + tid; i < top; i += NT) list[i] = ~0ull;
       for (int size = 2; size <= top; size <<= 1) {
@@ -397,24 +414,32 @@ __global__ __launch_bounds__(NT, 2) void sample_kernel(const SampleArgs a) {
   auto key_in = [](u64 item) -> uint32_t { return ~(uint32_t)(item >> 32); };
   auto x_of = [](uint32_t key) -> float { return __uint_as_float((key >> 31) ? key & 0x7fffffffu : ~key); };
 
+  // A logit below this is in no bin up to `to` (with room for rounding; a NaN, from an infinite
+  // maximum, bounds nothing).
+  auto floor_of = [&](uint32_t to, int shift) {
+    return best - (float)((to + 1) << shift) / to_q * 1.0001f - 1e-6f * fabsf(best);
+  };
+
   Cut cut = {0, 0x7fffffff};                                     // everything
-  auto passes = [&](uint32_t key, int i) { return key > cut.key || (key == cut.key && i <= cut.index); };
+  constexpr int EACH = kList / NT;                               // list entries of a thread
+  bool cuts_any = false;
+  auto passes = [&](uint32_t key, int i) { return !cuts_any || key > cut.key || (key == cut.key && i <= cut.index); };
   // Collects the tokens of bins [from, to], those that pass the cut, and sorts them into `all` (in the
   // first CTA only, or in every one): their number, or -1 when they are too many.
   auto collect = [&](int shift, uint32_t from, uint32_t to, bool leader) -> int {
     if (tid == 0) list_n = 0;
     __syncthreads();
-    // below `floor` nothing can be in the bins: most vectors are passed over by their maximum
-    const float reach = (float)((to + 1) << shift) / to_q;
-    const float floor = best - reach * 1.0001f - 1e-6f * fabsf(best);
+    // below `floor` and above `roof` nothing can be in the bins: most vectors are passed over at once
+    const float floor = floor_of(to, shift);
+    const float roof = best - (float)(from << shift) / to_q * 0.9999f + 1e-6f * fabsf(best);
     each([&](const float (&x)[V], int i) {
-      float top = x[0];
+      bool any = false;
 #pragma unroll
-      for (int j = 1; j < V; ++j) top = fmaxf(top, x[j]);
-      if (top < floor) return;
+      for (int j = 0; j < V; ++j) any |= !(x[j] < floor) && !(x[j] > roof);
+      if (!any) return;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        if (x[j] < floor) continue;
+        if (x[j] < floor || x[j] > roof) continue;
         const uint32_t q = q_of(x[j]), bin = q >> shift, key = key_of(x[j]);
         if (bin >= from && bin <= to && q < 16777216u && passes(key, i + j)) {
           const int at = atomicAdd(&list_n, 1);
@@ -459,45 +484,45 @@ __global__ __launch_bounds__(NT, 2) void sample_kernel(const SampleArgs a) {
     clear_hist();
     if (what == 0) {
       limit = (u64)top_k;
-      // The k-th largest of the threads' maxima is no larger than the k-th largest logit, and few more than
-      // k logits reach it: its bin bounds the list without a pass over all logits.  Failing that
-      // (many equal ones, few threads) all logits are counted.
-      int count = -1;
-      if (2 * top_k <= CS * NT) {
+      // The k-th largest of the threads' maxima is no larger than the k-th largest logit, and only about
+      // k + k^2 / threads logits reach it: its bin bounds what has to be looked at, and where so many fit
+      // the list they are all collected at once.  Otherwise the logits down to there are counted.
+      int count = -1, bound = kCountBins - 1;
+      const int64_t threads = CS * NT;
+      if (2 * (int64_t)top_k <= threads) {
         const uint32_t q = q_of(mine_best);
         if (q < 16777216u) atomicAdd(hist + (q >> kCountShift), 1u);
-        cluster.sync();
-        const bool cuts = find_bin(false, limit, total, false);
-        const int bin = s_bin;
-        cluster.sync();                                          // the bins have been read
-        if (cuts) count = collect(kCountShift, 0, bin, true);
+        if (find_bin(false, 0, total, [&](u64) { return limit; })) {
+          bound = s_bin;
+          if (top_k + (int64_t)top_k * top_k / threads <= kFinish * 7 / 8) count = collect(kCountShift, 0, bound, true);
+        }
         clear_hist();
       }
       int bin = 0;
       if (count < 0) {
+        const float floor = floor_of(bound, kCountShift);
         each([&](const float (&x)[V], int) {
 #pragma unroll
           for (int j = 0; j < V; ++j) {
+            if (x[j] < floor) continue;
             const uint32_t q = q_of(x[j]);
             if (q < 16777216u) atomicAdd(hist + (q >> kCountShift), 1u);
           }
         });
-        cluster.sync();
-        const bool cuts = find_bin(false, limit, total, false);
-        cluster.sync();                                          // the bins have been read
-        if (!cuts) continue;                                     // every token that has weight is among the first
+        // below the limit: every token that has weight is among the first
+        if (!find_bin(false, 0, total, [&](u64) { return limit; })) continue;
         above = s_above;
         bin = s_bin;
-        if (above + s_in <= kList) count = collect(kCountShift, 0, bin, true);
+        if (above + s_in <= kFinish) count = collect(kCountShift, 0, bin, true);
       }
       if (count >= 0) {
         // all that may be kept, in one list
         if (rank != 0) return;
         count = min(count, top_k);
-        u64 w[4], sum = 0;                                       // four consecutive tokens a thread
+        u64 w[EACH], sum = 0;                                    // consecutive tokens a thread
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          w[j] = 4 * tid + j < count ? soft.weight(x_of(key_in(all[4 * tid + j]))) : 0;
+        for (int j = 0; j < EACH; ++j) {
+          w[j] = EACH * tid + j < count ? soft.weight(x_of(key_in(all[EACH * tid + j]))) : 0;
           sum += w[j];
         }
         u64 run = scan(sum, total) - sum;
@@ -513,10 +538,10 @@ __global__ __launch_bounds__(NT, 2) void sample_kernel(const SampleArgs a) {
         limit = s_kept;
         int kept = 0;                                            // the kept ones are the first of the list
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < EACH; ++j) {
           if (w[j] && w[j] >= least && run < limit) ++kept;
           run += w[j];
-          sums[4 * tid + j] = run;
+          sums[EACH * tid + j] = run;
         }
         kept = __reduce_add_sync(0xffffffffu, kept);
         if (lane == 0 && kept) atomicAdd(&list_n, kept);
@@ -529,17 +554,17 @@ __global__ __launch_bounds__(NT, 2) void sample_kernel(const SampleArgs a) {
         const u64 goal = min(s_goal, total - 1);
         sum = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int i = 4 * tid + j < kept ? (int)(uint32_t)own[4 * tid + j] : -1;
+        for (int j = 0; j < EACH; ++j) {
+          const int i = EACH * tid + j < kept ? (int)(uint32_t)own[EACH * tid + j] : -1;
           w[j] = i < 0 ? 0 : sums[i] - (i ? sums[i - 1] : 0);
           sum += w[j];
         }
         u64 all_mass;
         run = scan(sum, all_mass) - sum;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < EACH; ++j) {
           if (run <= goal && goal < run + w[j]) {
-            a.ids[row] = (int32_t)(own[4 * tid + j] >> 32);
+            a.ids[row] = (int32_t)(own[EACH * tid + j] >> 32);
             if (a.logp) a.logp[row] = logf((float)w[j] / (float)total);
           }
           run += w[j];
@@ -554,59 +579,55 @@ __global__ __launch_bounds__(NT, 2) void sample_kernel(const SampleArgs a) {
       for (;;) {
         u64 rest = 0;
         each([&](const float (&x)[V], int i) {
+          u64 w[V];
+#pragma unroll
+          for (int j = 0; j < V; ++j) w[j] = passes(key_of(x[j]), i + j) ? soft.weight(x[j]) : 0;
 #pragma unroll
           for (int j = 0; j < V; ++j) {
-            const u64 w = passes(key_of(x[j]), i + j) ? soft.weight(x[j]) : 0;
             const uint32_t q = min(q_of(x[j]), 16777215u);
             if (q >= reach) {
-              rest += w;
-            } else if (w) {
-              const uint32_t b = q >> kMassShift, low = (uint32_t)w;
+              rest += w[j];
+            } else if (w[j]) {
+              const uint32_t b = q >> kMassShift, low = (uint32_t)w[j];
               const uint32_t old = atomicAdd(hist + b, low);     // a 64-bit sum in two words: the carry is seen here
-              const uint32_t up = (uint32_t)(w >> 32) + (old + low < old ? 1u : 0u);
+              const uint32_t up = (uint32_t)(w[j] >> 32) + (old + low < old ? 1u : 0u);
               if (up) atomicAdd(hi + b, up);
             }
           }
         });
         u64 sum;
         scan(rest, sum);
-        if (tid == 0) ex[turn].mass[0] = sum;
-        cluster.sync();
-        const u64 others = warp_add(lane < CS ? cluster.map_shared_rank(&ex[turn], lane)->mass[0] : 0);
-        turn ^= 1;
-        find_bin(true, 0, kept_mass, true);
-        const u64 head = kept_mass;
-        kept_mass += others;
-        if (tid == 0) {                                          // one thread: fp64 is slow here
-          const double goal = ceil((double)fmaxf(top_p, 0.f) * (double)kept_mass);
-          s_kept = goal > 1.0 ? (u64)goal : 1ull;
-        }
-        __syncthreads();
+        const bool found = find_bin(true, sum, kept_mass, [&](u64 all_mass) -> u64 {
+          if (tid == 0) {                                        // one thread: fp64 is slow here
+            const double goal = ceil((double)fmaxf(top_p, 0.f) * (double)all_mass);
+            s_kept = goal > 1.0 ? (u64)goal : 1ull;
+          }
+          __syncthreads();
+          return s_kept;
+        });
         limit = s_kept;
-        if (limit <= head) break;
-        cluster.sync();                                          // the bins have been read
+        if (found || reach == 16777216u) break;
         reach = 16777216u;
         clear_hist();
       }
-      find_bin(true, limit, total, false);
-      cluster.sync();                                            // the bins have been read
       above_mass = s_above;
     }
     const int bin = s_bin, count = collect(what == 0 ? kCountShift : kMassShift, bin, bin, false);
     if (count >= 0) {
-      u64 v[4], sum = 0;
+      u64 v[EACH], sum = 0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[j] = 4 * tid + j < count ? what == 0 ? 1ull : soft.weight(x_of(key_in(all[4 * tid + j]))) : 0ull;
+      for (int j = 0; j < EACH; ++j) {
+        v[j] = EACH * tid + j < count ? what == 0 ? 1ull : soft.weight(x_of(key_in(all[EACH * tid + j]))) : 0ull;
         sum += v[j];
       }
       u64 run = (what == 0 ? above : above_mass) + scan(sum, total) - sum;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (run < limit && run + v[j] >= limit) s_cut = Cut{key_in(all[4 * tid + j]), (int32_t)(uint32_t)all[4 * tid + j]};
+      for (int j = 0; j < EACH; ++j) {
+        if (run < limit && run + v[j] >= limit) s_cut = Cut{key_in(all[EACH * tid + j]), (int32_t)(uint32_t)all[EACH * tid + j]};
         run += v[j];
       }
       __syncthreads();
+      cuts_any = true;
       cut = s_cut;                                               // never above an earlier cut: its tokens alone were counted
       __syncthreads();
       continue;
@@ -615,16 +636,16 @@ __global__ __launch_bounds__(NT, 2) void sample_kernel(const SampleArgs a) {
     constexpr int kLastShift = sizeof(T) == 2 ? 16 : 0;        // a bf16's lower key bits say nothing more
     above = 0;
     uint32_t prefix = 0;
-    for (int shift = 28; shift >= kLastShift; shift -= 4) {
+    for (int shift = 32 - DIGIT; shift >= kLastShift; shift -= DIGIT) {
       clear();
       for (int i = tid; i < n; i += NT) {
         const float x = (float)(xs[i]);
         const uint32_t key = key_of(x);
-        if (shift == 28 || (key >> (shift + 4)) == prefix)
-          bins[((key >> shift) & 15) * NT + tid] += (1ull << 48) + soft.weight(x);
+        if (shift == 32 - DIGIT || (key >> (shift + DIGIT)) == prefix)
+          bins[((key >> shift) & (BINS - 1)) * NT + tid] += (1ull << 48) + soft.weight(x);
       }
       add_up();
-      prefix = prefix << 4 | find(what == 1, limit, above);
+      prefix = prefix << DIGIT | find(what == 1, limit, above);
       __syncthreads();
     }
     uint32_t key = prefix << kLastShift;
@@ -663,6 +684,7 @@ __global__ __launch_bounds__(NT, 2) void sample_kernel(const SampleArgs a) {
     Cut found = {key, 0x7fffffff};
     for (int c = 0; c < CS; ++c) found.index = min(found.index, cluster.map_shared_rank(&ex[turn], c)->first);
     if (found.key > cut.key || (found.key == cut.key && found.index < cut.index)) cut = found;
+    cuts_any = true;
     cluster.sync();                                            // read by all before it is written again
   }
 
@@ -673,7 +695,7 @@ __global__ __launch_bounds__(NT, 2) void sample_kernel(const SampleArgs a) {
     if (i >= end) return 0;
     const float x = (float)(xs[i]);
     const uint32_t key = key_of(x);
-    if (key < cut.key || (key == cut.key && i0 + i > cut.index)) return 0;
+    if (!passes(key, i0 + i)) return 0;
     const u64 w = soft.weight(x);
     return w >= least ? w : 0;
   };
@@ -745,17 +767,36 @@ __global__ __launch_bounds__(NT, 2) void sample_kernel(const SampleArgs a) {
   cluster.sync();                                                // no CTA leaves while its memory is read
 }
 
+// Clusters of c CTAs that the GPU holds at once, with one or two CTAs on an SM: a GPC's SMs do not
+// divide by every size (as cudaOccupancyMaxActiveClusters says for GB300).
+int clusters_at_once(int c, int per_sm) {
+  static const int at[2][kMaxCluster] = {{152, 76, 46, 36, 28, 23, 15, 15}, {304, 152, 97, 74, 58, 46, 38, 36}};
+  return at[per_sm - 1][c - 1];
+}
+
 template <typename T>
 cudaError_t launch(SampleArgs a, cudaStream_t s) {
-  // CTAs per row: as many as fill the GPU once (a second round costs more than longer shares), each
-  // with 2048 logits or more, and no fewer than hold the row in shared memory
-  const int64_t fit = (kShared - (int64_t)sizeof(u64) * BINS * NT) / sizeof(T) / 8 * 8;
-  const int least = (int)((a.vocab + fit - 1) / fit);
-  int cs = sm_count() / a.rows;
-  cs = cs < (a.vocab + 2047) / 2048 ? cs : (a.vocab + 2047) / 2048;
-  cs = cs < least ? least : cs > kMaxCluster ? kMaxCluster : cs;
+  // CTAs per row: those that need the least time by a simple account.  A CTA takes as long as kFixed
+  // logits beside its own, and two on an SM get about 0.6 of its pace each; clusters that do not fit
+  // at once take another round (48 rows of 100277 fp32 logits: 3 CTAs each, two rounds, 92 us with
+  // top-p; 5 CTAs each, two on an SM, one round, 57 us).
+  constexpr int64_t kFixed = 12000;
+  int cs = 0;
+  int64_t cheapest = 0;
+  for (int c = 1; c <= kMaxCluster; ++c) {
+    const int64_t chunk = ((a.vocab + c - 1) / c + 7) / 8 * 8, bytes = kScratch + chunk * (int64_t)sizeof(T);
+    if (bytes > kShared || (c > 1 && chunk < 2048)) continue;
+    const int per_sm = 2 * (bytes + 3072) <= 233472 ? 2 : 1;     // 228 KB an SM; 1 KB each is the system's
+    const int64_t fit = clusters_at_once(c, per_sm), rounds = (a.rows + fit - 1) / fit;
+    const bool shared = per_sm == 2 && (int64_t)a.rows * c > sm_count();
+    const int64_t cost = rounds * (kFixed + (shared ? chunk * 5 / 3 : chunk));
+    if (cs == 0 || cost < cheapest) {
+      cs = c;
+      cheapest = cost;
+    }
+  }
   a.chunk = ((a.vocab + cs - 1) / cs + 7) / 8 * 8;               // every share is aligned as the row is
-  const size_t bytes = sizeof(u64) * BINS * NT + (size_t)a.chunk * sizeof(T);
+  const size_t bytes = kScratch + (size_t)a.chunk * sizeof(T);
   static std::atomic<uint64_t> ready{0};                         // devices whose kernel has the attribute
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
