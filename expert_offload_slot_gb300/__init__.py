@@ -364,7 +364,8 @@ def make_attn_config(num_q_heads, num_kv_heads, head_dim, page_size, dtype=MOE_B
 
 
 # The calls below run once per layer and step, beside kernels of a few microseconds, so their checks
-# are written flat: type, device, shape and layout of each tensor, since the library sees addresses only.
+# are written flat: type, device, element count and contiguity of each tensor, since the library sees
+# addresses only.  (len(tensor) is a Python function of torch's; size(0) is not.)
 _kinds = {}
 
 
@@ -378,28 +379,28 @@ def _torch_kinds():
     return _kinds
 
 
-def _refuse(name, t, kind, shape):
-    raise ValueError(f"{name} must be a contiguous CUDA tensor of {kind} and shape {tuple(shape)}, "
+def _flat(name, t, kind, count):
+    """Address of a contiguous CUDA tensor of this type with `count` elements."""
+    if t.dtype is kind and t.numel() == count and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous CUDA tensor of {kind} with {count} elements, "
                      f"got {t.dtype}, {tuple(t.shape)}, strides {t.stride()}, on {t.device}")
 
 
-def _flat(name, t, kind, shape):
-    """Address of a contiguous CUDA tensor of exactly this type and shape."""
-    if t.dtype is not kind or t.shape != shape or not t.is_cuda or not t.is_contiguous():
-        _refuse(name, t, kind, shape)
-    return t.data_ptr()
-
-
-def _rows(name, t, kind, rows, inner):
-    """Address and row stride in elements of a CUDA tensor [rows, *inner] whose rows are contiguous."""
-    if t.dtype is not kind or t.shape != (rows, *inner) or not t.is_cuda:
-        _refuse(name, t, kind, (rows, *inner))
-    width = 1
-    for n, st in zip(reversed(inner), reversed(t.stride())):
-        if n != 1 and st != width:
-            _refuse(name, t, kind, (rows, *inner))
-        width *= n
-    return t.data_ptr(), (t.stride(0) if rows > 1 else width)
+def _rows(name, t, kind, rows, width):
+    """Address and row stride in elements of a CUDA tensor [rows, ...] whose rows hold `width` contiguous elements."""
+    if t.dtype is kind and t.numel() == rows * width and t.is_cuda:
+        if t.is_contiguous():
+            return t.data_ptr(), width
+        inner = 1
+        for n, st in zip(reversed(t.shape[1:]), reversed(t.stride())):
+            if n != 1 and st != inner:
+                break
+            inner *= n
+        else:
+            return t.data_ptr(), (t.stride(0) if rows > 1 else width)
+    raise ValueError(f"{name} must be a CUDA tensor of {kind} with {rows} rows of {width} contiguous elements, "
+                     f"got {t.dtype}, {tuple(t.shape)}, strides {t.stride()}, on {t.device}")
 
 
 class Attention:
@@ -418,10 +419,10 @@ class Attention:
         kinds = _torch_kinds()
         self._kind, self._i32, self._f32 = kinds[cfg.dtype], kinds["i32"], kinds[MOE_F32]
         self._current, self._device = kinds["stream"], device
-        self._q_shape = (cfg.num_q_heads, cfg.head_dim)
-        self._qkv_shape = ((cfg.num_q_heads + 2 * cfg.num_kv_heads) * cfg.head_dim,)
-        self._page_shape = (cfg.num_kv_heads, cfg.page_size, cfg.head_dim)
-        self._norm_shape, self._rotary = (cfg.head_dim,), cfg.rotary_dim
+        self._q_width = cfg.num_q_heads * cfg.head_dim
+        self._qkv_width = self._q_width + 2 * cfg.num_kv_heads * cfg.head_dim
+        self._page = cfg.num_kv_heads * cfg.page_size * cfg.head_dim
+        self._dim, self._rotary = cfg.head_dim, cfg.rotary_dim
 
     def close(self):
         if self.h:
@@ -434,49 +435,48 @@ class Attention:
         except Exception:
             pass
 
-    def _on(self, stream):
-        return self._current(self._device) if stream is None else _stream(stream)
-
     def tables(self, ctx_len, new_len, block_table, free_pages, free_head, free_head_out, row_start, seq_len, positions,
                slot_map, stream=None):
         """Fill block_table, free_head_out, row_start, seq_len, positions and slot_map for the step."""
-        i32, n, rows, free, width = self._i32, len(ctx_len), len(positions), len(free_pages), block_table.shape[1]
-        one, per = (1,), (n,)
+        i32, n, rows, free = self._i32, ctx_len.size(0), positions.size(0), free_pages.size(0)
+        width = block_table.size(1)
         st = _lib.moe_attn_tables(
-            self.h, _flat("ctx_len", ctx_len, i32, per), _flat("new_len", new_len, i32, per), n,
-            _flat("block_table", block_table, i32, (n, width)), width, _flat("free_pages", free_pages, i32, (free,)), free,
-            _flat("free_head", free_head, i32, one), _flat("free_head_out", free_head_out, i32, one), rows,
-            _flat("row_start", row_start, i32, (n + 1,)), _flat("seq_len", seq_len, i32, per),
-            _flat("positions", positions, i32, (rows,)), _flat("slot_map", slot_map, i32, (rows,)), self._on(stream))
+            self.h, _flat("ctx_len", ctx_len, i32, n), _flat("new_len", new_len, i32, n), n,
+            _flat("block_table", block_table, i32, n * width), width, _flat("free_pages", free_pages, i32, free), free,
+            _flat("free_head", free_head, i32, 1), _flat("free_head_out", free_head_out, i32, 1), rows,
+            _flat("row_start", row_start, i32, n + 1), _flat("seq_len", seq_len, i32, n),
+            _flat("positions", positions, i32, rows), _flat("slot_map", slot_map, i32, rows),
+            self._current(self._device) if stream is None else _stream(stream))
         if st:
             _check(st, "moe_attn_tables")
 
     def qkv(self, qkv, q_norm, k_norm, rope, positions, slot_map, q, k_cache, v_cache, stream=None):
         """Norm, rotation and cache write of qkv [rows, (Hq + 2 Hkv) * D]; queries go to q [rows, Hq, D]."""
-        kind, i32, rows, pages = self._kind, self._i32, len(qkv), len(k_cache)
-        length = 0 if rope is None else len(rope)
-        at, stride = _rows("qkv", qkv, kind, rows, self._qkv_shape)
+        kind, i32, rows, pages, dim = self._kind, self._i32, qkv.size(0), k_cache.size(0), self._dim
+        length = 0 if rope is None else rope.size(0)
+        at, stride = _rows("qkv", qkv, kind, rows, self._qkv_width)
         st = _lib.moe_attn_qkv(
-            self.h, at, stride, rows, None if q_norm is None else _flat("q_norm", q_norm, kind, self._norm_shape),
-            None if k_norm is None else _flat("k_norm", k_norm, kind, self._norm_shape),
-            None if rope is None else _flat("rope", rope, self._f32, (length, self._rotary)), length,
-            _flat("positions", positions, i32, (rows,)), _flat("slot_map", slot_map, i32, (rows,)),
-            _flat("q", q, kind, (rows, *self._q_shape)), _flat("k_cache", k_cache, kind, (pages, *self._page_shape)),
-            _flat("v_cache", v_cache, kind, (pages, *self._page_shape)), pages, self._on(stream))
+            self.h, at, stride, rows, None if q_norm is None else _flat("q_norm", q_norm, kind, dim),
+            None if k_norm is None else _flat("k_norm", k_norm, kind, dim),
+            None if rope is None else _flat("rope", rope, self._f32, length * self._rotary), length,
+            _flat("positions", positions, i32, rows), _flat("slot_map", slot_map, i32, rows),
+            _flat("q", q, kind, rows * self._q_width), _flat("k_cache", k_cache, kind, pages * self._page),
+            _flat("v_cache", v_cache, kind, pages * self._page), pages,
+            self._current(self._device) if stream is None else _stream(stream))
         if st:
             _check(st, "moe_attn_qkv")
 
     def forward(self, q, row_start, seq_len, max_new, k_cache, v_cache, block_table, out, stream=None):
         """Attention of q [rows, Hq, D] over the cache, into out [rows, Hq, D]."""
-        kind, i32, rows, n, pages, width = (self._kind, self._i32, len(q), len(seq_len), len(k_cache),
-                                            block_table.shape[1])
-        at, stride = _rows("q", q, kind, rows, self._q_shape)
+        kind, i32, rows, n, pages = self._kind, self._i32, q.size(0), seq_len.size(0), k_cache.size(0)
+        width = block_table.size(1)
+        at, stride = _rows("q", q, kind, rows, self._q_width)
         st = _lib.moe_attn_forward(
-            self.h, at, stride, rows, _flat("row_start", row_start, i32, (n + 1,)), _flat("seq_len", seq_len, i32, (n,)), n,
-            max_new, _flat("k_cache", k_cache, kind, (pages, *self._page_shape)),
-            _flat("v_cache", v_cache, kind, (pages, *self._page_shape)), pages,
-            _flat("block_table", block_table, i32, (n, width)), width, _flat("out", out, kind, (rows, *self._q_shape)),
-            self._on(stream))
+            self.h, at, stride, rows, _flat("row_start", row_start, i32, n + 1), _flat("seq_len", seq_len, i32, n), n,
+            max_new, _flat("k_cache", k_cache, kind, pages * self._page),
+            _flat("v_cache", v_cache, kind, pages * self._page), pages,
+            _flat("block_table", block_table, i32, n * width), width, _flat("out", out, kind, rows * self._q_width),
+            self._current(self._device) if stream is None else _stream(stream))
         if st:
             _check(st, "moe_attn_forward")
 
@@ -492,14 +492,13 @@ def moe_sample(logits, u, ids, logp=None, temperature=None, top_k=None, top_p=No
     kinds = _torch_kinds()
     f32, i32 = kinds[MOE_F32], kinds["i32"]
     rows, vocab = logits.shape
-    per = (rows,)
     dtype = MOE_F32 if logits.dtype is f32 else MOE_BF16
-    at, stride = _rows("logits", logits, f32 if dtype == MOE_F32 else kinds[MOE_BF16], rows, (vocab,))
+    at, stride = _rows("logits", logits, f32 if dtype == MOE_F32 else kinds[MOE_BF16], rows, vocab)
     st = _lib.moe_sample(
-        at, dtype, rows, vocab, stride, None if temperature is None else _flat("temperature", temperature, f32, per),
-        None if top_k is None else _flat("top_k", top_k, i32, per), None if top_p is None else _flat("top_p", top_p, f32, per),
-        None if min_p is None else _flat("min_p", min_p, f32, per), _flat("u", u, f32, per), _flat("ids", ids, i32, per),
-        None if logp is None else _flat("logp", logp, f32, per),
+        at, dtype, rows, vocab, stride, None if temperature is None else _flat("temperature", temperature, f32, rows),
+        None if top_k is None else _flat("top_k", top_k, i32, rows), None if top_p is None else _flat("top_p", top_p, f32, rows),
+        None if min_p is None else _flat("min_p", min_p, f32, rows), _flat("u", u, f32, rows), _flat("ids", ids, i32, rows),
+        None if logp is None else _flat("logp", logp, f32, rows),
         kinds["stream"](logits.device.index) if stream is None else _stream(stream))
     if st:
         _check(st, "moe_sample")

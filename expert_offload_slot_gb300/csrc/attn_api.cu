@@ -23,6 +23,10 @@ struct moe_attn {
   uint32_t* ticket = nullptr;
   int32_t* status = nullptr;
   size_t zero_bytes = 0;       // counters and status, from `arrived` on
+  // tensor maps of caches of map_pages pages, for the row kernel [0] and the tile kernel [1]: K and V
+  // differ in the box; a call sets its caches' addresses into a copy
+  CUtensorMap maps[2][2];
+  int32_t map_pages[2] = {0, 0};
 };
 
 namespace {
@@ -71,18 +75,21 @@ moe_status check_config(const moe_attn_config* c) {
   return MOE_OK;
 }
 
+template <typename F>
+F driver_call(const char* name) {
+  void* p = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  if (cudaGetDriverEntryPointByVersion(name, &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+      q != cudaDriverEntryPointSuccess)
+    p = nullptr;
+  return reinterpret_cast<F>(p);
+}
+
 // A cache [num_pages][Hkv][P][D] as [D / cols][num_pages * Hkv * P][cols] bf16, cols 64 or 32: a box
 // of `rows` consecutive keys of one head comes as `blocks` tiles of rows of 2 cols bytes, swizzled
 // over as many.
 bool cache_map(CUtensorMap* m, const void* base, int64_t keys, int D, int rows, int cols, int blocks) {
-  static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      p = nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  }();
+  static const auto encode = driver_call<PFN_cuTensorMapEncodeTiled_v12000>("cuTensorMapEncodeTiled");
   if (!encode) return false;
   const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)keys, (cuuint64_t)(D / cols)};
   const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)cols * 2};
@@ -91,6 +98,30 @@ bool cache_map(CUtensorMap* m, const void* base, int64_t keys, int D, int rows, 
                 CU_TENSOR_MAP_INTERLEAVE_NONE, cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// This call's maps: made anew when the number of pages changes, else the kept ones with this call's
+// addresses (making two costs more than the launch).
+bool call_maps(moe_attn* A, bool few, const void* k, const void* v, int32_t num_pages, CUtensorMap& mk, CUtensorMap& mv) {
+  static const auto replace = driver_call<PFN_cuTensorMapReplaceAddress_v12000>("cuTensorMapReplaceAddress");
+  if (!replace) return false;
+  const moe_attn_config& c = A->cfg;
+  CUtensorMap* kept = A->maps[few ? 0 : 1];
+  if (A->map_pages[few ? 0 : 1] != num_pages) {
+    const int64_t keys = (int64_t)num_pages * c.num_kv_heads * c.page_size;
+    const int D = c.head_dim;
+    A->map_pages[few ? 0 : 1] = 0;
+    // the row kernel takes 16 keys of a head at a time, all columns; of the tile kernel's pairs each CTA
+    // takes half a K tile, 64 keys, and half a V tile, half the columns
+    const bool ok = few ? cache_map(kept, k, keys, D, 16, 64, D / 64) && cache_map(kept + 1, v, keys, D, 16, 64, D / 64)
+                        : cache_map(kept, k, keys, D, c.page_size < 64 ? c.page_size : 64, 64, 1) &&
+                              cache_map(kept + 1, v, keys, D, c.page_size, D / 2, 1);
+    if (!ok) return false;
+    A->map_pages[few ? 0 : 1] = num_pages;
+  }
+  mk = kept[0];
+  mv = kept[1];
+  return replace(&mk, const_cast<void*>(k)) == CUDA_SUCCESS && replace(&mv, const_cast<void*>(v)) == CUDA_SUCCESS;
 }
 
 moe_status check_cache(const moe_attn* A, const void* k, const void* v, int32_t num_pages) {
@@ -270,21 +301,14 @@ MOE_API moe_status moe_attn_forward(moe_attn* A, const void* q, int64_t q_stride
   divider(a.group, a.group_mul, a.group_shift);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (c.dtype == MOE_F32) return launched(launch_attn_f32(a, c.head_dim, attn_grid(A->sms), s), "moe_attn_forward");
-  CUtensorMap mk, mv;
-  const int64_t keys = (int64_t)num_pages * c.num_kv_heads * c.page_size;
   // Up to two row tiles of 16 the row kernel is ahead of the tile kernel although it reads the keys
   // once for each: 16 requests of 8192 keys, 4 kv heads, 24 and 32 query rows per kv head: 90 and 91 us
   // against 96 and 95; with 64 rows 168 against 97.
   const bool few = (int64_t)max_new * a.group <= 2 * kAttnRowsTile;
+  CUtensorMap mk, mv;
+  if (!call_maps(A, few, k_cache, v_cache, num_pages, mk, mv))
+    return fail(MOE_ERR_CUDA, "the driver made no tensor map of the caches");
   const int D = c.head_dim;
-  bool ok;
-  if (few) {                   // 16 keys of a head at a time, all columns
-    ok = cache_map(&mk, k_cache, keys, D, 16, 64, D / 64) && cache_map(&mv, v_cache, keys, D, 16, 64, D / 64);
-  } else {                     // half a K tile is 64 keys, half a V tile half the columns: a CTA's share of a pair
-    ok = cache_map(&mk, k_cache, keys, D, c.page_size < 64 ? c.page_size : 64, 64, 1) &&
-         cache_map(&mv, v_cache, keys, D, c.page_size, D / 2, 1);
-  }
-  if (!ok) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for the caches");
   return launched(few ? launch_attn_rows(a, mk, mv, D, A->sms, s) : launch_attn_tiles(a, mk, mv, D, A->sms / 2 * 2, s),
                   "moe_attn_forward");
 }
