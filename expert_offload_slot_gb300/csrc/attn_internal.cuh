@@ -155,14 +155,16 @@ struct AttnSplit {
 };
 
 // Called by all threads of the CTA (NT of them) for part c of at most `most`.  `sm` holds 64 ints.
-// False when the part has no work.
+// False when the part has no work.  Up to 32 requests, every warp finds the part by itself with a
+// request in each lane: no barrier stands before the first load of the cache.
 template <int BM, int NT>
 __device__ __forceinline__ bool attn_find_range(const AttnArgs& a, int unit, int overhead, int c, int most, int32_t* sm,
                                                 AttnSplit& sp, AttnCursor& cur) {
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   constexpr int NW = NT / 32;
-  const int per = (a.R + NT - 1) / NT;
-  const int r0 = min(tid * per, a.R), r1 = min(r0 + per, a.R);
+  const bool alone = a.R <= 32;
+  const int per = alone ? 1 : (a.R + NT - 1) / NT;
+  const int r0 = alone ? lane : min(tid * per, a.R), r1 = alone ? min(lane + 1, a.R) : min(r0 + per, a.R);
   AttnRequest q = {0, 0, 0};                   // of the last request looked at: the only one when per is 1
   int mine = 0, longest = 0;
   for (int k = 0; k < per; ++k) {
@@ -172,121 +174,128 @@ __device__ __forceinline__ bool attn_find_range(const AttnArgs& a, int unit, int
     attn_count_units<BM>(a, q, attn_tiles<BM>(a, q), unit, sum, longest);
     mine += sum * a.Hkv;
   }
-  int inc = mine;
+  // sum over the requests before this thread's, and over all
+  auto scan = [&](int v, int& before, int& total) {
+    int run = v;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += v;
-  }
-  if (lane == 31) sm[wid] = inc;
-  __syncthreads();
-  int base = 0, W = 0;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += x;
+    }
+    before = run - v;
+    total = __shfl_sync(0xffffffffu, run, 31);
+    if (alone) return;
+    __syncthreads();
+    if (lane == 31) sm[wid] = run;
+    __syncthreads();
+    total = 0;
 #pragma unroll
-  for (int w = 0; w < NW; ++w) {
-    const int v = sm[w];
-    base += w < wid ? v : 0;
-    W += v;
-  }
+    for (int w = 0; w < NW; ++w) {
+      before += w < wid ? sm[w] : 0;
+      total += sm[w];
+    }
+  };
+  int lo, W;
+  scan(mine, lo, W);
   sp.W = W;
   sp.parts = max(1, min(most, W));
   sp.count = 0;
-  if (W > 0 && per == 1) {
+  if (W == 0) return false;
+  int found[12] = {-1};                        // r, tile, head, first and last unit, request, u0, nu, first part, pieces
+  bool here = false, pieces = false;
+  if (per == 1) {
     const int items = attn_tiles<BM>(a, q) * a.Hkv;                    // of this thread's request
-    // pieces of at most L units: the parts that takes, and with `mine` those of the requests before
-    auto parts_for = [&](int L, int& before, int& own) -> int {
+    int before, own, total;
+    auto parts_for = [&](int L) -> int {       // parts for pieces of at most L units
       own = items > 0 ? items * ((longest + L - 1) / L) : 0;
-      int run = own;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, run, o);
-        if (lane >= o) run += v;
-      }
-      __syncthreads();
-      if (lane == 31) sm[wid] = run;
-      __syncthreads();
-      int total = 0, ahead = 0;
-#pragma unroll
-      for (int w = 0; w < NW; ++w) {
-        ahead += w < wid ? sm[w] : 0;
-        total += sm[w];
-      }
-      before = ahead + run - own;
+      scan(own, before, total);
       return total;
     };
-    int lo = (W + most - 1) / most, hi = lo + overhead, before, own;
-    if (parts_for(hi, before, own) <= most) {
-      while (lo < hi) {
-        const int mid = (lo + hi) / 2;
-        if (parts_for(mid, before, own) <= most) hi = mid;
-        else lo = mid + 1;
+    int least = (W + most - 1) / most, top = least + overhead;
+    if (parts_for(top) <= most) {
+      pieces = true;
+      while (least < top) {
+        const int mid = (least + top) / 2;
+        if (parts_for(mid) <= most) top = mid;
+        else least = mid + 1;
       }
-      parts_for(lo, before, own);
-      if (tid == 0) sm[40] = -1;
-      __syncthreads();
-      if (c >= before && c < before + own) {                           // one thread
+      parts_for(least);
+      if (c >= total) return false;
+      if (c >= before && c < before + own) {                           // one thread (of each warp)
         const int per_item = own / items, local = c - before, item = local / per_item, p = local - item * per_item;
         const int i = item / a.Hkv;
         int u0, nu;
         attn_units<BM>(a, q, i, unit, u0, nu);
         const int n = min(per_item, nu);                               // a short tile has fewer pieces
+        here = true;
         if (p < n) {
-          sm[40] = r0; sm[41] = i; sm[42] = item - i * a.Hkv;
-          sm[43] = (int)((int64_t)p * nu / n); sm[44] = (int)((int64_t)(p + 1) * nu / n);
-          sm[45] = q.start; sm[46] = q.n; sm[47] = q.seq; sm[48] = u0; sm[49] = nu;
-          sm[50] = c - p; sm[51] = n;
+          found[0] = r0; found[1] = i; found[2] = item - i * a.Hkv;
+          found[3] = (int)((int64_t)p * nu / n); found[4] = (int)((int64_t)(p + 1) * nu / n);
+          found[5] = q.start; found[6] = q.n; found[7] = q.seq; found[8] = u0; found[9] = nu;
+          found[10] = c - p; found[11] = n;
         }
       }
-      __syncthreads();
-      if (sm[40] < 0) return false;
-      cur.r = sm[40]; cur.i = sm[41]; cur.h = sm[42]; cur.at = sm[43]; cur.left = sm[44] - sm[43];
-      cur.q.start = sm[45]; cur.q.n = sm[46]; cur.q.seq = sm[47]; cur.u0 = sm[48]; cur.nu = sm[49];
-      cur.item_first = 0;
-      sp.first = sm[50];
-      sp.count = sm[51];
-      return true;
     }
   }
-  if (W == 0 || c >= sp.parts) return false;
-  const int x0 = sp.begin(c), x1 = sp.begin(c + 1);
-  int lo = base + inc - mine;
-  const uint32_t has = __ballot_sync(0xffffffffu, x0 >= lo && x0 < lo + mine);
-  if (has) {                                   // one warp, whose lane `src` has the request
-    const int src = __ffs(has) - 1;
-    int r = __shfl_sync(0xffffffffu, r0, src);
-    lo = __shfl_sync(0xffffffffu, lo, src);
-    q.start = __shfl_sync(0xffffffffu, q.start, src);
-    q.n = __shfl_sync(0xffffffffu, q.n, src);
-    q.seq = __shfl_sync(0xffffffffu, q.seq, src);
-    for (;; ++r) {                             // the whole warp, over the lane's requests and 32 tiles at a time
-      if (per > 1) q = attn_request(a, r);
-      const int nt = attn_tiles<BM>(a, q);
-      bool found = false;
-      for (int i0 = 0; i0 < nt && !found; i0 += 32) {
-        int u0 = 0, nu = 0;
-        if (i0 + lane < nt) attn_units<BM>(a, q, i0 + lane, unit, u0, nu);
-        int run = nu * a.Hkv;
+  if (!pieces) {
+    if (c >= sp.parts) return false;
+    const int x0 = sp.begin(c), x1 = sp.begin(c + 1);
+    const uint32_t has = __ballot_sync(0xffffffffu, x0 >= lo && x0 < lo + mine);
+    if (has) {                                 // one warp (or each), whose lane `src` has the request
+      const int src = __ffs(has) - 1;
+      int r = __shfl_sync(0xffffffffu, r0, src);
+      lo = __shfl_sync(0xffffffffu, lo, src);
+      AttnRequest y;
+      y.start = __shfl_sync(0xffffffffu, q.start, src);
+      y.n = __shfl_sync(0xffffffffu, q.n, src);
+      y.seq = __shfl_sync(0xffffffffu, q.seq, src);
+      for (;; ++r) {                           // the whole warp, over the lane's requests and 32 tiles at a time
+        if (per > 1) y = attn_request(a, r);
+        const int nt = attn_tiles<BM>(a, y);
+        for (int i0 = 0; i0 < nt && !__any_sync(0xffffffffu, here); i0 += 32) {
+          int u0 = 0, nu = 0;
+          if (i0 + lane < nt) attn_units<BM>(a, y, i0 + lane, unit, u0, nu);
+          int run = nu * a.Hkv;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int v = __shfl_up_sync(0xffffffffu, run, o);
-          if (lane >= o) run += v;
+          for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, run, o);
+            if (lane >= o) run += v;
+          }
+          const int before = lo + run - nu * a.Hkv;
+          if (nu > 0 && x0 >= before && x0 < before + nu * a.Hkv) {
+            const int h = (x0 - before) / nu;
+            here = true;
+            found[0] = r; found[1] = i0 + lane; found[2] = h;
+            found[3] = x0 - before - h * nu; found[4] = found[3] + x1 - x0;
+            found[5] = y.start; found[6] = y.n; found[7] = y.seq; found[8] = u0; found[9] = nu;
+            found[10] = before + h * nu; found[11] = 0;
+          }
+          lo += __shfl_sync(0xffffffffu, run, 31);
         }
-        const int before = lo + run - nu * a.Hkv;
-        const bool here = nu > 0 && x0 >= before && x0 < before + nu * a.Hkv;
-        if (here) {
-          const int h = (x0 - before) / nu;
-          sm[40] = r; sm[41] = i0 + lane; sm[42] = h; sm[43] = x0 - before - h * nu; sm[44] = before + h * nu;
-          sm[45] = q.start; sm[46] = q.n; sm[47] = q.seq; sm[48] = u0; sm[49] = nu;
-        }
-        found = __any_sync(0xffffffffu, here);
-        lo += __shfl_sync(0xffffffffu, run, 31);
+        if (__any_sync(0xffffffffu, here) || r + 1 >= a.R) break;
       }
-      if (found || r + 1 >= a.R) break;
     }
   }
-  __syncthreads();
-  cur.r = sm[40]; cur.i = sm[41]; cur.h = sm[42]; cur.at = sm[43]; cur.item_first = sm[44];
-  cur.q.start = sm[45]; cur.q.n = sm[46]; cur.q.seq = sm[47]; cur.u0 = sm[48]; cur.nu = sm[49];
-  cur.left = x1 - x0;
+  if (alone) {
+    const int src = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+#pragma unroll
+    for (int k = 0; k < 12; ++k) found[k] = __shfl_sync(0xffffffffu, found[k], src);
+  } else {
+    __syncthreads();
+    if (here) {
+#pragma unroll
+      for (int k = 0; k < 12; ++k) sm[40 + k] = found[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 12; ++k) found[k] = sm[40 + k];
+  }
+  if (found[0] < 0) return false;
+  cur.r = found[0]; cur.i = found[1]; cur.h = found[2]; cur.at = found[3]; cur.left = found[4] - found[3];
+  cur.q.start = found[5]; cur.q.n = found[6]; cur.q.seq = found[7]; cur.u0 = found[8]; cur.nu = found[9];
+  cur.item_first = pieces ? 0 : found[10];
+  sp.first = found[10];
+  sp.count = found[11];
   return true;
 }
 

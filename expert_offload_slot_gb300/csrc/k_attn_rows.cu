@@ -46,7 +46,7 @@ __global__ __launch_bounds__(NT, 1) void attn_rows_kernel(const __grid_constant_
   extern __shared__ uint8_t raw[];
   __shared__ int32_t sched[64];
   __shared__ __align__(8) uint64_t bars[NW * C::kStages];
-  __shared__ float sm_m[NW / 2][BM], sm_l[NW / 2][BM];
+  __shared__ float sm_m[NW / 2][BM], sm_l[NW / 2][BM], all_m[NW][8], all_l[NW][8];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   float* join = reinterpret_cast<float*>(smem + C::kRing);
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
@@ -237,66 +237,108 @@ __global__ __launch_bounds__(NT, 1) void attn_rows_kernel(const __grid_constant_
       l[hh] += __shfl_xor_sync(0xffffffffu, l[hh], 1);
       l[hh] += __shfl_xor_sync(0xffffffffu, l[hh], 2);
     }
-    // join the warps in a fixed tree: 4..7 into 0..3, 2..3 into 0..1, 1 into 0; rows 8..15 only if there are any
-    const int used = rows > 8 ? 2 : 1;
+    const bool whole = attn_piece(c) == c.nu;
+    if (rows <= 8) {
+      // All warps' results side by side, then a warp per row over them in order: one barrier.
 #pragma unroll
-    for (int half = NW / 2; half > 0; half >>= 1) {
-      if (wid >= half && wid < 2 * half) {
-        float* dst = join + (wid - half) * BM * D;
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          if (hh >= used) break;
-          const int row = g + 8 * hh;
-          if (t4 == 0) {
-            sm_m[wid - half][row] = m[hh];
-            sm_l[wid - half][row] = l[hh];
-          }
-#pragma unroll
-          for (int d = 0; d < ND; ++d)
-            *reinterpret_cast<float2*>(dst + row * D + ((d ^ g) * 8) % D + 2 * t4) = make_float2(o[d][2 * hh], o[d][2 * hh + 1]);
-        }
+      for (int d = 0; d < ND; ++d)
+        *reinterpret_cast<float2*>(join + (wid * 8 + g) * D + ((d ^ g) * 8) % D + 2 * t4) = make_float2(o[d][0], o[d][1]);
+      if (t4 == 0) {
+        all_m[wid][g] = m[0];
+        all_l[wid][g] = l[0];
       }
       __syncthreads();
-      if (wid < half) {
-        const float* src = join + wid * BM * D;
+      if (wid < rows) {
+        constexpr int COLS = D / 32;
+        float top = -INFINITY;
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          if (hh >= used) break;
-          const int row = g + 8 * hh;
-          const float m2 = sm_m[wid][row], l2 = sm_l[wid][row];
-          const float top = fmaxf(m[hh], m2), base = top == -INFINITY ? 0.f : top;
-          const float f1 = ex2(m[hh] - base), f2 = ex2(m2 - base);
-          m[hh] = top;
-          l[hh] = l[hh] * f1 + l2 * f2;
+        for (int w = 0; w < NW; ++w) top = fmaxf(top, all_m[w][wid]);
+        const float base = top == -INFINITY ? 0.f : top;
+        float sum = 0.f, x[COLS];
 #pragma unroll
-          for (int d = 0; d < ND; ++d) {
-            const float2 v = *reinterpret_cast<const float2*>(src + row * D + ((d ^ g) * 8) % D + 2 * t4);
-            o[d][2 * hh] = o[d][2 * hh] * f1 + v.x * f2;
-            o[d][2 * hh + 1] = o[d][2 * hh + 1] * f1 + v.y * f2;
-          }
+        for (int k = 0; k < COLS; ++k) x[k] = 0.f;
+        const int col = lane * COLS, at = ((col >> 3) ^ wid) * 8 + (col & 7);
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+          const float f = ex2(all_m[w][wid] - base);
+          sum += f * all_l[w][wid];
+          const float* src = join + (w * 8 + wid) * D + at;
+#pragma unroll
+          for (int k = 0; k < COLS; ++k) x[k] += f * src[k];
+        }
+        const int fr = c.i * BM + wid;
+        if (whole) {
+          const float inv = sum > 0.f ? 1.f / sum : 0.f;
+          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) +
+                               ((size_t)(c.q.start + a.token(fr)) * a.Hq + c.h * a.group + a.head_of(fr)) * D + col;
+#pragma unroll
+          for (int k = 0; k < COLS; k += 2) *reinterpret_cast<uint32_t*>(dst + k) = pack_bf16(x[k] * inv, x[k + 1] * inv);
+        } else {
+          const size_t slot = (size_t)attn_slot(c, blockIdx.x) * BM + wid;
+          if (lane == 0) a.part_ml[slot] = make_float2(top, sum);
+#pragma unroll
+          for (int k = 0; k < COLS; k += 2)
+            *reinterpret_cast<float2*>(a.part_o + slot * D + col + k) = make_float2(x[k], x[k + 1]);
         }
       }
-      if (half > 1) __syncthreads();
-    }
-    const bool whole = attn_piece(c) == c.nu;
-    if (wid == 0) {
+    } else {
+      // join the warps in a fixed tree: 4..7 into 0..3, 2..3 into 0..1, 1 into 0
 #pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        const int row = g + 8 * hh, f = c.i * BM + row;
-        if (row >= rows) continue;
-        if (whole) {
-          const float inv = l[hh] > 0.f ? 1.f / l[hh] : 0.f;
-          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) +
-                               ((size_t)(c.q.start + a.token(f)) * a.Hq + c.h * a.group + a.head_of(f)) * D + 2 * t4;
+      for (int half = NW / 2; half > 0; half >>= 1) {
+        if (wid >= half && wid < 2 * half) {
+          float* dst = join + (wid - half) * BM * D;
 #pragma unroll
-          for (int d = 0; d < ND; ++d)
-            *reinterpret_cast<uint32_t*>(dst + 8 * d) = pack_bf16(o[d][2 * hh] * inv, o[d][2 * hh + 1] * inv);
-        } else {
-          const size_t at = (size_t)attn_slot(c, blockIdx.x) * BM + row;
-          if (t4 == 0) a.part_ml[at] = make_float2(m[hh], l[hh]);
+          for (int hh = 0; hh < 2; ++hh) {
+            const int row = g + 8 * hh;
+            if (t4 == 0) {
+              sm_m[wid - half][row] = m[hh];
+              sm_l[wid - half][row] = l[hh];
+            }
 #pragma unroll
-          for (int d = 0; d < ND; ++d)
-            *reinterpret_cast<float2*>(a.part_o + at * D + 8 * d + 2 * t4) = make_float2(o[d][2 * hh], o[d][2 * hh + 1]);
+            for (int d = 0; d < ND; ++d)
+              *reinterpret_cast<float2*>(dst + row * D + ((d ^ g) * 8) % D + 2 * t4) = make_float2(o[d][2 * hh], o[d][2 * hh + 1]);
+          }
+        }
+        __syncthreads();
+        if (wid < half) {
+          const float* src = join + wid * BM * D;
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            const int row = g + 8 * hh;
+            const float m2 = sm_m[wid][row], l2 = sm_l[wid][row];
+            const float top = fmaxf(m[hh], m2), base = top == -INFINITY ? 0.f : top;
+            const float f1 = ex2(m[hh] - base), f2 = ex2(m2 - base);
+            m[hh] = top;
+            l[hh] = l[hh] * f1 + l2 * f2;
+#pragma unroll
+            for (int d = 0; d < ND; ++d) {
+              const float2 v = *reinterpret_cast<const float2*>(src + row * D + ((d ^ g) * 8) % D + 2 * t4);
+              o[d][2 * hh] = o[d][2 * hh] * f1 + v.x * f2;
+              o[d][2 * hh + 1] = o[d][2 * hh + 1] * f1 + v.y * f2;
+            }
+          }
+        }
+        if (half > 1) __syncthreads();
+      }
+      if (wid == 0) {
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          const int row = g + 8 * hh, f = c.i * BM + row;
+          if (row >= rows) continue;
+          if (whole) {
+            const float inv = l[hh] > 0.f ? 1.f / l[hh] : 0.f;
+            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) +
+                                 ((size_t)(c.q.start + a.token(f)) * a.Hq + c.h * a.group + a.head_of(f)) * D + 2 * t4;
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+              *reinterpret_cast<uint32_t*>(dst + 8 * d) = pack_bf16(o[d][2 * hh] * inv, o[d][2 * hh + 1] * inv);
+          } else {
+            const size_t at = (size_t)attn_slot(c, blockIdx.x) * BM + row;
+            if (t4 == 0) a.part_ml[at] = make_float2(m[hh], l[hh]);
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+              *reinterpret_cast<float2*>(a.part_o + at * D + 8 * d + 2 * t4) = make_float2(o[d][2 * hh], o[d][2 * hh + 1]);
+          }
         }
       }
     }
