@@ -38,7 +38,6 @@ struct AttnArgs {
   uint32_t* ticket;            // [2]
   int32_t* status;             // sticky
   uint32_t group_mul;          // token of a row without a division: (row * group_mul) >> group_shift,
-  int32_t out_32;              // out is 32-byte aligned
   int32_t group_shift;         // exact below 2^31 (group_mul = ceil(2^group_shift / group))
   __device__ __forceinline__ int token(int row) const { return (int)(((uint64_t)(uint32_t)row * group_mul) >> group_shift); }
   __device__ __forceinline__ int head_of(int row) const { return row - token(row) * group; }

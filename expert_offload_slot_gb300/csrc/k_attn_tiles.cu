@@ -44,8 +44,9 @@ struct TileCfg {
   static constexpr int kQ = 128 * D * 2;                 // this CTA's rows of a Q tile: [D / 64][128][128 bytes]
   static constexpr int kTile = 64 * D * 2;               // its half of a K tile [D / 64][64 keys][128 bytes]
                                                          // or of a V tile [128 keys][D bytes]
-  static constexpr int kStages = D == 128 ? 10 : 16;
-  static constexpr int kBytes = 2 * kQ + kStages * kTile + 1024;
+  static constexpr int kStages = D == 128 ? 8 : 16;
+  static constexpr int kOut = 8 * 32 * 128;              // a warp's rows on their way out, 64 columns at a time
+  static constexpr int kBytes = 2 * kQ + kStages * kTile + kOut + 1024;
 };
 
 // A call's work is divided in one of two ways, chosen from the lengths by every CTA alike.
@@ -208,11 +209,7 @@ void attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_cons
   const uint32_t sq = smem_addr(smem), ring = sq + 2 * C::kQ;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int rank = (int)pair_rank(), part = (int)blockIdx.x / 2;
-  grid_wait();
-  TileWork work;
-  TileCursor c;
-  work.list = items;
-  if (!tile_work(a, sched, smem, work, c)) return;             // the same answer in every thread of the pair
+  // What needs no input comes first: with the launch set up early it runs beside the previous kernel's end.
   if (tid == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       bar_init(full + s, 2);
@@ -231,10 +228,19 @@ void attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_cons
   }
   if (wid == 9) tmem_alloc(&tmem_slot, 512);
   tc_fence_before();
-  fence_async_smem();                                    // the scratch of tile_work becomes the loads' memory
   __syncthreads();
   pair_sync();                                           // the other CTA's barriers are ready, too
   tc_fence_after();
+  grid_wait();
+  TileWork work;
+  TileCursor c;
+  work.list = items;
+  if (!tile_work(a, sched, smem, work, c)) {             // the same answer in every thread of the pair
+    if (wid == 9) tmem_free(tmem_slot, 512);
+    return;
+  }
+  fence_async_smem();                                    // the scratch of tile_work becomes the loads' memory
+  __syncthreads();
   const uint32_t tmem = tmem_slot;
 
   bool alive = true;
@@ -517,30 +523,42 @@ void attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_cons
       const size_t part_slot = (size_t)attn_slot(c, part) * BM;
       float* part_dst = a.part_o + (part_slot + warp_rows) * D + lane * 4;
       const float inv = l > 0.f ? 1.f / l : 0.f;
-      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out);
-      if (row < rows) dst += ((size_t)(c.q.start + a.token(f)) * a.Hq + c.h * a.group + a.head_of(f)) * D;
-#pragma unroll 1
-      for (int d = 0; d < D; d += 32) {
-        float o[32];
+      auto out_row = [&](int r) {                        // of this CTA's part of the tile
+        const int token = a.token(f0 + r);
+        return static_cast<__nv_bfloat16*>(a.out) +
+               ((size_t)(c.q.start + token) * a.Hq + c.h * a.group + f0 + r - token * a.group) * D;
+      };
+      // A row per thread would touch 32 lines with every store; turned in shared memory, a store
+      // writes 128 bytes of each of four rows.
+      const uint32_t turn = sq + 2 * C::kQ + C::kStages * C::kTile + wid * (32 * 128);
+      auto send = [&](const uint32_t* w, int d) {        // 64 columns of the warp's rows from column d on
         __syncwarp();
-        tmem_ld32(o_addr + d, o);
-        if (row >= rows) continue;
+#pragma unroll
+        for (int ch = 0; ch < 8; ++ch)
+          *reinterpret_cast<uint4*>(smem + (turn - sq) + lane * 128 + ((ch ^ (lane & 7)) << 4)) =
+              make_uint4(w[4 * ch], w[4 * ch + 1], w[4 * ch + 2], w[4 * ch + 3]);
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int r = 4 * k + lane / 8, ch = lane % 8;
+          const uint4 v = *reinterpret_cast<const uint4*>(smem + (turn - sq) + r * 128 + ((ch ^ (r & 7)) << 4));
+          const int tr = (wid & 3) * 32 + r;
+          if (tr < rows) *reinterpret_cast<uint4*>(out_row(tr) + d + 8 * ch) = v;
+        }
+      };
+#pragma unroll 1
+      for (int d = 0; d < D; d += 64) {
+        float o[64];
+        __syncwarp();
+        tmem_ld64(o_addr + d, o);
         if (whole) {
+          uint32_t w[32];
 #pragma unroll
-          for (int i = 0; i < 32; i += 16) {
-            uint32_t w[8];
+          for (int i = 0; i < 32; ++i) w[i] = pack_bf16(o[2 * i] * inv, o[2 * i + 1] * inv);
+          send(w, d);
+        } else if (row < rows) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) w[k] = pack_bf16(o[i + 2 * k] * inv, o[i + 2 * k + 1] * inv);
-            if (a.out_32) {                              // a row per thread: whole 32-byte sectors, where aligned
-              store_32(dst + d + i, w);
-            } else {
-              *reinterpret_cast<uint4*>(dst + d + i) = make_uint4(w[0], w[1], w[2], w[3]);
-              *reinterpret_cast<uint4*>(dst + d + i + 8) = make_uint4(w[4], w[5], w[6], w[7]);
-            }
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; i += 4)
+          for (int i = 0; i < 64; i += 4)
             attn_store4(part_dst + (d + i) * 32, make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]));
         }
       }
@@ -557,8 +575,8 @@ void attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_cons
           last_flag[t] = last;
         }
         named_sync(1 + t, 128);
-        if (last_flag[t] && row < rows) {                // the last of the item's pieces to arrive joins these rows, in
-          __threadfence();                               // piece order
+        if (last_flag[t]) {                              // the last of the item's pieces to arrive joins these rows, in
+          __threadfence();                               // piece order (rows past the end as they come: not sent)
           auto slot = [&](int p) { return (size_t)(2 * (c0 + p) + (p == 0)) * BM; };
           const float2* ml = a.part_ml + f_off + row;
           float M = -INFINITY, sum = 0.f;
@@ -592,10 +610,10 @@ void attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_cons
                 o[4 * i + 3] += g * v[i].w;
               }
             }
+            uint32_t w[32];
 #pragma unroll
-            for (int i = 0; i < 64; i += 8)
-              *reinterpret_cast<uint4*>(dst + d + i) = make_uint4(pack_bf16(o[i], o[i + 1]), pack_bf16(o[i + 2], o[i + 3]),
-                                                                  pack_bf16(o[i + 4], o[i + 5]), pack_bf16(o[i + 6], o[i + 7]));
+            for (int i = 0; i < 32; ++i) w[i] = pack_bf16(o[2 * i], o[2 * i + 1]);
+            send(w, d);
           }
         }
       }
