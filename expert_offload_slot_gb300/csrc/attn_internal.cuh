@@ -16,8 +16,8 @@ moe_status set_last_error(moe_status st, const char* msg);   // text for moe_las
 
 constexpr int kAttnRowsTile = 16;     // query rows per item of the row kernel
 constexpr int kAttnTile = 512;        // and of the tile kernel, by a pair of CTAs
-constexpr int kAttnF32Tile = 32;       // of the fp32 kernel
-constexpr int kAttnF32Few = 8;         // and of the one for few rows
+constexpr int kAttnF32Tile = 64;      // of the fp32 kernel
+constexpr int kAttnF32Few = 8;        // and of the one for few rows
 
 struct AttnArgs {
   const void* q;               // [rows][q_stride] elements, heads contiguous

@@ -7,8 +7,13 @@
 //
 // One pass over the keys with the running maximum m and sum l of the softmax:
 // a tile's scores s raise m to m', and O and l are scaled by exp(m - m').
-// A CTA holds 32 query rows (all heads of a kv head's group together, so a key
-// read once serves the whole group) and walks its units of 32 keys.
+// A CTA holds 64 query rows (all heads of a kv head's group together, so that a key
+// read once serves the whole group) and walks its units of 32 keys.  A thread has
+// four rows with two keys' scores, then with D / 16 output columns, so that its 32
+// products need six (then three) reads of shared memory; two CTAs share an SM, so
+// that one's loads run beside the other's products.  With half the rows and one product
+// for each read of K and V a 512-token prompt (32 q heads) took 225 us; so it takes 92 us,
+// 23 TFLOP/s, and 200 tokens over 2000 keys 203 instead of 573 us, 31 TFLOP/s.  Shared memory's reads bound it.
 #include "attn_internal.cuh"
 #include "sm103.cuh"
 
@@ -18,125 +23,151 @@ namespace {
 constexpr int NT = 256, BM = kAttnF32Tile, BN = 32;
 
 template <int D>
-__global__ __launch_bounds__(NT) void attn_f32_kernel(const AttnArgs a) {
-  constexpr int LD = D + 4;                 // padded rows: eight rows' float4 reads hit 32 banks
+struct F32Cfg {
+  static constexpr int LD = D + 4, LP = BM + 4;       // padded rows: eight rows' float4 reads hit 32 banks
+  static constexpr int kBytes = (BM * LD + 2 * BN * LD + BN * LP) * 4;
+};
+
+template <int D>
+__global__ __launch_bounds__(NT, 2) void attn_f32_kernel(const AttnArgs a) {
+  using C = F32Cfg<D>;
+  constexpr int LD = C::LD, LP = C::LP, COLS = D / 16;
   extern __shared__ __align__(16) float smem[];
   float* sq = smem;                         // [BM][LD]
   float* sk = sq + BM * LD;                 // [BN][LD]
   float* sv = sk + BN * LD;                 // [BN][LD]
-  float* spr = sv + BN * LD;                // [BM][BN + 1]
-  __shared__ int32_t sched[128];
+  float* prob = sv + BN * LD;               // [BN][LP] probabilities, rows innermost
+  __shared__ int32_t sched[64];
   sm103::grid_wait();
   AttnSplit sp;
   AttnCursor c;
   if (!attn_find_range<BM, NT>(a, BN, 4, blockIdx.x, gridDim.x, sched, sp, c)) return;
-  const int tid = threadIdx.x, row = tid / 8, sub = tid % 8;
+  const int tid = threadIdx.x, tx = tid % 16, r0 = tid / 16 * 4;
   do {
     const int rows = min(BM, c.q.n * a.group - c.i * BM);
-    const int fr = c.i * BM + row;
-    const int pos = row < rows ? c.q.seq - c.q.n + a.token(fr) : -1;
-    const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
     const int first = a.token(c.i * BM), last = min(c.q.n - 1, a.token((c.i + 1) * BM - 1));
     const int tile_hi = c.q.seq - c.q.n + last + 1;
     const int tile_lo = a.window > 0 ? max(0, c.q.seq - c.q.n + first - a.window + 1) : 0;
+    int pos[4], lo[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      pos[i] = r0 + i < rows ? c.q.seq - c.q.n + a.token(c.i * BM + r0 + i) : -1;
+      lo[i] = a.window > 0 ? max(0, pos[i] - a.window + 1) : 0;
+    }
     __syncthreads();
     for (int e = tid * 4; e < BM * D; e += NT * 4) {
-      const int rr = e / D, d = e % D;
+      const int rr = e / D, d = e % D, f = c.i * BM + rr;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (rr < rows) {
-        const int f = c.i * BM + rr;
-        v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) +
-                                             (size_t)(c.q.start + a.token(f)) * a.q_stride +
+      if (rr < rows)
+        v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + (size_t)(c.q.start + a.token(f)) * a.q_stride +
                                              (size_t)(c.h * a.group + a.head_of(f)) * D + d);
-      }
       *reinterpret_cast<float4*>(sq + rr * LD + d) = v;
     }
-    float o[D / 8];
+    float o[4][COLS], m[4], l[4];
 #pragma unroll
-    for (int k = 0; k < D / 8; ++k) o[k] = 0.f;
-    float m = -INFINITY, l = 0.f;
+    for (int i = 0; i < 4; ++i) {
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+#pragma unroll
+      for (int k = 0; k < COLS; ++k) o[i][k] = 0.f;
+    }
     const int piece = attn_piece(c);
     for (int u = 0; u < piece; ++u) {
       const int key0 = (c.u0 + c.at + u) * BN;
       __syncthreads();
-      for (int e = tid * 4; e < BN * D; e += NT * 4) {
-        const int kr = e / D, d = e % D, key = key0 + kr;
-        float4 kv = make_float4(0.f, 0.f, 0.f, 0.f), vv = kv;
+      constexpr int LANES = D / 4;
+#pragma unroll 4
+      for (int kr = tid / LANES; kr < BN; kr += NT / LANES) {
+        const int key = key0 + kr, d = tid % LANES * 4;
+        size_t at = 0;
+        uint32_t bytes = 0;
         if (key >= tile_lo && key < tile_hi) {   // what no row of the tile sees may hold anything: it counts as zero
           const int page = a.table[(size_t)c.r * a.table_stride + (key >> a.page_log2)];
           if ((uint32_t)page < (uint32_t)a.num_pages) {
-            const size_t at = ((((size_t)page * a.Hkv + c.h) << a.page_log2) + (key & (a.page - 1))) * D + d;
-            kv = *reinterpret_cast<const float4*>(static_cast<const float*>(a.k_cache) + at);
-            vv = *reinterpret_cast<const float4*>(static_cast<const float*>(a.v_cache) + at);
+            at = ((((size_t)page * a.Hkv + c.h) << a.page_log2) + (key & (a.page - 1))) * D + d;
+            bytes = 16;
           } else {
             attn_status(a.status, MOE_ERR_BOUNDS);
           }
         }
-        *reinterpret_cast<float4*>(sk + kr * LD + d) = kv;
-        *reinterpret_cast<float4*>(sv + kr * LD + d) = vv;
+        const uint32_t dst = sm103::smem_addr(sk + kr * LD + d);
+        sm103::cp_async16(dst, static_cast<const float*>(a.k_cache) + at, bytes);
+        sm103::cp_async16(dst + BN * LD * 4, static_cast<const float*>(a.v_cache) + at, bytes);
       }
+      sm103::cp_async_wait();
       __syncthreads();
-      float s[4] = {0.f, 0.f, 0.f, 0.f};
+      float s[4][2] = {};
 #pragma unroll 4
       for (int d = 0; d < D; d += 4) {
-        const float4 x = *reinterpret_cast<const float4*>(sq + row * LD + d);
+        const float4 k0 = *reinterpret_cast<const float4*>(sk + tx * LD + d);
+        const float4 k1 = *reinterpret_cast<const float4*>(sk + (tx + 16) * LD + d);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float4 y = *reinterpret_cast<const float4*>(sk + (sub + 8 * j) * LD + d);
-          s[j] += x.x * y.x + x.y * y.y + x.z * y.z + x.w * y.w;
+        for (int i = 0; i < 4; ++i) {
+          const float4 x = *reinterpret_cast<const float4*>(sq + (r0 + i) * LD + d);
+          s[i][0] += x.x * k0.x + x.y * k0.y + x.z * k0.z + x.w * k0.w;
+          s[i][1] += x.x * k1.x + x.y * k1.y + x.z * k1.z + x.w * k1.w;
         }
       }
-      float top = -INFINITY;
+      float p[2][4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int key = key0 + sub + 8 * j;
-        s[j] = key >= lo && key <= pos ? s[j] * a.scale : -INFINITY;
-        top = fmaxf(top, s[j]);
+      for (int i = 0; i < 4; ++i) {
+        float top = m[i];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int key = key0 + tx + 16 * j;
+          s[i][j] = key >= lo[i] && key <= pos[i] ? s[i][j] * a.scale : -INFINITY;
+          top = fmaxf(top, s[i][j]);
+        }
+#pragma unroll
+        for (int k = 8; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+        const float base = top == -INFINITY ? 0.f : top;   // no key yet: every exponential is 0, not NaN
+        const float f = expf(m[i] - base);
+        m[i] = top;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) p[j][i] = expf(s[i][j] - base);
+        l[i] = l[i] * f + (p[0][i] + p[1][i]);             // this thread's keys; the row's 16 threads sum at the end
+#pragma unroll
+        for (int k = 0; k < COLS; ++k) o[i][k] *= f;
       }
+      // a row's probabilities are written and read by the same 16 lanes
 #pragma unroll
-      for (int k = 4; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-      const float mn = fmaxf(m, top);
-      const float base = mn == -INFINITY ? 0.f : mn;     // no key yet: every exponential is 0, not NaN
-      const float f = expf(m - base);
-      float sum = 0.f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float p = expf(s[j] - base);
-        spr[row * (BN + 1) + sub + 8 * j] = p;
-        sum += p;
-      }
-#pragma unroll
-      for (int k = 4; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
-      l = l * f + sum;
-      m = mn;
-#pragma unroll
-      for (int k = 0; k < D / 8; ++k) o[k] *= f;
+      for (int j = 0; j < 2; ++j)
+        *reinterpret_cast<float4*>(prob + (tx + 16 * j) * LP + r0) = make_float4(p[j][0], p[j][1], p[j][2], p[j][3]);
       __syncwarp();
 #pragma unroll 4
-      for (int j = 0; j < BN; ++j) {
-        const float p = spr[row * (BN + 1) + j];
+      for (int k = 0; k < BN; ++k) {
+        const float4 w = *reinterpret_cast<const float4*>(prob + k * LP + r0);
 #pragma unroll
-        for (int k = 0; k < D / 32; ++k) {
-          const float4 v = *reinterpret_cast<const float4*>(sv + j * LD + sub * 4 + 32 * k);
-          o[4 * k] += p * v.x; o[4 * k + 1] += p * v.y; o[4 * k + 2] += p * v.z; o[4 * k + 3] += p * v.w;
+        for (int j = 0; j < COLS / 4; ++j) {
+          const float4 v = *reinterpret_cast<const float4*>(sv + k * LD + tx * 4 + 64 * j);
+          const float pw[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            o[i][4 * j] += pw[i] * v.x; o[i][4 * j + 1] += pw[i] * v.y;
+            o[i][4 * j + 2] += pw[i] * v.z; o[i][4 * j + 3] += pw[i] * v.w;
+          }
         }
       }
     }
-    if (piece == c.nu) {
-      if (row < rows) {
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        float* dst = static_cast<float*>(a.out) +
-                     ((size_t)(c.q.start + a.token(fr)) * a.Hq + c.h * a.group + a.head_of(fr)) * D + sub * 4;
+    const bool whole = piece == c.nu;
 #pragma unroll
-        for (int k = 0; k < D / 32; ++k)
-          attn_store4(dst + 32 * k, make_float4(o[4 * k] * inv, o[4 * k + 1] * inv, o[4 * k + 2] * inv, o[4 * k + 3] * inv));
-      }
-    } else {
-      const size_t at = (size_t)attn_slot(c, blockIdx.x) * BM + row;
-      if (sub == 0) a.part_ml[at] = make_float2(m, l);
+    for (int i = 0; i < 4; ++i) {
 #pragma unroll
-      for (int k = 0; k < D / 32; ++k)
-        attn_store4(a.part_o + at * D + sub * 4 + 32 * k, make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]));
+      for (int k = 8; k > 0; k >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], k);
+      if (r0 + i >= rows) continue;
+      const int fr = c.i * BM + r0 + i;
+      const float inv = whole ? (l[i] > 0.f ? 1.f / l[i] : 0.f) : 1.f;
+      const size_t slot = (size_t)attn_slot(c, blockIdx.x) * BM + r0 + i;
+      float* dst = whole ? static_cast<float*>(a.out) +
+                               ((size_t)(c.q.start + a.token(fr)) * a.Hq + c.h * a.group + a.head_of(fr)) * D
+                         : a.part_o + slot * D;
+      if (!whole && tx == 0) a.part_ml[slot] = make_float2(m[i], l[i]);
+#pragma unroll
+      for (int j = 0; j < COLS / 4; ++j)
+        attn_store4(dst + tx * 4 + 64 * j, make_float4(o[i][4 * j] * inv, o[i][4 * j + 1] * inv, o[i][4 * j + 2] * inv,
+                                                       o[i][4 * j + 3] * inv));
+    }
+    if (!whole) {
       int c0, n;
       if (attn_arrive(a, sp, c, sched, c0, n)) attn_join<float, D, BM, NT, false>(a, c, c0, n);
     }
@@ -144,8 +175,8 @@ __global__ __launch_bounds__(NT) void attn_f32_kernel(const AttnArgs a) {
 }
 
 // ------------------------------------------------- few query rows per request (decode)
-// Eight query rows a CTA: the kernel above would compute 32 rows for every key (16 requests of 5000
-// keys, 8 kv heads: 707 us; this one 185 us, 3.5 TB/s).  Tiles of 32 keys come by 16-byte asynchronous copies into
+// Eight query rows a CTA: the kernel above computes 64 for every key (16 requests of 5000 keys, 8 kv
+// heads: 707 us with 32; this one 185 us, 3.5 TB/s).  Tiles of 32 keys come by 16-byte asynchronous copies into
 // three stages; two CTAs share an SM, so that the copies and the phases between barriers of one run
 // beside the other's.  Scores: a lane has one key, a warp an eighth of D, so that K is read once from
 // shared memory and q by broadcast; softmax: a warp per row; output: a thread per column and group
@@ -323,21 +354,18 @@ __global__ __launch_bounds__(NT, 2) void attn_f32_few_kernel(const AttnArgs a) {
 }
 
 template <int D>
-constexpr int f32_bytes() {
-  return ((BM + 2 * BN) * (D + 4) + BM * (BN + 1)) * 4;
-}
-
-template <int D>
 cudaError_t launch(const AttnArgs& a, int grid, cudaStream_t s) {
-  // up to two tiles of eight rows the few-row kernel is ahead although it reads the keys once for each
-  if ((int64_t)a.max_new * a.group <= 2 * FM)
+  // Up to four tiles of eight rows the few-row kernel is ahead although it reads the keys once for each:
+  // 8 requests of 3000 keys, 8 kv heads, 16, 24 and 32 rows per kv head: 113, 168 and 218 us against the
+  // other's 228 to 230 (a fifth tile would add 55 us); 2 requests of 400 keys, 32 rows: 19 us against 25.
+  if ((int64_t)a.max_new * a.group <= 4 * FM)
     return sm103::launch(attn_f32_few_kernel<D>, grid, NT, FewCfg<D>::kBytes, s, a);
-  return sm103::launch(attn_f32_kernel<D>, grid, NT, f32_bytes<D>(), s, a);
+  return sm103::launch(attn_f32_kernel<D>, grid, NT, F32Cfg<D>::kBytes, s, a);
 }
 
 template <int D>
 cudaError_t prepare() {
-  const cudaError_t e = cudaFuncSetAttribute(attn_f32_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, f32_bytes<D>());
+  const cudaError_t e = cudaFuncSetAttribute(attn_f32_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, F32Cfg<D>::kBytes);
   if (e != cudaSuccess) return e;
   return cudaFuncSetAttribute(attn_f32_few_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, FewCfg<D>::kBytes);
 }
