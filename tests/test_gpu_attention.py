@@ -263,6 +263,61 @@ def test_attention_prefill_of_many_rows():
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("count", [31, 33, 260, 500, 1024])
+@pytest.mark.parametrize("most", [1, 5, 60])
+def test_attention_of_many_requests(dtype, count, most):
+    rng = np.random.default_rng(count + most)
+    new = rng.integers(0, most + 1, count)
+    new[count // 2], new[-1] = most, 0
+    if most > 1:                                           # most requests add one token or none
+        new[rng.random(count) < 0.8] = 1
+        new[rng.random(count) < 0.1] = 0
+        new[0] = most
+    ctx = rng.integers(0, 40, count)
+    ctx[rng.integers(0, count, 3)] = 500
+    check_attention(Step(ctx.tolist(), new.tolist(), dtype, 4, 2, 64, pad=1))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("new", [2, 3, 4, 5, 63, 64, 65])
+@pytest.mark.parametrize("window", [0, 37])
+def test_attention_of_row_tiles_full_and_not(dtype, new, window):
+    check_attention(Step([333, 4], [new, 1], dtype, 8, 1, window=window))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_offsets_past_32_bits(dtype):
+    # pages of 2 heads x 16 x 128 elements: 2^32 elements lie below page 2^20
+    s = Step([100, 7], [1, 40], dtype)
+    far = (1 << 20) + 9
+    need = torch.unique(s.table[(s.table < s.pages)])
+    kc, vc = (torch.empty(far + s.pages, s.hkv, s.page, s.dim, device="cuda", dtype=s.dtype) for _ in range(2))
+    gen = torch.Generator("cuda").manual_seed(4)
+    near = s.cache(gen)
+    for c, n in zip((kc, vc), near):
+        c[far:] = n
+    moved = torch.where(s.table < s.pages, s.table + far, s.table)
+    assert need.numel() and kc.numel() > 1 << 32
+    q = torch.randn(s.rows, s.hq, s.dim, generator=gen, device="cuda").to(s.dtype)
+    for start, seq, new, table, rows in ((s.start, s.seq, 40, moved, slice(0, None)),                       # a chunk
+                                         (ints([0, 1]), s.seq[:1].contiguous(), 1, moved[:1].contiguous(), slice(0, 1))):
+        out, ref = torch.zeros_like(q), torch.zeros_like(q)
+        s.handle.forward(q, start, seq, new, kc, vc, table, out)
+        s.handle.forward(q, start, seq, new, *near, s.table[:len(seq)].contiguous(), ref)
+        assert torch.equal(out[rows], ref[rows]) and ref[rows].any()
+    # and the write of new rows there
+    qkv = torch.randn(s.rows, (s.hq + 2 * s.hkv) * s.dim, generator=gen, device="cuda").to(s.dtype)
+    rope = torch.randn(200, s.dim, generator=gen, device="cuda")
+    outs = []
+    for c, slot in (((kc, vc), s.slot + far * s.page), (near, s.slot)):
+        q2 = torch.empty_like(q)
+        s.handle.qkv(qkv, None, None, rope, s.pos, slot, q2, *c)
+        outs.append(q2)
+    assert torch.equal(*outs) and torch.equal(kc[far:], near[0]) and torch.equal(vc[far:], near[1])
+    assert s.handle.status() == moe.MOE_OK
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_rows_before_the_first_key_are_zero(dtype):
     s = Step([0], [6], dtype)
     gen = torch.Generator("cuda").manual_seed(1)
