@@ -44,15 +44,6 @@ moe_status launched(cudaError_t e, const char* what) {
   return e == cudaSuccess ? MOE_OK : fail(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-// floor(n / d) as (n * mul) >> shift for n below 2^31: mul = ceil(2^(31 + l) / d) with 2^l >= d; what
-// that adds to n / d is below n / 2^(31 + l) <= 1 / d, too little to reach the next integer.
-void divider(uint32_t d, uint32_t& mul, int32_t& shift) {
-  int l = 0;
-  while ((1u << l) < d) ++l;
-  shift = 31 + l;
-  mul = (uint32_t)(((1ull << shift) + d - 1) / d);
-}
-
 bool misaligned(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
 
 moe_status check_config(const moe_attn_config* c) {
@@ -148,6 +139,7 @@ MOE_API moe_status moe_attn_create(const moe_attn_config* cfg, int device, moe_a
   if (e != cudaSuccess) return launched(e, "cudaSetDevice");
   e = cfg->dtype == MOE_F32 ? prepare_attn_f32(cfg->head_dim) : prepare_attn_rows(cfg->head_dim);
   if (e == cudaSuccess && cfg->dtype == MOE_BF16) e = prepare_attn_tiles(cfg->head_dim);
+  if (e == cudaSuccess) e = prepare_attn_qkv(cfg->dtype, cfg->head_dim);
   if (e != cudaSuccess) return launched(e, "preparing the attention kernels");
   moe_attn* A = new (std::nothrow) moe_attn;
   if (!A) return fail(MOE_ERR_OOM, "host allocation failed");
@@ -266,8 +258,7 @@ MOE_API moe_status moe_attn_qkv(moe_attn* A, const void* qkv, int64_t qkv_stride
   a.page_log2 = A->page_log2; a.rotary = c.rotary_dim; a.pairs = c.rotary_style == MOE_ROTARY_PAIRS; a.rope_len = rope_len;
   a.eps = c.norm_eps;
   a.heads = a.Hq + 2 * a.Hkv;
-  divider(a.heads, a.heads_mul, a.heads_shift);
-  return launched(launch_attn_qkv(a, c.dtype, c.head_dim, static_cast<cudaStream_t>(stream)), "moe_attn_qkv");
+  return launched(launch_attn_qkv(a, c.dtype, c.head_dim, A->sms, static_cast<cudaStream_t>(stream)), "moe_attn_qkv");
 }
 
 MOE_API moe_status moe_attn_forward(moe_attn* A, const void* q, int64_t q_stride, int32_t rows, const int32_t* row_start,

@@ -19,6 +19,15 @@ constexpr int kAttnTile = 512;        // and of the tile kernel, by a pair of CT
 constexpr int kAttnF32Tile = 64;      // of the fp32 kernel
 constexpr int kAttnF32Few = 8;        // and of the one for few rows
 
+// floor(n / d) as (n * mul) >> shift for n below 2^31: mul = ceil(2^(31 + l) / d) with 2^l >= d; what
+// that adds to n / d is below n / 2^(31 + l) <= 1 / d, too little to reach the next integer.
+inline void divider(uint32_t d, uint32_t& mul, int32_t& shift) {
+  int l = 0;
+  while ((1u << l) < d) ++l;
+  shift = 31 + l;
+  mul = (uint32_t)(((1ull << shift) + d - 1) / d);
+}
+
 struct AttnArgs {
   const void* q;               // [rows][q_stride] elements, heads contiguous
   void* out;                   // [rows][Hq][D]
@@ -434,10 +443,12 @@ struct QkvArgs {
   int32_t* status;
   int64_t qkv_stride, num_slots;
   int32_t rows, heads, Hq, Hkv, page_log2, rotary, pairs, rope_len;
-  uint32_t heads_mul;          // row of a (row, head) unit without a division, as AttnArgs::group_mul
-  int32_t heads_shift;
+  int32_t chunks, chunk_heads; // pieces of a row, and heads in each but the last
+  uint32_t unit_mul;           // row of a (row, head) or (row, piece) unit without a division, as AttnArgs::group_mul
+  int32_t unit_shift;
   float eps;
 };
-cudaError_t launch_attn_qkv(const QkvArgs& a, int dtype, int D, cudaStream_t s);
+cudaError_t prepare_attn_qkv(int dtype, int D);
+cudaError_t launch_attn_qkv(const QkvArgs& a, int dtype, int D, int sms, cudaStream_t s);
 
 }  // namespace moeslot
