@@ -21,6 +21,12 @@
 // collected instead and the first CTA does the rest on its sorted list.  A bin with
 // more tokens than the list holds (equal logits) is resolved by a radix descent over
 // the ordered bits of x and a count of the ties in index order.
+//
+// What bounds it: few CTAs walk a row (48 rows of 100277 fp32 logits: 240 CTAs, 40000 logits
+// an SM), so a pass over all logits costs 3 to 8 us by its instructions, and each cut two or
+// three exchanges in the cluster of about 3 us; HBM's part is 4 us.  48 such rows, read from
+// HBM: greedy 11.8 us, temperature alone 16.9, top-k of 50 20.1 and of 1000 31.5, top-p of 0.9
+// 38.1, of 1000 with top-p and min-p 46.9.  One row of 131072 bf16 logits: 4.8, 7.5, 12, 20, 24.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -38,7 +44,7 @@ namespace {
 namespace cg = cooperative_groups;
 typedef unsigned long long u64;
 
-constexpr int NT = 512, NWARP = NT / 32, PAR = 4;   // PAR: logits a thread weighs at once
+constexpr int NT = 512, NWARP = NT / 32;
 constexpr int DIGIT = 2, BINS = 1 << DIGIT;    // bits a pass of the radix descent
 constexpr int kMaxCluster = 8;
 constexpr int kList = 1024;                    // tokens that are collected and sorted
@@ -58,8 +64,8 @@ struct Exchange {                              // what a CTA shows its cluster; 
   int32_t first;
 };
 
-struct Cut {                                   // kept: key above it, or equal and index not above it
-  uint32_t key;
+struct Cut {                                   // kept: logits above it, and of the equal ones those up to an index
+  float x;
   int32_t index;
 };
 
@@ -72,25 +78,46 @@ __device__ __forceinline__ uint32_t key_of(float x) {
   const uint32_t u = __float_as_uint(x);
   return (u >> 31) ? ~u : u | 0x80000000u;
 }
-// z / T and the weight.  The quotient is the correctly rounded one: with r = 1/T correctly
-// rounded, a quotient within one unit in the last place becomes the rounded one by one more step
-// q + (z - q T) r in fused arithmetic (Markstein), and the first step makes it that close.  T in
-// [1e-30, 1e30], so that r has all its bits.
+// The weight of a logit: floor(2^40 e), e = 2^((x - best) log2(e) / T).  log2(e) / T is held in two
+// floats, so the exponent is off by the roundings of x - best and of the product alone.  T in
+// [1e-30, 1e30], best finite.
 struct Softener {
-  float best, temp, inv;
-  __device__ __forceinline__ Softener(float b, float t) : best(b), temp(t), inv(1.f / t) {}
-  __device__ __forceinline__ u64 weight(float x) const {
-    if (x == best) return 1ull << 40;
-    const float d = x - best;
-    float z = d * inv;
-    z = fmaf(fmaf(-z, temp, d), inv, z);
-    z = fmaf(fmaf(-z, temp, d), inv, z);
-    const float e = expf(z) * 1099511627776.f;
-    if (!(e >= 1.f)) return 0;                 // also the NaN of an infinite d
-    // the integer part from the bits: 64-bit conversions run at a small part of the integer rate
-    const uint32_t bits = __float_as_uint(e), m = (bits & 0x7fffffu) | 0x800000u;
-    return ((u64)m << 17) >> (167 - (int)(bits >> 23));      // e = m 2^(exponent - 150), at most 2^40
+  float best, hi, lo, least;
+  __device__ __forceinline__ Softener(float b, float temp) : best(b), least(-30.f * temp) {
+    constexpr double l2e = 1.4426950408889634074;
+    constexpr float l2e_hi = (float)l2e, l2e_lo = (float)(l2e - (double)l2e_hi);
+    hi = l2e_hi / temp;
+    lo = (fmaf(-hi, temp, l2e_hi) + l2e_lo) / temp;
   }
+  __device__ __forceinline__ float power(float x) const {
+    const float d = fmaxf(x - best, least);      // 30 T below the maximum nothing is left of 2^40
+    return sm103::ex2(fmaf(d, hi, d * lo));
+  }
+};
+// floor(2^40 e) of e in [0, 1] as `high` 2^20 + `low`: the sum with 2^23, rounded towards zero, has the
+// integer part in its lowest bits (64-bit conversions run at a small part of the rate).  Both come
+// with the bits of 2^23 on top.
+constexpr uint32_t kMagic = 0x4b000000u;
+__device__ __forceinline__ void fixed(float e, uint32_t& high, uint32_t& low) {
+  const float h = __fmaf_rz(e, 1048576.f, 8388608.f), l = fmaf(e, 1048576.f, 8388608.f - h);
+  high = __float_as_uint(h);
+  low = __float_as_uint(__fmaf_rz(l, 1048576.f, 8388608.f));
+}
+__device__ __forceinline__ u64 weight_of(float e) {
+  uint32_t h, l;
+  fixed(e, h, l);
+  return ((u64)(h - kMagic) << 20) + (l - kMagic);
+}
+// A sum of weights, up to 4000 of them: the two parts apart.
+struct Mass {
+  uint32_t high = 0, low = 0;
+  __device__ __forceinline__ void add(float e) {
+    uint32_t h, l;
+    fixed(e, h, l);
+    high += h - kMagic;
+    low += l - kMagic;
+  }
+  __device__ __forceinline__ u64 sum() const { return ((u64)high << 20) + low; }
 };
 __device__ __forceinline__ u64 warp_add(u64 v) {
 #pragma unroll
@@ -225,6 +252,13 @@ __global__ __launch_bounds__(NT, 2) void sample_kernel(const SampleArgs a) {
     return;
   }
 
+  float mine = mine_best;
+  if (best == INFINITY) {                                        // infinite ones share all mass: as zeros above nothing
+    for (int i = tid; i < n; i += NT) xs[i] = (float)xs[i] == INFINITY ? (T)0.f : (T)-INFINITY;
+    mine = mine_best == INFINITY ? 0.f : -INFINITY;
+    best = 0.f;
+    __syncthreads();
+  }
   const Softener soft(best, temp);
   // The cluster's sums over the threads' counters, into t_mass and t_count.
   auto add_up = [&]() {
@@ -288,16 +322,17 @@ __global__ __launch_bounds__(NT, 2) void sample_kernel(const SampleArgs a) {
   // Walks this CTA's logits, a vector at a time: f(values, index of the first).
   constexpr int V = kVec<T>;
   auto each = [&](auto&& f) {
-    for (int v = tid; v < (n + V - 1) / V; v += NT) {
+    const int nv = (n + V - 1) / V;
+    for (int v = tid; v - lane < nv; v += NT) {                  // whole warps; past the end -inf
       float x[V];
-      unpack(reinterpret_cast<const uint4*>(xs)[v], x);
+#pragma unroll
+      for (int j = 0; j < V; ++j) x[j] = -INFINITY;
+      if (v < nv) unpack(reinterpret_cast<const uint4*>(xs)[v], x);
       f(x, i0 + v * V);
     }
   };
   const float to_q = 16777216.f / 28.f / temp;                   // d in [0, 28 T) to [0, 2^24)
-  auto q_of = [&](float x) -> uint32_t {                          // a NaN (infinities) goes to the end
-    return x == best ? 0u : (uint32_t)fminf((best - x) * to_q, 16777216.f);
-  };
+  auto q_of = [&](float x) -> uint32_t { return (uint32_t)fminf((best - x) * to_q, 16777216.f); };
 
   // Inclusive sum over the threads; every thread gets the total.
   auto scan = [&](u64 v, u64& total) -> u64 {
@@ -414,16 +449,14 @@ __global__ __launch_bounds__(NT, 2) void sample_kernel(const SampleArgs a) {
   auto key_in = [](u64 item) -> uint32_t { return ~(uint32_t)(item >> 32); };
   auto x_of = [](uint32_t key) -> float { return __uint_as_float((key >> 31) ? key & 0x7fffffffu : ~key); };
 
-  // A logit below this is in no bin up to `to` (with room for rounding; a NaN, from an infinite
-  // maximum, bounds nothing).
+  // A logit below this is in no bin up to `to` (with room for rounding).
   auto floor_of = [&](uint32_t to, int shift) {
     return best - (float)((to + 1) << shift) / to_q * 1.0001f - 1e-6f * fabsf(best);
   };
 
-  Cut cut = {0, 0x7fffffff};                                     // everything
+  Cut cut = {-INFINITY, 0x7fffffff};                             // everything
   constexpr int EACH = kList / NT;                               // list entries of a thread
-  bool cuts_any = false;
-  auto passes = [&](uint32_t key, int i) { return !cuts_any || key > cut.key || (key == cut.key && i <= cut.index); };
+  auto passes = [&](float x, int i) { return x > cut.x || (x == cut.x && i <= cut.index); };
   // Collects the tokens of bins [from, to], those that pass the cut, and sorts them into `all` (in the
   // first CTA only, or in every one): their number, or -1 when they are too many.
   auto collect = [&](int shift, uint32_t from, uint32_t to, bool leader) -> int {
@@ -441,7 +474,7 @@ __global__ __launch_bounds__(NT, 2) void sample_kernel(const SampleArgs a) {
       for (int j = 0; j < V; ++j) {
         if (x[j] < floor || x[j] > roof) continue;
         const uint32_t q = q_of(x[j]), bin = q >> shift, key = key_of(x[j]);
-        if (bin >= from && bin <= to && q < 16777216u && passes(key, i + j)) {
+        if (bin >= from && bin <= to && q < 16777216u && passes(x[j], i + j)) {
           const int at = atomicAdd(&list_n, 1);
           if (at < kList) own[at] = (u64)(~key) << 32 | (uint32_t)(i + j);
         }
@@ -476,7 +509,8 @@ __global__ __launch_bounds__(NT, 2) void sample_kernel(const SampleArgs a) {
   };
 
   const bool cut_p = top_p < 1.f;
-  const u64 least = min_p > 0.f ? (u64)ceilf(fminf(min_p, 1.f) * 1099511627776.f) : 0ull;   // exact: a scaling by 2^40
+  const float scale40 = 1099511627776.f;
+  const float least = min_p > 0.f ? ceilf(fminf(min_p, 1.f) * scale40) / scale40 : 0.f;   // exact: scalings by 2^40
   u64 kept_mass = 0;
   for (int what = 0; what < 2; ++what) {                         // 0: top-k by count, 1: top-p by mass
     u64 limit = 0, above = 0, above_mass = 0, total;
@@ -490,7 +524,7 @@ __global__ __launch_bounds__(NT, 2) void sample_kernel(const SampleArgs a) {
       int count = -1, bound = kCountBins - 1;
       const int64_t threads = CS * NT;
       if (2 * (int64_t)top_k <= threads) {
-        const uint32_t q = q_of(mine_best);
+        const uint32_t q = q_of(mine);
         if (q < 16777216u) atomicAdd(hist + (q >> kCountShift), 1u);
         if (find_bin(false, 0, total, [&](u64) { return limit; })) {
           bound = s_bin;
@@ -520,9 +554,11 @@ __global__ __launch_bounds__(NT, 2) void sample_kernel(const SampleArgs a) {
         if (rank != 0) return;
         count = min(count, top_k);
         u64 w[EACH], sum = 0;                                    // consecutive tokens a thread
+        float e[EACH];
 #pragma unroll
         for (int j = 0; j < EACH; ++j) {
-          w[j] = EACH * tid + j < count ? soft.weight(x_of(key_in(all[EACH * tid + j]))) : 0;
+          e[j] = EACH * tid + j < count ? soft.power(x_of(key_in(all[EACH * tid + j]))) : 0.f;
+          w[j] = weight_of(e[j]);
           sum += w[j];
         }
         u64 run = scan(sum, total) - sum;
@@ -539,7 +575,7 @@ __global__ __launch_bounds__(NT, 2) void sample_kernel(const SampleArgs a) {
         int kept = 0;                                            // the kept ones are the first of the list
 #pragma unroll
         for (int j = 0; j < EACH; ++j) {
-          if (w[j] && w[j] >= least && run < limit) ++kept;
+          if (w[j] && e[j] >= least && run < limit) ++kept;
           run += w[j];
           sums[EACH * tid + j] = run;
         }
@@ -574,29 +610,41 @@ __global__ __launch_bounds__(NT, 2) void sample_kernel(const SampleArgs a) {
     } else {
       // Bins for the tokens up to kHead T below the maximum; the mass of the others in one sum, unless
       // the cut turns out to lie among them.
+      // A warp's atomic takes as long for one logit as for 32, and few are near the maximum: each thread
+      // queues its own.
       uint32_t* hi = hist + kMassBins;
-      uint32_t reach = (uint32_t)(16777216.f / 28.f * kHead);
+      constexpr int kQueue = 3 * kList * 2 / NT;
+      float* queue = reinterpret_cast<float*>(own) + tid;
+      int queued = 0;
+      auto to_bins = [&]() {
+        for (int k = 0; __any_sync(0xffffffffu, k < queued); ++k) {
+          if (k >= queued) continue;
+          const float x = queue[k * NT];
+          const uint32_t b = min(q_of(x), 16777215u) >> kMassShift;
+          const u64 w = weight_of(soft.power(x));
+          const uint32_t low = (uint32_t)w;
+          const uint32_t old = atomicAdd(hist + b, low);         // a 64-bit sum in two words: the carry is seen here
+          const uint32_t up = (uint32_t)(w >> 32) + (old + low < old ? 1u : 0u);
+          if (up) atomicAdd(hi + b, up);
+        }
+        queued = 0;
+      };
+      float edge = best - kHead * temp;
       for (;;) {
-        u64 rest = 0;
+        Mass rest;
         each([&](const float (&x)[V], int i) {
-          u64 w[V];
-#pragma unroll
-          for (int j = 0; j < V; ++j) w[j] = passes(key_of(x[j]), i + j) ? soft.weight(x[j]) : 0;
 #pragma unroll
           for (int j = 0; j < V; ++j) {
-            const uint32_t q = min(q_of(x[j]), 16777215u);
-            if (q >= reach) {
-              rest += w[j];
-            } else if (w[j]) {
-              const uint32_t b = q >> kMassShift, low = (uint32_t)w[j];
-              const uint32_t old = atomicAdd(hist + b, low);     // a 64-bit sum in two words: the carry is seen here
-              const uint32_t up = (uint32_t)(w[j] >> 32) + (old + low < old ? 1u : 0u);
-              if (up) atomicAdd(hi + b, up);
-            }
+            const bool kept = passes(x[j], i + j), near = kept && x[j] > edge;
+            const float e = soft.power(x[j]);
+            rest.add(kept && !near ? e : 0.f);
+            if (near) queue[queued++ * NT] = x[j];
           }
+          if (__any_sync(0xffffffffu, queued > kQueue - V)) to_bins();
         });
+        to_bins();
         u64 sum;
-        scan(rest, sum);
+        scan(rest.sum(), sum);
         const bool found = find_bin(true, sum, kept_mass, [&](u64 all_mass) -> u64 {
           if (tid == 0) {                                        // one thread: fp64 is slow here
             const double goal = ceil((double)fmaxf(top_p, 0.f) * (double)all_mass);
@@ -606,8 +654,8 @@ __global__ __launch_bounds__(NT, 2) void sample_kernel(const SampleArgs a) {
           return s_kept;
         });
         limit = s_kept;
-        if (found || reach == 16777216u) break;
-        reach = 16777216u;
+        if (found || edge == -INFINITY) break;
+        edge = -INFINITY;
         clear_hist();
       }
       above_mass = s_above;
@@ -617,17 +665,16 @@ __global__ __launch_bounds__(NT, 2) void sample_kernel(const SampleArgs a) {
       u64 v[EACH], sum = 0;
 #pragma unroll
       for (int j = 0; j < EACH; ++j) {
-        v[j] = EACH * tid + j < count ? what == 0 ? 1ull : soft.weight(x_of(key_in(all[EACH * tid + j]))) : 0ull;
+        v[j] = EACH * tid + j < count ? what == 0 ? 1ull : weight_of(soft.power(x_of(key_in(all[EACH * tid + j])))) : 0ull;
         sum += v[j];
       }
       u64 run = (what == 0 ? above : above_mass) + scan(sum, total) - sum;
 #pragma unroll
       for (int j = 0; j < EACH; ++j) {
-        if (run < limit && run + v[j] >= limit) s_cut = Cut{key_in(all[EACH * tid + j]), (int32_t)(uint32_t)all[EACH * tid + j]};
+        if (run < limit && run + v[j] >= limit) s_cut = Cut{x_of(key_in(all[EACH * tid + j])), (int32_t)(uint32_t)all[EACH * tid + j]};
         run += v[j];
       }
       __syncthreads();
-      cuts_any = true;
       cut = s_cut;                                               // never above an earlier cut: its tokens alone were counted
       __syncthreads();
       continue;
@@ -642,7 +689,7 @@ __global__ __launch_bounds__(NT, 2) void sample_kernel(const SampleArgs a) {
         const float x = (float)(xs[i]);
         const uint32_t key = key_of(x);
         if (shift == 32 - DIGIT || (key >> (shift + DIGIT)) == prefix)
-          bins[((key >> shift) & (BINS - 1)) * NT + tid] += (1ull << 48) + soft.weight(x);
+          bins[((key >> shift) & (BINS - 1)) * NT + tid] += (1ull << 48) + weight_of(soft.power(x));
       }
       add_up();
       prefix = prefix << DIGIT | find(what == 1, limit, above);
@@ -650,7 +697,7 @@ __global__ __launch_bounds__(NT, 2) void sample_kernel(const SampleArgs a) {
     }
     uint32_t key = prefix << kLastShift;
     if (sizeof(T) == 2 && !(key >> 31)) key |= 0xffffu;        // a negative bf16's low key bits are ones
-    const u64 w = soft.weight(__uint_as_float((key >> 31) ? key & 0x7fffffffu : ~key));
+    const u64 w = weight_of(soft.power(x_of(key)));
     const u64 ties = what == 0 ? limit - above : w ? (limit - above + w - 1) / w : 1;   // kept of the equal ones
     const int span = ((n + NWARP - 1) / NWARP + 31) / 32 * 32;
     const int w0 = min(wid * span, n), w1 = min(w0 + span, n);
@@ -681,32 +728,23 @@ __global__ __launch_bounds__(NT, 2) void sample_kernel(const SampleArgs a) {
       }
     }
     cluster.sync();
-    Cut found = {key, 0x7fffffff};
+    Cut found = {x_of(key), 0x7fffffff};
     for (int c = 0; c < CS; ++c) found.index = min(found.index, cluster.map_shared_rank(&ex[turn], c)->first);
-    if (found.key > cut.key || (found.key == cut.key && found.index < cut.index)) cut = found;
-    cuts_any = true;
+    if (found.x > cut.x || (found.x == cut.x && found.index < cut.index)) cut = found;
     cluster.sync();                                            // read by all before it is written again
   }
 
   // kept mass of every warp's span of indices
   const int span = ((n + NWARP - 1) / NWARP + 31) / 32 * 32;
   const int w0 = min(wid * span, n), w1 = min(w0 + span, n);
-  auto kept = [&](int i, int end) -> u64 {                       // weight of the token if it is kept
-    if (i >= end) return 0;
-    const float x = (float)(xs[i]);
-    const uint32_t key = key_of(x);
-    if (!passes(key, i0 + i)) return 0;
-    const u64 w = soft.weight(x);
-    return w >= least ? w : 0;
+  auto kept = [&](int i, int end) -> float {                     // 2^-40 of the token's weight if it is kept
+    const float x = i < end ? (float)xs[i] : -INFINITY, e = soft.power(x);
+    return passes(x, i0 + i) && e >= least ? e : 0.f;
   };
-  u64 mass = 0;
-  for (int i = w0 + lane; i < w1; i += 32 * PAR) {
-    u64 w[PAR];
-#pragma unroll
-    for (int j = 0; j < PAR; ++j) w[j] = kept(i + 32 * j, w1);
-#pragma unroll
-    for (int j = 0; j < PAR; ++j) mass += w[j];
-  }
+  Mass spans;
+#pragma unroll 4
+  for (int i = w0 + lane; i < w1; i += 32) spans.add(kept(i, w1));
+  u64 mass = spans.sum();
   mass = warp_add(mass);
   if (lane == 0) s_mass[wid] = mass;
   __syncthreads();
@@ -737,15 +775,15 @@ __global__ __launch_bounds__(NT, 2) void sample_kernel(const SampleArgs a) {
   if (list_n >= 0) {                                             // its span, by all warps of its CTA
     const int sub = (span / NWARP + 31) / 32 * 32;
     const int end = min(list_n * span + span, n), v0 = min(list_n * span + wid * sub, end), v1 = min(v0 + sub, end);
-    u64 part = 0;
-    for (int i = v0 + lane; i < v1; i += 32) part += kept(i, v1);
-    part = warp_add(part);
+    Mass sub_mass;
+    for (int i = v0 + lane; i < v1; i += 32) sub_mass.add(kept(i, v1));
+    const u64 part = warp_add(sub_mass.sum());
     if (lane == 0) s_mass[wid] = part;
     __syncthreads();
     u64 run = s_kept + warp_add(lane < wid ? s_mass[lane & (NWARP - 1)] : 0);
     if (goal >= run && goal < run + part) {
       for (int i = v0; i < v1; i += 32) {
-        const u64 w = kept(i + lane, v1);
+        const u64 w = weight_of(kept(i + lane, v1));
         u64 inc = w;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -778,15 +816,15 @@ template <typename T>
 cudaError_t launch(SampleArgs a, cudaStream_t s) {
   // CTAs per row: those that need the least time by a simple account.  A CTA takes as long as kFixed
   // logits beside its own, and two on an SM get about 0.6 of its pace each; clusters that do not fit
-  // at once take another round (48 rows of 100277 fp32 logits: 3 CTAs each, two rounds, 92 us with
-  // top-p; 5 CTAs each, two on an SM, one round, 57 us).
+  // at once take another round (48 rows of 100277 fp32 logits with top-p: 5 CTAs each, two on an SM, one
+  // round, take 0.6 of the time of 3 CTAs each in two rounds).
   constexpr int64_t kFixed = 12000;
   int cs = 0;
   int64_t cheapest = 0;
   for (int c = 1; c <= kMaxCluster; ++c) {
     const int64_t chunk = ((a.vocab + c - 1) / c + 7) / 8 * 8, bytes = kScratch + chunk * (int64_t)sizeof(T);
     if (bytes > kShared || (c > 1 && chunk < 2048)) continue;
-    const int per_sm = 2 * (bytes + 3072) <= 233472 ? 2 : 1;     // 228 KB an SM; 1 KB each is the system's
+    const int per_sm = 2 * (bytes + 3 * 1024) <= 228 * 1024 ? 2 : 1;   // 1 KB of each is the system's, 2 KB static
     const int64_t fit = clusters_at_once(c, per_sm), rounds = (a.rows + fit - 1) / fit;
     const bool shared = per_sm == 2 && (int64_t)a.rows * c > sm_count();
     const int64_t cost = rounds * (kFixed + (shared ? chunk * 5 / 3 : chunk));
