@@ -29,6 +29,14 @@
 // scores, so the third warpgroup gives registers up: launched with 168 each (384 x 168 =
 // 64512), 216 for the first two and 72 for the third (256 x 216 + 128 x 72 = 64512).
 // Tensor memory (512 columns): S/P of A, S/P of B, O of A, O of B.
+//
+// Measured, 32 q heads of 128: 1024 tokens over 31000 keys, 8 kv heads (531 GFLOP) 351 to 357 us,
+// 1.5 PFLOP/s or 77 % of cuBLAS's burst rate and 87 % of its rate under the power cap, which such a
+// call reaches; over 16000 keys the tensor cores are active 56 % of the time and an SM's exponentials
+// 28 %: what is left is the wait of one tile's softmax for the other's products.  Three prompts of
+// 700 to 2048 tokens, 4 kv heads: 39.5 us, of which the products are 11: about 10 us go to the launch,
+// the first loads and the last output, and about 5 to each of the two or three items of a pair, whose
+// first scores and last output have nothing to run beside.
 #include "attn_internal.cuh"
 #include "sm103.cuh"
 

@@ -816,8 +816,8 @@ template <typename T>
 cudaError_t launch(SampleArgs a, cudaStream_t s) {
   // CTAs per row: those that need the least time by a simple account.  A CTA takes as long as kFixed
   // logits beside its own, and two on an SM get about 0.6 of its pace each; clusters that do not fit
-  // at once take another round (48 rows of 100277 fp32 logits with top-p: 5 CTAs each, two on an SM, one
-  // round, take 0.6 of the time of 3 CTAs each in two rounds).
+  // at once take another round (48 rows of 100277 fp32 logits with top-p of 0.9: 3 CTAs each, two
+  // rounds, 67.7 us; 5 CTAs each, two on an SM, one round, 38.1 us).
   constexpr int64_t kFixed = 12000;
   int cs = 0;
   int64_t cheapest = 0;
