@@ -175,20 +175,26 @@ __device__ __forceinline__ bool tile_work(const AttnArgs& a, int32_t* sm, uint8_
     // Of several requests: the place by length.  More tiles than threads go as they come: then a pair
     // has so many items that they even out.
     if (sort) {
-      s_nu[x] = nu;
+      s_nu[tid] = x0 + tid < T ? nu : 0;         // T <= NT: one turn; a tile has one unit or more
       __syncthreads();
       place = 0;
-      for (int z = 0; z < T; ++z) {
-        const int v = s_nu[z];
-        place += v > nu || (v == nu && z < x) ? 1 : 0;
+      for (int z = 0; z < T; z += 4) {
+        const int4 v = *reinterpret_cast<const int4*>(s_nu + z);         // past the end: nothing counts
+        place += (v.x > nu || (v.x == nu && z < x)) + (v.y > nu || (v.y == nu && z + 1 < x)) +
+                 (v.z > nu || (v.z == nu && z + 2 < x)) + (v.w > nu || (v.w == nu && z + 3 < x));
       }
     }
     if (x0 + tid >= T) continue;
+    int j = place * a.Hkv / G, pos = place * a.Hkv - j * G;  // round and place in it
     for (int h = 0; h < a.Hkv; ++h) {
-      const int k = place * a.Hkv + h, j = k / G, pos = k - j * G;
-      if (pos != ((j & 1) ? G - 1 - pair : pair)) continue;
-      w.list[2 * j] = make_int4(lo, h, i, nu);
-      w.list[2 * j + 1] = make_int4(y.start, y.n, y.seq, u0);
+      if (pos == ((j & 1) ? G - 1 - pair : pair)) {
+        w.list[2 * j] = make_int4(lo, h, i, nu);
+        w.list[2 * j + 1] = make_int4(y.start, y.n, y.seq, u0);
+      }
+      if (++pos == G) {
+        pos = 0;
+        ++j;
+      }
     }
   }
   const int last = (all - 1) / G;              // round of the last item; only that round may lack one
@@ -453,7 +459,6 @@ void attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_cons
       const int all_lo = a.window > 0 ? max(0, base_pos + a.token(f0 + max(0, min(rows, 128) - 1)) - a.window + 1) : 0;
       float m = -INFINITY, l = 0.f;
       const int units = attn_piece(c);
-      bool next_mine = false;
       for (int j = 0; j < units; ++j) {
         const int key0 = (c.u0 + c.at + j) * UNIT;
         wait(s_full + t, ns++ & 1);
@@ -462,16 +467,16 @@ void attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_cons
         float s[UNIT];
         tmem_ld64(s_addr, s);
         tmem_ld64(s_addr + 64, s + 64);
-        if (j == units - 1) {                            // every product that reads this tile's Q has ended
-          TileCursor nx = c;
-          more = tile_next(a, work, nx);
-          next_mine = more && has_tile(nx);
-          if (next_mine) load_q(nx);
-        }
         if (key0 < all_lo || key0 + UNIT > all_hi) {
+          const int first = lo - key0, last = pos - key0;
+          if (a.window > 0) {
+#pragma unroll
+            for (int i = 0; i < UNIT; ++i)
+              if (i < first) s[i] = -INFINITY;
+          }
 #pragma unroll
           for (int i = 0; i < UNIT; ++i)
-            if (key0 + i < lo || key0 + i > pos) s[i] = -INFINITY;
+            if (i > last) s[i] = -INFINITY;
         }
         float top[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
@@ -520,7 +525,12 @@ void attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_cons
         unpack2(add2(sum2[0], sum2[1]), x, y);
         l += x + y;
       }
-      if (next_mine) q_loaded();
+      // Every product that reads this tile's Q has ended with the last scores; the next Q comes while the
+      // last product and the output run.
+      TileCursor nx = c;
+      more = tile_next(a, work, nx);
+      const bool next_mine = more && has_tile(nx);
+      if (next_mine) load_q(nx);
       wait(o_full + t, no++ & 1);
       __syncwarp();
       tc_fence_after();
@@ -531,11 +541,13 @@ void attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_cons
       const size_t part_slot = (size_t)attn_slot(c, part) * BM;
       float* part_dst = a.part_o + (part_slot + warp_rows) * D + lane * 4;
       const float inv = l > 0.f ? 1.f / l : 0.f;
-      auto out_row = [&](int r) {                        // of this CTA's part of the tile
-        const int token = a.token(f0 + r);
-        return static_cast<__nv_bfloat16*>(a.out) +
-               ((size_t)(c.q.start + token) * a.Hq + c.h * a.group + f0 + r - token * a.group) * D;
-      };
+      __nv_bfloat16* out_rows[8];                        // this lane's part of rows lane / 8, + 4, ... of the warp's
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int r = f0 + (wid & 3) * 32 + 4 * k + lane / 8, token = a.token(r);
+        out_rows[k] = static_cast<__nv_bfloat16*>(a.out) +
+                      ((size_t)(c.q.start + token) * a.Hq + c.h * a.group + r - token * a.group) * D + lane % 8 * 8;
+      }
       // A row per thread would touch 32 lines with every store; turned in shared memory, a store
       // writes 128 bytes of each of four rows.
       const uint32_t turn = sq + 2 * C::kQ + C::kStages * C::kTile + wid * (32 * 128);
@@ -551,7 +563,7 @@ void attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_cons
           const int r = 4 * k + lane / 8, ch = lane % 8;
           const uint4 v = *reinterpret_cast<const uint4*>(smem + (turn - sq) + r * 128 + ((ch ^ (r & 7)) << 4));
           const int tr = (wid & 3) * 32 + r;
-          if (tr < rows) *reinterpret_cast<uint4*>(out_row(tr) + d + 8 * ch) = v;
+          if (tr < rows) *reinterpret_cast<uint4*>(out_rows[k] + d) = v;
         }
       };
 #pragma unroll 1
@@ -559,6 +571,7 @@ void attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_cons
         float o[64];
         __syncwarp();
         tmem_ld64(o_addr + d, o);
+        if (d + 64 == D && next_mine) q_loaded();        // the next item's first scores run beside the rest
         if (whole) {
           uint32_t w[32];
 #pragma unroll
