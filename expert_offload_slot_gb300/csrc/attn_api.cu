@@ -287,7 +287,7 @@ MOE_API moe_status moe_attn_forward(moe_attn* A, const void* q, int64_t q_stride
   a.num_pages = num_pages; a.Hq = c.num_q_heads; a.Hkv = c.num_kv_heads; a.group = c.num_q_heads / c.num_kv_heads;
   a.page = c.page_size; a.page_log2 = A->page_log2; a.window = c.window; a.scale = c.softmax_scale;
   a.scale_log2 = c.softmax_scale * 1.44269504088896340736f;
-  a.part_o = A->part_o; a.part_ml = A->part_ml; a.arrived = A->arrived; a.ticket = A->ticket; a.status = A->status;
+  a.part_o = A->part_o; a.part_ml = A->part_ml; a.arrived = A->arrived; a.status = A->status;
   divider(a.group, a.group_mul, a.group_shift);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (c.dtype == MOE_F32) return launched(launch_attn_f32(a, c.head_dim, attn_grid(A->sms), s), "moe_attn_forward");

@@ -44,7 +44,6 @@ struct AttnArgs {
   float* part_o;               // [2 * grid][rows per slot][D]
   float2* part_ml;             // [2 * grid][rows per slot]  (running maximum, sum of exponentials)
   uint32_t* arrived;           // [grid] pieces of the split item that starts in CTA c; self-resetting
-  uint32_t* ticket;            // [2]
   int32_t* status;             // sticky
   uint32_t group_mul;          // token of a row without a division: (row * group_mul) >> group_shift,
   int32_t group_shift;         // exact below 2^31 (group_mul = ceil(2^group_shift / group))
@@ -220,13 +219,22 @@ __device__ __forceinline__ bool attn_find_range(const AttnArgs& a, int unit, int
       return total;
     };
     int least = (W + most - 1) / most, top = least + overhead;
-    if (parts_for(top) <= most) {
+    if (alone) {                               // all lengths at once, none waiting for another's sum
+      uint32_t fit = 0;
+#pragma unroll
+      for (int k = 0; k <= overhead; ++k)
+        fit |= (__reduce_add_sync(0xffffffffu, items > 0 ? items * ((longest + least + k - 1) / (least + k)) : 0) <= most) << k;
+      pieces = fit != 0;
+      least += pieces ? __ffs(fit) - 1 : 0;
+    } else if (parts_for(top) <= most) {
       pieces = true;
       while (least < top) {
         const int mid = (least + top) / 2;
         if (parts_for(mid) <= most) top = mid;
         else least = mid + 1;
       }
+    }
+    if (pieces) {
       parts_for(least);
       if (c >= total) return false;
       if (c >= before && c < before + own) {                           // one thread (of each warp)
@@ -369,29 +377,31 @@ __device__ __forceinline__ void attn_join(const AttnArgs& a, const AttnCursor& c
   const int lane = threadIdx.x & 31, rows = min(BM, c.q.n * a.group - c.i * BM);
   auto slot = [&](int p) { return (size_t)(2 * (c0 + p) + (p == 0 ? 1 : 0)) * BM; };
   for (int row = threadIdx.x / 32; row < rows; row += NT / 32) {
-    float M = -INFINITY, l = 0.f, o[COLS];
-    for (int p = lane; p < n; p += 32) M = fmaxf(M, __ldcg(a.part_ml + slot(p) + row).x);
+    float v[U][COLS], l = 0.f, o[COLS];
+    auto load = [&](int p0) {                  // columns of pieces p0 .. p0 + U - 1
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float* src = a.part_o + (slot(min(p0 + u, n - 1)) + row) * D + lane * COLS;
+        if constexpr (COLS == 4) *reinterpret_cast<float4*>(v[u]) = __ldcg(reinterpret_cast<const float4*>(src));
+        else *reinterpret_cast<float2*>(v[u]) = __ldcg(reinterpret_cast<const float2*>(src));
+      }
+    };
+    auto stats = [&](int p) { return p < n ? __ldcg(a.part_ml + slot(p) + row) : make_float2(-INFINITY, 0.f); };
+    float2 ml = stats(lane);
+    load(0);                                   // one latency for both
+    float M = ml.x;
+    for (int p = lane + 32; p < n; p += 32) M = fmaxf(M, stats(p).x);
 #pragma unroll
     for (int k = 16; k > 0; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
     const float top = M == -INFINITY ? 0.f : M;
 #pragma unroll
     for (int k = 0; k < COLS; ++k) o[k] = 0.f;
     for (int p0 = 0; p0 < n; p0 += 32) {
-      float g = 0.f, gl = 0.f;
-      if (p0 + lane < n) {
-        const float2 ml = __ldcg(a.part_ml + slot(p0 + lane) + row);
-        g = LOG2 ? exp2f(ml.x - top) : expf(ml.x - top);
-        gl = g * ml.y;
-      }
+      if (p0 > 0) ml = stats(p0 + lane);
+      const float g = LOG2 ? exp2f(ml.x - top) : expf(ml.x - top), gl = g * ml.y;
       const int m = min(32, n - p0);
       for (int p = 0; p < m; p += U) {
-        float v[U][COLS];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const float* src = a.part_o + (slot(p0 + min(p + u, m - 1)) + row) * D + lane * COLS;
-          if constexpr (COLS == 4) *reinterpret_cast<float4*>(v[u]) = __ldcg(reinterpret_cast<const float4*>(src));
-          else *reinterpret_cast<float2*>(v[u]) = __ldcg(reinterpret_cast<const float2*>(src));
-        }
+        if (p0 + p > 0) load(p0 + p);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const float w = __shfl_sync(0xffffffffu, g, (p + u) & 31), x = __shfl_sync(0xffffffffu, gl, (p + u) & 31);

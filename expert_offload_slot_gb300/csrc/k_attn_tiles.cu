@@ -30,13 +30,15 @@
 // 64512), 216 for the first two and 72 for the third (256 x 216 + 128 x 72 = 64512).
 // Tensor memory (512 columns): S/P of A, S/P of B, O of A, O of B.
 //
-// Measured, 32 q heads of 128: 1024 tokens over 31000 keys, 8 kv heads (531 GFLOP) 351 to 357 us,
-// 1.5 PFLOP/s or 77 % of cuBLAS's burst rate and 87 % of its rate under the power cap, which such a
-// call reaches; over 16000 keys the tensor cores are active 56 % of the time and an SM's exponentials
-// 28 %: what is left is the wait of one tile's softmax for the other's products.  Three prompts of
-// 700 to 2048 tokens, 4 kv heads: 39.5 us, of which the products are 11: about 10 us go to the launch,
-// the first loads and the last output, and about 5 to each of the two or three items of a pair, whose
-// first scores and last output have nothing to run beside.
+// Measured, 32 q heads of 128: 1024 tokens over 31000 keys, 8 kv heads (531 GFLOP) 345 to 354 us,
+// 1.5 PFLOP/s or 79 % of cuBLAS's burst rate and 89 % of its rate under the power cap, which such a
+// call reaches.  Three prompts of 700 to 1100 tokens, 4 kv heads: 36.5 us, of which the products are 11
+// and the causal tiles' masked part another 3: the first scores are there after 8.5 us (lengths, page
+// table, first keys and queries from HBM one after another), a unit of 128 keys takes 1.4 us, and an
+// item ends in 2.2 us of masked scores, output and the next item's first scores, two or three times a
+// pair.  Two threads a row (16 softmax warps) made the large call 352 instead of 327 us, steps of 64
+// keys with their scores a step ahead 357: an MMA of 64 columns reads the queries from shared memory
+// as often as one of 128.
 #include "attn_internal.cuh"
 #include "sm103.cuh"
 
@@ -178,7 +180,7 @@ __device__ __forceinline__ bool tile_work(const AttnArgs& a, int32_t* sm, uint8_
       s_nu[tid] = x0 + tid < T ? nu : 0;         // T <= NT: one turn; a tile has one unit or more
       __syncthreads();
       place = 0;
-      for (int z = 0; z < T; z += 4) {
+      for (int z = 0; z < T && wid * 32 < T; z += 4) {                   // the warps that have a tile
         const int4 v = *reinterpret_cast<const int4*>(s_nu + z);         // past the end: nothing counts
         place += (v.x > nu || (v.x == nu && z < x)) + (v.y > nu || (v.y == nu && z + 1 < x)) +
                  (v.z > nu || (v.z == nu && z + 2 < x)) + (v.w > nu || (v.w == nu && z + 3 < x));
