@@ -164,9 +164,9 @@ struct AttnSplit {
 // Called by all threads of the CTA (NT of them) for part c of at most `most`.  `sm` holds 64 ints.
 // False when the part has no work.  Up to 32 requests, every warp finds the part by itself with a
 // request in each lane: no barrier stands before the first load of the cache.
-template <int BM, int NT>
-__device__ __forceinline__ bool attn_find_range(const AttnArgs& a, int unit, int overhead, int c, int most, int32_t* sm,
-                                                AttnSplit& sp, AttnCursor& cur) {
+template <int BM, int NT, int unit, int overhead>
+__device__ __forceinline__ bool attn_find_range(const AttnArgs& a, int c, int most, int32_t* sm, AttnSplit& sp,
+                                                AttnCursor& cur) {
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   constexpr int NW = NT / 32;
   const bool alone = a.R <= 32;
@@ -219,13 +219,18 @@ __device__ __forceinline__ bool attn_find_range(const AttnArgs& a, int unit, int
       return total;
     };
     int least = (W + most - 1) / most, top = least + overhead;
-    if (alone) {                               // all lengths at once, none waiting for another's sum
-      uint32_t fit = 0;
+    if (alone) {                               // the even share, which few keys get; then all others at once
+      auto fits = [&](int L) {
+        return __reduce_add_sync(0xffffffffu, items > 0 ? items * ((longest + L - 1) / L) : 0) <= most;
+      };
+      pieces = fits(least);
+      if (!pieces) {
+        uint32_t fit = 0;
 #pragma unroll
-      for (int k = 0; k <= overhead; ++k)
-        fit |= (__reduce_add_sync(0xffffffffu, items > 0 ? items * ((longest + least + k - 1) / (least + k)) : 0) <= most) << k;
-      pieces = fit != 0;
-      least += pieces ? __ffs(fit) - 1 : 0;
+        for (int k = 1; k <= overhead; ++k) fit |= (uint32_t)fits(least + k) << k;
+        pieces = fit != 0;
+        least += pieces ? __ffs(fit) - 1 : 0;
+      }
     } else if (parts_for(top) <= most) {
       pieces = true;
       while (least < top) {

@@ -41,7 +41,7 @@ __global__ __launch_bounds__(NT, 2) void attn_f32_kernel(const AttnArgs a) {
   sm103::grid_wait();
   AttnSplit sp;
   AttnCursor c;
-  if (!attn_find_range<BM, NT>(a, BN, 4, blockIdx.x, gridDim.x, sched, sp, c)) return;
+  if (!attn_find_range<BM, NT, BN, 4>(a, blockIdx.x, gridDim.x, sched, sp, c)) return;
   const int tid = threadIdx.x, tx = tid % 16, r0 = tid / 16 * 4;
   do {
     const int rows = min(BM, c.q.n * a.group - c.i * BM);
@@ -205,7 +205,7 @@ __global__ __launch_bounds__(NT, 2) void attn_f32_few_kernel(const AttnArgs a) {
   sm103::grid_wait();
   AttnSplit sp;
   AttnCursor c;
-  if (!attn_find_range<FM, NT>(a, FN, 4, blockIdx.x, gridDim.x, sched, sp, c)) return;
+  if (!attn_find_range<FM, NT, FN, 4>(a, blockIdx.x, gridDim.x, sched, sp, c)) return;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int col = tid % D, kg = tid / D;                         // output phase
   AttnCursor pc = c;                                             // the loading side, FSTAGES - 1 units ahead

@@ -21,9 +21,10 @@
 //
 // Measured: four requests of 100000 keys, 8 kv heads (1.6 GB) 252 us, 6.4 TB/s or
 // 95 % of a plain copy's rate; 16 requests of 60 to 8191 keys, 4 kv heads (114 MB)
-// 29 us, where the first loads' latency, the join and uneven pieces take a third.
-// Units of 64 and 32 keys in place of 128 take 250 and 254 us, 28 and 29 us, but one
-// request of 1000 keys then 10.6 and 12.6 us in place of 9.9: more pieces to join.
+// 28.5 us: 4 pass before the first load is out (lengths, then pages, each an HBM
+// latency), 3 to 5 after the last (warps and pieces joined), and pieces are uneven.  One
+// request of 1000 keys takes 8.8 us.  Units of 64 and 32 keys in place of 128 gain 1 % or
+// nothing, and the one request then takes 0.7 and 2.7 us longer: more pieces to join.
 #include "attn_internal.cuh"
 #include "sm103.cuh"
 
@@ -63,7 +64,7 @@ __global__ __launch_bounds__(NT, 1) void attn_rows_kernel(const __grid_constant_
   grid_wait();
   AttnSplit sp;
   AttnCursor c;
-  if (!attn_find_range<BM, NT>(a, UNIT, 5, blockIdx.x, gridDim.x, sched, sp, c)) return;
+  if (!attn_find_range<BM, NT, UNIT, 5>(a, blockIdx.x, gridDim.x, sched, sp, c)) return;
 
   uint64_t* bar = bars + wid * C::kStages;
   const uint32_t ring = smem_addr(smem) + wid * C::kStages * 2 * C::kTile;
