@@ -164,7 +164,10 @@ struct AttnSplit {
 // Called by all threads of the CTA (NT of them) for part c of at most `most`.  `sm` holds 64 ints.
 // False when the part has no work.  Up to 32 requests, every warp finds the part by itself with a
 // request in each lane: no barrier stands before the first load of the cache.
-template <int BM, int NT, int unit, int overhead>
+// `join`: units that the join of one piece takes; k pieces of an item of nu units take nu / k + join k,
+// so shorter ones than sqrt(join nu) are not made (tile kernel, 204 tokens over 2000 keys, 8 q heads and
+// one kv head: 37 us with pieces of one unit, 24 with 4).  0 where a join takes a small part of a unit.
+template <int BM, int NT, int unit, int overhead, int join>
 __device__ __forceinline__ bool attn_find_range(const AttnArgs& a, int c, int most, int32_t* sm, AttnSplit& sp,
                                                 AttnCursor& cur) {
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
@@ -218,7 +221,9 @@ __device__ __forceinline__ bool attn_find_range(const AttnArgs& a, int c, int mo
       scan(own, before, total);
       return total;
     };
-    int least = (W + most - 1) / most, top = least + overhead;
+    int least = (W + most - 1) / most;
+    if (join > 0 && alone) least = max(least, (int)sqrtf((float)join * (float)__reduce_max_sync(0xffffffffu, longest)));
+    int top = least + overhead;
     if (alone) {                               // the even share, which few keys get; then all others at once
       auto fits = [&](int L) {
         return __reduce_add_sync(0xffffffffu, items > 0 ? items * ((longest + L - 1) / L) : 0) <= most;
@@ -374,50 +379,20 @@ __device__ __forceinline__ void attn_store4(__nv_bfloat16* p, float4 v) {
 }
 
 // Joins the n pieces of a split item, in piece order (so the sum does not depend on which CTA
-// arrives last), and writes the item's output rows: a warp per row, whose lanes take the pieces'
-// maxima and sums at once and then D / 32 columns each.  LOG2: the maxima are in log2 units.
-template <typename T, int D, int BM, int NT, bool LOG2>
-__device__ __forceinline__ void attn_join(const AttnArgs& a, const AttnCursor& c, int c0, int n) {
-  constexpr int COLS = D / 32, U = 8;
-  const int lane = threadIdx.x & 31, rows = min(BM, c.q.n * a.group - c.i * BM);
+// arrives last), and writes the item's output rows.  All threads; a warp per row, whose lanes take
+// the pieces' maxima and sums at once and then D / 32 columns each; of few rows a power of two of
+// warps per row, over equal shares of the pieces, joined through `scratch` (NT / 32 * (D + 4)
+// floats).  U: pieces whose columns are in flight together (one token over 64000 keys, 8 q heads and
+// one kv head, 152 pieces: 22 us with 8, 20 with 16; 16 decodes of few pieces 28.7 and 29.0).  LOG2: the maxima are in log2 units.
+template <typename T, int D, int BM, int NT, int U, bool LOG2>
+__device__ __forceinline__ void attn_join(const AttnArgs& a, const AttnCursor& c, int c0, int n, float* scratch) {
+  constexpr int COLS = D / 32, NW = NT / 32, LD = D + 4;
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, rows = min(BM, c.q.n * a.group - c.i * BM);
+  int log_parts = 0;
+  while ((rows << log_parts) * 2 <= NW && (16 << log_parts) < n) ++log_parts;
   auto slot = [&](int p) { return (size_t)(2 * (c0 + p) + (p == 0 ? 1 : 0)) * BM; };
-  for (int row = threadIdx.x / 32; row < rows; row += NT / 32) {
-    float v[U][COLS], l = 0.f, o[COLS];
-    auto load = [&](int p0) {                  // columns of pieces p0 .. p0 + U - 1
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const float* src = a.part_o + (slot(min(p0 + u, n - 1)) + row) * D + lane * COLS;
-        if constexpr (COLS == 4) *reinterpret_cast<float4*>(v[u]) = __ldcg(reinterpret_cast<const float4*>(src));
-        else *reinterpret_cast<float2*>(v[u]) = __ldcg(reinterpret_cast<const float2*>(src));
-      }
-    };
-    auto stats = [&](int p) { return p < n ? __ldcg(a.part_ml + slot(p) + row) : make_float2(-INFINITY, 0.f); };
-    float2 ml = stats(lane);
-    load(0);                                   // one latency for both
-    float M = ml.x;
-    for (int p = lane + 32; p < n; p += 32) M = fmaxf(M, stats(p).x);
-#pragma unroll
-    for (int k = 16; k > 0; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
-    const float top = M == -INFINITY ? 0.f : M;
-#pragma unroll
-    for (int k = 0; k < COLS; ++k) o[k] = 0.f;
-    for (int p0 = 0; p0 < n; p0 += 32) {
-      if (p0 > 0) ml = stats(p0 + lane);
-      const float g = LOG2 ? exp2f(ml.x - top) : expf(ml.x - top), gl = g * ml.y;
-      const int m = min(32, n - p0);
-      for (int p = 0; p < m; p += U) {
-        if (p0 + p > 0) load(p0 + p);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const float w = __shfl_sync(0xffffffffu, g, (p + u) & 31), x = __shfl_sync(0xffffffffu, gl, (p + u) & 31);
-          if (p + u < m) {
-            l += x;
-#pragma unroll
-            for (int k = 0; k < COLS; ++k) o[k] += w * v[u][k];
-          }
-        }
-      }
-    }
+  auto power = [](float x) { return LOG2 ? exp2f(x) : expf(x); };
+  auto finish = [&](int row, float l, const float (&o)[COLS]) {
     const float inv = l > 0.f ? 1.f / l : 0.f;
     const int fr = c.i * BM + row;
     T* dst = static_cast<T*>(a.out) + ((size_t)(c.q.start + a.token(fr)) * a.Hq + c.h * a.group + a.head_of(fr)) * D + lane * COLS;
@@ -427,7 +402,82 @@ __device__ __forceinline__ void attn_join(const AttnArgs& a, const AttnCursor& c
 #pragma unroll
       for (int k = 0; k < COLS; ++k) dst[k] = (T)(o[k] * inv);
     }
+  };
+  for (int x = wid; x < rows << log_parts; x += NW) {
+    const int row = x >> log_parts, part = x & ((1 << log_parts) - 1);
+    const int q0 = (int)((int64_t)part * n >> log_parts), q1 = (int)((int64_t)(part + 1) * n >> log_parts);
+    float v[U][COLS], M = -INFINITY, l = 0.f, o[COLS];
+    auto load = [&](int p0) {                  // columns of pieces p0 .. p0 + U - 1
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float* src = a.part_o + (slot(min(p0 + u, q1 - 1)) + row) * D + lane * COLS;
+        if constexpr (COLS == 4) *reinterpret_cast<float4*>(v[u]) = __ldcg(reinterpret_cast<const float4*>(src));
+        else *reinterpret_cast<float2*>(v[u]) = __ldcg(reinterpret_cast<const float2*>(src));
+      }
+    };
+    auto stats = [&](int p) { return p < q1 ? __ldcg(a.part_ml + slot(p) + row) : make_float2(-INFINITY, 0.f); };
+    float2 next = stats(q0 + lane);
+    load(q0);                                  // one latency for both
+#pragma unroll
+    for (int k = 0; k < COLS; ++k) o[k] = 0.f;
+    for (int p0 = q0; p0 < q1; p0 += 32) {
+      const float2 ml = next;
+      next = stats(p0 + 32 + lane);
+      float top = ml.x;
+#pragma unroll
+      for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+      const float last = M;
+      M = fmaxf(M, top);
+      top = M == -INFINITY ? 0.f : M;
+      const float f = power(last - top), g = power(ml.x - top), gl = g * ml.y;
+      l *= f;
+#pragma unroll
+      for (int k = 0; k < COLS; ++k) o[k] *= f;
+      const int m = min(32, q1 - p0);
+      for (int p = 0; p < m; p += U) {
+        if (p0 + p > q0) load(p0 + p);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const float w = __shfl_sync(0xffffffffu, g, p + u), y = __shfl_sync(0xffffffffu, gl, p + u);
+          if (p + u < m) {
+            l += y;
+#pragma unroll
+            for (int k = 0; k < COLS; ++k) o[k] += w * v[u][k];
+          }
+        }
+      }
+    }
+    if (log_parts == 0) {
+      finish(row, l, o);
+      continue;
+    }
+    float* to = scratch + wid * LD;
+#pragma unroll
+    for (int k = 0; k < COLS; ++k) to[lane * COLS + k] = o[k];
+    if (lane == 0) {
+      to[D] = M;
+      to[D + 1] = l;
+    }
   }
+  if (log_parts == 0) return;
+  __syncthreads();
+  if (wid < rows) {
+    const float* from = scratch + (wid << log_parts) * LD;
+    const int parts = 1 << log_parts;
+    float M = -INFINITY, l = 0.f, o[COLS];
+    for (int k = 0; k < parts; ++k) M = fmaxf(M, from[k * LD + D]);
+    const float top = M == -INFINITY ? 0.f : M;
+#pragma unroll
+    for (int k = 0; k < COLS; ++k) o[k] = 0.f;
+    for (int p = 0; p < parts; ++p) {
+      const float g = power(from[p * LD + D] - top);
+      l += g * from[p * LD + D + 1];
+#pragma unroll
+      for (int k = 0; k < COLS; ++k) o[k] += g * from[p * LD + lane * COLS + k];
+    }
+    finish(wid, l, o);
+  }
+  __syncthreads();                             // the scratch is read
 }
 
 // ------------------------------------------------------------------ launchers

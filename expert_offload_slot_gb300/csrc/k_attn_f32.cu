@@ -41,7 +41,7 @@ __global__ __launch_bounds__(NT, 2) void attn_f32_kernel(const AttnArgs a) {
   sm103::grid_wait();
   AttnSplit sp;
   AttnCursor c;
-  if (!attn_find_range<BM, NT, BN, 4>(a, blockIdx.x, gridDim.x, sched, sp, c)) return;
+  if (!attn_find_range<BM, NT, BN, 4, 0>(a, blockIdx.x, gridDim.x, sched, sp, c)) return;
   const int tid = threadIdx.x, tx = tid % 16, r0 = tid / 16 * 4;
   do {
     const int rows = min(BM, c.q.n * a.group - c.i * BM);
@@ -169,7 +169,7 @@ __global__ __launch_bounds__(NT, 2) void attn_f32_kernel(const AttnArgs a) {
     }
     if (!whole) {
       int c0, n;
-      if (attn_arrive(a, sp, c, sched, c0, n)) attn_join<float, D, BM, NT, false>(a, c, c0, n);
+      if (attn_arrive(a, sp, c, sched, c0, n)) attn_join<float, D, BM, NT, 8, false>(a, c, c0, n, prob);
     }
   } while (attn_next<BM>(a, BN, c));
 }
@@ -205,7 +205,7 @@ __global__ __launch_bounds__(NT, 2) void attn_f32_few_kernel(const AttnArgs a) {
   sm103::grid_wait();
   AttnSplit sp;
   AttnCursor c;
-  if (!attn_find_range<FM, NT, FN, 4>(a, blockIdx.x, gridDim.x, sched, sp, c)) return;
+  if (!attn_find_range<FM, NT, FN, 4, 0>(a, blockIdx.x, gridDim.x, sched, sp, c)) return;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int col = tid % D, kg = tid / D;                         // output phase
   AttnCursor pc = c;                                             // the loading side, FSTAGES - 1 units ahead
@@ -347,7 +347,7 @@ __global__ __launch_bounds__(NT, 2) void attn_f32_few_kernel(const AttnArgs a) {
     if (!whole) {
       if (tid < rows) a.part_ml[(size_t)attn_slot(c, blockIdx.x) * FM + tid] = make_float2(fac[FM + tid], fac[2 * FM + tid]);
       int c0, n;
-      if (attn_arrive(a, sp, c, sched, c0, n)) attn_join<float, D, FM, NT, false>(a, c, c0, n);
+      if (attn_arrive(a, sp, c, sched, c0, n)) attn_join<float, D, FM, NT, 16, false>(a, c, c0, n, part);
     }
   } while (attn_next<FM>(a, FN, c));
   asm volatile("cp.async.wait_all;" ::: "memory");

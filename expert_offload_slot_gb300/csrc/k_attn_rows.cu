@@ -64,7 +64,7 @@ __global__ __launch_bounds__(NT, 1) void attn_rows_kernel(const __grid_constant_
   grid_wait();
   AttnSplit sp;
   AttnCursor c;
-  if (!attn_find_range<BM, NT, UNIT, 5>(a, blockIdx.x, gridDim.x, sched, sp, c)) return;
+  if (!attn_find_range<BM, NT, UNIT, 5, 0>(a, blockIdx.x, gridDim.x, sched, sp, c)) return;
 
   uint64_t* bar = bars + wid * C::kStages;
   const uint32_t ring = smem_addr(smem) + wid * C::kStages * 2 * C::kTile;
@@ -352,7 +352,7 @@ __global__ __launch_bounds__(NT, 1) void attn_rows_kernel(const __grid_constant_
     __syncthreads();                         // the join's memory is read: the next piece may write it
     if (!whole) {
       int c0, n;
-      if (attn_arrive(a, sp, c, sched, c0, n)) attn_join<__nv_bfloat16, D, BM, NT, true>(a, c, c0, n);
+      if (attn_arrive(a, sp, c, sched, c0, n)) attn_join<__nv_bfloat16, D, BM, NT, 16, true>(a, c, c0, n, join);
     }
   } while (attn_next<BM>(a, UNIT, c));
   if (!alive)                                // bounded: let the copies in flight land before the memory is given up

@@ -151,7 +151,7 @@ __device__ __forceinline__ bool tile_work(const AttnArgs& a, int32_t* sm, uint8_
   w.count = 0;
   if (!w.whole) {
     __syncthreads();
-    return attn_find_range<BM, NT, UNIT, kJoin>(a, pair, G, sm, w.sp, c);
+    return attn_find_range<BM, NT, UNIT, kJoin, 1>(a, pair, G, sm, w.sp, c);
   }
   int at = base + inc - tiles;
   for (int r = r0; r < r1; ++r) {
