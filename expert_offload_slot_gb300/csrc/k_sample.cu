@@ -17,16 +17,18 @@
 // one pass adds the tokens up in 2048 bins of count or 1024 of mass with shared-memory
 // atomics on integers, the cluster adds its CTAs' bins over distributed shared memory,
 // and the tokens of the bin that holds the cut are collected and sorted by (x, index).
-// Where top-k leaves 256 tokens or fewer down to the end of that bin, all of them are
-// collected instead and the first CTA does the rest on its sorted list.  A bin with
+// Where top-k leaves 256 tokens or fewer down to the end of that bin (1024 where top-p
+// follows), all of them are collected instead and the first CTA does the rest on its
+// sorted list.  A bin with
 // more tokens than the list holds (equal logits) is resolved by a radix descent over
 // the ordered bits of x and a count of the ties in index order.
 //
 // What bounds it: few CTAs walk a row (48 rows of 100277 fp32 logits: 240 CTAs, 40000 logits
 // an SM), so a pass over all logits costs 3 to 8 us by its instructions, and each cut two or
 // three exchanges in the cluster of about 3 us; HBM's part is 4 us.  48 such rows, read from
-// HBM: greedy 11.8 us, temperature alone 16.9, top-k of 50 20.1 and of 1000 31.5, top-p of 0.9
-// 38.1, of 1000 with top-p and min-p 46.9.  One row of 131072 bf16 logits: 4.8, 7.5, 12, 20, 24.
+// HBM: greedy 11.8 us, temperature alone 16.9, top-k of 50 20.5 and of 1000 31.5, top-p of 0.9
+// 37.5, top-k of 1000 with top-p and min-p 36.5.  One row of 131072 bf16 logits: 4.7, 7.4, 12.3,
+// 20, 23, 25.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -48,7 +50,7 @@ constexpr int NT = 512, NWARP = NT / 32;
 constexpr int DIGIT = 2, BINS = 1 << DIGIT;    // bits a pass of the radix descent
 constexpr int kMaxCluster = 8;
 constexpr int kList = 1024;                    // tokens that are collected and sorted
-constexpr int kFinish = 256;                   // of top-k, so many that one CTA does the rest on the list
+constexpr int kFinish = 256;                   // of top-k alone, so many that one CTA does the rest on the list
 constexpr float kHead = 10.f;
 constexpr int kCountBins = 2048, kMassBins = 1024, kCountShift = 13, kMassShift = 14;
 constexpr int kScratch = kCountBins * 4 + 3 * kList * 8;       // bins and three lists, or the descent's counters
@@ -413,11 +415,13 @@ __global__ __launch_bounds__(NT, 2) void sample_kernel(const SampleArgs a) {
     cluster.sync();
     return all >= limit;
   };
-  // Sorts the first m of list (at most kList, all different), ascending: one a thread by counting the
-  // smaller ones, more in a bitonic network over the next power of two (0.2 us for each of its passes).
+  // Sorts the first m of list (at most kList, all different), ascending: few, one a thread, by counting the
+  // smaller ones; more in a bitonic network (Batcher) over the next power of two, two neighbours a thread.
+  // Partners within a warp meet by shuffles; only those further apart pass through memory (10 of the
+  // 55 steps of 1024).
   auto sort = [&](u64* list, int m) {
-    __syncthreads();
-    if (m <= NT) {
+    if (m <= NT / 2) {
+      __syncthreads();
       const u64 x = tid < m ? list[tid] : 0;
       int place = 0;
       if (tid < m) {
@@ -426,24 +430,45 @@ __global__ __launch_bounds__(NT, 2) void sample_kernel(const SampleArgs a) {
       }
       __syncthreads();
       if (tid < m) list[place] = x;
-    } else {
-      int top = 2 * NT;
-      while (top < m) top <<= 1;
-      for (int i = m + tid; i < top; i += NT) list[i] = ~0ull;
-      for (int size = 2; size <= top; size <<= 1) {
-        for (int stride = size >> 1; stride > 0; stride >>= 1) {
-          __syncthreads();
-          for (int p = tid; p < top / 2; p += NT) {
-            const int i = 2 * p - (p & (stride - 1)), j = i + stride;
-            const u64 x = list[i], y = list[j];
-            if ((x > y) == ((i & size) == 0)) {
-              list[i] = y;
-              list[j] = x;
-            }
-          }
+      __syncthreads();
+      return;
+    }
+    int top = NT;
+    while (top < m) top <<= 1;
+    const bool on = tid < top / 2;                               // whole warps
+    u64 a = ~0ull, b = ~0ull;
+    __syncthreads();
+    if (2 * tid < m) a = list[2 * tid];
+    if (2 * tid + 1 < m) b = list[2 * tid + 1];
+    for (int size = 2; size <= top; size <<= 1) {
+      const bool up = ((2 * tid) & size) == 0;
+      int apart = size / 4;                                      // threads between partners; 0: the thread's own two
+      for (; apart >= 32; apart >>= 1) {
+        __syncthreads();
+        if (on) *reinterpret_cast<ulonglong2*>(list + 2 * tid) = make_ulonglong2(a, b);
+        __syncthreads();
+        if (on) {
+          const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(list + 2 * (tid ^ apart));
+          const bool least = ((tid & apart) == 0) == up;
+          a = (o.x < a) == least ? o.x : a;
+          b = (o.y < b) == least ? o.y : b;
         }
       }
+      if (!on) continue;
+      for (; apart >= 1; apart >>= 1) {
+        const u64 x = __shfl_xor_sync(0xffffffffu, a, apart), y = __shfl_xor_sync(0xffffffffu, b, apart);
+        const bool least = ((tid & apart) == 0) == up;
+        a = (x < a) == least ? x : a;
+        b = (y < b) == least ? y : b;
+      }
+      if ((b < a) == up) {
+        const u64 x = a;
+        a = b;
+        b = x;
+      }
     }
+    __syncthreads();
+    if (on) *reinterpret_cast<ulonglong2*>(list + 2 * tid) = make_ulonglong2(a, b);
     __syncthreads();
   };
   auto key_in = [](u64 item) -> uint32_t { return ~(uint32_t)(item >> 32); };
@@ -503,6 +528,11 @@ __global__ __launch_bounds__(NT, 2) void sample_kernel(const SampleArgs a) {
     cluster.sync();                                              // every list has been read
     return total;
   };
+  auto add_to = [&](uint32_t* bin, u64 w) {                      // a 64-bit sum in two words: the carry is seen here
+    const uint32_t low = (uint32_t)w, old = atomicAdd(bin, low);
+    const uint32_t up = (uint32_t)(w >> 32) + (old + low < old ? 1u : 0u);
+    if (up) atomicAdd(bin + kMassBins, up);
+  };
   auto clear_hist = [&]() {
     for (int b = tid; b < kCountBins; b += NT) hist[b] = 0;
     __syncthreads();
@@ -523,12 +553,15 @@ __global__ __launch_bounds__(NT, 2) void sample_kernel(const SampleArgs a) {
       // the list they are all collected at once.  Otherwise the logits down to there are counted.
       int count = -1, bound = kCountBins - 1;
       const int64_t threads = CS * NT;
+      // With a top-p cut to follow, the list saves a pass of weights: worth sorting up to all of it (48 rows
+      // of 100277, top-k of 1000: 37 against 47 us, but without top-p 37 against 31).
+      const int finish = cut_p ? kList : kFinish;
       if (2 * (int64_t)top_k <= threads) {
         const uint32_t q = q_of(mine);
         if (q < 16777216u) atomicAdd(hist + (q >> kCountShift), 1u);
         if (find_bin(false, 0, total, [&](u64) { return limit; })) {
           bound = s_bin;
-          if (top_k + (int64_t)top_k * top_k / threads <= kFinish * 7 / 8) count = collect(kCountShift, 0, bound, true);
+          if (top_k + (int64_t)top_k * top_k / threads <= finish * 7 / 8) count = collect(kCountShift, 0, bound, true);
         }
         clear_hist();
       }
@@ -547,7 +580,7 @@ __global__ __launch_bounds__(NT, 2) void sample_kernel(const SampleArgs a) {
         if (!find_bin(false, 0, total, [&](u64) { return limit; })) continue;
         above = s_above;
         bin = s_bin;
-        if (above + s_in <= kFinish) count = collect(kCountShift, 0, bin, true);
+        if (above + s_in <= (u64)finish) count = collect(kCountShift, 0, bin, true);
       }
       if (count >= 0) {
         // all that may be kept, in one list
@@ -585,8 +618,41 @@ __global__ __launch_bounds__(NT, 2) void sample_kernel(const SampleArgs a) {
         kept = list_n;
         total = sums[kept - 1];
         if (tid == 0) s_goal = u > 0.f ? (u64)((double)u * (double)total) : 0ull;
-        for (int i = tid; i < kept; i += NT) own[i] = (u64)(uint32_t)all[i] << 32 | (uint32_t)i;
-        sort(own, kept);                                         // by index
+        // in the order of the index; of many only those of the bin of indices that holds the goal
+        u64 before = 0;
+        const bool narrow = kept > NT / 4;
+        int shift = 0;
+        while (a.vocab - 1 >> shift >= kMassBins) ++shift;
+        if (narrow) {
+          clear_hist();
+#pragma unroll
+          for (int j = 0; j < EACH; ++j) {
+            const int i = EACH * tid + j;
+            if (i < kept) add_to(hist + ((uint32_t)all[i] >> shift), w[j]);
+          }
+          __syncthreads();
+          const u64 v0 = (u64)hist[2 * tid + kMassBins] << 32 | hist[2 * tid];
+          const u64 v1 = (u64)hist[2 * tid + 1 + kMassBins] << 32 | hist[2 * tid + 1];
+          u64 sum_all;
+          const u64 inc = scan(v0 + v1, sum_all), goal = min(s_goal, total - 1);
+          if (goal < inc && goal >= inc - v0 - v1) {             // one thread
+            const bool second = goal >= inc - v1;
+            s_bin = 2 * tid + second;
+            s_above = second ? inc - v1 : inc - v0 - v1;
+          }
+          if (tid == 0) list_n = 0;
+          __syncthreads();
+          before = s_above;
+          for (int i = tid; i < kept; i += NT) {
+            const uint32_t index = (uint32_t)all[i];
+            if ((int)(index >> shift) == s_bin) own[atomicAdd(&list_n, 1)] = (u64)index << 32 | (uint32_t)i;
+          }
+          __syncthreads();
+          kept = list_n;
+        } else {
+          for (int i = tid; i < kept; i += NT) own[i] = (u64)(uint32_t)all[i] << 32 | (uint32_t)i;
+        }
+        sort(own, kept);
         const u64 goal = min(s_goal, total - 1);
         sum = 0;
 #pragma unroll
@@ -596,7 +662,7 @@ __global__ __launch_bounds__(NT, 2) void sample_kernel(const SampleArgs a) {
           sum += w[j];
         }
         u64 all_mass;
-        run = scan(sum, all_mass) - sum;
+        run = before + scan(sum, all_mass) - sum;
 #pragma unroll
         for (int j = 0; j < EACH; ++j) {
           if (run <= goal && goal < run + w[j]) {
@@ -612,7 +678,6 @@ __global__ __launch_bounds__(NT, 2) void sample_kernel(const SampleArgs a) {
       // the cut turns out to lie among them.
       // A warp's atomic takes as long for one logit as for 32, and few are near the maximum: each thread
       // queues its own.
-      uint32_t* hi = hist + kMassBins;
       constexpr int kQueue = 3 * kList * 2 / NT;
       float* queue = reinterpret_cast<float*>(own) + tid;
       int queued = 0;
@@ -621,11 +686,7 @@ __global__ __launch_bounds__(NT, 2) void sample_kernel(const SampleArgs a) {
           if (k >= queued) continue;
           const float x = queue[k * NT];
           const uint32_t b = min(q_of(x), 16777215u) >> kMassShift;
-          const u64 w = weight_of(soft.power(x));
-          const uint32_t low = (uint32_t)w;
-          const uint32_t old = atomicAdd(hist + b, low);         // a 64-bit sum in two words: the carry is seen here
-          const uint32_t up = (uint32_t)(w >> 32) + (old + low < old ? 1u : 0u);
-          if (up) atomicAdd(hi + b, up);
+          add_to(hist + b, weight_of(soft.power(x)));
         }
         queued = 0;
       };

@@ -75,6 +75,31 @@ def test_ties_go_to_the_lowest_index(dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("vocab", [1500, 20011, 150000])
+def test_long_lists_with_a_mass_cut(dtype, vocab):
+    rng = np.random.default_rng(vocab)
+    gen = torch.Generator("cuda").manual_seed(vocab)
+    ks = [129, 256, 257, 300, 512, 513, 900, 1000, 1024, 1025]
+    x = (2 * torch.randn(len(ks), vocab, generator=gen, device="cuda")).to(dtype)
+    host, u = x.double().cpu().numpy(), rng.random(len(ks)).astype(np.float32)
+    t, p = [], []
+    for r, k in enumerate(ks):                                 # hot rows keep hundreds of tokens, cold ones few
+        while True:
+            one = float(np.float32(rng.uniform(0.3, 4.0))), float(np.float32(rng.uniform(0.2, 0.999)))
+            if cut_is_far(host[r], one[0], k, one[1], 0.0):
+                break
+        t.append(one[0])
+        p.append(one[1])
+    ids, logp = run(x, u, t, ks, p)
+    for r, k in enumerate(ks):
+        ref, lp, margin = oracle.sample(host[r], t[r], k, p[r], 0.0, float(u[r]))
+        assert ids[r] >= 0
+        if margin > 1e-5:
+            assert ids[r] == ref, (k, t[r], p[r])
+            assert abs(logp[r] - lp) <= 2e-5
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_infinities_and_nan(dtype):
     inf, nan, low = float("inf"), float("nan"), torch.finfo(dtype).min
     x = torch.full((6, 5000), -inf, device="cuda", dtype=dtype)
