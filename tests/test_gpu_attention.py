@@ -201,6 +201,63 @@ def test_qkv(dtype, dim, rotary, pairs, norm, heads):
         assert torch.equal(c.permute(0, 2, 1, 3)[keep], c0.permute(0, 2, 1, 3)[keep])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dim,rotary,pairs,norm,heads,rows", [
+    (128, 128, False, True, (32, 8), 2100), (128, 64, True, False, (60, 10), 1003), (64, 64, False, True, (96, 32), 1200),
+    (64, 16, True, True, (7, 7), 7500), (128, 0, False, True, (20, 1), 3700), (128, 128, False, True, (300, 100), 170)])
+def test_qkv_of_many_rows(dtype, dim, rotary, pairs, norm, heads, rows):
+    # one request's rows, every 97th of them padding, over a pool with the slots in no order
+    hq, hkv = heads
+    s = Step([0], [4], dtype, hq, hkv, dim, rotary_dim=rotary, rotary_style=moe.MOE_ROTARY_PAIRS if pairs else moe.MOE_ROTARY_HALF,
+             norm_eps=1e-5)
+    gen = torch.Generator("cuda").manual_seed(rows)
+    wide = torch.randn(rows, (hq + 2 * hkv) * dim + 8, generator=gen, device="cuda").mul_(3).to(s.dtype)
+    qkv = wide[:, :(hq + 2 * hkv) * dim]
+    w = [torch.randn(dim, generator=gen, device="cuda").to(s.dtype) if norm else None for _ in range(2)]
+    rope = torch.randn(2 * rows, rotary, generator=gen, device="cuda") if rotary else None
+    pos = torch.randint(0, 2 * rows, (rows,), generator=gen, device="cuda").int()
+    pages = -(-rows // s.page) + 2
+    slot = torch.randperm(pages * s.page, generator=gen, device="cuda")[:rows].int()
+    slot[::97] = -1
+    q = torch.full((rows, hq, dim), 7.0, device="cuda", dtype=s.dtype)
+    caches = [torch.full((pages, hkv, s.page, dim), 7.0, device="cuda", dtype=s.dtype) for _ in range(2)]
+    s.handle.qkv(qkv, *w, rope, pos, slot, q, *caches)
+    assert s.handle.status() == moe.MOE_OK
+    x = qkv.double().view(rows, hq + 2 * hkv, dim)
+    size = x.abs().amax(-1, keepdim=True)
+    if norm:
+        scale = torch.cat([w[0].double().expand(hq, dim), w[1].double().expand(hkv, dim)])
+        y = x[:, :hq + hkv] / (x[:, :hq + hkv].square().mean(-1, keepdim=True) + 1e-5).sqrt() * scale
+        size = torch.cat([y.abs().amax(-1, keepdim=True), size[:, hq + hkv:]], 1)
+    else:
+        y = x[:, :hq + hkv].clone()
+    if rotary:
+        cos, sin = rope.double()[pos.long()].split(rotary // 2, -1)
+        cos, sin = cos[:, None], sin[:, None]
+        a, b = (y[..., 0:rotary:2], y[..., 1:rotary:2]) if pairs else (y[..., :rotary // 2], y[..., rotary // 2:rotary])
+        a, b = a * cos - b * sin, b * cos + a * sin
+        size = size * 2 * rope.abs().max().double()                      # bounds |a cos| + |b sin|
+        y[..., :rotary] = torch.stack([a, b], -1).flatten(-2) if pairs else torch.cat([a, b], -1)
+    one = 2.0 ** -8 if s.dtype is torch.bfloat16 else 2.0 ** -24
+    ref = torch.cat([y, x[:, hq + hkv:]], 1)
+
+    def close(got, ref, size):
+        return bool(((got.double() - ref).abs() <= one * ref.abs() + 1e-6 * size).all())
+    assert close(q, ref[:, :hq], size[:, :hq])
+    live = slot >= 0
+    at = slot[live].long()
+    for c, h in zip(caches, (hq, hq + hkv)):
+        assert close(c[at // s.page, :, at % s.page], ref[live, h:h + hkv], size[live, h:h + hkv])
+        flat = c.permute(0, 2, 1, 3).reshape(-1, hkv, dim)
+        rest = torch.ones(len(flat), dtype=torch.bool, device="cuda")
+        rest[at] = False
+        assert (flat[rest] == 7.0).all()
+    # a position and a slot outside are reported, the rest is done
+    pos[rows // 2], slot[rows // 3] = 2 * rows, pages * s.page
+    s.handle.qkv(qkv, *w, rope, pos, slot, q, *caches)
+    assert s.handle.status() == moe.MOE_ERR_BOUNDS
+
+
 def test_qkv_reports_positions_and_slots_out_of_range():
     s = Step([0], [4], hq=2, hkv=1)
     gen = torch.Generator("cuda").manual_seed(3)
@@ -255,6 +312,20 @@ def test_attention_long_rows_are_split(dtype):
     check_attention(Step([9000, 17, 4000], [1, 1, 1], dtype, 8, 1, page=64), poison=False)
     check_attention(Step([30011], [1], dtype, 4, 1, page=32), poison=False)
     check_attention(Step([6000], [9], dtype, 8, 2), poison=False)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("hq", [1, 2, 3, 4, 8, 16])
+def test_attention_of_few_rows_in_many_pieces(dtype, dim, hq):
+    check_attention(Step([20500], [1], dtype, hq, 1, dim, page=128), poison=False)
+    check_attention(Step([2100], [3], dtype, hq, 1, dim), poison=False)
+
+
+@pytest.mark.parametrize("new", [40, 100, 203])
+def test_attention_of_a_chunk_in_many_pieces(new):
+    check_attention(Step([5000], [new], "bf16", 8, 1), poison=False)
+    check_attention(Step([2000, 30], [new, 7], "bf16", 4, 1, 64, window=700))
 
 
 def test_attention_prefill_of_many_rows():
