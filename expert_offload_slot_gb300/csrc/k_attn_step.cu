@@ -5,6 +5,7 @@
 //   off_r  = sum over earlier requests of (need - have)
 //   table[r, j] = free_pages[head + off_r + j - have_r]      have_r <= j < need_r
 //   row t of request r: pos = ctx_r + t - row_start_r, slot = table[r, pos / P] * P + pos % P
+// Without a free list every page is in the table already: nothing is written there or taken.
 // Every CTA scans the lengths of all requests itself (they are a few KB that L2
 // serves), so one launch does it all and no CTA waits for another.  A step moves
 // a few hundred KB at most, so the launch bounds it: 384 requests with 25k new
@@ -83,7 +84,8 @@ __global__ __launch_bounds__(TT) void attn_tables_kernel(const TablesArgs a) {
   }
   if (a.R == 0 && tid == 0) s_row[0] = 0;
   __syncthreads();
-  const int total = s_row[a.R], taken = s_carry[1];
+  const bool given = a.num_free == 0;        // the tables are complete: only the maps are wanted
+  const int total = s_row[a.R], taken = given ? 0 : s_carry[1];
   full |= total > a.rows;
   auto fresh_page = [&](int at) -> int {     // entry `at` of the free list beyond the head; -1 when it is short
     if (head < 0 || (int64_t)head + at >= a.num_free) { full = true; return -1; }
@@ -95,6 +97,7 @@ __global__ __launch_bounds__(TT) void attn_tables_kernel(const TablesArgs a) {
   for (int r = blockIdx.x * (TT / 32) + wid; r < a.R; r += warps) {
     const Lens v = lens_of(a, r, bad);
     full |= v.need > a.table_stride;
+    if (given) continue;
     for (int j = v.have + lane; j < min(v.need, a.table_stride); j += 32)
       a.table[(size_t)r * a.table_stride + j] = fresh_page(s_off[r] + j - v.have);
   }
@@ -112,9 +115,10 @@ __global__ __launch_bounds__(TT) void attn_tables_kernel(const TablesArgs a) {
       pos = v.ctx + t - s_row[lo];
       const int j = pos >> a.page_log2;
       if (j < a.table_stride) {
-        const int page = j >= v.have ? fresh_page(s_off[lo] + j - v.have) : a.table[(size_t)lo * a.table_stride + j];
+        const bool fresh = j >= v.have && !given;
+        const int page = fresh ? fresh_page(s_off[lo] + j - v.have) : a.table[(size_t)lo * a.table_stride + j];
         if (page >= 0) slot = (page << a.page_log2) + (pos & (a.page - 1));
-        else bad = bad || j < v.have;
+        else bad = bad || !fresh;
       }
     }
     a.positions[t] = pos;

@@ -482,7 +482,8 @@ MOE_API moe_status moe_attn_clear_status(moe_attn* attn);
  *   free_pages        device int32 [num_free]; free_head, free_head_out device
  *                     int32: how many of them are taken before and after (the two
  *                     may be the same address).  num_free 0: the tables are
- *                     complete already and only the maps are wanted
+ *                     complete already and only the maps are wanted; block_table
+ *                     is not written and the head stays as it is
  *   rows              rows of the step's tensors, at least the sum of new_len
  *   row_start         out int32 [R+1]: first row of each request, then the sum
  *   seq_len           out int32 [R]: ctx + new

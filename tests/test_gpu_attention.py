@@ -480,3 +480,31 @@ def test_refusals():
     assert lib.moe_attn_tables(h, s.seq.data_ptr(), s.seq.data_ptr(), 1, s.table.data_ptr(), s.width, s.free_d.data_ptr(), 1,
                                s.head.data_ptr(), s.head.data_ptr(), 2, s.start.data_ptr(), s.seq.data_ptr(),
                                s.pos.data_ptr(), s.slot.data_ptr(), st) == moe.MOE_ERR_INVALID
+
+
+@pytest.mark.parametrize("page", [16, 64])
+def test_tables_that_are_complete_are_only_mapped(page):
+    # growth over page ends, requests that rest or begin, and no free list: the pages come from the table itself
+    ctx, new, rows = [16, 5, 0, 127, 200, 64, 0], [1, 30, 40, 2, 0, 64, 0], 140
+    rng = np.random.default_rng(page)
+    need = [-(-(c + n) // page) for c, n in zip(ctx, new)]
+    table = np.full((len(ctx), max(need) + 1), 1 << 30)
+    order = rng.permutation(sum(need))
+    for r, n in enumerate(need):
+        table[r, :n] = order[sum(need[:r]):sum(need[:r + 1])]
+    handle = moe.Attention(moe.make_attn_config(8, 2, 128, page))
+    given, none = ints(table), ints([])
+    head, start, seq, pos, slot = ints([5]), ints(np.zeros(len(ctx) + 1)), ints(np.zeros(len(ctx))), ints(np.zeros(rows)), ints(np.zeros(rows))
+    handle.tables(ints(ctx), ints(new), given, none, ints([7]), head, start, seq, pos, slot)
+    assert handle.status() == moe.MOE_OK
+    assert given.cpu().tolist() == table.tolist() and int(head) == 7         # nothing is taken or written
+    where = [(r, p) for r, (c, n) in enumerate(zip(ctx, new)) for p in range(c, c + n)]
+    pad = rows - len(where)
+    assert pos.cpu().tolist() == [p for _, p in where] + [0] * pad
+    assert slot.cpu().tolist() == [int(table[r, p // page]) * page + p % page for r, p in where] + [-1] * pad
+    assert start.cpu().tolist() == [0, *np.cumsum(new).tolist()]
+    assert seq.cpu().tolist() == [c + n for c, n in zip(ctx, new)]
+    # a page that is missing all the same is reported, and its rows have no slot
+    given[1, (5 + 30 - 1) // page] = -1
+    handle.tables(ints(ctx), ints(new), given, none, ints([7]), head, start, seq, pos, slot)
+    assert handle.status() == moe.MOE_ERR_BOUNDS and int(slot[30]) == -1 and int(slot[0]) >= 0
