@@ -44,6 +44,29 @@ moe_status launched(cudaError_t e, const char* what) {
   return e == cudaSuccess ? MOE_OK : fail(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
+// Makes a handle's device current for a call and gives the thread its own back at the end: the stream
+// of a call may be the default one, which is that of the current device.
+class DeviceGuard {
+ public:
+  explicit DeviceGuard(int device) {
+    error = cudaGetDevice(&before);
+    if (error == cudaSuccess && before != device) {
+      error = cudaSetDevice(device);
+      changed = error == cudaSuccess;
+    }
+  }
+  ~DeviceGuard() {
+    if (changed) cudaSetDevice(before);
+  }
+  DeviceGuard(const DeviceGuard&) = delete;
+  DeviceGuard& operator=(const DeviceGuard&) = delete;
+  cudaError_t error;
+
+ private:
+  int before = 0;
+  bool changed = false;
+};
+
 bool misaligned(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
 
 moe_status check_config(const moe_attn_config* c) {
@@ -135,8 +158,8 @@ MOE_API moe_status moe_attn_create(const moe_attn_config* cfg, int device, moe_a
   cudaError_t e = cudaGetDeviceCount(&ndev);
   if (e != cudaSuccess) return launched(e, "cudaGetDeviceCount");
   if (device < 0 || device >= ndev) return fail(MOE_ERR_INVALID, "device %d out of range", device);
-  e = cudaSetDevice(device);
-  if (e != cudaSuccess) return launched(e, "cudaSetDevice");
+  const DeviceGuard guard(device);
+  if (guard.error != cudaSuccess) return launched(guard.error, "selecting the device");
   e = cfg->dtype == MOE_F32 ? prepare_attn_f32(cfg->head_dim) : prepare_attn_rows(cfg->head_dim);
   if (e == cudaSuccess && cfg->dtype == MOE_BF16) e = prepare_attn_tiles(cfg->head_dim);
   if (e == cudaSuccess) e = prepare_attn_qkv(cfg->dtype, cfg->head_dim);
@@ -178,7 +201,7 @@ MOE_API moe_status moe_attn_create(const moe_attn_config* cfg, int device, moe_a
 
 MOE_API moe_status moe_attn_destroy(moe_attn* A) {
   if (!A) return MOE_OK;
-  cudaSetDevice(A->device);
+  const DeviceGuard guard(A->device);
   cudaDeviceSynchronize();
   cudaFree(A->work);
   delete A;
@@ -188,7 +211,8 @@ MOE_API moe_status moe_attn_destroy(moe_attn* A) {
 MOE_API moe_status moe_attn_get_status(moe_attn* A) {
   if (!A) return fail(MOE_ERR_INVALID, "handle is NULL");
   int32_t st = 0;
-  cudaError_t e = cudaSetDevice(A->device);
+  const DeviceGuard guard(A->device);
+  cudaError_t e = guard.error;
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
   if (e == cudaSuccess) e = cudaMemcpy(&st, A->status, sizeof st, cudaMemcpyDeviceToHost);
   return e == cudaSuccess ? static_cast<moe_status>(st) : launched(e, "reading the status");
@@ -196,7 +220,8 @@ MOE_API moe_status moe_attn_get_status(moe_attn* A) {
 
 MOE_API moe_status moe_attn_clear_status(moe_attn* A) {
   if (!A) return fail(MOE_ERR_INVALID, "handle is NULL");
-  cudaError_t e = cudaSetDevice(A->device);
+  const DeviceGuard guard(A->device);
+  cudaError_t e = guard.error;
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
   if (e == cudaSuccess) e = cudaMemset(A->arrived, 0, A->zero_bytes);   // counters a timed-out call may have left, too
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
@@ -227,6 +252,8 @@ MOE_API moe_status moe_attn_tables(moe_attn* A, const int32_t* ctx_len, const in
   a.head_out = free_head_out; a.row_start = row_start; a.seq_len = seq_len; a.positions = positions; a.slots = slot_map;
   a.status = A->status; a.ticket = A->ticket; a.R = R; a.table_stride = table_stride; a.num_free = num_free; a.rows = rows;
   a.page = A->cfg.page_size; a.page_log2 = A->page_log2;
+  const DeviceGuard guard(A->device);
+  if (guard.error != cudaSuccess) return launched(guard.error, "selecting the device");
   return launched(launch_attn_tables(a, static_cast<cudaStream_t>(stream)), "moe_attn_tables");
 }
 
@@ -258,6 +285,8 @@ MOE_API moe_status moe_attn_qkv(moe_attn* A, const void* qkv, int64_t qkv_stride
   a.page_log2 = A->page_log2; a.rotary = c.rotary_dim; a.pairs = c.rotary_style == MOE_ROTARY_PAIRS; a.rope_len = rope_len;
   a.eps = c.norm_eps;
   a.heads = a.Hq + 2 * a.Hkv;
+  const DeviceGuard guard(A->device);
+  if (guard.error != cudaSuccess) return launched(guard.error, "selecting the device");
   return launched(launch_attn_qkv(a, c.dtype, c.head_dim, A->sms, static_cast<cudaStream_t>(stream)), "moe_attn_qkv");
 }
 
@@ -289,6 +318,8 @@ MOE_API moe_status moe_attn_forward(moe_attn* A, const void* q, int64_t q_stride
   a.scale_log2 = c.softmax_scale * 1.44269504088896340736f;
   a.part_o = A->part_o; a.part_ml = A->part_ml; a.arrived = A->arrived; a.status = A->status;
   divider(a.group, a.group_mul, a.group_shift);
+  const DeviceGuard guard(A->device);
+  if (guard.error != cudaSuccess) return launched(guard.error, "selecting the device");
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (c.dtype == MOE_F32) return launched(launch_attn_f32(a, c.head_dim, attn_grid(A->sms), s), "moe_attn_forward");
   // Up to two row tiles of 16 the row kernel is ahead of the tile kernel although it reads the keys

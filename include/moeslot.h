@@ -437,7 +437,9 @@ MOE_API moe_status moe_route_topk_noalloc(int32_t num_experts, int32_t top_k, in
  *
  * The handle owns a workspace (partial results of split rows, counters, the
  * status word) that all layers and steps share: calls on one handle must be
- * ordered (one stream, or streams joined by events).  Only moe_attn_create
+ * ordered (one stream, or streams joined by events).  A call runs on the handle's
+ * device, whichever is current (a NULL stream is that device's default stream),
+ * and leaves the thread's current device as it was.  Only moe_attn_create
  * allocates and no call synchronises except the status calls, so a step can
  * be captured into a CUDA graph; lengths, tables and free list are read on the
  * device at run time.  Sizes the device finds inconsistent are clamped, never
