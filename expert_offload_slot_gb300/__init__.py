@@ -370,26 +370,27 @@ _kinds = {}
 
 
 def _torch_kinds():
-    """(float32, bfloat16, int32) and the raw-stream getter, looked up once."""
+    """(float32, bfloat16, int32), the raw-stream getter and the current device, looked up once."""
     if not _kinds:
         import torch
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         _kinds["stream"] = raw or (lambda device: torch.cuda.current_stream(device).cuda_stream)
+        _kinds["device"], _kinds["on"] = torch.cuda.current_device, torch.cuda.device
         _kinds[MOE_F32], _kinds[MOE_BF16], _kinds["i32"] = torch.float32, torch.bfloat16, torch.int32
     return _kinds
 
 
-def _flat(name, t, kind, count):
-    """Address of a contiguous CUDA tensor of this type with `count` elements."""
-    if t.dtype is kind and t.numel() == count and t.is_cuda and t.is_contiguous():
+def _flat(name, t, kind, count, device):
+    """Address of a contiguous tensor of this type with `count` elements on GPU `device` (a host tensor's is -1)."""
+    if t.dtype is kind and t.numel() == count and t.get_device() == device and t.is_contiguous():
         return t.data_ptr()
-    raise ValueError(f"{name} must be a contiguous CUDA tensor of {kind} with {count} elements, "
+    raise ValueError(f"{name} must be a contiguous tensor of {kind} with {count} elements on cuda:{device}, "
                      f"got {t.dtype}, {tuple(t.shape)}, strides {t.stride()}, on {t.device}")
 
 
-def _rows(name, t, kind, rows, width):
-    """Address and row stride in elements of a CUDA tensor [rows, ...] whose rows hold `width` contiguous elements."""
-    if t.dtype is kind and t.numel() == rows * width and t.is_cuda:
+def _rows(name, t, kind, rows, width, device):
+    """Address and row stride in elements of a tensor [rows, ...] on GPU `device` whose rows hold `width` contiguous elements."""
+    if t.dtype is kind and t.numel() == rows * width and t.get_device() == device:
         if t.is_contiguous():
             return t.data_ptr(), width
         inner = 1
@@ -399,7 +400,7 @@ def _rows(name, t, kind, rows, width):
             inner *= n
         else:
             return t.data_ptr(), (t.stride(0) if rows > 1 else width)
-    raise ValueError(f"{name} must be a CUDA tensor of {kind} with {rows} rows of {width} contiguous elements, "
+    raise ValueError(f"{name} must be a tensor of {kind} with {rows} rows of {width} contiguous elements on cuda:{device}, "
                      f"got {t.dtype}, {tuple(t.shape)}, strides {t.stride()}, on {t.device}")
 
 
@@ -438,45 +439,46 @@ class Attention:
     def tables(self, ctx_len, new_len, block_table, free_pages, free_head, free_head_out, row_start, seq_len, positions,
                slot_map, stream=None):
         """Fill block_table, free_head_out, row_start, seq_len, positions and slot_map for the step."""
-        i32, n, rows, free = self._i32, ctx_len.size(0), positions.size(0), free_pages.size(0)
+        i32, n, rows, free, dev = self._i32, ctx_len.size(0), positions.size(0), free_pages.size(0), self._device
         width = block_table.size(1)
         st = _lib.moe_attn_tables(
-            self.h, _flat("ctx_len", ctx_len, i32, n), _flat("new_len", new_len, i32, n), n,
-            _flat("block_table", block_table, i32, n * width), width, _flat("free_pages", free_pages, i32, free), free,
-            _flat("free_head", free_head, i32, 1), _flat("free_head_out", free_head_out, i32, 1), rows,
-            _flat("row_start", row_start, i32, n + 1), _flat("seq_len", seq_len, i32, n),
-            _flat("positions", positions, i32, rows), _flat("slot_map", slot_map, i32, rows),
-            self._current(self._device) if stream is None else _stream(stream))
+            self.h, _flat("ctx_len", ctx_len, i32, n, dev), _flat("new_len", new_len, i32, n, dev), n,
+            _flat("block_table", block_table, i32, n * width, dev), width,
+            _flat("free_pages", free_pages, i32, free, dev), free, _flat("free_head", free_head, i32, 1, dev),
+            _flat("free_head_out", free_head_out, i32, 1, dev), rows, _flat("row_start", row_start, i32, n + 1, dev),
+            _flat("seq_len", seq_len, i32, n, dev), _flat("positions", positions, i32, rows, dev),
+            _flat("slot_map", slot_map, i32, rows, dev), self._current(dev) if stream is None else _stream(stream))
         if st:
             _check(st, "moe_attn_tables")
 
     def qkv(self, qkv, q_norm, k_norm, rope, positions, slot_map, q, k_cache, v_cache, stream=None):
         """Norm, rotation and cache write of qkv [rows, (Hq + 2 Hkv) * D]; queries go to q [rows, Hq, D]."""
-        kind, i32, rows, pages, dim = self._kind, self._i32, qkv.size(0), k_cache.size(0), self._dim
+        kind, i32, rows, pages, dim, dev = self._kind, self._i32, qkv.size(0), k_cache.size(0), self._dim, self._device
         length = 0 if rope is None else rope.size(0)
-        at, stride = _rows("qkv", qkv, kind, rows, self._qkv_width)
+        at, stride = _rows("qkv", qkv, kind, rows, self._qkv_width, dev)
         st = _lib.moe_attn_qkv(
-            self.h, at, stride, rows, None if q_norm is None else _flat("q_norm", q_norm, kind, dim),
-            None if k_norm is None else _flat("k_norm", k_norm, kind, dim),
-            None if rope is None else _flat("rope", rope, self._f32, length * self._rotary), length,
-            _flat("positions", positions, i32, rows), _flat("slot_map", slot_map, i32, rows),
-            _flat("q", q, kind, rows * self._q_width), _flat("k_cache", k_cache, kind, pages * self._page),
-            _flat("v_cache", v_cache, kind, pages * self._page), pages,
-            self._current(self._device) if stream is None else _stream(stream))
+            self.h, at, stride, rows, None if q_norm is None else _flat("q_norm", q_norm, kind, dim, dev),
+            None if k_norm is None else _flat("k_norm", k_norm, kind, dim, dev),
+            None if rope is None else _flat("rope", rope, self._f32, length * self._rotary, dev), length,
+            _flat("positions", positions, i32, rows, dev), _flat("slot_map", slot_map, i32, rows, dev),
+            _flat("q", q, kind, rows * self._q_width, dev), _flat("k_cache", k_cache, kind, pages * self._page, dev),
+            _flat("v_cache", v_cache, kind, pages * self._page, dev), pages,
+            self._current(dev) if stream is None else _stream(stream))
         if st:
             _check(st, "moe_attn_qkv")
 
     def forward(self, q, row_start, seq_len, max_new, k_cache, v_cache, block_table, out, stream=None):
         """Attention of q [rows, Hq, D] over the cache, into out [rows, Hq, D]."""
-        kind, i32, rows, n, pages = self._kind, self._i32, q.size(0), seq_len.size(0), k_cache.size(0)
+        kind, i32, rows, n, pages, dev = self._kind, self._i32, q.size(0), seq_len.size(0), k_cache.size(0), self._device
         width = block_table.size(1)
-        at, stride = _rows("q", q, kind, rows, self._q_width)
+        at, stride = _rows("q", q, kind, rows, self._q_width, dev)
         st = _lib.moe_attn_forward(
-            self.h, at, stride, rows, _flat("row_start", row_start, i32, n + 1), _flat("seq_len", seq_len, i32, n), n,
-            max_new, _flat("k_cache", k_cache, kind, pages * self._page),
-            _flat("v_cache", v_cache, kind, pages * self._page), pages,
-            _flat("block_table", block_table, i32, n * width), width, _flat("out", out, kind, rows * self._q_width),
-            self._current(self._device) if stream is None else _stream(stream))
+            self.h, at, stride, rows, _flat("row_start", row_start, i32, n + 1, dev), _flat("seq_len", seq_len, i32, n, dev), n,
+            max_new, _flat("k_cache", k_cache, kind, pages * self._page, dev),
+            _flat("v_cache", v_cache, kind, pages * self._page, dev), pages,
+            _flat("block_table", block_table, i32, n * width, dev), width,
+            _flat("out", out, kind, rows * self._q_width, dev),
+            self._current(dev) if stream is None else _stream(stream))
         if st:
             _check(st, "moe_attn_forward")
 
@@ -493,12 +495,19 @@ def moe_sample(logits, u, ids, logp=None, temperature=None, top_k=None, top_p=No
     f32, i32 = kinds[MOE_F32], kinds["i32"]
     rows, vocab = logits.shape
     dtype = MOE_F32 if logits.dtype is f32 else MOE_BF16
-    at, stride = _rows("logits", logits, f32 if dtype == MOE_F32 else kinds[MOE_BF16], rows, vocab)
-    st = _lib.moe_sample(
-        at, dtype, rows, vocab, stride, None if temperature is None else _flat("temperature", temperature, f32, rows),
-        None if top_k is None else _flat("top_k", top_k, i32, rows), None if top_p is None else _flat("top_p", top_p, f32, rows),
-        None if min_p is None else _flat("min_p", min_p, f32, rows), _flat("u", u, f32, rows), _flat("ids", ids, i32, rows),
-        None if logp is None else _flat("logp", logp, f32, rows),
-        kinds["stream"](logits.device.index) if stream is None else _stream(stream))
+    dev = max(logits.get_device(), 0)          # a host tensor (-1) is refused below
+    at, stride = _rows("logits", logits, f32 if dtype == MOE_F32 else kinds[MOE_BF16], rows, vocab, dev)
+    args = (
+        at, dtype, rows, vocab, stride, None if temperature is None else _flat("temperature", temperature, f32, rows, dev),
+        None if top_k is None else _flat("top_k", top_k, i32, rows, dev),
+        None if top_p is None else _flat("top_p", top_p, f32, rows, dev),
+        None if min_p is None else _flat("min_p", min_p, f32, rows, dev), _flat("u", u, f32, rows, dev),
+        _flat("ids", ids, i32, rows, dev), None if logp is None else _flat("logp", logp, f32, rows, dev),
+        kinds["stream"](dev) if stream is None else _stream(stream))
+    if kinds["device"]() == dev:               # the library's call runs on the current device
+        st = _lib.moe_sample(*args)
+    else:
+        with kinds["on"](dev):
+            st = _lib.moe_sample(*args)
     if st:
         _check(st, "moe_sample")
