@@ -98,10 +98,23 @@ __device__ __forceinline__ int attn_tiles(const AttnArgs& a, const AttnRequest& 
   return (q.n * a.group + BM - 1) / BM;
 }
 
+// Units of a call, at most: more are refused, so that counts of them fit in 32 bits.  So many would take
+// any of the kernels seconds (heads of 128: bf16, 512 rows by 128 keys a unit, 36 PFLOP or 24 s; 16 rows, 70
+// TB of keys and values; fp32, 64 rows by 32 keys, 1.1 PFLOP or 36 s; 8 rows, 35 TB).
+constexpr int64_t kAttnMaxUnits = 1 << 30;
+
+// Sum over the warp's lanes of 64-bit counts below 2^52.
+__device__ __forceinline__ int64_t attn_warp_sum(int64_t v) {
+  const uint32_t low = __reduce_add_sync(0xffffffffu, (uint32_t)v & 0x3ffffffu);
+  const uint32_t high = __reduce_add_sync(0xffffffffu, (uint32_t)(v >> 26));
+  return ((int64_t)high << 26) + low;
+}
+
 // Units of a request's row tiles for one kv head, and the most of one tile: its lane by itself where
-// there are few tiles, else the whole warp for one lane after another.
+// there are few tiles, else the whole warp for one lane after another.  2^20 rows of 1024 heads over
+// 2^31 keys have 2^24 tiles of 2^26 units, so the sum has 64 bits.
 template <int BM>
-__device__ __forceinline__ void attn_count_units(const AttnArgs& a, const AttnRequest& q, int nt, int unit, int& sum,
+__device__ __forceinline__ void attn_count_units(const AttnArgs& a, const AttnRequest& q, int nt, int unit, int64_t& sum,
                                                  int& longest) {
   const int lane = threadIdx.x & 31;
   sum = longest = 0;
@@ -118,13 +131,14 @@ __device__ __forceinline__ void attn_count_units(const AttnArgs& a, const AttnRe
     x.n = __shfl_sync(0xffffffffu, q.n, src);
     x.seq = __shfl_sync(0xffffffffu, q.seq, src);
     const int xt = __shfl_sync(0xffffffffu, nt, src);
-    int total = 0, top = 0;
+    int64_t total = 0;
+    int top = 0;
     for (int i = lane; i < xt; i += 32) {
       attn_units<BM>(a, x, i, unit, u0, nu);
       total += nu;
       top = max(top, nu);
     }
-    total = __reduce_add_sync(0xffffffffu, total);
+    total = attn_warp_sum(total);
     top = __reduce_max_sync(0xffffffffu, top);
     if (lane == src) {
       sum = total;
@@ -161,9 +175,10 @@ struct AttnSplit {
   }
 };
 
-// Called by all threads of the CTA (NT of them) for part c of at most `most`.  `sm` holds 64 ints.
-// False when the part has no work.  Up to 32 requests, every warp finds the part by itself with a
-// request in each lane: no barrier stands before the first load of the cache.
+// Called by all threads of the CTA (NT of them) for part c of at most `most`.  `sm` holds 64 ints, on 8
+// bytes.  False when the part has no work, or the call too many units (reported).  Up to 32 requests, every
+// warp finds the part by itself with a request in each lane: no barrier stands before the first load of the
+// cache.
 // `join`: units that the join of one piece takes; k pieces of an item of nu units take nu / k + join k,
 // so shorter ones than sqrt(join nu) are not made (tile kernel, 204 tokens over 2000 keys, 8 q heads and
 // one kv head: 37 us with pieces of one unit, 24 with 4).  0 where a join takes a small part of a unit.
@@ -176,14 +191,29 @@ __device__ __forceinline__ bool attn_find_range(const AttnArgs& a, int c, int mo
   const int per = alone ? 1 : (a.R + NT - 1) / NT;
   const int r0 = alone ? lane : min(tid * per, a.R), r1 = alone ? min(lane + 1, a.R) : min(r0 + per, a.R);
   AttnRequest q = {0, 0, 0};                   // of the last request looked at: the only one when per is 1
-  int mine = 0, longest = 0;
+  int64_t units = 0;
+  int longest = 0;
   for (int k = 0; k < per; ++k) {
     if (r0 + k < r1) q = attn_request(a, r0 + k);
     else q.n = 0;
-    int sum;
+    int64_t sum;
     attn_count_units<BM>(a, q, attn_tiles<BM>(a, q), unit, sum, longest);
-    mine += sum * a.Hkv;
+    units += sum * a.Hkv;
   }
+  int64_t all = 0;                             // of all requests: 32 small numbers need no adding up
+  if (!alone || __any_sync(0xffffffffu, units > kAttnMaxUnits / 32)) all = attn_warp_sum(units);
+  if (!alone) {
+    if (lane == 0) reinterpret_cast<int2*>(sm)[wid] = make_int2((int)(all & 0x3ffffff), (int)(all >> 26));
+    __syncthreads();
+    all = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) all += ((int64_t)sm[2 * w + 1] << 26) + sm[2 * w];
+  }
+  if (all > kAttnMaxUnits) {                   // no CTA takes any
+    if (tid == 0) attn_status(a.status, MOE_ERR_CAPACITY);
+    return false;
+  }
+  const int mine = (int)units;
   // sum over the requests before this thread's, and over all
   auto scan = [&](int v, int& before, int& total) {
     int run = v;

@@ -37,7 +37,7 @@ __global__ __launch_bounds__(NT, 2) void attn_f32_kernel(const AttnArgs a) {
   float* sk = sq + BM * LD;                 // [BN][LD]
   float* sv = sk + BN * LD;                 // [BN][LD]
   float* prob = sv + BN * LD;               // [BN][LP] probabilities, rows innermost
-  __shared__ int32_t sched[64];
+  __shared__ __align__(8) int32_t sched[64];
   sm103::grid_wait();
   AttnSplit sp;
   AttnCursor c;
@@ -201,7 +201,7 @@ __global__ __launch_bounds__(NT, 2) void attn_f32_few_kernel(const AttnArgs a) {
   float* part = sq + FM * D;                                     // [DQ][FM][FN] scores over a part of D each
   float* prob = part + DQ * FM * FN;                             // [FN][FM]
   float* fac = prob + FN * FM;                                   // [FM] scale of this step; then m, l
-  __shared__ int32_t sched[64];
+  __shared__ __align__(8) int32_t sched[64];
   sm103::grid_wait();
   AttnSplit sp;
   AttnCursor c;

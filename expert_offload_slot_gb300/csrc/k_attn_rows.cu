@@ -51,7 +51,7 @@ __global__ __launch_bounds__(NT, 1) void attn_rows_kernel(const __grid_constant_
   using C = RowsCfg<D>;
   constexpr int KS = D / 16, ND = D / 8;
   extern __shared__ uint8_t raw[];
-  __shared__ int32_t sched[64];
+  __shared__ __align__(8) int32_t sched[64];
   __shared__ __align__(8) uint64_t bars[NW * C::kStages];
   __shared__ float sm_m[NW / 2][BM], sm_l[NW / 2][BM], all_m[NW][8], all_l[NW][8];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));

@@ -109,7 +109,8 @@ __device__ __forceinline__ bool tile_work(const AttnArgs& a, int32_t* sm, uint8_
   const int per = (a.R + NT - 1) / NT;
   const int r0 = min(tid * per, a.R), r1 = min(r0 + per, a.R);
   AttnRequest q = {0, 0, 0};
-  int units = 0, tiles = 0, longest = 0;
+  int64_t units = 0;
+  int tiles = 0, longest = 0;
   for (int k = 0; k < per; ++k) {
     q.n = 0;
     if (r0 + k < r1) {
@@ -117,7 +118,8 @@ __device__ __forceinline__ bool tile_work(const AttnArgs& a, int32_t* sm, uint8_
       s_req[r0 + k] = make_int4(q.start, q.n, q.seq, 0);
     }
     const int nt = attn_tiles<BM>(a, q);
-    int sum, top;
+    int64_t sum;
+    int top;
     attn_count_units<BM>(a, q, nt, UNIT, sum, top);
     units += sum;
     tiles += nt;
@@ -129,22 +131,29 @@ __device__ __forceinline__ bool tile_work(const AttnArgs& a, int32_t* sm, uint8_
     const int v = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += v;
   }
-  units = __reduce_add_sync(0xffffffffu, units);
+  units = attn_warp_sum(units);
   longest = __reduce_max_sync(0xffffffffu, longest);
   if (lane == 31) sm[wid] = inc;
   if (lane == 0) {
-    sm[16 + wid] = units;
-    sm[32 + wid] = longest;
+    sm[16 + wid] = (int)(units & 0x3ffffff);
+    sm[32 + wid] = (int)(units >> 26);
+    sm[48 + wid] = longest;
   }
   __syncthreads();
-  int base = 0, T = 0, W = 0, top = 0;                       // row tiles, units and the most of one tile
+  int base = 0, T = 0, top = 0;                              // row tiles, and the most units of one
+  int64_t sum = 0;                                           // units of one kv head
 #pragma unroll
   for (int k = 0; k < NT / 32; ++k) {
     base += k < wid ? sm[k] : 0;
     T += sm[k];
-    W += sm[16 + k] * a.Hkv;
-    top = max(top, sm[32 + k]);
+    sum += ((int64_t)sm[32 + k] << 26) + sm[16 + k];
+    top = max(top, sm[48 + k]);
   }
+  if (sum * a.Hkv > kAttnMaxUnits) {                         // no CTA takes any
+    if (tid == 0) attn_status(a.status, MOE_ERR_CAPACITY);
+    return false;
+  }
+  const int W = (int)(sum * a.Hkv);
   if (W == 0) return false;
   const int all = T * a.Hkv;
   w.whole = top <= (W + G - 1) / G + kJoin && all <= G * kListMax;
@@ -214,7 +223,7 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
 void attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const AttnArgs a) {
   using C = TileCfg<D>;
   extern __shared__ uint8_t raw[];
-  __shared__ int32_t sched[64];
+  __shared__ __align__(8) int32_t sched[64];
   // full, q_full and p_full are the first CTA's, who issues the products, for both; the others are of each its own
   __shared__ __align__(8) uint64_t full[C::kStages], empty[C::kStages], edge[C::kStages], drain, q_full[2], s_full[2],
       p_full[2][2], o_full[2];

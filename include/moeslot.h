@@ -444,7 +444,8 @@ MOE_API moe_status moe_route_topk_noalloc(int32_t num_experts, int32_t top_k, in
  * be captured into a CUDA graph; lengths, tables and free list are read on the
  * device at run time.  Sizes the device finds inconsistent are clamped, never
  * followed out of range, and reported once in the sticky status:
- * MOE_ERR_CAPACITY (free list short, table_stride or rows exceeded) or
+ * MOE_ERR_CAPACITY (free list short, table_stride or rows exceeded, too many keys
+ * times rows in one moe_attn_forward) or
  * MOE_ERR_BOUNDS (a negative length, a page, position or slot out of range).
  * ---------------------------------------------------------------------- */
 enum { MOE_ROTARY_HALF = 0,    /* element i turns with i + rotary_dim/2     */
@@ -529,6 +530,10 @@ MOE_API moe_status moe_attn_qkv(moe_attn* attn, const void* qkv, int64_t qkv_str
  *   q         device [rows] rows of [num_q_heads][head_dim], q_stride elements apart
  *   max_new   bound of new_r over the requests, known to the host (1 in a decode step)
  *   out       device [rows][num_q_heads][head_dim] of dtype
+ * A call counts units, query rows by keys of one kv head: 512 by 128 in bf16 (16 by 128
+ * where max_new * group is at most 32, group = num_q_heads / num_kv_heads), 64 by 32 in
+ * fp32 (8 by 32 there).  One of more than 2^30 units, seconds of work, is refused on
+ * the device: MOE_ERR_CAPACITY, out not written.  Give it in smaller chunks.
  * The result does not depend on the order in which CTAs finish.  q, its rows and out
  * 16-byte aligned. */
 MOE_API moe_status moe_attn_forward(moe_attn* attn, const void* q, int64_t q_stride, int32_t rows,

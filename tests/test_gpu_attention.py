@@ -508,3 +508,27 @@ def test_tables_that_are_complete_are_only_mapped(page):
     given[1, (5 + 30 - 1) // page] = -1
     handle.tables(ints(ctx), ints(new), given, none, ints([7]), head, start, seq, pos, slot)
     assert handle.status() == moe.MOE_ERR_BOUNDS and int(slot[30]) == -1 and int(slot[0]) >= 0
+
+
+@pytest.mark.parametrize("dtype,hq,hkv,page,width,requests,new", [
+    ("f32", 64, 1, 16, 1 << 20, 1, 2100), ("f32", 64, 1, 16, 1 << 20, 1, 4200),        # above 2^30 units, 2^31
+    ("f32", 64, 1, 16, 1 << 20, 1, 8300), ("f32", 64, 1, 16, 1 << 20, 34, 70),         # and 2^32; many requests
+    ("f32", 64, 64, 16, 1 << 20, 33, 1), ("f32", 64, 64, 16, 1 << 20, 32, 9),          # few rows
+    ("bf16", 64, 64, 128, 1 << 20, 20, 1), ("bf16", 64, 64, 128, 1 << 19, 40, 1),
+    ("bf16", 512, 8, 128, 1 << 20, 1, 1100), ("bf16", 512, 8, 128, 1 << 20, 40, 28)])  # chunks
+def test_steps_of_more_units_than_are_counted_are_refused(dtype, hq, hkv, page, width, requests, new):
+    # every table entry names the one page of the cache, so that the lengths are long but the memory is not
+    dt = DT[dtype][0]
+    handle = moe.Attention(moe.make_attn_config(hq, hkv, 64, page, DT[dtype][1]))
+    rows = requests * new
+    table = torch.zeros(requests, width, dtype=torch.int32, device="cuda")
+    start, seq = ints(np.arange(requests + 1) * new), ints([width * page] * requests)
+    kc, vc = torch.ones(1, hkv, page, 64, dtype=dt, device="cuda"), torch.full((1, hkv, page, 64), 3.0, dtype=dt, device="cuda")
+    q = torch.zeros(rows, hq, 64, dtype=dt, device="cuda")
+    out = torch.full_like(q, 7.0)
+    handle.forward(q, start, seq, new, kc, vc, table, out)
+    assert handle.status() == moe.MOE_ERR_CAPACITY and (out == 7.0).all()
+    handle.clear_status()
+    seq.fill_(new)                                         # the same rows over as many keys; 3 n * fl(1 / n), joined or not
+    handle.forward(q, start, seq, new, kc, vc, table, out)
+    assert handle.status() == moe.MOE_OK and ((out - 3.0).abs() <= 2.0 ** -20).all()
