@@ -89,7 +89,9 @@ __global__ __launch_bounds__(NT, 1) void attn_rows_kernel(const __grid_constant_
     if (p_page_base < 0 || idx >= p_page_base + 32) {
       p_page_base = idx;
       const int key = (pc.u0 + pc.at) * UNIT + (p_step + lane * NW) * STEP;
-      p_page = p_step + lane * NW < p_steps && key < pc.q.seq
+      // the entries of pages that lie wholly before the tile's first window may be anything, too
+      const int lo = a.window > 0 ? pc.q.seq - pc.q.n + a.token(pc.i * BM) - a.window + 1 : 0;
+      p_page = p_step + lane * NW < p_steps && key < pc.q.seq && key + STEP > lo
                    ? a.table[(size_t)pc.r * a.table_stride + (key >> a.page_log2)] : -2;
     }
     const int page = __shfl_sync(0xffffffffu, p_page, idx - p_page_base);

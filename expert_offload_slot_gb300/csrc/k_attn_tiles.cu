@@ -287,8 +287,10 @@ void attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_cons
       const int k_col = lane / k_boxes, my_key = rank * 64 + lane % k_boxes * k_box;
       const uint32_t k_dst = k_col * (64 * 128) + lane % k_boxes * k_box * 128, v_dst = lane * v_box * D;
       uint32_t n = 0, edge_phase = 0;
-      auto row_of = [&](int key) -> int {                // row of the cache map that holds the key
-        if (key >= c.q.seq) return row_limit;
+      // Row of the cache map where a box of keys begins.  No table entry is read for one that no row of the
+      // item sees: behind the first row's window it may be anything.
+      auto row_of = [&](int key, int box, int lo) -> int {
+        if (key >= c.q.seq || key + box <= lo) return row_limit;
         const int page = a.table[(size_t)c.r * a.table_stride + (key >> a.page_log2)];
         if ((uint32_t)page < (uint32_t)a.num_pages) return ((page * a.Hkv + c.h) << a.page_log2) + (key & (a.page - 1));
         attn_status(a.status, MOE_ERR_BOUNDS);
@@ -302,12 +304,13 @@ void attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_cons
         // a unit's pages are looked up while the one before it is issued: a lookup takes about half as long
         // as the boxes of a unit of small pages
         const int piece0 = (c.u0 + c.at) * UNIT;
-        int k_at = my_k ? row_of(piece0 + my_key) : 0, v_at = my_v ? row_of(piece0 + lane * v_box) : 0;
+        int k_at = my_k ? row_of(piece0 + my_key, k_box, lo) : 0;
+        int v_at = my_v ? row_of(piece0 + lane * v_box, v_box, lo) : 0;
         for (int j = 0; j < units; ++j) {
           const int key0 = piece0 + j * UNIT;
           const bool ahead = j + 1 < units;
-          const int k_next = my_k && ahead ? row_of(key0 + UNIT + my_key) : 0;
-          const int v_next = my_v && ahead ? row_of(key0 + UNIT + lane * v_box) : 0;
+          const int k_next = my_k && ahead ? row_of(key0 + UNIT + my_key, k_box, lo) : 0;
+          const int v_next = my_v && ahead ? row_of(key0 + UNIT + lane * v_box, v_box, lo) : 0;
           for (int kv = 0; kv < 2; ++kv, ++n) {
             const int st = n % C::kStages;
             const uint32_t stage = ring + st * C::kTile, lead_full = lead_addr(full + st);

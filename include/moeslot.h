@@ -525,7 +525,8 @@ MOE_API moe_status moe_attn_qkv(moe_attn* attn, const void* qkv, int64_t qkv_str
  * with the keys of kv head  head / (num_q_heads / num_kv_heads).  A row that sees no key
  * (p < 0) gives zeros; rows of no request are not written.  Scores, the softmax's maximum
  * and sum and the output sums are fp32.  Cache rows that no token of the call sees (the
- * rest of a last page, pages out of the window) may hold anything, NaN included; the
+ * rest of a last page, pages out of the window) may hold anything, NaN included, and so
+ * may the table's entries of pages that lie wholly before a request's first window; the
  * values of a key that some token of a request's call sees must be finite for the others.
  *   q         device [rows] rows of [num_q_heads][head_dim], q_stride elements apart
  *   max_new   bound of new_r over the requests, known to the host (1 in a decode step)

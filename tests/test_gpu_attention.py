@@ -532,3 +532,25 @@ def test_steps_of_more_units_than_are_counted_are_refused(dtype, hq, hkv, page, 
     seq.fill_(new)                                         # the same rows over as many keys; 3 n * fl(1 / n), joined or not
     handle.forward(q, start, seq, new, kc, vc, table, out)
     assert handle.status() == moe.MOE_OK and ((out - 3.0).abs() <= 2.0 ** -20).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("ctx,new,window", [([700, 1000], [1, 1], 20), ([1100, 5], [40, 1], 50), ([400, 3000], [3, 130], 129)])
+def test_pages_behind_the_window_may_be_gone(dtype, page, ctx, new, window):
+    # a server gives the pages that no token of the call sees to others and marks their entries
+    s = Step(ctx, new, dtype, page=page, window=window)
+    gen = torch.Generator("cuda").manual_seed(5)
+    kc, vc = s.cache(gen)
+    q = torch.randn(s.rows, s.hq, s.dim, generator=gen, device="cuda").to(s.dtype)
+    ref, out = torch.full_like(q, 7.0), torch.full_like(q, 9.0)
+    s.handle.forward(q, s.start, s.seq, max(new), kc, vc, s.table, ref)
+    assert s.handle.status() == moe.MOE_OK
+    for mark in (-1, s.pages, 1 << 30):
+        table = s.table.clone()
+        for r, c in enumerate(ctx):
+            gone = max(0, c - window + 1) // page              # pages wholly before the first token's window
+            table[r, :gone] = mark
+        s.handle.forward(q, s.start, s.seq, max(new), kc, vc, table, out)
+        assert s.handle.status() == moe.MOE_OK, mark
+        assert torch.equal(out, ref)
