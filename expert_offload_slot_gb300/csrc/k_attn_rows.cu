@@ -153,7 +153,7 @@ __global__ __launch_bounds__(NT, 1) void attn_rows_kernel(const __grid_constant_
       const int st = taken % C::kStages;
       const uint32_t parity = (taken / C::kStages) & 1;
       if (alive) {
-        alive = bar_wait(bar + st, parity);
+        alive = bar_wait_warp(bar + st, parity);
         if (!alive) {
           attn_status(a.status, MOE_ERR_TIMEOUT);
           p_more = false;                    // load nothing more; the results are void

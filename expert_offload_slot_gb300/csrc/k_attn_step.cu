@@ -324,7 +324,7 @@ __global__ __launch_bounds__(ST, 4) void attn_qkv_rows_kernel(const QkvArgs a) {
   for (uint32_t unit = blockIdx.x; unit < units; unit += gridDim.x, ++it) {
     const int t = (int)(((uint64_t)unit * a.unit_mul) >> a.unit_shift), h0 = (int)(unit - (uint32_t)t * a.chunks) * a.chunk_heads;
     const int n = min(a.chunk_heads, a.heads - h0), st = it % kRing;
-    if (!sm103::bar_wait(full + st, (it / kRing) & 1)) {
+    if (!sm103::bar_wait_warp(full + st, (it / kRing) & 1)) {
       atomicCAS(a.status, 0, MOE_ERR_TIMEOUT);
       return;
     }

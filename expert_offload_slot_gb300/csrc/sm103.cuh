@@ -75,6 +75,11 @@ __device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity) {
     if ((it & 255u) == 0 && now_ns() - t0 > kWaitNs) return false;
   }
 }
+// The same by a whole warp, with one answer in all its lanes: each reads the clock for itself, so at the
+// limit some could see the barrier complete and others not.  For waits after which the warp's way differs.
+__device__ __forceinline__ bool bar_wait_warp(uint64_t* b, uint32_t parity) {
+  return __all_sync(0xffffffffu, bar_wait(b, parity));
+}
 
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
