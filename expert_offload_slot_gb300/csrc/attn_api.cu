@@ -314,7 +314,7 @@ MOE_API moe_status moe_attn_forward(moe_attn* A, const void* q, int64_t q_stride
   a.q = q; a.out = out; a.k_cache = k_cache; a.v_cache = v_cache; a.row_start = row_start; a.seq_len = seq_len;
   a.table = block_table; a.q_stride = q_stride; a.R = R; a.rows = rows; a.max_new = max_new; a.table_stride = table_stride;
   a.num_pages = num_pages; a.Hq = c.num_q_heads; a.Hkv = c.num_kv_heads; a.group = c.num_q_heads / c.num_kv_heads;
-  a.page = c.page_size; a.page_log2 = A->page_log2; a.window = c.window; a.scale = c.softmax_scale;
+  a.page = c.page_size; a.page_log2 = A->page_log2; a.window = c.window < kAttnMaxKeys ? c.window : 0; a.scale = c.softmax_scale;
   a.scale_log2 = c.softmax_scale * 1.44269504088896340736f;
   a.part_o = A->part_o; a.part_ml = A->part_ml; a.arrived = A->arrived; a.status = A->status;
   divider(a.group, a.group_mul, a.group_shift);

@@ -18,6 +18,9 @@ constexpr int kAttnRowsTile = 16;     // query rows per item of the row kernel
 constexpr int kAttnTile = 512;        // and of the tile kernel, by a pair of CTAs
 constexpr int kAttnF32Tile = 64;      // of the fp32 kernel
 constexpr int kAttnF32Few = 8;        // and of the one for few rows
+// Cached + new tokens of a request, at most: positions, down to MOE_ATTN_MAX_ROWS below zero, less a window
+// and plus a unit stay within 32 bits.
+constexpr int kAttnMaxKeys = 0x7fffffff - 2 * MOE_ATTN_MAX_ROWS;
 
 // floor(n / d) as (n * mul) >> shift for n below 2^31: mul = ceil(2^(31 + l) / d) with 2^l >= d; what
 // that adds to n / d is below n / 2^(31 + l) <= 1 / d, too little to reach the next integer.
@@ -68,7 +71,7 @@ __device__ __forceinline__ AttnRequest attn_request(const AttnArgs& a, int r) {
   q.start = a.row_start[r];
   int n = a.row_start[r + 1] - q.start;
   int seq = a.seq_len[r];
-  const int64_t cap = (int64_t)a.table_stride * a.page;
+  const int64_t cap = min((int64_t)a.table_stride * a.page, (int64_t)kAttnMaxKeys);
   bool bad = q.start < 0 || n < 0 || n > a.max_new || seq < 0 || seq > cap || (int64_t)q.start + n > a.rows;
   if (q.start < 0 || q.start >= a.rows || n < 0) n = 0;
   n = min(n, min(a.max_new, a.rows - q.start));

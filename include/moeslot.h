@@ -451,7 +451,7 @@ MOE_API moe_status moe_route_topk_noalloc(int32_t num_experts, int32_t top_k, in
 enum { MOE_ROTARY_HALF = 0,    /* element i turns with i + rotary_dim/2     */
        MOE_ROTARY_PAIRS = 1 }; /* element 2i turns with 2i + 1              */
 #define MOE_ATTN_MAX_REQUESTS 1024
-#define MOE_ATTN_MAX_ROWS 1048576
+#define MOE_ATTN_MAX_ROWS 1048576       /* and seq_len at most 2^31 - 1 - 2 * this */
 #define MOE_SAMPLE_MAX_VOCAB 327680
 
 typedef struct {

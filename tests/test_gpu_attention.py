@@ -554,3 +554,43 @@ def test_pages_behind_the_window_may_be_gone(dtype, page, ctx, new, window):
         s.handle.forward(q, s.start, s.seq, max(new), kc, vc, table, out)
         assert s.handle.status() == moe.MOE_OK, mark
         assert torch.equal(out, ref)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("new,seq", [(1, 1), (6, 2), (60, 7), (9, 40)])
+def test_a_window_of_any_size_sees_all_keys(dtype, new, seq):
+    # rows before the first key have negative positions, from which a window near 2^31 is subtracted
+    outs = []
+    for window in (0, (1 << 31) - 1, (1 << 31) - 3, 1 << 30):
+        s = Step([max(0, seq - new)], [new], dtype, window=window)
+        gen = torch.Generator("cuda").manual_seed(1)
+        kc, vc = s.cache(gen)
+        q = torch.randn(new, s.hq, s.dim, generator=gen, device="cuda").to(s.dtype)
+        outs.append(torch.full_like(q, 7.0))
+        s.handle.forward(q, s.start, ints([seq]), new, kc, vc, s.table, outs[-1])
+        assert s.handle.status() == moe.MOE_OK
+        assert torch.equal(outs[-1], outs[0]), window
+    assert (outs[0][:max(0, new - seq)] == 0).all() and (outs[0][new - 1] != 0).any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("new", [1, 40])
+def test_lengths_near_31_bits(dtype, new):
+    # every table entry names the one page, so keys repeat every 128; the window keeps the work small
+    s = Step([0], [new], dtype, page=128, window=30)
+    gen = torch.Generator("cuda").manual_seed(1)
+    kc, vc = (torch.randn(1, s.hkv, 128, s.dim, generator=gen, device="cuda").to(s.dtype) for _ in range(2))
+    q = torch.randn(new, s.hq, s.dim, generator=gen, device="cuda").to(s.dtype)
+    table = torch.zeros(1, 1 << 24, dtype=torch.int32, device="cuda")
+    ref, out = torch.full_like(q, 7.0), torch.full_like(q, 9.0)
+    most = (1 << 31) - 1 - 2 * moe.MOE_ATTN_MAX_ROWS
+    for seq in (most, most - 1, most - 60, 1 << 30):
+        s.handle.forward(q, s.start, ints([256 + seq % 128]), new, kc, vc, table, ref)
+        s.handle.forward(q, s.start, ints([seq]), new, kc, vc, table, out)
+        assert s.handle.status() == moe.MOE_OK
+        # two results over the same keys in other places of their units, each off by at most 2^-7 sum p|v| (about 1 here)
+        assert ((out.float() - ref.float()).abs() <= 2.0 ** -6).all() and ref.float().abs().max() > 0.1
+    for seq in (most + 1, (1 << 31) - 1):                  # longer ones are reported and cut there
+        s.handle.forward(q, s.start, ints([seq]), new, kc, vc, table, out)
+        assert s.handle.status() == moe.MOE_ERR_BOUNDS
+        s.handle.clear_status()
