@@ -87,8 +87,9 @@ __global__ __launch_bounds__(TT) void attn_tables_kernel(const TablesArgs a) {
   const bool given = a.num_free == 0;        // the tables are complete: only the maps are wanted
   const int total = s_row[a.R], taken = given ? 0 : s_carry[1];
   full |= total > a.rows;
+  auto is_short = [&](int at) { return head < 0 || (int64_t)head + at >= a.num_free; };
   auto fresh_page = [&](int at) -> int {     // entry `at` of the free list beyond the head; -1 when it is short
-    if (head < 0 || (int64_t)head + at >= a.num_free) { full = true; return -1; }
+    if (is_short(at)) { full = true; return -1; }
     return a.free_pages[head + at];
   };
   // the row starts, and the new table entries: a warp per request
@@ -116,9 +117,10 @@ __global__ __launch_bounds__(TT) void attn_tables_kernel(const TablesArgs a) {
       const int j = pos >> a.page_log2;
       if (j < a.table_stride) {
         const bool fresh = j >= v.have && !given;
-        const int page = fresh ? fresh_page(s_off[lo] + j - v.have) : a.table[(size_t)lo * a.table_stride + j];
-        if (page >= 0) slot = (page << a.page_log2) + (pos & (a.page - 1));
-        else bad = bad || !fresh;
+        const int at = s_off[lo] + j - v.have, page = fresh ? fresh_page(at) : a.table[(size_t)lo * a.table_stride + j];
+        // a page whose slots need more than 31 bits would come out as the slots of another
+        if ((uint32_t)page <= 0x7fffffffu >> a.page_log2) slot = (page << a.page_log2) + (pos & (a.page - 1));
+        else bad |= !(fresh && is_short(at));
       }
     }
     a.positions[t] = pos;

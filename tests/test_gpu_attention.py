@@ -594,3 +594,24 @@ def test_lengths_near_31_bits(dtype, new):
         s.handle.forward(q, s.start, ints([seq]), new, kc, vc, table, out)
         assert s.handle.status() == moe.MOE_ERR_BOUNDS
         s.handle.clear_status()
+
+
+@pytest.mark.parametrize("page", [16, 128])
+@pytest.mark.parametrize("where", ["table", "free"])
+def test_tables_report_pages_whose_slots_have_no_number(page, where):
+    # page * page_size past 31 bits would come out as the slot of another page; so would a negative entry
+    handle = moe.Attention(moe.make_attn_config(8, 2, 128, page))
+    for bad in ((1 << 31) // page, (1 << 32) // page + 3, (1 << 31) - 1, -5):
+        if bad >= 1 << 31:
+            continue
+        table, free = ints([[4, 9], [6, 8]]), ints([3, 2])
+        if where == "table":
+            table[0, 0] = bad                                  # request 0 goes on in its first page
+            ctx = [1, 1]
+        else:
+            free[0] = bad                                      # or takes it anew
+            ctx = [0, 1]
+        start, seq, pos, slot = ints([0, 0, 0]), ints([0, 0]), ints([0] * 2), ints([99] * 2)
+        handle.tables(ints(ctx), ints([1, 1]), table, free, ints([0]), ints([0]), start, seq, pos, slot)
+        assert handle.status() == moe.MOE_ERR_BOUNDS and slot.tolist() == [-1, 6 * page + 1], bad
+        handle.clear_status()
