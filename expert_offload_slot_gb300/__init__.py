@@ -365,7 +365,7 @@ def make_attn_config(num_q_heads, num_kv_heads, head_dim, page_size, dtype=MOE_B
 
 # The calls below run once per layer and step, beside kernels of a few microseconds, so their checks
 # are written flat: type, device, element count and contiguity of each tensor, since the library sees
-# addresses only.  (len(tensor) is a Python function of torch's; size(0) is not.)
+# addresses only.  (numel() takes a third of size(0)'s time, and len(tensor) is a Python function of torch's.)
 _kinds = {}
 
 
@@ -439,7 +439,7 @@ class Attention:
     def tables(self, ctx_len, new_len, block_table, free_pages, free_head, free_head_out, row_start, seq_len, positions,
                slot_map, stream=None):
         """Fill block_table, free_head_out, row_start, seq_len, positions and slot_map for the step."""
-        i32, n, rows, free, dev = self._i32, ctx_len.size(0), positions.size(0), free_pages.size(0), self._device
+        i32, n, rows, free, dev = self._i32, ctx_len.numel(), positions.numel(), free_pages.numel(), self._device
         width = block_table.size(1)
         st = _lib.moe_attn_tables(
             self.h, _flat("ctx_len", ctx_len, i32, n, dev), _flat("new_len", new_len, i32, n, dev), n,
@@ -469,7 +469,7 @@ class Attention:
 
     def forward(self, q, row_start, seq_len, max_new, k_cache, v_cache, block_table, out, stream=None):
         """Attention of q [rows, Hq, D] over the cache, into out [rows, Hq, D]."""
-        kind, i32, rows, n, pages, dev = self._kind, self._i32, q.size(0), seq_len.size(0), k_cache.size(0), self._device
+        kind, i32, rows, n, pages, dev = self._kind, self._i32, q.size(0), seq_len.numel(), k_cache.size(0), self._device
         width = block_table.size(1)
         at, stride = _rows("q", q, kind, rows, self._q_width, dev)
         st = _lib.moe_attn_forward(
