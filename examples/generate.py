@@ -113,8 +113,10 @@ class Server:
 
 
 def generate(server, prompts, count, temperature=0.8, top_k=50, top_p=0.95, min_p=0.0, seed=0):
-    """Token ids [R, count] that follow the prompts (lists of ids)."""
+    """Token ids [R, count] that follow the prompts (lists of ids, none empty: a first token follows its prompt's last)."""
     R = len(prompts)
+    if R != server.R or not all(prompts):
+        raise ValueError(f"{server.R} prompts of one token or more are wanted, got lengths {[len(p) for p in prompts]}")
     per = lambda v, t: torch.full((R,), v, dtype=t, device="cuda")  # noqa: E731
     knobs = dict(temperature=per(temperature, torch.float32), top_k=per(top_k, torch.int32),
                  top_p=per(top_p, torch.float32), min_p=per(min_p, torch.float32))
