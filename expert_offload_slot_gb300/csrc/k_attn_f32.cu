@@ -12,8 +12,10 @@
 // four rows with two keys' scores, then with D / 16 output columns, so that its 32
 // products need six (then three) reads of shared memory; two CTAs share an SM, so
 // that one's loads run beside the other's products.  With half the rows and one product
-// for each read of K and V a 512-token prompt (32 q heads) took 225 us; so it takes 92 us,
-// 23 TFLOP/s, and 200 tokens over 2000 keys 203 instead of 573 us, 31 TFLOP/s.  Shared memory's reads bound it.
+// for each read of K and V a 512-token prompt (32 q heads) took 225 us; so it takes 92 to 95 us,
+// 23 TFLOP/s, and the last 200 of 2000 tokens 203 instead of 573 us, 31 TFLOP/s.  Shared memory and the
+// instructions bound it together: its pipe is busy 66 % of the time, issue slots 67 %, the FMA pipe 52 %, as
+// loads of a tile and its products take turns behind two barriers.
 #include "attn_internal.cuh"
 #include "sm103.cuh"
 
@@ -176,9 +178,10 @@ __global__ __launch_bounds__(NT, 2) void attn_f32_kernel(const AttnArgs a) {
 
 // ------------------------------------------------- few query rows per request (decode)
 // Eight query rows a CTA: the kernel above computes 64 for every key (16 requests of 5000 keys, 8 kv
-// heads: 707 us with 32; this one 185 us, 3.5 TB/s).  Tiles of 32 keys come by 16-byte asynchronous copies into
-// three stages; two CTAs share an SM, so that the copies and the phases between barriers of one run
-// beside the other's.  Scores: a lane has one key, a warp an eighth of D, so that K is read once from
+// heads: 707 us with 32; this one 185 us, 3.5 TB/s, half of HBM's rate: four barriers a tile of 32 keys keep
+// its products and softmax apart, with shared memory's pipe busy 59 % of the time and issue slots 54 %).
+// Tiles of 32 keys come by 16-byte asynchronous copies into three stages; two CTAs share an SM, so that the
+// copies and the phases between barriers of one run beside the other's.  Scores: a lane has one key, a warp an eighth of D, so that K is read once from
 // shared memory and q by broadcast; softmax: a warp per row; output: a thread per column and group
 // of keys, eight rows in its registers.
 constexpr int FM = kAttnF32Few, FN = 32, FSTAGES = 3, DQ = NT / 32;

@@ -6,8 +6,10 @@
 //
 // One pass over the keys with the running maximum m and sum l of the softmax,
 // both fp32; scores and outputs accumulate in fp32.  The probabilities are
-// rounded to bf16 for the second product (relative 2^-9, in the output's own
-// precision); l sums them before that rounding.
+// rounded to bf16 for the second product, whose other factor is bf16: each is off
+// by at most 2^-8 of itself, as the output is by its own rounding, and over many
+// keys the errors average out (off from 64 bits by 1.7 to 1.8 10^-3 of the outputs'
+// norm where probabilities in fp32 give 1.7).  l sums them before that rounding.
 //
 // An item's query rows are all heads of one kv head's group (times the new
 // tokens), so that a key is read from HBM once for the whole group.  The eight
@@ -21,9 +23,9 @@
 //
 // Measured: four requests of 100000 keys, 8 kv heads (1.6 GB) 252 us, 6.4 TB/s or
 // 95 % of a plain copy's rate; 16 requests of 60 to 8191 keys, 4 kv heads (114 MB)
-// 28.5 us: 4 pass before the first load is out (lengths, then pages, each an HBM
+// 29 us: 4 pass before the first load is out (lengths, then pages, each an HBM
 // latency), 3 to 5 after the last (warps and pieces joined), and pieces are uneven.  One
-// request of 1000 keys takes 8.8 us.  Units of 64 and 32 keys in place of 128 gain 1 % or
+// request of 1000 keys takes 9.0 us.  Units of 64 and 32 keys in place of 128 gain 1 % or
 // nothing, and the one request then takes 0.7 and 2.7 us longer: more pieces to join.
 #include "attn_internal.cuh"
 #include "sm103.cuh"

@@ -9,7 +9,7 @@
 // Every CTA scans the lengths of all requests itself (they are a few KB that L2
 // serves), so one launch does it all and no CTA waits for another.  A step moves
 // a few hundred KB at most, so the launch bounds it: 384 requests with 25k new
-// rows take 7.7 us a call, 16 requests with one row each 7.6.
+// rows take 7.6 us a call, 16 requests with one row each 7.5.
 //
 // moe_attn_qkv: y = x / sqrt(mean(x^2) + eps) * w for each query and key head,
 // then the rotation (a, b) -> (a cos - b sin, b cos + a sin) of its first
@@ -262,7 +262,7 @@ __global__ __launch_bounds__(QT) void attn_qkv_kernel(const QkvArgs a) {
 // into a ring in shared memory by bulk copies, so that HBM is read ahead of the work: in the kernel
 // above a group of lanes waits for its position, then for the rotation's row, and nothing is in
 // flight while it does.  HBM bounds it: 16384 rows of 32 + 2 x 4 heads of 128, bf16 (344 MB moved),
-// 58 us or 5.9 TB/s, 75 us by the kernel above; 2048 rows with 2 x 8 heads (51 MB) 13.2 us, 15.6.
+// 58 us or 5.9 TB/s, 75 us by the kernel above; 2048 rows with 2 x 8 heads (51 MB) 13.1 us, 15.6.
 // With 1024 such rows, 48 heads of 8 lanes, the two are level (8.5 and 8.9 us), below that the one
 // above is ahead (256 rows: 3.1 and 4.3 us): so it takes up to 4096 lanes per SM.
 constexpr int ST = QT + 32, kRing = 4, kPiece = 16384;       // kPiece: bytes of a piece at most

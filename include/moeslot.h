@@ -535,6 +535,9 @@ MOE_API moe_status moe_attn_qkv(moe_attn* attn, const void* qkv, int64_t qkv_str
  * where max_new * group is at most 32, group = num_q_heads / num_kv_heads), 64 by 32 in
  * fp32 (8 by 32 there).  One of more than 2^30 units, seconds of work, is refused on
  * the device: MOE_ERR_CAPACITY, out not written.  Give it in smaller chunks.
+ * max_new chooses the kernel for the whole call, so decodes beside a long chunk are
+ * faster in a call of their own: the slices of row_start, seq_len and block_table that
+ * belong to them, with the same q, rows and out.
  * The result does not depend on the order in which CTAs finish.  q, its rows and out
  * 16-byte aligned. */
 MOE_API moe_status moe_attn_forward(moe_attn* attn, const void* q, int64_t q_stride, int32_t rows,
