@@ -25,6 +25,8 @@ MOE_GATE_SOFTMAX_RENORM, MOE_GATE_SIGMOID_RENORM = 0, 1
 MOE_EVICT_CORE, MOE_EVICT_MRS, MOE_EVICT_LRU = 0, 1, 2
 MOE_MODE_AUTO, MOE_MODE_DECODE, MOE_MODE_PREFILL_STAGED = 0, 1, 2
 MOE_ROTARY_HALF, MOE_ROTARY_PAIRS = 0, 1
+MOE_RESIDUAL_GATE_NONE, MOE_RESIDUAL_GATE_ROW, MOE_RESIDUAL_GATE_CHANNEL, MOE_RESIDUAL_GATE_ELEMENT = 0, 1, 2, 3
+MOE_NORM_MAX_HIDDEN, MOE_LINEAR_MAX_IN, MOE_LINEAR_MAX_OUT, MOE_LOGPROBS_MAX_TOP = 16384, 65536, 1 << 20, 32
 MOE_ATTN_MAX_REQUESTS, MOE_ATTN_MAX_ROWS, MOE_SAMPLE_MAX_VOCAB = 1024, 1 << 20, 327680
 STAGES = ("route", "plan", "copy", "ffn")
 MOE_NUM_STAGES = len(STAGES)
@@ -55,8 +57,13 @@ class moe_attn_config(ctypes.Structure):
                [("softmax_scale", ctypes.c_float), ("norm_eps", ctypes.c_float)]
 
 
+class moe_norm_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("hidden", "dtype", "residual_dtype", "gate", "gate_sigmoid")] + \
+               [(n, ctypes.c_float) for n in ("residual_scale", "norm_eps", "weight_offset")]
+
+
 _vp, _i32, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
-_P = ctypes.POINTER
+_P, _i64 = ctypes.POINTER, ctypes.c_int64
 _sig = {
     "moe_expert_layout": (_i32, [_P(moe_config), _P(_sz), _P(_sz), _P(_sz), _P(_sz), _P(_sz)]),
     "moe_pack_expert_record": (_i32, [_P(moe_config), _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz]),
@@ -95,6 +102,10 @@ _sig = {
     "moe_attn_forward": (_i32, [_vp, _vp, ctypes.c_int64, _i32, _vp, _vp, _i32, _i32, _vp, _vp, _i32, _vp, _i32, _vp,
                                 _vp]),
     "moe_sample": (_i32, [_vp, _i32, _i32, _i32, ctypes.c_int64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "moe_residual_norm": (_i32, [_P(moe_norm_config), _vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i32, _vp]),
+    "moe_q4_pack": (_i32, [_vp, _i32, _i32, _i32, _vp, _vp]),
+    "moe_linear_q4": (_i32, [_vp, _i32, _i64, _i32, _i32, _vp, _vp, _i32, _i32, _vp, _i32, _vp, _i32, _i64, _vp]),
+    "moe_logprobs": (_i32, [_vp, _i32, _i32, _i32, _i64, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp]),
     "moe_last_error": (ctypes.c_char_p, []),
     "moe_route_topk_noalloc": (_i32, [_i32, _i32, _i32, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
 }
@@ -377,6 +388,7 @@ def _torch_kinds():
         _kinds["stream"] = raw or (lambda device: torch.cuda.current_stream(device).cuda_stream)
         _kinds["device"], _kinds["on"] = torch.cuda.current_device, torch.cuda.device
         _kinds[MOE_F32], _kinds[MOE_BF16], _kinds["i32"] = torch.float32, torch.bfloat16, torch.int32
+        _kinds["u8"] = torch.uint8
     return _kinds
 
 
@@ -511,3 +523,117 @@ def moe_sample(logits, u, ids, logp=None, temperature=None, top_k=None, top_p=No
             st = _lib.moe_sample(*args)
     if st:
         _check(st, "moe_sample")
+
+
+def _launch(name, dev, stream, *args):
+    """A call of the library that has no handle and so runs on the current device: on `dev` and its stream."""
+    kinds = _kinds
+    args += (kinds["stream"](dev) if stream is None else _stream(stream),)
+    if kinds["device"]() == dev:
+        st = getattr(_lib, name)(*args)
+    else:
+        with kinds["on"](dev):
+            st = getattr(_lib, name)(*args)
+    if st:
+        _check(st, name)
+
+
+_norm_configs = {}
+
+
+def moe_residual_norm(x, residual, residual_out, y, post_weight=None, pre_weight=None, gate=None, gate_sigmoid=False,
+                      residual_scale=1.0, eps=1e-6, weight_offset=0.0, stream=None):
+    """residual_out = residual + residual_scale gate norm(x, post_weight), y = norm(residual_out, pre_weight).
+
+    x, residual, residual_out and y are [rows, hidden] with contiguous rows; x (then residual_out, too) or y may be
+    None.  The block's output is normed only where post_weight [hidden] is given.  gate is [rows, 1], [hidden] or
+    [rows, hidden].
+    """
+    kinds = _torch_kinds()
+    f32, bf16 = kinds[MOE_F32], kinds[MOE_BF16]
+    rows, hidden = residual.shape
+    dev = max(residual.get_device(), 0)        # a host tensor (-1) is refused below
+    first = y if x is None else x
+    if first is None:
+        raise ValueError("x and y must not both be None")
+    dtype = f32 if first.dtype is f32 else bf16
+    stream_type = f32 if residual.dtype is f32 else dtype
+    kind = MOE_RESIDUAL_GATE_NONE
+    gate_at, gate_step = None, 0
+    if gate is not None:
+        if gate.dim() == 1:
+            kind, gate_at = MOE_RESIDUAL_GATE_CHANNEL, _flat("gate", gate, dtype, hidden, dev)
+        elif gate.size(-1) == 1:
+            kind = MOE_RESIDUAL_GATE_ROW
+            gate_at, gate_step = _rows("gate", gate, dtype, rows, 1, dev)
+        else:
+            kind = MOE_RESIDUAL_GATE_ELEMENT
+            gate_at, gate_step = _rows("gate", gate, dtype, rows, hidden, dev)
+    key = (hidden, dtype, stream_type, kind, gate_sigmoid, residual_scale, eps, weight_offset)
+    cfg = _norm_configs.get(key)
+    if cfg is None:
+        if len(_norm_configs) > 256:
+            _norm_configs.clear()
+        cfg = _norm_configs[key] = moe_norm_config(hidden, MOE_F32 if dtype is f32 else MOE_BF16,
+                                                   MOE_F32 if stream_type is f32 else MOE_BF16, kind, int(bool(gate_sigmoid)),
+                                                   residual_scale, eps, weight_offset)
+    x_at, x_step = (None, 0) if x is None else _rows("x", x, dtype, rows, hidden, dev)
+    r_at, r_step = _rows("residual", residual, stream_type, rows, hidden, dev)
+    s_at, s_step = (None, 0) if residual_out is None else _rows("residual_out", residual_out, stream_type, rows, hidden, dev)
+    y_at, y_step = (None, 0) if y is None else _rows("y", y, dtype, rows, hidden, dev)
+    _launch("moe_residual_norm", dev, stream, ctypes.byref(cfg), x_at, x_step, gate_at, gate_step,
+            None if post_weight is None else _flat("post_weight", post_weight, dtype, hidden, dev), r_at, r_step, s_at, s_step,
+            None if pre_weight is None else _flat("pre_weight", pre_weight, dtype, hidden, dev), y_at, y_step, rows)
+
+
+def moe_q4_pack(w, group=128):
+    """4-bit codes (uint8 [out, in / 2]) and scales (float32 [out, ceil(in / group)]) of weights [out, in], host numpy."""
+    w = np.ascontiguousarray(w, np.float32)
+    if w.ndim != 2:
+        raise ValueError(f"weights must be [out, in], got {w.shape}")
+    if group not in (32, 64, 128):
+        raise ValueError("group must be 32, 64 or 128")
+    n, k = w.shape
+    codes, scales = np.zeros((n, k // 2), np.uint8), np.zeros((n, -(-k // group)), np.float32)
+    _check(_lib.moe_q4_pack(w.ctypes.data, n, k, group, codes.ctypes.data, scales.ctypes.data), "moe_q4_pack")
+    return codes, scales
+
+
+def moe_linear_q4(x, codes, scales, out, group=128, bias=None, stream=None):
+    """out [rows, out] = x [rows, in] times the 4-bit weights (codes [out, in / 2], scales [out, ceil(in / group)]) + bias [out]."""
+    kinds = _torch_kinds()
+    f32, bf16 = kinds[MOE_F32], kinds[MOE_BF16]
+    rows, k = x.shape
+    n = codes.size(0)
+    dev = max(x.get_device(), 0)               # a host tensor (-1) is refused below
+    dtype = f32 if x.dtype is f32 else bf16
+    out_type = f32 if out.dtype is f32 else dtype
+    scale_type = f32 if scales.dtype is f32 else bf16
+    if group not in (32, 64, 128):
+        raise ValueError("group must be 32, 64 or 128")
+    x_at, x_step = _rows("x", x, dtype, rows, k, dev)
+    out_at, out_step = _rows("out", out, out_type, rows, n, dev)
+    _launch("moe_linear_q4", dev, stream, x_at, MOE_F32 if dtype is f32 else MOE_BF16, x_step, rows, k,
+            _flat("codes", codes, kinds["u8"], n * (k // 2), dev),
+            _flat("scales", scales, scale_type, n * -(-k // group), dev), MOE_F32 if scale_type is f32 else MOE_BF16, group,
+            None if bias is None else _flat("bias", bias, dtype, n, dev), n, out_at, MOE_F32 if out_type is f32 else MOE_BF16,
+            out_step)
+
+
+def moe_logprobs(logits, targets, logp, entropy=None, rank=None, top_ids=None, top_logp=None, stream=None):
+    """Log probability (logp) and rank of a token of each row of logits [rows, vocab], the rows' entropy and their best
+    tokens (top_ids and top_logp, [rows, top])."""
+    kinds = _torch_kinds()
+    f32, i32 = kinds[MOE_F32], kinds["i32"]
+    rows, vocab = logits.shape
+    dtype = MOE_F32 if logits.dtype is f32 else MOE_BF16
+    dev = max(logits.get_device(), 0)          # a host tensor (-1) is refused below
+    at, step = _rows("logits", logits, f32 if dtype == MOE_F32 else kinds[MOE_BF16], rows, vocab, dev)
+    if (top_ids is None) != (top_logp is None):
+        raise ValueError("top_ids and top_logp go together")
+    top = 0 if top_ids is None else top_ids.size(1)
+    _launch("moe_logprobs", dev, stream, at, dtype, rows, vocab, step, _flat("targets", targets, i32, rows, dev), top,
+            _flat("logp", logp, f32, rows, dev), None if entropy is None else _flat("entropy", entropy, f32, rows, dev),
+            None if rank is None else _flat("rank", rank, i32, rows, dev),
+            None if top_ids is None else _flat("top_ids", top_ids, i32, rows * top, dev),
+            None if top_logp is None else _flat("top_logp", top_logp, f32, rows * top, dev))

@@ -1,0 +1,486 @@
+// moe_logprobs: the log probability and rank of a given token in each row of logits, the
+// row's entropy and its most probable tokens.
+//
+//   lse = max + log sum exp(x - max), logp = x_t - lse, entropy = lse - sum p x
+//
+// One pass over the row, shared by the CTAs of a cluster: each thread keeps the running
+// maximum m of its logits in log2 units (rounded, so one number is the reference of all) and,
+// relative to it, s = sum e and w = sum e z with z = x log2(e) - m, one rounding, e = 2^z; when
+// m grows by -d, s becomes 2^d s and w 2^d (w + d s).  Then logp = (z_t - log2 s) log(2) and
+// entropy = (log2 s - w / s) log(2): differences of numbers of different signs, nothing cancels.
+//
+// The best tokens need no second pass over the row: the n-th largest of 64 groups' maxima
+// is a bound that n logits reach, only threads whose own maximum reaches it look at their
+// logits again, and the few that do are sorted by (x, index).  Rows where the bound does
+// not help (equal logits in thousands, hardly any token) are searched by bisection.
+//
+// NaN counts as -inf.  Logits far from zero, where the products with log2(e) lose the
+// differences, and rows without a token take a second, careful pass.
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "sm103.cuh"
+#include "step_internal.cuh"
+
+namespace moeslot {
+namespace {
+namespace cg = cooperative_groups;
+typedef __nv_bfloat16 bf16;
+typedef unsigned long long u64;
+
+constexpr int kMaxCluster = 8;
+constexpr int kTop = MOE_LOGPROBS_MAX_TOP;
+constexpr int kGroups = 64;                    // whose maxima bound the best tokens; twice kTop
+constexpr int kList = 256;                     // tokens that reach the bound, at most
+static_assert(kGroups >= 2 * kTop && kList >= kMaxCluster * kTop, "room for every list");
+constexpr float kLow = -1e38f;                 // logits are held above it (so -inf and NaN are there, too) and, below
+constexpr float kNone = -9e37f;                // this first maximum, add nothing; rows without a larger one are `far`
+constexpr float kFar = 1048576.f;              // up to it (log2 units) the rounding of m leaves e below 1.05
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+
+struct Soft {                                  // part of a row: see above; m in log2 units
+  float m, s, w;
+};
+__device__ __forceinline__ void join(Soft& a, const Soft& b) {
+  const float m = fmaxf(a.m, b.m);
+  const float da = a.m - m, db = b.m - m, fa = sm103::ex2(da), fb = sm103::ex2(db);
+  // an exponential of zero ends a part, whatever its sums are
+  const float wa = fa > 0.f ? fa * fmaf(da, a.s, a.w) : 0.f, wb = fb > 0.f ? fb * fmaf(db, b.s, b.w) : 0.f;
+  a.m = m;
+  a.s = fa * a.s + fb * b.s;
+  a.w = wa + wb;
+}
+
+struct Shared {                                // of a CTA; the cluster reads the second part
+  Soft warp[32];
+  int32_t count[32];
+  float best[1024];
+  u64 list[kList];
+  float bound;
+  int32_t found;
+  u64 bits[32];
+  // shown to the cluster
+  Soft soft;
+  float most;
+  int32_t rank, kept;
+  u64 top[kTop];
+};
+
+__device__ __forceinline__ float clean(float x) {  // NaN counts as -inf, -0 as +0
+  x += 0.f;
+  return x == x ? x : -INFINITY;
+}
+// Descending logits, equal ones by ascending index, as descending keys.
+__device__ __forceinline__ uint32_t ordered(float x) {
+  const uint32_t u = __float_as_uint(x);
+  return (u >> 31) ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ u64 key_of(float x, int i) { return (u64)ordered(x) << 32 | (0xffffffffu - (uint32_t)i); }
+__device__ __forceinline__ int index_of(u64 key) { return (int)(0xffffffffu - (uint32_t)key); }
+__device__ __forceinline__ float value_of(u64 key) {
+  const uint32_t u = (uint32_t)(key >> 32);
+  return __uint_as_float((u >> 31) ? u & 0x7fffffffu : ~u);
+}
+
+__device__ __forceinline__ float raw(float v) { return v; }
+__device__ __forceinline__ float raw(bf16 v) { return __bfloat162float(v); }
+
+// 16 bytes of logits: their maximum, the logits held above kLow, and how many are above the target
+// (or equal: before it).
+template <typename T>
+struct Vec;
+template <>
+struct Vec<float> {
+  static constexpr int W = 4;
+  static __device__ __forceinline__ int above(const uint4& u, float xt, bool before) {
+    const float v[4] = {__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w)};
+    int n = 0;
+    if (before) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) n += v[k] >= xt;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) n += v[k] > xt;
+    }
+    return n;
+  }
+  static __device__ __forceinline__ float hold(const uint4& u, float (&v)[4]) {
+    v[0] = fmaxf(__uint_as_float(u.x), kLow);
+    v[1] = fmaxf(__uint_as_float(u.y), kLow);
+    v[2] = fmaxf(__uint_as_float(u.z), kLow);
+    v[3] = fmaxf(__uint_as_float(u.w), kLow);
+    return fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+  }
+};
+template <>
+struct Vec<bf16> {
+  static constexpr int W = 8;
+  static __device__ __forceinline__ __nv_bfloat162 pair(uint32_t u) { return *reinterpret_cast<const __nv_bfloat162*>(&u); }
+  static __device__ __forceinline__ int above(const uint4& u, float xt, bool before) {
+    const __nv_bfloat162 t = __float2bfloat162_rn(xt);               // a logit: exact
+    __nv_bfloat162 n;
+    if (before) {
+      n = __hadd2(__hadd2(__hge2(pair(u.x), t), __hge2(pair(u.y), t)), __hadd2(__hge2(pair(u.z), t), __hge2(pair(u.w), t)));
+    } else {
+      n = __hadd2(__hadd2(__hgt2(pair(u.x), t), __hgt2(pair(u.y), t)), __hadd2(__hgt2(pair(u.z), t), __hgt2(pair(u.w), t)));
+    }
+    return (int)(__low2float(n) + __high2float(n));
+  }
+  static __device__ __forceinline__ float hold(const uint4& u, float (&v)[8]) {
+    const __nv_bfloat162 low = __float2bfloat162_rn(kLow);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    __nv_bfloat162 p[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      p[k] = __hmax2(pair(w[k]), low);
+      v[2 * k] = __low2float(p[k]);
+      v[2 * k + 1] = __high2float(p[k]);
+    }
+    const __nv_bfloat162 m = __hmax2(__hmax2(p[0], p[1]), __hmax2(p[2], p[3]));
+    return fmaxf(__low2float(m), __high2float(m));
+  }
+};
+
+// The logits of a CTA: [head | vectors v0 .. v1 | tail], the vectors on 16-byte boundaries; head and tail
+// are less than a vector and belong to the first and the last CTA.
+template <typename T>
+struct Share {
+  static constexpr int W = Vec<T>::W;
+  const T* x;
+  int lead, v0, v1, head, tail0, tail;         // logit of vector 0; elements before it; first of and elements of the tail
+  __device__ __forceinline__ const uint4* vectors() const { return reinterpret_cast<const uint4*>(x + lead); }
+  // the element of thread `tid` outside of the vectors, or -1
+  __device__ __forceinline__ int single(int tid) const {
+    if (tid < head) return tid;
+    return tid >= 32 && tid - 32 < tail ? tail0 + tid - 32 : -1;
+  }
+  // f(x, index) for every logit, spread over the CTA's threads
+  template <typename F>
+  __device__ __forceinline__ void each(int tid, int nt, F f) const {
+    const int i = single(tid);
+    if (i >= 0) f(clean(raw(x[i])), i);
+    const int from = lead + v0 * W, to = lead + v1 * W;
+    for (int k = from + tid; k < to; k += nt) f(clean(raw(x[k])), k);
+  }
+};
+
+template <typename T, int NT>
+__global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const LogprobArgs a) {
+  constexpr int W = Vec<T>::W, NW = NT / 32, U = 4;
+  __shared__ Shared sm;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int cs = (int)cluster.num_blocks(), rank = (int)cluster.block_rank(), row = blockIdx.x / cs;
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  sm103::grid_wait();
+  Share<T> in;
+  in.x = static_cast<const T*>(a.logits) + (int64_t)row * a.row_stride;
+  in.lead = min((int)((16 - (reinterpret_cast<uintptr_t>(in.x) & 15)) & 15) / (int)sizeof(T), a.vocab);
+  const int vectors = (a.vocab - in.lead) / W;
+  in.v0 = (int)((int64_t)rank * vectors / cs);
+  in.v1 = (int)((int64_t)(rank + 1) * vectors / cs);
+  in.head = rank == 0 ? in.lead : 0;
+  in.tail0 = in.lead + vectors * W;
+  in.tail = rank == cs - 1 ? a.vocab - in.tail0 : 0;
+
+  const int target = a.targets[row];
+  const bool asked = target >= 0 && target < a.vocab;
+  const float xt = asked ? clean(raw(in.x[target])) : INFINITY;
+
+  // ------------------------------------------------ one pass
+  Soft soft = {kNone * kLog2e, 0.f, 0.f};
+  float mine = kNone;                          // this thread's maximum
+  int above = 0;
+  {
+    auto grow = [&](float m) {                 // to a maximum m
+      mine = m;
+      m *= kLog2e;
+      const float d = soft.m - m, f = sm103::ex2(d);
+      soft.w = f > 0.f ? f * fmaf(d, soft.s, soft.w) : 0.f;
+      soft.s *= f;
+      soft.m = m;
+    };
+    const int i = in.single(tid);
+    if (i >= 0) {
+      const float x = raw(in.x[i]), v = fmaxf(x, kLow);
+      above += i < target ? x >= xt : x > xt;
+      if (v > mine) grow(v);
+      const float z = fmaf(v, kLog2e, -soft.m), e = sm103::ex2(z);
+      soft.s += e;
+      soft.w = fmaf(e, z, soft.w);
+    }
+    const uint4* p = in.vectors();
+    auto take = [&](const uint4& u, int vec) {
+      above += Vec<T>::above(u, xt, in.lead + vec * W < target);
+      float v[W];
+      const float m = Vec<T>::hold(u, v);
+      if (m > mine) grow(m);
+#pragma unroll
+      for (int k = 0; k < W; ++k) {
+        const float z = fmaf(v[k], kLog2e, -soft.m), e = sm103::ex2(z);
+        soft.s += e;
+        soft.w = fmaf(e, z, soft.w);
+      }
+    };
+    int v = in.v0 + tid;
+    for (; v + (U - 1) * NT < in.v1; v += U * NT) {
+      uint4 u[U];
+#pragma unroll
+      for (int k = 0; k < U; ++k) u[k] = __ldg(p + v + k * NT);
+#pragma unroll
+      for (int k = 0; k < U; ++k) take(u[k], v + k * NT);
+    }
+    for (; v < in.v1; v += NT) take(__ldg(p + v), v);
+  }
+  // the target's own vector counted all its equals: those from the target on do not stand before it
+  if (asked && target > in.lead && target < in.tail0) {
+    const int vec = (target - in.lead) / W;
+    if (vec >= in.v0 && vec < in.v1 && (vec - in.v0) % NT == tid && in.lead + vec * W < target)
+      for (int i = target; i < in.lead + (vec + 1) * W; ++i) above -= raw(in.x[i]) == xt;
+  }
+  if (asked && xt == -INFINITY) {              // NaN is equal to it, which the comparisons do not see
+    above = 0;
+    in.each(tid, NT, [&](float x, int i) { above += x > xt || i < target; });
+  }
+
+  auto reduce = [&](Soft& v, int& n) {         // over the CTA, into every thread
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      Soft other;
+      other.m = __shfl_xor_sync(0xffffffffu, v.m, o);
+      other.s = __shfl_xor_sync(0xffffffffu, v.s, o);
+      other.w = __shfl_xor_sync(0xffffffffu, v.w, o);
+      join(v, other);
+    }
+    n = (int)__reduce_add_sync(0xffffffffu, (uint32_t)n);
+    __syncthreads();
+    if (lane == 0) {
+      sm.warp[wid] = v;
+      sm.count[wid] = n;
+    }
+    __syncthreads();
+    v = sm.warp[0];
+    n = sm.count[0];
+    for (int w = 1; w < NW; ++w) {
+      join(v, sm.warp[w]);
+      n += sm.count[w];
+    }
+  };
+  sm.best[tid] = mine;
+  reduce(soft, above);                         // its barriers show the maxima, too
+  if (tid == 0) {
+    sm.soft = soft;
+    sm.rank = above;
+    sm.found = 0;
+  }
+
+  // ------------------------------------------------ the CTA's best tokens, sorted
+  const int n = min(a.top, a.vocab);
+  if (n > 0) {
+    auto count = [&](auto pred) -> int {       // logits of the CTA that satisfy it
+      int c = 0;
+      in.each(tid, NT, [&](float x, int i) { c += pred(x, i); });
+      c = (int)__reduce_add_sync(0xffffffffu, (uint32_t)c);
+      __syncthreads();
+      if (lane == 0) sm.count[wid] = c;
+      __syncthreads();
+      c = 0;
+      for (int w = 0; w < NW; ++w) c += sm.count[w];
+      return c;
+    };
+    if (wid == 0) {                            // the n-th largest maximum of 64 groups
+      float g[2] = {kNone, kNone};
+      for (int k = 0; k < NT / kGroups; ++k) {
+        g[0] = fmaxf(g[0], sm.best[lane + k * kGroups]);
+        g[1] = fmaxf(g[1], sm.best[lane + 32 + k * kGroups]);
+      }
+      int larger[2] = {0, 0};
+      for (int k = 0; k < 32; ++k) {
+        const float p = __shfl_sync(0xffffffffu, g[0], k), q = __shfl_sync(0xffffffffu, g[1], k);
+        larger[0] += (p > g[0]) + (q > g[0]);
+        larger[1] += (p > g[1]) + (q > g[1]);
+      }
+      const uint32_t least = min(larger[0] < n ? ordered(g[0]) : 0xffffffffu, larger[1] < n ? ordered(g[1]) : 0xffffffffu);
+      const uint32_t bound = __reduce_min_sync(0xffffffffu, least);
+      if (lane == 0) sm.bound = value_of((u64)bound << 32);
+    }
+    __syncthreads();
+    const float bound = sm.bound;
+    bool listed = bound > kNone;
+    if (listed) {
+      // a warp looks at the logits of one thread of its own after another
+      for (uint32_t todo = __ballot_sync(0xffffffffu, mine >= bound); todo; todo &= todo - 1) {
+        const int owner = wid * 32 + __ffs(todo) - 1;
+        auto offer = [&](float x, int i) {
+          if (x >= bound) {
+            const int at = atomicAdd(&sm.found, 1);
+            if (at < kList) sm.list[at] = key_of(x + 0.f, i);
+          }
+        };
+        if (lane == 0 && in.single(owner) >= 0) offer(raw(in.x[in.single(owner)]), in.single(owner));
+        for (int v = in.v0 + owner + lane * NT; v < in.v1; v += 32 * NT) {
+          const T* x = in.x + in.lead + v * W;
+#pragma unroll
+          for (int k = 0; k < W; ++k) offer(raw(x[k]), in.lead + v * W + k);
+        }
+      }
+      __syncthreads();
+      listed = sm.found <= kList;
+    }
+    if (!listed) {                             // bisection over the ordered logits, then over the index of the last ones
+      __syncthreads();
+      if (tid == 0) sm.found = 0;
+      const uint32_t none = ordered(-INFINITY);
+      const int want = min(n, count([&](float x, int) { return ordered(x) > none; }));
+      if (want > 0) {
+        uint32_t lo = none + 1, hi = 0xffffffffu;                    // the largest key that `want` logits reach
+        while (lo < hi) {
+          const uint32_t mid = lo + (hi - lo) / 2 + 1;
+          if (count([&](float x, int) { return ordered(x) >= mid; }) >= want) lo = mid;
+          else hi = mid - 1;
+        }
+        const int ties = want - count([&](float x, int) { return ordered(x) > lo; });
+        int first = 0, last = a.vocab - 1;     // the lowest index up to which enough are equal to it
+        while (first < last) {
+          const int mid = first + (last - first) / 2;
+          if (count([&](float x, int i) { return ordered(x) == lo && i <= mid; }) >= ties) last = mid;
+          else first = mid + 1;
+        }
+        in.each(tid, NT, [&](float x, int i) {
+          if (ordered(x) > lo || (ordered(x) == lo && i <= first)) sm.list[atomicAdd(&sm.found, 1)] = key_of(x, i);
+        });
+      }
+      __syncthreads();
+    }
+    const int m = sm.found;
+    if (tid < m) {                             // sorted by counting: keys are unique
+      const u64 key = sm.list[tid];
+      int at = 0;
+      for (int k = 0; k < m; ++k) at += sm.list[k] > key;
+      if (at < n) sm.top[at] = key;
+    }
+    if (tid == 0) sm.kept = min(m, n);
+  }
+
+  // ------------------------------------------------ the cluster's parts joined
+  cluster.sync();
+  auto gather = [&] {
+    soft = {kNone * kLog2e, 0.f, 0.f};
+    above = 0;
+    for (int c = 0; c < cs; ++c) {
+      const Shared* o = cluster.map_shared_rank(&sm, c);
+      join(soft, o->soft);
+      above += o->rank;
+    }
+  };
+  gather();
+  float entropy;
+  const bool far = !(fabsf(soft.m) <= kFar);
+  if (far) {              // a careful pass: the same for all CTAs of the row
+    float m = -INFINITY;
+    in.each(tid, NT, [&](float x, int) { m = fmaxf(m, x); });
+    auto whole = [&](auto op, float v, float* slot) {                // over the cluster
+      for (int o = 16; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
+      __syncthreads();
+      if (lane == 0) sm.warp[wid].m = v;
+      __syncthreads();
+      v = sm.warp[0].m;
+      for (int w = 1; w < NW; ++w) v = op(v, sm.warp[w].m);
+      cluster.sync();
+      if (tid == 0) *slot = v;
+      cluster.sync();
+      v = *cluster.map_shared_rank(slot, 0);
+      for (int c = 1; c < cs; ++c) v = op(v, *cluster.map_shared_rank(slot, c));
+      return v;
+    };
+    auto larger = [](float p, float q) { return fmaxf(p, q); };
+    auto plus = [](float p, float q) { return p + q; };
+    m = whole(larger, m, &sm.most);
+    float s = 0.f, w = 0.f;
+    in.each(tid, NT, [&](float x, int) {
+      const float d = x == m ? 0.f : x - m, e = expf(d);
+      s += e;
+      if (e > 0.f) w = fmaf(e, d, w);
+    });
+    s = whole(plus, s, &sm.most);
+    w = whole(plus, w, &sm.most);
+    const float ls = logf(s);
+    entropy = m == -INFINITY ? 0.f : ls - w / s;
+    soft.m = m;
+    soft.s = ls;
+  } else {
+    const float ls = log2f(soft.s);
+    entropy = (ls - soft.w / soft.s) * kLn2;
+    soft.s = ls;
+  }
+  auto log_p = [&](float x) {
+    if (x == -INFINITY) return x;
+    const float l = far ? (x == soft.m ? 0.f : x - soft.m) - soft.s
+                        : x < -1e30f ? x : (fmaf(x, kLog2e, -soft.m) - soft.s) * kLn2;
+    return fminf(l, 0.f);
+  };
+  if (rank == 0) {
+    if (tid == 0) {
+      a.logp[row] = asked ? log_p(xt) : 0.f;
+      if (a.entropy) a.entropy[row] = fmaxf(entropy, 0.f);
+      if (a.rank) a.rank[row] = asked ? above : -1;
+    }
+    if (a.top > 0) {
+      int have = 0;
+      __syncthreads();
+      for (int c = 0; c < cs; ++c) {           // the CTAs' lists, one after another
+        const Shared* o = cluster.map_shared_rank(&sm, c);
+        const int kept = o->kept;
+        if (tid < kept) sm.list[have + tid] = o->top[tid];
+        have += kept;
+      }
+      __syncthreads();
+      if (tid < have) {
+        const u64 key = sm.list[tid];
+        int at = 0;
+        for (int k = 0; k < have; ++k) at += sm.list[k] > key;
+        if (at < a.top) {
+          const int64_t to = (int64_t)row * a.top + at;
+          a.top_ids[to] = index_of(key);
+          a.top_logp[to] = log_p(value_of(key));
+        }
+      }
+      for (int at = have + tid; at < a.top; at += NT) {              // fewer tokens than asked for
+        const int64_t to = (int64_t)row * a.top + at;
+        a.top_ids[to] = -1;
+        a.top_logp[to] = -INFINITY;
+      }
+    }
+  }
+  cluster.sync();                              // no CTA leaves while its memory is read
+}
+
+template <typename T>
+cudaError_t run(const LogprobArgs& a, cudaStream_t s) {
+  const int sms = sm_count();
+  int cs = 1;
+  while (cs < kMaxCluster && (int64_t)a.rows * cs * 2 <= sms && a.vocab / (2 * cs) >= 4096) cs *= 2;
+  const bool few = cs > 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.rows * cs));
+  cfg.blockDim = dim3(few ? 512 : 256);
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = cs;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  const cudaError_t e = few ? cudaLaunchKernelEx(&cfg, logprobs_kernel<T, 512>, a) : cudaLaunchKernelEx(&cfg, logprobs_kernel<T, 256>, a);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_logprobs(const LogprobArgs& a, int dtype, cudaStream_t s) {
+  return dtype == MOE_F32 ? run<float>(a, s) : run<bf16>(a, s);
+}
+
+}  // namespace moeslot

@@ -565,6 +565,95 @@ MOE_API moe_status moe_sample(const void* logits, int32_t dtype, int32_t rows, i
                               const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
                               const float* u, int32_t* ids, float* logp, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Between the attention, the experts and the token choice of a step
+ *
+ * Three operators that need no handle and no workspace: the join of a block's
+ * output into the residual stream with the norms on either side of it, the dense
+ * projections with 4-bit weights, and the scores of given tokens.  They run on the
+ * current device and on `stream`, neither allocate nor synchronise, and so can be
+ * captured into a CUDA graph.
+ * ---------------------------------------------------------------------- */
+enum { MOE_RESIDUAL_GATE_NONE = 0,
+       MOE_RESIDUAL_GATE_ROW = 1,       /* one number for each row             */
+       MOE_RESIDUAL_GATE_CHANNEL = 2,   /* one for each channel, in all rows   */
+       MOE_RESIDUAL_GATE_ELEMENT = 3 }; /* one for each element                */
+#define MOE_NORM_MAX_HIDDEN 16384
+#define MOE_LINEAR_MAX_IN 65536
+#define MOE_LINEAR_MAX_OUT 1048576
+#define MOE_LOGPROBS_MAX_TOP 32
+
+typedef struct {
+  int32_t hidden;          /* 1..MOE_NORM_MAX_HIDDEN                             */
+  int32_t dtype;           /* MOE_F32 or MOE_BF16: x, gate, weights and y        */
+  int32_t residual_dtype;  /* dtype or MOE_F32: residual and residual_out        */
+  int32_t gate;            /* MOE_RESIDUAL_GATE_*                                */
+  int32_t gate_sigmoid;    /* 1: the gate's sigmoid is taken                     */
+  float residual_scale;
+  float norm_eps;          /* >= 0                                               */
+  float weight_offset;     /* added to the weights (1 where they are stored less 1) */
+} moe_norm_config;
+
+/* The end of one block and the start of the next, in one pass over the rows:
+ *   n = x / sqrt(mean(x^2) + norm_eps) * (weight_offset + post_weight)   (x where post_weight is NULL)
+ *   residual_out = residual + residual_scale * gate * n
+ *   y = r / sqrt(mean(r^2) + norm_eps) * (weight_offset + pre_weight),   r = residual_out before its rounding
+ *   x, residual, residual_out, y   device [rows] rows of [hidden], *_stride elements apart
+ *   gate       MOE_RESIDUAL_GATE_ROW: [rows], gate_stride elements apart; _CHANNEL: [hidden];
+ *              _ELEMENT: [rows] rows of [hidden], gate_stride elements apart
+ *   post_weight, pre_weight  device [hidden]; pre_weight NULL: y is not weighted
+ *   x NULL     nothing is added: y is the norm of residual; residual_out and post_weight must be
+ *              NULL and the config without a gate
+ *   y NULL     only residual_out is wanted
+ * Computed in fp32, rounded once.  residual_out may be residual and y may be x (the same address,
+ * stride and type); other overlaps of an output with an input are not allowed.  Rows that lie on
+ * 16-byte boundaries with a hidden that is a multiple of 8 are faster. */
+MOE_API moe_status moe_residual_norm(const moe_norm_config* cfg, const void* x, int64_t x_stride, const void* gate,
+                                     int64_t gate_stride, const void* post_weight, const void* residual,
+                                     int64_t residual_stride, void* residual_out, int64_t residual_out_stride,
+                                     const void* pre_weight, void* y, int64_t y_stride, int32_t rows, void* stream);
+
+/* 4-bit weights of a projection: codes [out_features][in_features / 2] bytes, the code of input 2j in
+ * the low four bits of byte j, of 2j + 1 in the high four, in two's complement (-8..7); scales
+ * [out_features][ceil(in_features / group)], one for each `group` inputs (the last group may be
+ * shorter).  in_features is a multiple of 32, group 32, 64 or 128.
+ * moe_q4_pack (host only) makes both from fp32 weights w [out_features][in_features], as the
+ * residual-split records are made: scale = max |w| / 7 (1 for a group of zeros), code =
+ * round-half-even(w / scale) within +-7.  A weight that is not finite is refused. */
+MOE_API moe_status moe_q4_pack(const float* w, int32_t out_features, int32_t in_features, int32_t group, uint8_t* codes,
+                               float* scales);
+
+/* out[t, n] = sum_k code[n, k] scale[n, k / group] x[t, k] + bias[n]
+ *   x        device [rows] rows of [in_features] of dtype (MOE_F32 or MOE_BF16), x_stride elements apart
+ *   codes, scales  as above, on the device; scales of scale_dtype (MOE_F32 or MOE_BF16), codes 16-byte
+ *            aligned
+ *   bias     device [out_features] of dtype, or NULL
+ *   out      device [rows] rows of [out_features] of out_dtype (dtype or MOE_F32), out_stride elements apart
+ * Products are exact, sums fp32, in the same order in every call with the same sizes; rounded once.
+ * out must not overlap an input. */
+MOE_API moe_status moe_linear_q4(const void* x, int32_t dtype, int64_t x_stride, int32_t rows, int32_t in_features,
+                                 const uint8_t* codes, const void* scales, int32_t scale_dtype, int32_t group,
+                                 const void* bias, int32_t out_features, void* out, int32_t out_dtype, int64_t out_stride,
+                                 void* stream);
+
+/* Scores of given tokens: with lse = log sum_i exp(logits[row, i]) over the row,
+ *   logits    device [rows] rows of [vocab] of dtype (MOE_F32 or MOE_BF16), row_stride elements apart;
+ *             vocab up to MOE_SAMPLE_MAX_VOCAB
+ *   targets   device int32 [rows]: a token of each row; outside 0..vocab-1: none is asked for, logp is 0 and
+ *             rank -1
+ *   logp      out fp32 [rows]: logits[row, target] - lse
+ *   entropy   out fp32 [rows]: -sum_i p_i log p_i; may be NULL
+ *   rank      out int32 [rows]: how many tokens come before the target in descending order of their logits
+ *             (equal ones by index); may be NULL
+ *   top_ids, top_logp  out int32 and fp32 [rows][top]: the first `top` tokens (0..MOE_LOGPROBS_MAX_TOP) in that
+ *             order and their log probabilities; -1 and -inf where a row has fewer logits above -inf.  May be
+ *             NULL where top is 0
+ * NaN counts as -inf, and +inf takes all the mass.  A row without any logit above -inf has logp -inf and
+ * entropy 0.  Sums are fp32. */
+MOE_API moe_status moe_logprobs(const void* logits, int32_t dtype, int32_t rows, int32_t vocab, int64_t row_stride,
+                                const int32_t* targets, int32_t top, float* logp, float* entropy, int32_t* rank,
+                                int32_t* top_ids, float* top_logp, void* stream);
+
 /* Number of kernel launches the library issued since the pool was created. */
 MOE_API uint64_t moe_launch_count(const moe_pool* pool);
 
