@@ -106,6 +106,7 @@ _sig = {
     "moe_q4_pack": (_i32, [_vp, _i32, _i32, _i32, _vp, _vp]),
     "moe_linear_q4": (_i32, [_vp, _i32, _i64, _i32, _i32, _vp, _vp, _i32, _i32, _vp, _i32, _vp, _i32, _i64, _vp]),
     "moe_logprobs": (_i32, [_vp, _i32, _i32, _i32, _i64, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "moe_step_status": (_i32, []),
     "moe_last_error": (ctypes.c_char_p, []),
     "moe_route_topk_noalloc": (_i32, [_i32, _i32, _i32, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
 }
@@ -637,3 +638,8 @@ def moe_logprobs(logits, targets, logp, entropy=None, rank=None, top_ids=None, t
             None if rank is None else _flat("rank", rank, i32, rows, dev),
             None if top_ids is None else _flat("top_ids", top_ids, i32, rows * top, dev),
             None if top_logp is None else _flat("top_logp", top_logp, f32, rows * top, dev))
+
+
+def moe_step_status():
+    """MOE_OK, or MOE_ERR_TIMEOUT where a moe_linear_q4 on the current device gave up; blocking, resets it."""
+    return _lib.moe_step_status()

@@ -1,11 +1,15 @@
 // moe_linear_q4: out[t, n] = bias[n] + sum_g scale[n, g] sum_{k in group g} code[n, k] x[t, k],
 // 4-bit codes in -8..7 with one scale for each group of 32, 64 or 128 inputs.
 //
-// Row kernel.  A warp takes tiles of 16 outputs by up to 32 columns of x on mma.sync (M the
-// outputs, N the columns).  A code is exact in bf16, so products and the sums of a group
-// are the tensor core's, exact up to fp32 sums; a group's sum is scaled in fp32.  An fp32
-// x is cut into three bf16 numbers that add up to it (8 bits of its 24 each) and takes
-// three columns.
+// Row kernel, for up to 32 columns of x.  The codes are all there is to read, so the kernel is
+// a stream of them: a CTA takes tiles of 16 to 64 outputs, one warp copies their codes in
+// bulk, a row of a slice of K each, into a ring in shared memory, two more bring the scales, and 16 warps
+// share the slice, a block of 128 inputs each (two or one groups of warps share the rows), on
+// mma.sync with M the outputs and N the columns of x.  A code is exact in bf16, so products
+// and the sums of a group are the tensor core's, exact up to fp32 sums; a group's sum is
+// scaled in fp32.  At a tile's end the warps' parts are added up in their order.  An fp32 x is
+// cut into three bf16 numbers that add up to it (8 bits of its 24 each) and takes three
+// columns.
 //
 // The order of k inside a group is free as long as codes and x agree: lane (g, t) of the
 // warp takes for row g (and g + 8) the quarter t of each group, so that it reads its codes
@@ -25,18 +29,19 @@ namespace moeslot {
 namespace {
 
 typedef __nv_bfloat16 bf16;
-constexpr int NT = 512, NWARP = NT / 32;
-constexpr int kTile = 16;            // outputs of a warp's tile
-constexpr int kBlock = 128;          // inputs of a step
-constexpr int kColumn = 20;          // floats between the columns of a tile in shared memory: no bank conflicts
-constexpr int kShared = 220 * 1024;  // dynamic shared memory of a CTA
+constexpr int NWARP = 16, NT = NWARP * 32;     // consumers
+constexpr int kCodeWarps = 4, kScaleWarps = 2, kThreads = NT + 32 * (kCodeWarps + kScaleWarps);
+constexpr int kBlock = 128;                    // inputs of a warp's part of a slice
+constexpr int kRing = 8;                       // stages at most
+constexpr int kShared = 225 * 1024;            // dynamic shared memory of a CTA
 
 // Codes of a word as four pairs (k, k + 4) of bf16.
 __device__ __forceinline__ void widen(uint32_t w, uint32_t (&p)[4]) {
   const __nv_bfloat162 top = __halves2bfloat162(__ushort_as_bfloat16(0x4308), __ushort_as_bfloat16(0x4308));   // 136
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t u = ((w >> (4 * i)) & 0x000f000fu) ^ 0x43084308u;
+    uint32_t u;                                // ((w >> 4 i) & 0x000f000f) ^ 0x43084308
+    asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(u) : "r"(w >> (4 * i)), "r"(0x000f000fu), "r"(0x43084308u));
     const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u), top);
     p[i] = *reinterpret_cast<const uint32_t*>(&v);
   }
@@ -85,264 +90,296 @@ __device__ __forceinline__ uint4 column8(const LinearArgs& a, int64_t row, int p
 __device__ __forceinline__ float to_float(float v) { return v; }
 __device__ __forceinline__ float to_float(bf16 v) { return __bfloat162float(v); }
 
-// What a warp reads for one step of a tile: rows g and g + 8.
-template <int P>
-struct Step {
-  uint32_t code[2][4];
-  float scale[2][P];
+// Shapes of a row kernel: N8 * 8 columns of x; a warp has 16 * MT outputs; RG groups of warps have outputs of
+// their own, the 16 / RG warps of a group the blocks of a slice.
+template <int N8_, int MT_, int RG_, int G_>
+struct Shape {
+  static constexpr int N8 = N8_, MT = MT_, RG = RG_, G = G_;
+  static constexpr int COLS = 8 * N8, ROWS = 16 * MT * RG, PARTS = NWARP / RG, P = kBlock / G, WORDS = G / 32;
+  static constexpr int COLUMN = 16 * MT + 4;   // floats between a tile's columns in shared memory: no bank conflicts
+  static constexpr int RED = NWARP * COLS * COLUMN * 4;
+  static constexpr int X_BLOCK = 4 * COLS * 64;          // bytes of a block of x
 };
 
-template <typename S, int G>
-__device__ __forceinline__ void fetch(const LinearArgs& a, int tile, int block, Step<kBlock / G>& st) {
-  constexpr int P = kBlock / G, WORDS = G / 32;
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int64_t n = min(tile * kTile + g + 8 * i, a.N - 1);
-    const uint8_t* row = a.codes + n * (a.K / 2);
-    const S* scales = static_cast<const S*>(a.scales) + n * a.groups;
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const int k = block * kBlock + p * G + t * (G / 4);
-      uint32_t* c = st.code[i] + p * WORDS;
-      if (k < a.K) {
-        if constexpr (WORDS == 4) *reinterpret_cast<uint4*>(c) = __ldcs(reinterpret_cast<const uint4*>(row + k / 2));
-        else if constexpr (WORDS == 2) *reinterpret_cast<uint2*>(c) = __ldcs(reinterpret_cast<const uint2*>(row + k / 2));
-        else *c = __ldcs(reinterpret_cast<const uint32_t*>(row + k / 2));
-      } else {
-#pragma unroll
-        for (int j = 0; j < WORDS; ++j) c[j] = 0;
-      }
-      const int group = block * P + p;
-      st.scale[i][p] = group < a.groups ? to_float(scales[group]) : 0.f;
-    }
-  }
-}
-
 // Grid: for each pass over `pass_rows` rows of x, the CTAs that share the tiles.
-// Shared memory: x of the pass, [block][word][column][t][8], then the warps' tiles.
-template <typename S, int G, int N8>
-__global__ void __launch_bounds__(NT, 1) linear_q4_rows_kernel(const LinearArgs a) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  constexpr int P = kBlock / G, WORDS = G / 32, COLS = 8 * N8, U = 2;
+// Shared memory: x [block][word][column][t][8], the warps' parts, then the ring: codes, `pitch` bytes a row, and
+// scales, `scale_pitch` floats a row.  Rows are apart by half a group's bytes more than a multiple of 128: no bank
+// conflicts among the eight rows that a load instruction reads.
+template <typename H>
+__global__ void __launch_bounds__(kThreads, 1) linear_q4_rows_kernel(const LinearArgs a) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t full[kRing], empty[kRing];
+  constexpr int G = H::G, P = H::P, WORDS = H::WORDS, COLS = H::COLS, N8 = H::N8, MT = H::MT;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-  const int blocks = (a.K + kBlock - 1) / kBlock, chunk = min(a.chunk, blocks);
+  const int blocks = (a.K + kBlock - 1) / kBlock;
   uint4* xs = reinterpret_cast<uint4*>(smem);
-  float* red = reinterpret_cast<float*>(smem + (size_t)chunk * 4 * COLS * 64);
+  float* red = reinterpret_cast<float*>(smem + (size_t)a.chunk * a.slice * H::X_BLOCK);
+  uint8_t* ring = reinterpret_cast<uint8_t*>(red) + H::RED;
+  const int stage_bytes = H::ROWS * (a.pitch + a.scale_pitch * 4);
   const int pass = blockIdx.x / a.ctas, cta = blockIdx.x - pass * a.ctas;
   const int row0 = pass * a.pass_rows, rows = min(a.pass_rows, a.rows - row0);
-  const int splits = 1 << a.split_log2, team = wid >> a.split_log2, part = wid & (splits - 1), teams = NWARP >> a.split_log2;
-  const int tiles = (a.N + kTile - 1) / kTile;
-  const bool whole = chunk == blocks;
-  const int esize = a.x_f32 ? 4 : 2, parts = a.x_f32 ? 3 : 1;
-  const bool wide = (reinterpret_cast<uintptr_t>(a.x) & 15) == 0 && a.x_stride * esize % 16 == 0;
+  const int tiles = (a.N + H::ROWS - 1) / H::ROWS, mine = (tiles - cta + a.ctas - 1) / a.ctas;
+  const int slices = (blocks + a.slice - 1) / a.slice;
+  const int64_t steps = (int64_t)mine * slices;
+  if (tid == 0) {
+    for (int s = 0; s < a.depth; ++s) {
+      sm103::bar_init(full + s, 32 * kCodeWarps + 1);
+      sm103::bar_init(empty + s, NWARP);
+    }
+    sm103::bar_init_done();
+  }
+  __syncthreads();
   sm103::grid_wait();
 
-  auto stage = [&](int b0) {                   // blocks b0 .. of x; zeros past its end and its rows
-    const int groups8 = chunk * (kBlock / 8);
-    for (int u = tid; u < groups8 * COLS; u += NT) {
-      const int col = u / groups8, q = u - col * groups8, k0 = b0 * kBlock + q * 8;
-      const int in_block = q * 8 % kBlock, p = in_block / G, in_group = in_block % G;
-      const int t = in_group / (G / 4), word = p * WORDS + in_group % (G / 4) / 8;
-      const int row = a.x_f32 ? col / 3 : col;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (row < rows && col < rows * parts && k0 < a.K) v = column8(a, row0 + row, col - row * parts, k0, wide);
-      xs[((q / (kBlock / 8) * 4 + word) * COLS + col) * 4 + t] = v;
+  if (wid >= NWARP && wid < NWARP + kCodeWarps) {        // ---------------------- the codes
+    int st = 0, slice = 0, tile = cta;
+    uint32_t phase = 0;
+    for (int64_t i = 0; i < steps; ++i) {
+      if (i >= a.depth && !sm103::bar_wait_warp(empty + st, phase ^ 1)) {
+        if (lane == 0) atomicCAS(a.status, 0, MOE_ERR_TIMEOUT);
+        break;
+      }
+      const int at = slice * a.slice * (kBlock / 2), bytes = min(a.slice * (kBlock / 2), a.K / 2 - at);
+      const int n0 = tile * H::ROWS, n = min(H::ROWS, a.N - n0);
+      const uint32_t dst = sm103::smem_addr(ring) + st * stage_bytes;
+      const uint8_t* src = a.codes + (int64_t)n0 * (a.K / 2) + at;
+      for (int r = wid - NWARP; r < n; r += kCodeWarps)
+        for (int c = lane * 16; c < bytes; c += 512) sm103::cp_async16(dst + r * a.pitch + c, src + (int64_t)r * (a.K / 2) + c, 16);
+      sm103::cp_async_arrive(full + st);
+      if (++slice == slices) {
+        slice = 0;
+        tile += a.ctas;
+      }
+      if (++st == a.depth) {
+        st = 0;
+        phase ^= 1;
+      }
     }
-  };
-
-  const int stride = a.ctas * teams, first = cta * teams + team;
-  float acc[N8][4];
-  auto clear = [&] {
+    sm103::cp_async_wait();
+    return;
+  }
+  if (wid >= NWARP) {                          // ------------------------------- the scales, every other stage
+    const int per = a.slice * P;               // of a row in a stage
+    const uint32_t mul = 0xffffffffu / per + 1;          // k / per for k below 2^16 and per above 1
+    auto row_of = [&](uint32_t k) { return per == 1 ? k : __umulhi(k, mul); };
+    int slice = (wid - NWARP - kCodeWarps) % slices, tile = cta + (wid - NWARP - kCodeWarps) / slices * a.ctas;
+    for (int64_t i = wid - NWARP - kCodeWarps; i < steps; i += kScaleWarps) {
+      const int st = (int)(i % a.depth);
+      const uint32_t phase = (uint32_t)(i / a.depth) & 1;
+      if (i >= a.depth && !sm103::bar_wait_warp(empty + st, phase ^ 1)) return;
+      float* dst = reinterpret_cast<float*>(ring + st * stage_bytes + H::ROWS * a.pitch);
+      const int n0 = tile * H::ROWS, g0 = slice * per, groups = min(per, a.groups - g0);
+      for (int k0 = lane; k0 < H::ROWS * per; k0 += 32 * 16) {
+        float v[16];
 #pragma unroll
-    for (int j = 0; j < N8; ++j)
+        for (int j = 0; j < 16; ++j) {
+          const uint32_t k = k0 + 32 * j, r = row_of(k), g = k - r * per;
+          v[j] = 0.f;
+          if (k < H::ROWS * per && n0 + (int)r < a.N && (int)g < groups) {
+            const int64_t at = (int64_t)(n0 + r) * a.groups + g0 + g;
+            v[j] = a.scale_f32 ? static_cast<const float*>(a.scales)[at] : __bfloat162float(static_cast<const bf16*>(a.scales)[at]);
+          }
+        }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
-  };
-  auto work = [&](const Step<P>& st, int block) {       // block: within the staged ones
-    const uint4* xb = xs + (size_t)block * 4 * COLS * 4 + (lane >> 2) * 4 + (lane & 3);
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-      float sum[N8][4];
-#pragma unroll
-      for (int j = 0; j < N8; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sum[j][i] = 0.f;
-#pragma unroll
-      for (int w = p * WORDS; w < (p + 1) * WORDS; ++w) {
-        uint32_t lo[4], hi[4];
-        widen(st.code[0][w], lo);
-        widen(st.code[1][w], hi);
-        const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
-#pragma unroll
-        for (int j = 0; j < N8; ++j) {
-          const uint4 b = xb[(w * COLS + 8 * j) * 4];
-          sm103::mma16816(sum[j], a0, b.x, b.y);
-          sm103::mma16816(sum[j], a1, b.z, b.w);
+        for (int j = 0; j < 16; ++j) {
+          const uint32_t k = k0 + 32 * j, r = row_of(k), g = k - r * per;
+          if (k < H::ROWS * per) dst[r * a.scale_pitch + g] = v[j];
         }
       }
-#pragma unroll
-      for (int j = 0; j < N8; ++j) {
-        acc[j][0] = fmaf(st.scale[0][p], sum[j][0], acc[j][0]);
-        acc[j][1] = fmaf(st.scale[0][p], sum[j][1], acc[j][1]);
-        acc[j][2] = fmaf(st.scale[1][p], sum[j][2], acc[j][2]);
-        acc[j][3] = fmaf(st.scale[1][p], sum[j][3], acc[j][3]);
+      __syncwarp();
+      if (lane == 0) sm103::bar_arrive(full + st);
+      slice += kScaleWarps;
+      while (slice >= slices) {
+        slice -= slices;
+        tile += a.ctas;
       }
     }
-  };
-  int turn = 0;
-  auto finish = [&](int tile) {                // the team's parts joined, in their order, and written
-    float* mine = red + (size_t)(turn * NWARP + wid) * COLS * kColumn;
-    const float* base = red + (size_t)(turn * NWARP + team * splits) * COLS * kColumn;
-    turn ^= 1;
-    const int g = lane >> 2, t = lane & 3;
-#pragma unroll
-    for (int j = 0; j < N8; ++j) {
-      mine[(8 * j + 2 * t) * kColumn + g] = acc[j][0];
-      mine[(8 * j + 2 * t + 1) * kColumn + g] = acc[j][1];
-      mine[(8 * j + 2 * t) * kColumn + g + 8] = acc[j][2];
-      mine[(8 * j + 2 * t + 1) * kColumn + g + 8] = acc[j][3];
-    }
-    if (splits == 1) __syncwarp();
-    else sm103::named_sync(1 + team, splits * 32);
-    for (int u = part * 32 + lane; u < rows * kTile; u += splits * 32) {
-      const int row = u / kTile, i = u % kTile, n = tile * kTile + i;
-      if (n >= a.N) continue;
-      float v = 0.f;
-      for (int s = 0; s < splits; ++s) {
-        const float* from = base + (size_t)s * COLS * kColumn + i;
-        if (parts == 1) v += from[row * kColumn];
-        else v += from[3 * row * kColumn] + (from[(3 * row + 1) * kColumn] + from[(3 * row + 2) * kColumn]);
-      }
-      if (a.bias) v += a.x_f32 ? static_cast<const float*>(a.bias)[n] : to_float(static_cast<const bf16*>(a.bias)[n]);
-      const int64_t at = (row0 + row) * a.out_stride + n;
-      if (a.out_f32) static_cast<float*>(a.out)[at] = v;
-      else static_cast<bf16*>(a.out)[at] = __float2bfloat16_rn(v);
-    }
-    if (splits == 1) __syncwarp();
-  };
+    return;
+  }
 
-  if (whole) {
-    // the steps of all this warp's tiles in one run, U of them on their way
-    Step<P> st[U];
-    const int per = (blocks - part + splits - 1) / splits;               // steps of a tile (splits <= blocks)
-    const int mine = first < tiles ? (tiles - first + stride - 1) / stride : 0;
-    int ft = first, fb = part;
-    auto ahead = [&](Step<P>& s) {
-      if (ft < tiles) fetch<S, G>(a, ft, fb, s);
-      fb += splits;
-      if (fb >= blocks) {
-        fb = part;
-        ft += stride;
-      }
-    };
+  // ------------------------------------------------------------------------------ the products
+  const int g = lane >> 2, t = lane & 3, group = wid % H::RG, part = wid / H::RG;
+  const int esize = a.x_f32 ? 4 : 2, parts = a.x_f32 ? 3 : 1;
+  const bool wide = (reinterpret_cast<uintptr_t>(a.x) & 15) == 0 && a.x_stride * esize % 16 == 0;
+  auto stage_x = [&](int b0) {                 // `chunk` slices of x from block b0; zeros past its end and its rows
+    const int eights = a.chunk * a.slice * (kBlock / 8);
+    for (int u = tid; u < eights * COLS; u += NT) {
+      const int col = u / eights, q = u - col * eights, row = a.x_f32 ? col / 3 : col;
+      const int k0 = b0 * kBlock + q * 8, in_block = q * 8 % kBlock, p = in_block / G, in_group = in_block % G;
+      const int tx = in_group / (G / 4), word = p * WORDS + in_group % (G / 4) / 8;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (row < rows && k0 < a.K) v = column8(a, row0 + row, col - row * parts, k0, wide);
+      xs[((q / (kBlock / 8) * 4 + word) * COLS + col) * 4 + tx] = v;
+    }
+  };
+  float acc[MT][N8][4];
+  int st = 0, slice = 0, tile = cta;
+  uint32_t phase = 0;
+  bool alive = true;                           // without it the others' barriers are still met, and nothing waited for
+  for (int64_t i = 0; i < steps; ++i) {
+    const int held = slice % a.chunk;          // slice of x within the ones in shared memory
+    if (held == 0 && (i == 0 || a.chunk < slices)) {
+      if (i > 0) sm103::named_sync(1, NT);     // all are through with the last ones
+      stage_x(slice * a.slice);
+      sm103::named_sync(1, NT);
+    }
+    if (slice == 0) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) ahead(st[u]);
-    stage(0);
-    __syncthreads();
-    int tile = first, block = part;
-    clear();
-    const int total = mine * per;
-    for (int i = 0; i < total; i += U) {
+      for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (i + u < total) {
-          work(st[u], block);
-          ahead(st[u]);
-          block += splits;
-          if (block >= blocks) {
-            finish(tile);
-            clear();
-            block = part;
-            tile += stride;
+        for (int j = 0; j < N8; ++j)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[m][j][k] = 0.f;
+    }
+    if (alive && !(alive = sm103::bar_wait_warp(full + st, phase)) && lane == 0) atomicCAS(a.status, 0, MOE_ERR_TIMEOUT);
+    const int block = slice * a.slice + part;
+    if (part < a.slice && block < blocks) {
+      const uint8_t* codes = ring + st * stage_bytes + (group * 16 * MT + g) * a.pitch + part * (kBlock / 2) + t * (G / 8);
+      const float* scales = reinterpret_cast<const float*>(ring + st * stage_bytes + H::ROWS * a.pitch) +
+                            (group * 16 * MT + g) * a.scale_pitch + part * P;
+      const uint4* xb = xs + (size_t)(held * a.slice + part) * 4 * COLS * 4 + lane;
+      // past the end of K x is zero and any code finite
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        uint32_t code[MT][2][WORDS];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint8_t* c = codes + (m * 16 + h * 8) * a.pitch + p * (G / 2);
+            if constexpr (WORDS == 4) {
+              const uint4 u = *reinterpret_cast<const uint4*>(c);
+              code[m][h][0] = u.x; code[m][h][1] = u.y; code[m][h][2] = u.z; code[m][h][3] = u.w;
+            } else if constexpr (WORDS == 2) {
+              const uint2 u = *reinterpret_cast<const uint2*>(c);
+              code[m][h][0] = u.x; code[m][h][1] = u.y;
+            } else {
+              code[m][h][0] = *reinterpret_cast<const uint32_t*>(c);
+            }
+          }
+        float sum[MT][N8][4];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int j = 0; j < N8; ++j)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) sum[m][j][k] = 0.f;
+#pragma unroll
+        for (int w = 0; w < WORDS; ++w) {
+          uint4 b[N8];
+#pragma unroll
+          for (int j = 0; j < N8; ++j) b[j] = xb[((p * WORDS + w) * COLS + 8 * j) * 4];
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            uint32_t lo[4], hi[4];
+            widen(code[m][0][w], lo);
+            widen(code[m][1][w], hi);
+            const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
+#pragma unroll
+            for (int j = 0; j < N8; ++j) {
+              sm103::mma16816(sum[m][j], a0, b[j].x, b[j].y);
+              sm103::mma16816(sum[m][j], a1, b[j].z, b[j].w);
+            }
+          }
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const float s0 = scales[m * 16 * a.scale_pitch + p], s1 = scales[(m * 16 + 8) * a.scale_pitch + p];
+#pragma unroll
+          for (int j = 0; j < N8; ++j) {
+            acc[m][j][0] = fmaf(s0, sum[m][j][0], acc[m][j][0]);
+            acc[m][j][1] = fmaf(s0, sum[m][j][1], acc[m][j][1]);
+            acc[m][j][2] = fmaf(s1, sum[m][j][2], acc[m][j][2]);
+            acc[m][j][3] = fmaf(s1, sum[m][j][3], acc[m][j][3]);
           }
         }
       }
     }
-  } else {                                     // x in chunks: all warps of the CTA go through them together
-    const int rounds = (tiles + stride - 1) / stride;
-    for (int i = 0; i < rounds; ++i) {
-      const int tile = first + i * stride;
-      clear();
-      for (int b0 = 0; b0 < blocks; b0 += chunk) {
-        __syncthreads();
-        stage(b0);
-        __syncthreads();
-        for (int b = b0 + part; b < min(b0 + chunk, blocks) && tile < tiles; b += splits) {
-          Step<P> st;
-          fetch<S, G>(a, tile, b, st);
-          work(st, b - b0);
-        }
-      }
-      if (tile < tiles) finish(tile);
+    __syncwarp();
+    if (lane == 0) sm103::bar_arrive(empty + st);
+    if (++st == a.depth) {
+      st = 0;
+      phase ^= 1;
     }
+    if (++slice < slices) continue;
+    // ---------------------------------------------------- the parts added up, in their order
+    slice = 0;
+    sm103::named_sync(1, NT);                  // the last tile's have been read
+    float* to = red + (size_t)wid * COLS * H::COLUMN + g;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int j = 0; j < N8; ++j) {
+        to[(8 * j + 2 * t) * H::COLUMN + m * 16] = acc[m][j][0];
+        to[(8 * j + 2 * t + 1) * H::COLUMN + m * 16] = acc[m][j][1];
+        to[(8 * j + 2 * t) * H::COLUMN + m * 16 + 8] = acc[m][j][2];
+        to[(8 * j + 2 * t + 1) * H::COLUMN + m * 16 + 8] = acc[m][j][3];
+      }
+    sm103::named_sync(1, NT);
+    const int used = min(H::PARTS, min(a.slice, blocks));
+    for (int u = tid; u < rows * H::ROWS; u += NT) {
+      const int row = u / H::ROWS, o = u % H::ROWS, n = tile * H::ROWS + o;
+      if (n >= a.N) continue;
+      const float* from = red + (size_t)(o / (16 * MT)) * COLS * H::COLUMN + o % (16 * MT) + (size_t)row * parts * H::COLUMN;
+      float v = 0.f;
+      for (int s = 0; s < used; ++s, from += H::RG * COLS * H::COLUMN)
+        v += parts == 1 ? from[0] : from[0] + (from[H::COLUMN] + from[2 * H::COLUMN]);
+      if (a.bias) v += a.x_f32 ? static_cast<const float*>(a.bias)[n] : __bfloat162float(static_cast<const bf16*>(a.bias)[n]);
+      const int64_t at = (row0 + row) * a.out_stride + n;
+      if (a.out_f32) static_cast<float*>(a.out)[at] = v;
+      else static_cast<bf16*>(a.out)[at] = __float2bfloat16_rn(v);
+    }
+    tile += a.ctas;
   }
 }
 
-template <typename S, int G, int N8>
+template <typename H>
 cudaError_t run(LinearArgs a, cudaStream_t s) {
-  constexpr int cols = 8 * N8;
-  const int sms = sm_count(), blocks = (a.K + kBlock - 1) / kBlock, tiles = (a.N + kTile - 1) / kTile;
-  const size_t joint = (size_t)2 * NWARP * cols * kColumn * sizeof(float), block_bytes = (size_t)4 * cols * 64;
-  const int fit = (int)((kShared - joint) / block_bytes);
-  a.chunk = blocks < fit ? blocks : fit;
-  a.pass_rows = a.x_f32 ? cols / 3 : cols;
+  const int sms = sm_count(), blocks = (a.K + kBlock - 1) / kBlock, tiles = (a.N + H::ROWS - 1) / H::ROWS;
+  a.pass_rows = a.x_f32 ? H::COLS / 3 : H::COLS;
   const int passes = (a.rows + a.pass_rows - 1) / a.pass_rows;
-  // warps that share a tile's inputs: those that need the fewest steps, a tile's end counted as one
-  int64_t least = 0;
-  a.split_log2 = 0;
-  const int ctas = passes < sms ? sms / passes : 1;
-  for (int log = 0; log <= 4 && (1 << log) <= a.chunk; ++log) {
-    const int64_t at_once = (int64_t)ctas * (NWARP >> log), rounds = (tiles + at_once - 1) / at_once;
-    const int64_t cost = rounds * ((blocks + (1 << log) - 1) / (1 << log) + 1);
-    if (log == 0 || cost < least) {
-      least = cost;
-      a.split_log2 = log;
-    }
-  }
-  const int teams = NWARP >> a.split_log2, need = (tiles + teams - 1) / teams;
+  const int slices = (blocks + H::PARTS - 1) / H::PARTS;
+  a.slice = (blocks + slices - 1) / slices;
+  a.pitch = (a.slice * (kBlock / 2) + 127) / 128 * 128 + H::G / 2;
+  a.scale_pitch = a.slice * H::P | 1;
+  const int stage = H::ROWS * (a.pitch + a.scale_pitch * 4);
+  // all of x where three stages still fit beside it, else as many slices as do
+  const int room = kShared - H::RED, x_slice = a.slice * H::X_BLOCK;
+  a.chunk = (blocks + a.slice - 1) / a.slice;
+  while (a.chunk > 1 && a.chunk * x_slice + 3 * stage > room) --a.chunk;
+  a.depth = (room - a.chunk * x_slice) / stage;
+  if (a.depth > kRing) a.depth = kRing;
+  const size_t bytes = H::RED + (size_t)a.chunk * x_slice + (size_t)a.depth * stage;
+  const int share = passes < sms ? sms / passes : 1;
+  a.ctas = tiles < share ? tiles : share;
   static std::atomic<uint64_t> ready{0};       // devices whose kernel has the attribute
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (dev > 63 || !(ready.load(std::memory_order_relaxed) & bit)) {
-    e = cudaFuncSetAttribute(linear_q4_rows_kernel<S, G, N8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kShared);
+    e = cudaFuncSetAttribute(linear_q4_rows_kernel<H>, cudaFuncAttributeMaxDynamicSharedMemorySize, kShared);
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
-  cudaLaunchConfig_t cfg = {};
-  a.ctas = need < ctas ? need : ctas;
-  cfg.gridDim = dim3((unsigned)a.ctas * passes);
-  cfg.blockDim = dim3(NT);
-  cfg.dynamicSmemBytes = joint + a.chunk * block_bytes;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, linear_q4_rows_kernel<S, G, N8>, a);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return sm103::launch(linear_q4_rows_kernel<H>, a.ctas * passes, kThreads, bytes, s, a);
 }
 
-template <typename S, int G>
+template <int G>
 cudaError_t pick(const LinearArgs& a, cudaStream_t s) {
   const int64_t cols = (int64_t)a.rows * (a.x_f32 ? 3 : 1);
-  if (cols <= 8) return run<S, G, 1>(a, s);
-  if (cols <= 16) return run<S, G, 2>(a, s);
-  return run<S, G, 4>(a, s);
-}
-
-template <typename S>
-cudaError_t pick(const LinearArgs& a, int group, cudaStream_t s) {
-  return group == 32 ? pick<S, 32>(a, s) : group == 64 ? pick<S, 64>(a, s) : pick<S, 128>(a, s);
+  const bool large = a.N >= 64 * 2 * sm_count();
+  if (cols <= 8) return large ? run<Shape<1, 2, 2, G>>(a, s) : run<Shape<1, 1, 1, G>>(a, s);
+  if (cols <= 16) return large ? run<Shape<2, 2, 2, G>>(a, s) : run<Shape<2, 1, 1, G>>(a, s);
+  return large ? run<Shape<4, 1, 2, G>>(a, s) : run<Shape<4, 1, 1, G>>(a, s);
 }
 
 }  // namespace
 
-cudaError_t launch_linear_q4(const LinearArgs& a, int group, int scale_dtype, cudaStream_t s) {
-  return scale_dtype == MOE_F32 ? pick<float>(a, group, s) : pick<bf16>(a, group, s);
+cudaError_t launch_linear_q4(const LinearArgs& a, int group, cudaStream_t s) {
+  const bool tiles = !a.x_f32 && a.K >= 256 && a.N >= 128 && (reinterpret_cast<uintptr_t>(a.x) & 15) == 0 && a.x_stride % 8 == 0;
+  if (tiles && (a.rows > 16 || a.N > 20000)) return launch_linear_q4_tiles(a, group, s);
+  return group == 32 ? pick<32>(a, s) : group == 64 ? pick<64>(a, s) : pick<128>(a, s);
 }
 
 }  // namespace moeslot

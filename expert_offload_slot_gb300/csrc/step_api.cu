@@ -1,6 +1,7 @@
 // C ABI of the operators around a step's blocks (declared in include/moeslot.h):
 // argument checks and launches.  They need no handle and no workspace, run on the
 // current device and neither allocate nor synchronise.
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -10,6 +11,8 @@
 using namespace moeslot;
 
 namespace {
+
+__device__ int32_t g_step_status;              // set where a kernel's wait on its own copies ran out
 
 moe_status fail(moe_status st, const char* fmt, ...) {
   char buf[256];
@@ -29,6 +32,31 @@ bool bad_dtype(int32_t t) { return t != MOE_F32 && t != MOE_BF16; }
 int size_of(int32_t t) { return t == MOE_F32 ? 4 : 2; }
 
 }  // namespace
+
+namespace moeslot {
+int32_t* step_status() {
+  static std::atomic<int32_t*> at[64];         // by device
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev > 63) return nullptr;
+  int32_t* p = at[dev].load(std::memory_order_relaxed);
+  if (!p) {
+    void* q = nullptr;
+    if (cudaGetSymbolAddress(&q, g_step_status) != cudaSuccess) return nullptr;
+    at[dev].store(p = static_cast<int32_t*>(q), std::memory_order_relaxed);
+  }
+  return p;
+}
+}  // namespace moeslot
+
+MOE_API moe_status moe_step_status(void) {
+  int32_t* p = step_status();
+  if (!p) return fail(MOE_ERR_CUDA, "the status word of the current device was not found");
+  int32_t st = 0;
+  cudaError_t e = cudaDeviceSynchronize();
+  if (e == cudaSuccess) e = cudaMemcpy(&st, p, sizeof st, cudaMemcpyDeviceToHost);
+  if (e == cudaSuccess && st != 0) e = cudaMemset(p, 0, sizeof st);
+  return e == cudaSuccess ? static_cast<moe_status>(st) : launched(e, "reading the status");
+}
 
 MOE_API moe_status moe_residual_norm(const moe_norm_config* c, const void* x, int64_t x_stride, const void* gate,
                                      int64_t gate_stride, const void* post_weight, const void* residual,
@@ -128,8 +156,10 @@ MOE_API moe_status moe_linear_q4(const void* x, int32_t dtype, int64_t x_stride,
   LinearArgs a = {};
   a.x = x; a.codes = codes; a.scales = scales; a.bias = bias; a.out = out; a.x_stride = x_stride; a.out_stride = out_stride;
   a.rows = rows; a.K = in_features; a.N = out_features; a.groups = (in_features + group - 1) / group;
-  a.x_f32 = dtype == MOE_F32; a.out_f32 = out_dtype == MOE_F32;
-  return launched(launch_linear_q4(a, group, scale_dtype, static_cast<cudaStream_t>(stream)), "moe_linear_q4");
+  a.x_f32 = dtype == MOE_F32; a.out_f32 = out_dtype == MOE_F32; a.scale_f32 = scale_dtype == MOE_F32;
+  a.status = step_status();
+  if (!a.status) return fail(MOE_ERR_CUDA, "the status word of the current device was not found");
+  return launched(launch_linear_q4(a, group, static_cast<cudaStream_t>(stream)), "moe_linear_q4");
 }
 
 MOE_API moe_status moe_logprobs(const void* logits, int32_t dtype, int32_t rows, int32_t vocab, int64_t row_stride,

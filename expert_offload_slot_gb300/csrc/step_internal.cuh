@@ -11,6 +11,7 @@ namespace moeslot {
 
 moe_status set_last_error(moe_status st, const char* msg);   // text for moe_last_error()
 int sm_count();                                               // of the current device
+int32_t* step_status();                                       // sticky, on the current device; NULL: not found
 
 struct NormArgs {
   const void *x, *gate, *post, *residual, *pre;
@@ -27,11 +28,15 @@ struct LinearArgs {
   const void *scales, *bias;                                  // [N][groups], [N]
   void* out;
   int64_t x_stride, out_stride;
+  int32_t* status;
   int32_t rows, K, N, groups;
-  int32_t x_f32, out_f32;
-  int32_t pass_rows, split_log2, chunk, ctas;                       // of the row kernel: k_linear_q4.cu
+  int32_t x_f32, out_f32, scale_f32;
+  // of the row kernel: rows of x in a pass, CTAs of a pass, blocks of a slice, slices of x that shared memory
+  // holds, stages of the ring, bytes between their rows of codes and floats between those of scales
+  int32_t pass_rows, ctas, slice, chunk, depth, pitch, scale_pitch;
 };
-cudaError_t launch_linear_q4(const LinearArgs& a, int group, int scale_dtype, cudaStream_t s);
+cudaError_t launch_linear_q4(const LinearArgs& a, int group, cudaStream_t s);
+cudaError_t launch_linear_q4_tiles(const LinearArgs& a, int group, cudaStream_t s);      // bf16 x on 16-byte boundaries
 
 struct LogprobArgs {
   const void* logits;

@@ -636,6 +636,10 @@ MOE_API moe_status moe_linear_q4(const void* x, int32_t dtype, int64_t x_stride,
                                  const void* bias, int32_t out_features, void* out, int32_t out_dtype, int64_t out_stride,
                                  void* stream);
 
+/* Blocking: MOE_ERR_TIMEOUT if, on the current device, a kernel of moe_linear_q4 gave up waiting (a second) for its own
+ * copies since the last call, whose output is then undefined; else MOE_OK.  Resets it. */
+MOE_API moe_status moe_step_status(void);
+
 /* Scores of given tokens: with lse = log sum_i exp(logits[row, i]) over the row,
  *   logits    device [rows] rows of [vocab] of dtype (MOE_F32 or MOE_BF16), row_stride elements apart;
  *             vocab up to MOE_SAMPLE_MAX_VOCAB
