@@ -387,7 +387,7 @@ def _torch_kinds():
         import torch
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         _kinds["stream"] = raw or (lambda device: torch.cuda.current_stream(device).cuda_stream)
-        _kinds["device"], _kinds["on"] = torch.cuda.current_device, torch.cuda.device
+        _kinds["device"], _kinds["on"] = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device), torch.cuda.device
         _kinds[MOE_F32], _kinds[MOE_BF16], _kinds["i32"] = torch.float32, torch.bfloat16, torch.int32
         _kinds["u8"] = torch.uint8
     return _kinds

@@ -32,6 +32,7 @@ typedef unsigned long long u64;
 constexpr int kMaxCluster = 8;
 constexpr int kTop = MOE_LOGPROBS_MAX_TOP;
 constexpr int kGroups = 64;                    // whose maxima bound the best tokens; twice kTop
+constexpr int kFew = 20;                       // of 32 groups' maxima: some 32 ln(32 / 12) = 31 logits reach the 20th
 constexpr int kList = 256;                     // tokens that reach the bound, at most
 static_assert(kGroups >= 2 * kTop && kList >= kMaxCluster * kTop, "room for every list");
 constexpr float kLow = -1e38f;                 // logits are held above it (so -inf and NaN are there, too) and, below
@@ -86,59 +87,76 @@ __device__ __forceinline__ float value_of(u64 key) {
 __device__ __forceinline__ float raw(float v) { return v; }
 __device__ __forceinline__ float raw(bf16 v) { return __bfloat162float(v); }
 
-// 16 bytes of logits: their maximum, the logits held above kLow, and how many are above the target
-// (or equal: before it).
+// 16 bytes of logits: two at a time held above kLow, and the number above the target (or equal: before it),
+// summed up in `Count`s of up to 256 logits.
 template <typename T>
 struct Vec;
 template <>
 struct Vec<float> {
   static constexpr int W = 4;
-  static __device__ __forceinline__ int above(const uint4& u, float xt, bool before) {
+  typedef int Count;
+  static __device__ __forceinline__ Count none() { return 0; }
+  static __device__ __forceinline__ int total(Count n) { return n; }
+  template <bool before>
+  static __device__ __forceinline__ void above(const uint4& u, float xt, Count& n) {
     const float v[4] = {__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w)};
-    int n = 0;
-    if (before) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) n += v[k] >= xt;
-    } else {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) n += v[k] > xt;
-    }
-    return n;
+    for (int k = 0; k < 4; ++k) n += before ? v[k] >= xt : v[k] > xt;
   }
-  static __device__ __forceinline__ float hold(const uint4& u, float (&v)[4]) {
-    v[0] = fmaxf(__uint_as_float(u.x), kLow);
-    v[1] = fmaxf(__uint_as_float(u.y), kLow);
-    v[2] = fmaxf(__uint_as_float(u.z), kLow);
-    v[3] = fmaxf(__uint_as_float(u.w), kLow);
-    return fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+  static __device__ __forceinline__ void hold(uint4& u) {
+    u.x = __float_as_uint(fmaxf(__uint_as_float(u.x), kLow));
+    u.y = __float_as_uint(fmaxf(__uint_as_float(u.y), kLow));
+    u.z = __float_as_uint(fmaxf(__uint_as_float(u.z), kLow));
+    u.w = __float_as_uint(fmaxf(__uint_as_float(u.w), kLow));
+  }
+  template <int N>
+  static __device__ __forceinline__ float largest(const uint4 (&u)[N]) {
+    float m = kLow;
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(u[k].x), __uint_as_float(u[k].y)), fmaxf(__uint_as_float(u[k].z), __uint_as_float(u[k].w))));
+    return m;
+  }
+  template <typename F>
+  static __device__ __forceinline__ void pairs(const uint4& u, F f) {
+    f(__uint_as_float(u.x), __uint_as_float(u.y));
+    f(__uint_as_float(u.z), __uint_as_float(u.w));
   }
 };
 template <>
 struct Vec<bf16> {
   static constexpr int W = 8;
+  typedef __nv_bfloat162 Count;                // two counts, exact up to 256
+  static __device__ __forceinline__ Count none() { return __float2bfloat162_rn(0.f); }
+  static __device__ __forceinline__ int total(Count n) { return (int)(__low2float(n) + __high2float(n)); }
   static __device__ __forceinline__ __nv_bfloat162 pair(uint32_t u) { return *reinterpret_cast<const __nv_bfloat162*>(&u); }
-  static __device__ __forceinline__ int above(const uint4& u, float xt, bool before) {
+  static __device__ __forceinline__ uint32_t word(__nv_bfloat162 p) { return *reinterpret_cast<const uint32_t*>(&p); }
+  template <bool before>
+  static __device__ __forceinline__ void above(const uint4& u, float xt, Count& n) {
     const __nv_bfloat162 t = __float2bfloat162_rn(xt);               // a logit: exact
-    __nv_bfloat162 n;
-    if (before) {
-      n = __hadd2(__hadd2(__hge2(pair(u.x), t), __hge2(pair(u.y), t)), __hadd2(__hge2(pair(u.z), t), __hge2(pair(u.w), t)));
-    } else {
-      n = __hadd2(__hadd2(__hgt2(pair(u.x), t), __hgt2(pair(u.y), t)), __hadd2(__hgt2(pair(u.z), t), __hgt2(pair(u.w), t)));
-    }
-    return (int)(__low2float(n) + __high2float(n));
-  }
-  static __device__ __forceinline__ float hold(const uint4& u, float (&v)[8]) {
-    const __nv_bfloat162 low = __float2bfloat162_rn(kLow);
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    __nv_bfloat162 p[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      p[k] = __hmax2(pair(w[k]), low);
-      v[2 * k] = __low2float(p[k]);
-      v[2 * k + 1] = __high2float(p[k]);
-    }
-    const __nv_bfloat162 m = __hmax2(__hmax2(p[0], p[1]), __hmax2(p[2], p[3]));
+    for (int k = 0; k < 4; ++k) n = __hadd2(n, before ? __hge2(pair(w[k]), t) : __hgt2(pair(w[k]), t));
+  }
+  static __device__ __forceinline__ void hold(uint4& u) {
+    const __nv_bfloat162 low = __float2bfloat162_rn(kLow);
+    u.x = word(__hmax2(pair(u.x), low));
+    u.y = word(__hmax2(pair(u.y), low));
+    u.z = word(__hmax2(pair(u.z), low));
+    u.w = word(__hmax2(pair(u.w), low));
+  }
+  template <int N>
+  static __device__ __forceinline__ float largest(const uint4 (&u)[N]) {
+    __nv_bfloat162 m = pair(u[0].x);
+#pragma unroll
+    for (int k = 0; k < N; ++k) m = __hmax2(m, __hmax2(__hmax2(pair(u[k].x), pair(u[k].y)), __hmax2(pair(u[k].z), pair(u[k].w))));
     return fmaxf(__low2float(m), __high2float(m));
+  }
+  template <typename F>
+  static __device__ __forceinline__ void pairs(const uint4& u, F f) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) f(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
   }
 };
 
@@ -192,45 +210,78 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const LogprobAr
   float mine = kNone;                          // this thread's maximum
   int above = 0;
   {
+    using sm103::pack2;
+    const uint64_t log2e2 = pack2(kLog2e, kLog2e);
+    uint64_t s2 = 0, w2 = 0;                   // two sums each, of even and odd logits
     auto grow = [&](float m) {                 // to a maximum m
       mine = m;
       m *= kLog2e;
       const float d = soft.m - m, f = sm103::ex2(d);
-      soft.w = f > 0.f ? f * fmaf(d, soft.s, soft.w) : 0.f;
-      soft.s *= f;
+      float s0, s1, w0, w1;
+      sm103::unpack2(s2, s0, s1);
+      sm103::unpack2(w2, w0, w1);
+      w2 = f > 0.f ? pack2(f * fmaf(d, s0, w0), f * fmaf(d, s1, w1)) : 0;
+      s2 = pack2(s0 * f, s1 * f);
       soft.m = m;
+    };
+    auto add = [&](float x, float y) {
+      float z0, z1;
+      const uint64_t z = sm103::fma2(pack2(x, y), log2e2, pack2(-soft.m, -soft.m));
+      sm103::unpack2(z, z0, z1);
+      const uint64_t e = pack2(sm103::ex2(z0), sm103::ex2(z1));
+      s2 = sm103::add2(s2, e);
+      w2 = sm103::fma2(e, z, w2);
     };
     const int i = in.single(tid);
     if (i >= 0) {
       const float x = raw(in.x[i]), v = fmaxf(x, kLow);
       above += i < target ? x >= xt : x > xt;
       if (v > mine) grow(v);
-      const float z = fmaf(v, kLog2e, -soft.m), e = sm103::ex2(z);
-      soft.s += e;
-      soft.w = fmaf(e, z, soft.w);
+      add(v, kLow);
     }
     const uint4* p = in.vectors();
-    auto take = [&](const uint4& u, int vec) {
-      above += Vec<T>::above(u, xt, in.lead + vec * W < target);
-      float v[W];
-      const float m = Vec<T>::hold(u, v);
+    // N vectors, NT apart, from `vec` on
+    auto take = [&](auto& u, int vec) {
+      constexpr int N = sizeof(u) / sizeof(uint4);
+      typename Vec<T>::Count n = Vec<T>::none();
+      const int first = in.lead + vec * W;
+      if (first + (N - 1) * NT * W < target) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) Vec<T>::template above<true>(u[k], xt, n);
+      } else if (first >= target) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) Vec<T>::template above<false>(u[k], xt, n);
+      } else {
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          if (first + k * NT * W < target) Vec<T>::template above<true>(u[k], xt, n);
+          else Vec<T>::template above<false>(u[k], xt, n);
+        }
+      }
+      above += Vec<T>::total(n);
+#pragma unroll
+      for (int k = 0; k < N; ++k) Vec<T>::hold(u[k]);
+      const float m = Vec<T>::largest(u);
       if (m > mine) grow(m);
 #pragma unroll
-      for (int k = 0; k < W; ++k) {
-        const float z = fmaf(v[k], kLog2e, -soft.m), e = sm103::ex2(z);
-        soft.s += e;
-        soft.w = fmaf(e, z, soft.w);
-      }
+      for (int k = 0; k < N; ++k) Vec<T>::pairs(u[k], add);
     };
     int v = in.v0 + tid;
     for (; v + (U - 1) * NT < in.v1; v += U * NT) {
       uint4 u[U];
 #pragma unroll
       for (int k = 0; k < U; ++k) u[k] = __ldg(p + v + k * NT);
-#pragma unroll
-      for (int k = 0; k < U; ++k) take(u[k], v + k * NT);
+      take(u, v);
     }
-    for (; v < in.v1; v += NT) take(__ldg(p + v), v);
+    for (; v < in.v1; v += NT) {
+      uint4 u[1] = {__ldg(p + v)};
+      take(u, v);
+    }
+    float s0, s1, w0, w1;
+    sm103::unpack2(s2, s0, s1);
+    sm103::unpack2(w2, w0, w1);
+    soft.s = s0 + s1;
+    soft.w = w0 + w1;
   }
   // the target's own vector counted all its equals: those from the target on do not stand before it
   if (asked && target > in.lead && target < in.tail0) {
@@ -288,17 +339,27 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const LogprobAr
       for (int w = 0; w < NW; ++w) c += sm.count[w];
       return c;
     };
-    if (wid == 0) {                            // the n-th largest maximum of 64 groups
+    if (wid == 0) {                            // the n-th largest maximum of 64 groups, or of 32
       float g[2] = {kNone, kNone};
+#pragma unroll
       for (int k = 0; k < NT / kGroups; ++k) {
         g[0] = fmaxf(g[0], sm.best[lane + k * kGroups]);
         g[1] = fmaxf(g[1], sm.best[lane + 32 + k * kGroups]);
       }
       int larger[2] = {0, 0};
-      for (int k = 0; k < 32; ++k) {
-        const float p = __shfl_sync(0xffffffffu, g[0], k), q = __shfl_sync(0xffffffffu, g[1], k);
-        larger[0] += (p > g[0]) + (q > g[0]);
-        larger[1] += (p > g[1]) + (q > g[1]);
+      if (n <= kFew) {                         // 32 groups do
+        g[0] = fmaxf(g[0], g[1]);
+        g[1] = kNone;
+        larger[1] = n;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) larger[0] += __shfl_sync(0xffffffffu, g[0], k) > g[0];
+      } else {
+#pragma unroll 8
+        for (int k = 0; k < 32; ++k) {
+          const float p = __shfl_sync(0xffffffffu, g[0], k), q = __shfl_sync(0xffffffffu, g[1], k);
+          larger[0] += (p > g[0]) + (q > g[0]);
+          larger[1] += (p > g[1]) + (q > g[1]);
+        }
       }
       const uint32_t least = min(larger[0] < n ? ordered(g[0]) : 0xffffffffu, larger[1] < n ? ordered(g[1]) : 0xffffffffu);
       const uint32_t bound = __reduce_min_sync(0xffffffffu, least);
@@ -356,6 +417,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const LogprobAr
     if (tid < m) {                             // sorted by counting: keys are unique
       const u64 key = sm.list[tid];
       int at = 0;
+#pragma unroll 4
       for (int k = 0; k < m; ++k) at += sm.list[k] > key;
       if (at < n) sm.top[at] = key;
     }
@@ -364,16 +426,24 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const LogprobAr
 
   // ------------------------------------------------ the cluster's parts joined
   cluster.sync();
-  auto gather = [&] {
-    soft = {kNone * kLog2e, 0.f, 0.f};
-    above = 0;
-    for (int c = 0; c < cs; ++c) {
-      const Shared* o = cluster.map_shared_rank(&sm, c);
-      join(soft, o->soft);
-      above += o->rank;
+  {                                            // a lane a CTA, in every warp
+    const Shared* o = cluster.map_shared_rank(&sm, min(lane, cs - 1));
+    soft = o->soft;
+    above = lane < cs ? o->rank : 0;
+    if (lane >= cs) soft = {kNone * kLog2e, 0.f, 0.f};
+#pragma unroll
+    for (int k = kMaxCluster / 2; k > 0; k >>= 1) {
+      Soft other;
+      other.m = __shfl_xor_sync(0xffffffffu, soft.m, k);
+      other.s = __shfl_xor_sync(0xffffffffu, soft.s, k);
+      other.w = __shfl_xor_sync(0xffffffffu, soft.w, k);
+      join(soft, other);
+      above += __shfl_xor_sync(0xffffffffu, above, k);
     }
-  };
-  gather();
+    soft.m = __shfl_sync(0xffffffffu, soft.m, 0);        // lanes 0 .. 7 hold it
+    soft.s = __shfl_sync(0xffffffffu, soft.s, 0);
+    soft.w = __shfl_sync(0xffffffffu, soft.w, 0);
+  }
   float entropy;
   const bool far = !(fabsf(soft.m) <= kFar);
   if (far) {              // a careful pass: the same for all CTAs of the row
@@ -426,24 +496,30 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const LogprobAr
       if (a.rank) a.rank[row] = asked ? above : -1;
     }
     if (a.top > 0) {
-      int have = 0;
-      __syncthreads();
-      for (int c = 0; c < cs; ++c) {           // the CTAs' lists, one after another
+      int have = 0, place = 0;                 // tokens of all CTAs; this thread's place among its own CTA's
+      u64 key = 0;
+      const int c = tid / kTop, i = tid % kTop;
+      static_assert(kMaxCluster * kTop <= 256 && kTop == 32, "a thread a token");
+      if (c < cs) {                            // a warp a CTA: its sorted list, behind the others' in shared memory
         const Shared* o = cluster.map_shared_rank(&sm, c);
         const int kept = o->kept;
-        if (tid < kept) sm.list[have + tid] = o->top[tid];
-        have += kept;
+        key = i < kept ? o->top[i] : 0;        // no token's key is 0
+        sm.list[tid] = key;
       }
       __syncthreads();
-      if (tid < have) {
-        const u64 key = sm.list[tid];
-        int at = 0;
-        for (int k = 0; k < have; ++k) at += sm.list[k] > key;
-        if (at < a.top) {
-          const int64_t to = (int64_t)row * a.top + at;
-          a.top_ids[to] = index_of(key);
-          a.top_logp[to] = log_p(value_of(key));
-        }
+      for (int k = 0; k < cs; ++k) {           // sorted lists: how many of each are before this one
+        const u64* list = sm.list + k * kTop;
+        int lo = 0;
+#pragma unroll
+        for (int step = kTop / 2; step > 0; step >>= 1) lo += list[lo + step - 1] > key ? step : 0;
+        lo += list[lo] > key;
+        place += lo;
+        have += __popc(__ballot_sync(0xffffffffu, list[lane] != 0));
+      }
+      if (key != 0 && place < a.top) {
+        const int64_t to = (int64_t)row * a.top + place;
+        a.top_ids[to] = index_of(key);
+        a.top_logp[to] = log_p(value_of(key));
       }
       for (int at = have + tid; at < a.top; at += NT) {              // fewer tokens than asked for
         const int64_t to = (int64_t)row * a.top + at;

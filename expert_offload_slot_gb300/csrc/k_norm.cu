@@ -19,30 +19,37 @@ namespace {
 
 typedef __nv_bfloat16 bf16;
 
-// W consecutive elements: 8 (16-byte loads) or one.
-template <int W>
-__device__ __forceinline__ void load(const float* p, float (&v)[W]) {
-  if constexpr (W == 8) {
-    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  } else {
-    v[0] = *p;
+// W consecutive elements as they lie in memory, and as numbers: 8 (16-byte loads) or one.
+template <typename T, int W>
+struct Raw {
+  T v;
+  __device__ __forceinline__ void get(const T* p) { v = *p; }
+  __device__ __forceinline__ void to(float (&x)[1]) const { x[0] = (float)v; }
+};
+template <>
+struct Raw<float, 8> {
+  float4 a, b;
+  __device__ __forceinline__ void get(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
   }
-}
-template <int W>
-__device__ __forceinline__ void load(const bf16* p, float (&v)[W]) {
-  if constexpr (W == 8) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
+  __device__ __forceinline__ void to(float (&x)[8]) const {
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  }
+};
+template <>
+struct Raw<bf16, 8> {
+  uint4 u;
+  __device__ __forceinline__ void get(const bf16* p) { u = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void to(float (&x)[8]) const {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      v[2 * k] = __uint_as_float(w[k] << 16);
-      v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+      x[2 * k] = __uint_as_float(w[k] << 16);
+      x[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
     }
-  } else {
-    v[0] = __bfloat162float(*p);
   }
-}
+};
 template <int W>
 __device__ __forceinline__ void store(float* p, const float (&v)[W]) {
   if constexpr (W == 8) {
@@ -80,24 +87,50 @@ __device__ __forceinline__ float row_sum(float v, float* sm, int& turn) {
 }
 
 // TPR threads a row, C pieces of W elements each.  TPR 32: a warp a row, four rows a CTA; else a CTA a row.
-template <typename T, typename R, int TPR, int C, int W>
-__global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) residual_norm_kernel(const NormArgs a) {
+// Of one piece of 8 a thread (LEAN) the next row is asked for before this one is summed up, and 16-bit weights
+// stay in registers (KEEP).
+// GATED: by channel or element.
+template <int TPR, int W>
+constexpr int kCtas = TPR == 1024 ? 1 : (W == 8 ? 1024 : 1536) / (TPR == 32 ? 128 : TPR);      // of an SM
+
+template <typename T, typename R, int TPR, int C, int W, bool GATED>
+__global__ void __launch_bounds__(TPR == 32 ? 128 : TPR, (kCtas<TPR, W>)) residual_norm_kernel(const NormArgs a) {
   __shared__ float sm[TPR > 32 ? 2 * (TPR / 32) : 1];
   constexpr int PER_CTA = TPR == 32 ? 4 : 1;
+  constexpr bool LEAN = C == 1 && W == 8, KEEP = LEAN && sizeof(T) == 2;
   const int tid = TPR == 32 ? threadIdx.x & 31 : threadIdx.x, sub = TPR == 32 ? threadIdx.x >> 5 : 0;
   const float inv_n = 1.f / (float)a.hidden;
+  const int64_t stride = (int64_t)gridDim.x * PER_CTA;
   int turn = 0;
   sm103::grid_wait();
-  for (int64_t row = (int64_t)blockIdx.x * PER_CTA + sub; row < a.rows; row += (int64_t)gridDim.x * PER_CTA) {
-    float r[C][W], n[C][W];
-    const R* rp = static_cast<const R*>(a.residual) + row * a.residual_stride;
-    const T* xp = static_cast<const T*>(a.x) + row * a.x_stride;
+  Raw<T, W> x_raw[C], post, pre;
+  Raw<R, W> r_raw[C];
+  auto ask = [&](int64_t row) {
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int e = (c * TPR + tid) * W;
       if (e < a.hidden) {
-        load<W>(rp + e, r[c]);
-        if (a.x) load<W>(xp + e, n[c]);
+        r_raw[c].get(static_cast<const R*>(a.residual) + row * a.residual_stride + e);
+        if (a.x) x_raw[c].get(static_cast<const T*>(a.x) + row * a.x_stride + e);
+      }
+    }
+  };
+  int64_t row = (int64_t)blockIdx.x * PER_CTA + sub;
+  if (LEAN) {
+    if (row < a.rows) ask(row);
+    if (KEEP && tid * W < a.hidden) {
+      if (a.post) post.get(static_cast<const T*>(a.post) + tid * W);
+      if (a.y && a.pre) pre.get(static_cast<const T*>(a.pre) + tid * W);
+    }
+  }
+  for (; row < a.rows; row += stride) {
+    if (!LEAN) ask(row);
+    float r[C][W], n[C][W];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      if ((c * TPR + tid) * W < a.hidden) {
+        r_raw[c].to(r[c]);
+        if (a.x) x_raw[c].to(n[c]);
       } else {
 #pragma unroll
         for (int k = 0; k < W; ++k) r[c][k] = n[c][k] = 0.f;
@@ -109,6 +142,7 @@ __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) residual_norm_kernel(co
         const float g = (float)static_cast<const T*>(a.gate)[row * a.gate_stride];
         f *= a.gate_sigmoid ? 1.f / (1.f + expf(-g)) : g;
       }
+      if (LEAN && row + stride < a.rows) ask(row + stride);
       float inv = 1.f;
       if (a.post) {
         float ss = 0.f;
@@ -124,13 +158,16 @@ __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) residual_norm_kernel(co
         if (e >= a.hidden) continue;
         if (a.post) {
           float w[W];
-          load<W>(static_cast<const T*>(a.post) + e, w);
+          if (!KEEP) post.get(static_cast<const T*>(a.post) + e);
+          post.to(w);
 #pragma unroll
           for (int k = 0; k < W; ++k) n[c][k] = n[c][k] * inv * (a.offset + w[k]);
         }
-        if (a.gate_kind >= MOE_RESIDUAL_GATE_CHANNEL) {
+        if (GATED) {
+          Raw<T, W> raw;
           float g[W];
-          load<W>(static_cast<const T*>(a.gate) + row * a.gate_stride + e, g);
+          raw.get(static_cast<const T*>(a.gate) + row * a.gate_stride + e);
+          raw.to(g);
 #pragma unroll
           for (int k = 0; k < W; ++k) n[c][k] *= a.gate_sigmoid ? 1.f / (1.f + expf(-g[k])) : g[k];
         }
@@ -138,6 +175,8 @@ __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) residual_norm_kernel(co
         for (int k = 0; k < W; ++k) r[c][k] = fmaf(f, n[c][k], r[c][k]);
         store<W>(static_cast<R*>(a.sum) + row * a.sum_stride + e, r[c]);
       }
+    } else if (LEAN && row + stride < a.rows) {
+      ask(row + stride);
     }
     if (!a.y) continue;
     float ss = 0.f;
@@ -152,7 +191,8 @@ __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) residual_norm_kernel(co
       if (e >= a.hidden) continue;
       if (a.pre) {
         float w[W];
-        load<W>(static_cast<const T*>(a.pre) + e, w);
+        if (!KEEP) pre.get(static_cast<const T*>(a.pre) + e);
+        pre.to(w);
 #pragma unroll
         for (int k = 0; k < W; ++k) r[c][k] = r[c][k] * inv * (a.offset + w[k]);
       } else {
@@ -167,8 +207,11 @@ __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) residual_norm_kernel(co
 template <typename T, typename R, int TPR, int C, int W>
 cudaError_t run(const NormArgs& a, cudaStream_t s) {
   constexpr int threads = TPR == 32 ? 128 : TPR, per = TPR == 32 ? 4 : 1;
-  const int64_t ctas = ((int64_t)a.rows + per - 1) / per, most = (int64_t)sm_count() * (2048 / threads);
-  return sm103::launch(residual_norm_kernel<T, R, TPR, C, W>, (int)(ctas < most ? ctas : most), threads, 0, s, a);
+  const int64_t ctas = ((int64_t)a.rows + per - 1) / per, most = (int64_t)sm_count() * kCtas<TPR, W>;
+  const int grid = (int)(ctas < most ? ctas : most);
+  return a.gate_kind >= MOE_RESIDUAL_GATE_CHANNEL
+             ? sm103::launch(residual_norm_kernel<T, R, TPR, C, W, true>, grid, threads, 0, s, a)
+             : sm103::launch(residual_norm_kernel<T, R, TPR, C, W, false>, grid, threads, 0, s, a);
 }
 
 template <typename T, typename R>
@@ -190,10 +233,9 @@ cudaError_t pick(const NormArgs& a, cudaStream_t s) {
     return run<T, R, 1024, 2, 8>(a, s);
   }
   if (h <= 32 * 4) return run<T, R, 32, 4, 1>(a, s);
-  if (h <= 128 * 4) return run<T, R, 128, 4, 1>(a, s);
-  if (h <= 256 * 4) return run<T, R, 256, 4, 1>(a, s);
-  if (h <= 512 * 4) return run<T, R, 512, 4, 1>(a, s);
-  if (h <= 1024 * 4) return run<T, R, 1024, 4, 1>(a, s);
+  if (h <= 128 * 8) return run<T, R, 128, 8, 1>(a, s);
+  if (h <= 256 * 8) return run<T, R, 256, 8, 1>(a, s);
+  if (h <= 512 * 8) return run<T, R, 512, 8, 1>(a, s);
   return run<T, R, 1024, 16, 1>(a, s);
 }
 

@@ -167,14 +167,6 @@ __device__ __forceinline__ void tma_3d_pair(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-__device__ __forceinline__ void tma_2d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "
-      "[%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
-      : "memory");
-}
-
 // ------------------------------------------------------------------- tcgen05
 // All of it in its two-CTA form: a product has M = 256, rows 0..127 from and to the first CTA of
 // the pair and 128..255 the second; each holds half of B's N, and one thread of the first issues.

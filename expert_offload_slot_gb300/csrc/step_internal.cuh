@@ -34,6 +34,8 @@ struct LinearArgs {
   // of the row kernel: rows of x in a pass, CTAs of a pass, blocks of a slice, slices of x that shared memory
   // holds, stages of the ring, bytes between their rows of codes and floats between those of scales
   int32_t pass_rows, ctas, slice, chunk, depth, pitch, scale_pitch;
+  // of the tile kernel: K is whole blocks of 64; x stays in shared memory
+  int32_t x_blocks, resident;
 };
 cudaError_t launch_linear_q4(const LinearArgs& a, int group, cudaStream_t s);
 cudaError_t launch_linear_q4_tiles(const LinearArgs& a, int group, cudaStream_t s);      // bf16 x on 16-byte boundaries
