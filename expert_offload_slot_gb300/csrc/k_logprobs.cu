@@ -9,13 +9,19 @@
 // m grows by -d, s becomes 2^d s and w 2^d (w + d s).  Then logp = (z_t - log2 s) log(2) and
 // entropy = (log2 s - w / s) log(2): differences of numbers of different signs, nothing cancels.
 //
-// The best tokens need no second pass over the row: the n-th largest of 64 groups' maxima
-// is a bound that n logits reach, only threads whose own maximum reaches it look at their
-// logits again, and the few that do are sorted by (x, index).  Rows where the bound does
+// The best tokens need no second pass over the row: the n-th largest of 32 or 64 groups' maxima
+// is a bound that n logits reach, only the logits of threads whose own maximum reaches it are looked at
+// again, and the few that do are sorted by (x, index).  Rows where the bound does
 // not help (equal logits in thousands, hardly any token) are searched by bisection.
 //
 // NaN counts as -inf.  Logits far from zero, where the products with log2(e) lose the
 // differences, and rows without a token take a second, careful pass.
+//
+// What bounds it: of many rows HBM and, near it, the instructions of a logit, which therefore
+// are taken in pairs (bf16 comparisons and maxima, fp32 sums): 2048 rows of 131072 bf16 logits without
+// best tokens 90 us (6.0 TB/s, 88 % of a copy's rate), with five 102, with twenty 126; an exponential, a
+// product and two sums for each logit by itself took 128 (five).  One row of 131072: 5.0 us, 8.5 with twenty
+// best tokens: loads, two exchanges in the cluster, the bound and the sorting one after another.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -59,7 +65,8 @@ struct Shared {                                // of a CTA; the cluster reads th
   float best[1024];
   u64 list[kList];
   float bound;
-  int32_t found;
+  int32_t found, owners;
+  int16_t owner[1024];
   u64 bits[32];
   // shown to the cluster
   Soft soft;
@@ -184,7 +191,7 @@ struct Share {
 };
 
 template <typename T, int NT>
-__global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const LogprobArgs a) {
+__global__ void __launch_bounds__(NT, NT == 256 ? 5 : 2) logprobs_kernel(const LogprobArgs a) {
   constexpr int W = Vec<T>::W, NW = NT / 32, U = 4;
   __shared__ Shared sm;
   cg::cluster_group cluster = cg::this_cluster();
@@ -322,7 +329,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const LogprobAr
   if (tid == 0) {
     sm.soft = soft;
     sm.rank = above;
-    sm.found = 0;
+    sm.found = sm.owners = 0;
   }
 
   // ------------------------------------------------ the CTA's best tokens, sorted
@@ -369,20 +376,38 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const LogprobAr
     const float bound = sm.bound;
     bool listed = bound > kNone;
     if (listed) {
-      // a warp looks at the logits of one thread of its own after another
-      for (uint32_t todo = __ballot_sync(0xffffffffu, mine >= bound); todo; todo &= todo - 1) {
-        const int owner = wid * 32 + __ffs(todo) - 1;
-        auto offer = [&](float x, int i) {
-          if (x >= bound) {
-            const int at = atomicAdd(&sm.found, 1);
-            if (at < kList) sm.list[at] = key_of(x + 0.f, i);
-          }
-        };
-        if (lane == 0 && in.single(owner) >= 0) offer(raw(in.x[in.single(owner)]), in.single(owner));
-        for (int v = in.v0 + owner + lane * NT; v < in.v1; v += 32 * NT) {
-          const T* x = in.x + in.lead + v * W;
+      // the logits of the threads that reach it, by all threads, four vectors on their way
+      auto offer = [&](float x, int i) {
+        if (x >= bound) {
+          const int at = atomicAdd(&sm.found, 1);
+          if (at < kList) sm.list[at] = key_of(x + 0.f, i);
+        }
+      };
+      if (mine >= bound) {
+        sm.owner[atomicAdd(&sm.owners, 1)] = (int16_t)tid;
+        const int i = in.single(tid);
+        if (i >= 0) offer(raw(in.x[i]), i);
+      }
+      __syncthreads();
+      const int per = max(1, (in.v1 - in.v0 + NT - 1) / NT), all = sm.owners * per;
+      for (int j = tid; j < all; j += 4 * NT) {
+        uint4 u[4];
+        int at[4];
 #pragma unroll
-          for (int k = 0; k < W; ++k) offer(raw(x[k]), in.lead + v * W + k);
+        for (int k = 0; k < 4; ++k) {
+          const int which = (j + k * NT) / per, v = in.v0 + (j + k * NT - which * per) * NT + (j + k * NT < all ? sm.owner[which] : 0);
+          at[k] = j + k * NT < all && v < in.v1 ? v : -1;
+          if (at[k] >= 0) u[k] = __ldg(in.vectors() + v);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (at[k] < 0) continue;
+          int i = in.lead + at[k] * W;
+          Vec<T>::pairs(u[k], [&](float x, float y) {
+            offer(x, i);
+            offer(y, i + 1);
+            i += 2;
+          });
         }
       }
       __syncthreads();
@@ -534,9 +559,13 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const LogprobAr
 template <typename T>
 cudaError_t run(const LogprobArgs& a, cudaStream_t s) {
   const int sms = sm_count();
+  // CTAs a row: as many of 512 threads as the GPU holds at once, two on an SM, with 4096 logits each or more; where
+  // even one does not fit, of 256 threads, five on an SM, and two a row if those fit (48 rows of 131072 bf16 logits: 4 CTAs
+  // of 512 threads each 12.6 us, 8 of 256 14.8, 2 of 512 14.4; 333 rows of 50257: 2 of 256 15.6, one of 256 19.8).
   int cs = 1;
-  while (cs < kMaxCluster && (int64_t)a.rows * cs * 2 <= sms && a.vocab / (2 * cs) >= 4096) cs *= 2;
-  const bool few = cs > 1;
+  while (cs < kMaxCluster && (int64_t)a.rows * cs * 2 <= 2 * sms && a.vocab / (2 * cs) >= 4096) cs *= 2;
+  const bool few = (int64_t)a.rows * cs <= 2 * sms;
+  if (!few && (int64_t)a.rows * 2 <= 5 * sms && a.vocab >= 8192) cs = 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.rows * cs));
   cfg.blockDim = dim3(few ? 512 : 256);
