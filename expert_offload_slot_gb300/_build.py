@@ -18,7 +18,8 @@ LIB = os.path.join(PKG, "libmoeslot.so")
 
 SOURCES = ["api.cu", "pack.cu", "quota.cu", "k_route.cu", "k_plan.cu", "k_copy.cu", "k_ffn.cu", "k_noalloc.cu", "k_tc.cu",
            "attn_api.cu", "k_attn_step.cu", "k_attn_f32.cu", "k_attn_rows.cu", "k_attn_tiles.cu", "k_sample.cu",
-           "step_api.cu", "k_norm.cu", "k_linear_q4.cu", "k_linear_q4_tiles.cu", "k_logprobs.cu"]
+           "step_api.cu", "k_norm.cu", "k_linear_q4.cu", "k_linear_q4_tiles.cu", "k_linear_q4_split.cu",
+           "k_logprobs.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden,-ffp-contract=off", f"-I{INCLUDE}"]
 

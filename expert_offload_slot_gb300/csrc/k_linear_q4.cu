@@ -34,6 +34,7 @@ constexpr int kCodeWarps = 4, kScaleWarps = 2, kThreads = NT + 32 * (kCodeWarps 
 constexpr int kBlock = 128;                    // inputs of a warp's part of a slice
 constexpr int kRing = 8;                       // stages at most
 constexpr int kShared = 225 * 1024;            // dynamic shared memory of a CTA
+__device__ int32_t g_status;                   // set where a wait ran out
 
 // Codes of a word as four pairs (k, k + 4) of bf16.
 __device__ __forceinline__ void widen(uint32_t w, uint32_t (&p)[4]) {
@@ -45,15 +46,6 @@ __device__ __forceinline__ void widen(uint32_t w, uint32_t (&p)[4]) {
     const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u), top);
     p[i] = *reinterpret_cast<const uint32_t*>(&v);
   }
-}
-
-// x as three bf16 numbers by cutting off bits: the sum is x.  Nothing is left of an infinity or a NaN.
-__device__ __forceinline__ float part_of(float x, int part) {
-  const float h = __uint_as_float(__float_as_uint(x) & 0xffff0000u);
-  if (part == 0) return (__float_as_uint(x) & 0x7fffffffu) > 0x7f800000u ? __uint_as_float(0x7fc00000u) : h;
-  if ((__float_as_uint(x) & 0x7f800000u) == 0x7f800000u) return 0.f;
-  const float rest = x - h, m = __uint_as_float(__float_as_uint(rest) & 0xffff0000u);
-  return part == 1 ? m : rest - m;
 }
 
 // Eight inputs k0 .. k0 + 7 of a column, in the order of widen()'s pairs.
@@ -71,7 +63,7 @@ __device__ __forceinline__ uint4 column8(const LinearArgs& a, int64_t row, int p
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      w[i] = __float_as_uint(part_of(v[i], part)) >> 16 | (__float_as_uint(part_of(v[i + 4], part)) & 0xffff0000u);
+      w[i] = __float_as_uint(bf16_part(v[i], part)) >> 16 | (__float_as_uint(bf16_part(v[i + 4], part)) & 0xffff0000u);
   } else {
     const uint16_t* p = static_cast<const uint16_t*>(a.x) + row * a.x_stride + k0;
     uint16_t v[8];
@@ -136,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_q4_rows_kernel(const Linea
     uint32_t phase = 0;
     for (int64_t i = 0; i < steps; ++i) {
       if (i >= a.depth && !sm103::bar_wait_warp(empty + st, phase ^ 1)) {
-        if (lane == 0) atomicCAS(a.status, 0, MOE_ERR_TIMEOUT);
+        if (lane == 0) atomicCAS(&g_status, 0, MOE_ERR_TIMEOUT);
         break;
       }
       const int at = slice * a.slice * (kBlock / 2), bytes = min(a.slice * (kBlock / 2), a.K / 2 - at);
@@ -231,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_q4_rows_kernel(const Linea
 #pragma unroll
           for (int k = 0; k < 4; ++k) acc[m][j][k] = 0.f;
     }
-    if (alive && !(alive = sm103::bar_wait_warp(full + st, phase)) && lane == 0) atomicCAS(a.status, 0, MOE_ERR_TIMEOUT);
+    if (alive && !(alive = sm103::bar_wait_warp(full + st, phase)) && lane == 0) atomicCAS(&g_status, 0, MOE_ERR_TIMEOUT);
     const int block = slice * a.slice + part;
     if (part < a.slice && block < blocks) {
       const uint8_t* codes = ring + st * stage_bytes + (group * 16 * MT + g) * a.pitch + part * (kBlock / 2) + t * (G / 8);
@@ -376,9 +368,12 @@ cudaError_t pick(const LinearArgs& a, cudaStream_t s) {
 
 }  // namespace
 
+cudaError_t linear_q4_rows_status(int32_t* st) { return take_status(g_status, st); }
+
 cudaError_t launch_linear_q4(const LinearArgs& a, int group, cudaStream_t s) {
-  const bool tiles = !a.x_f32 && a.K >= 256 && a.N >= 128 && (reinterpret_cast<uintptr_t>(a.x) & 15) == 0 && a.x_stride % 8 == 0;
-  if (tiles && (a.rows > 16 || a.N > 20000)) return launch_linear_q4_tiles(a, group, s);
+  const bool tiles = a.K >= 256 && a.N >= 128, aligned = (reinterpret_cast<uintptr_t>(a.x) & 15) == 0 && a.x_stride % 8 == 0;
+  if (tiles && !a.x_f32 && aligned && (a.rows > 16 || a.N > 20000)) return launch_linear_q4_tiles(a, group, s);
+  if (tiles && (a.x_f32 ? a.rows > 5 : a.rows > 32 && !aligned)) return launch_linear_q4_split(a, group, s);
   return group == 32 ? pick<32>(a, s) : group == 64 ? pick<64>(a, s) : pick<128>(a, s);
 }
 

@@ -1,18 +1,16 @@
 // C ABI of the operators around a step's blocks (declared in include/moeslot.h):
 // argument checks and launches.  They need no handle and no workspace, run on the
 // current device and neither allocate nor synchronise.
-#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <initializer_list>
 
 #include "step_internal.cuh"
 
 using namespace moeslot;
 
 namespace {
-
-__device__ int32_t g_step_status;              // set where a kernel's wait on its own copies ran out
 
 moe_status fail(moe_status st, const char* fmt, ...) {
   char buf[256];
@@ -33,29 +31,15 @@ int size_of(int32_t t) { return t == MOE_F32 ? 4 : 2; }
 
 }  // namespace
 
-namespace moeslot {
-int32_t* step_status() {
-  static std::atomic<int32_t*> at[64];         // by device
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev > 63) return nullptr;
-  int32_t* p = at[dev].load(std::memory_order_relaxed);
-  if (!p) {
-    void* q = nullptr;
-    if (cudaGetSymbolAddress(&q, g_step_status) != cudaSuccess) return nullptr;
-    at[dev].store(p = static_cast<int32_t*>(q), std::memory_order_relaxed);
-  }
-  return p;
-}
-}  // namespace moeslot
-
 MOE_API moe_status moe_step_status(void) {
-  int32_t* p = step_status();
-  if (!p) return fail(MOE_ERR_CUDA, "the status word of the current device was not found");
-  int32_t st = 0;
   cudaError_t e = cudaDeviceSynchronize();
-  if (e == cudaSuccess) e = cudaMemcpy(&st, p, sizeof st, cudaMemcpyDeviceToHost);
-  if (e == cudaSuccess && st != 0) e = cudaMemset(p, 0, sizeof st);
-  return e == cudaSuccess ? static_cast<moe_status>(st) : launched(e, "reading the status");
+  int32_t first = 0;
+  for (auto take : {linear_q4_rows_status, linear_q4_tiles_status, linear_q4_split_status}) {
+    int32_t st = 0;
+    if (e == cudaSuccess) e = take(&st);
+    if (first == 0) first = st;
+  }
+  return e == cudaSuccess ? static_cast<moe_status>(first) : launched(e, "reading the status");
 }
 
 MOE_API moe_status moe_residual_norm(const moe_norm_config* c, const void* x, int64_t x_stride, const void* gate,
@@ -157,8 +141,6 @@ MOE_API moe_status moe_linear_q4(const void* x, int32_t dtype, int64_t x_stride,
   a.x = x; a.codes = codes; a.scales = scales; a.bias = bias; a.out = out; a.x_stride = x_stride; a.out_stride = out_stride;
   a.rows = rows; a.K = in_features; a.N = out_features; a.groups = (in_features + group - 1) / group;
   a.x_f32 = dtype == MOE_F32; a.out_f32 = out_dtype == MOE_F32; a.scale_f32 = scale_dtype == MOE_F32;
-  a.status = step_status();
-  if (!a.status) return fail(MOE_ERR_CUDA, "the status word of the current device was not found");
   return launched(launch_linear_q4(a, group, static_cast<cudaStream_t>(stream)), "moe_linear_q4");
 }
 

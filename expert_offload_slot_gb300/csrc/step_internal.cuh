@@ -11,7 +11,6 @@ namespace moeslot {
 
 moe_status set_last_error(moe_status st, const char* msg);   // text for moe_last_error()
 int sm_count();                                               // of the current device
-int32_t* step_status();                                       // sticky, on the current device; NULL: not found
 
 struct NormArgs {
   const void *x, *gate, *post, *residual, *pre;
@@ -28,7 +27,6 @@ struct LinearArgs {
   const void *scales, *bias;                                  // [N][groups], [N]
   void* out;
   int64_t x_stride, out_stride;
-  int32_t* status;
   int32_t rows, K, N, groups;
   int32_t x_f32, out_f32, scale_f32;
   // of the row kernel: rows of x in a pass, CTAs of a pass, blocks of a slice, slices of x that shared memory
@@ -39,6 +37,26 @@ struct LinearArgs {
 };
 cudaError_t launch_linear_q4(const LinearArgs& a, int group, cudaStream_t s);
 cudaError_t launch_linear_q4_tiles(const LinearArgs& a, int group, cudaStream_t s);      // bf16 x on 16-byte boundaries
+cudaError_t launch_linear_q4_split(const LinearArgs& a, int group, cudaStream_t s);      // any x
+// The first error of each file's kernels on the current device since the last call (blocking).
+template <typename T>
+cudaError_t take_status(T& symbol, int32_t* st) {
+  const int32_t none = 0;
+  const cudaError_t e = cudaMemcpyFromSymbol(st, symbol, sizeof none);
+  return e == cudaSuccess && *st != 0 ? cudaMemcpyToSymbol(symbol, &none, sizeof none) : e;
+}
+cudaError_t linear_q4_rows_status(int32_t* st);
+cudaError_t linear_q4_tiles_status(int32_t* st);
+cudaError_t linear_q4_split_status(int32_t* st);
+
+// x as three bf16 numbers by cutting off bits: the sum is x.  Nothing is left of an infinity or a NaN.
+__device__ __forceinline__ float bf16_part(float x, int part) {
+  const float h = __uint_as_float(__float_as_uint(x) & 0xffff0000u);
+  if (part == 0) return (__float_as_uint(x) & 0x7fffffffu) > 0x7f800000u ? __uint_as_float(0x7fc00000u) : h;
+  if ((__float_as_uint(x) & 0x7f800000u) == 0x7f800000u) return 0.f;
+  const float rest = x - h, m = __uint_as_float(__float_as_uint(rest) & 0xffff0000u);
+  return part == 1 ? m : rest - m;
+}
 
 struct LogprobArgs {
   const void* logits;
