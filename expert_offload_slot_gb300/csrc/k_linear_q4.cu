@@ -1,15 +1,21 @@
 // moe_linear_q4: out[t, n] = bias[n] + sum_g scale[n, g] sum_{k in group g} code[n, k] x[t, k],
 // 4-bit codes in -8..7 with one scale for each group of 32, 64 or 128 inputs.
 //
-// Row kernel, for up to 32 columns of x.  The codes are all there is to read, so the kernel is
-// a stream of them: a CTA takes tiles of 16 to 64 outputs, one warp copies their codes in
-// bulk, a row of a slice of K each, into a ring in shared memory, two more bring the scales, and 16 warps
-// share the slice, a block of 128 inputs each (two or one groups of warps share the rows), on
-// mma.sync with M the outputs and N the columns of x.  A code is exact in bf16, so products
-// and the sums of a group are the tensor core's, exact up to fp32 sums; a group's sum is
-// scaled in fp32.  At a tile's end the warps' parts are added up in their order.  An fp32 x is
-// cut into three bf16 numbers that add up to it (8 bits of its 24 each) and takes three
-// columns.
+// Row kernel, for few columns of x (launch_linear_q4 says when; linear_q4_tiles.cuh has the others).
+// The codes are all there is to read, so the kernel is a stream of them: a CTA takes tiles
+// of 16 to 64 outputs, four warps copy their codes (cp.async, a row of a slice of K each)
+// into a ring in shared memory, two more bring the scales, and 16 warps share the slice, a
+// block of 128 inputs each (one group of warps for all rows, or two), on mma.sync with M the
+// outputs and N the columns of x.  A code is exact in bf16, so products and the sums of a
+// group are the tensor core's, exact up to fp32 sums; a group's sum is scaled in fp32.  At a
+// tile's end the warps' parts are added up in their order.  An fp32 x is cut into three bf16
+// numbers that add up to it (8 bits of its 24 each) and takes three columns.
+//
+// What bounds it: for small matrices the launch and the latencies of x, codes and joins one
+// after another (one row, 2048 x 5120, 5.2 MB of codes: 6.0 us); for large ones the instructions that
+// expand a code (11 for a word of eight, most on a pipe of half rate) and feed the products, 66 us for
+// 2048 x 131072 where HBM needs 20: without the products 50, without the copies 38.  Registers filled by plain loads
+// instead of the ring took 59 there but 11.3 instead of 9.5 us for one row of 4096 x 6144; bulk copies instead of cp.async 71.
 //
 // The order of k inside a group is free as long as codes and x agree: lane (g, t) of the
 // warp takes for row g (and g + 8) the quarter t of each group, so that it reads its codes
@@ -368,11 +374,29 @@ cudaError_t pick(const LinearArgs& a, cudaStream_t s) {
 
 }  // namespace
 
+namespace {
+
+// Which kernel for up to 16 rows of bf16: the row kernel's time goes by the bytes of codes (us a MB: 0.56 up to 8
+// rows, 1 up to 16, twice that where x does not fit shared memory), the tile kernel's by steps of 128 inputs and rounds of its
+// pairs of CTAs, 0.47 us each; both begin with some 2.5 us.  Measured, row and tile kernel in us: one row, 2048 x 5120 6.0, 10.0;
+// 4096 x 6144 9.5, 16.3; 8192 x 8192 20, 30; 4096 x 16000 18.1, 17.5; 2048 x 131072 66, 48.  12 rows, 4096 x 6144 16.1, 16.6;
+// 2048 x 10000 12.1, 10.8; 8192 x 8192 68, 31.  More rows have the tile kernel: 32 rows, 4096 x 6144 57, 17.
+bool rows_are_faster(const LinearArgs& a) {
+  if (a.rows > 16) return false;
+  const int64_t pairs = sm_count() / 2, blocks = (a.K + kBlock - 1) / kBlock, cols = a.rows <= 8 ? 8 : 16;
+  const bool fits = blocks * 4 * cols * 64 <= 150 * 1024;
+  const int64_t rows_ns = (int64_t)a.N * (a.K / 2) * (a.rows <= 8 ? 56 : 100) * (fits ? 1 : 2) / 100000;
+  const int64_t tiles_ns = 470 * blocks * (((a.N + 255) / 256 + pairs - 1) / pairs);
+  return rows_ns <= tiles_ns;
+}
+
+}  // namespace
+
 cudaError_t linear_q4_rows_status(int32_t* st) { return take_status(g_status, st); }
 
 cudaError_t launch_linear_q4(const LinearArgs& a, int group, cudaStream_t s) {
   const bool tiles = a.K >= 256 && a.N >= 128, aligned = (reinterpret_cast<uintptr_t>(a.x) & 15) == 0 && a.x_stride % 8 == 0;
-  if (tiles && !a.x_f32 && aligned && (a.rows > 16 || a.N > 20000)) return launch_linear_q4_tiles(a, group, s);
+  if (tiles && !a.x_f32 && aligned && !rows_are_faster(a)) return launch_linear_q4_tiles(a, group, s);
   if (tiles && (a.x_f32 ? a.rows > 5 : a.rows > 32 && !aligned)) return launch_linear_q4_split(a, group, s);
   return group == 32 ? pick<32>(a, s) : group == 64 ? pick<64>(a, s) : pick<128>(a, s);
 }
