@@ -24,9 +24,16 @@
 // by many outputs are a stream of codes.
 // Tensor memory (512 columns): two to six steps of expanded codes of 64 columns, then three or four accumulators.
 //
-// A warp's own instructions, one after another, are what a role costs at small BN (an instruction that needs
-// the last one's result comes some 5 cycles later), so barriers' addresses and phases are kept, not computed,
-// and a wait that need not wait is one instruction and a branch.
+// What bounds it.  2048 rows by 4096 x 6144 (103 GFLOP): 77 us, 1.33 PFLOP/s or 68 % of cuBLAS's bf16 burst
+// rate; the products alone take 52, with the drain beside them 69: each accumulator's 64 KB pass
+// through tensor memory's port once more for every 512 cycles of products, and an SM's TMA unit, at some 35
+// bytes a cycle, needs 1170 cycles for the x and codes of a step whose products take 1024.  Groups of 64 and 32
+// have two and four accumulators a step: 124 and 218 us.  One tile of the drain's loop unrolled over four groups
+// made it 83 us.  16 rows by 2048 x 131072 (147 MB): 49 us, 3.0 TB/s: a step's own instructions, barriers and
+// waits, in each role one after another, take 475 cycles in the products' warp alone (28 us) and 850 with all
+// roles beside it; HBM would allow 350.  x brought in for every step instead of once made it 56, two converter
+// warpgroups instead of four with x resident no less, codes by cp.async of two warps 67.  A warp's own instructions
+// being the cost, barriers' phases are kept, not computed, and a wait that need not wait is a test and a branch.
 #pragma once
 
 #include <cudaTypedefs.h>
