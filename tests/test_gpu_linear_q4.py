@@ -67,6 +67,18 @@ def test_long_inputs_and_many_outputs(dtype, rows, n, k):
     check(inputs(rng, rows, k, dtype), codes, scales, 128)
 
 
+@pytest.mark.parametrize("dtype, rows, n, k, pad", [(BF16, 24, 40000, 512, 0), (BF16, 3, 39000, 1184, 0), (BF16, 300, 12100, 640, 0),
+                                                    (BF16, 70, 24000, 928, 8), (F32, 100, 20100, 384, 0), (F32, 12, 39937, 256, 1),
+                                                    (BF16, 40, 23000, 352, 1), (BF16, 100, 40001, 384, 0), (BF16, 128, 60000, 1664, 0),
+                                                    (BF16, 50, 60000, 640, 0), (BF16, 18, 80000, 288, 0), (BF16, 600, 20000, 896, 0),
+                                                    (F32, 84, 19300, 384, 0), (F32, 170, 20000, 288, 0), (BF16, 200, 19300, 352, 1)])
+def test_several_tiles_for_each_pair_of_ctas(dtype, rows, n, k, pad):
+    rng = np.random.default_rng(n)
+    for group in (128, 32):
+        codes, scales = weights(rng, n, k, group, F32)
+        check(inputs(rng, rows, k, dtype, pad), codes, scales, group, pad=5)
+
+
 @pytest.mark.parametrize("rows", [1, 40, 200])
 def test_every_code_and_input_is_in_its_place(rows):
     """One input at a time is 1: the outputs are its weights, exactly."""

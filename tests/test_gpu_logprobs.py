@@ -63,7 +63,7 @@ def test_rows_against_the_oracle(dtype, vocab):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
-@pytest.mark.parametrize("rows, vocab", [(1, 131072), (3, 50257), (20, 9000), (40, 8192), (77, 4100), (160, 2000), (700, 600)])
+@pytest.mark.parametrize("rows, vocab", [(1, 131072), (3, 50257), (20, 9000), (40, 8192), (77, 4100), (160, 2000), (333, 9000), (700, 600)])
 def test_numbers_of_rows(dtype, rows, vocab):
     gen = torch.Generator("cuda").manual_seed(rows)
     x = (3 * torch.randn(rows, vocab, generator=gen, device="cuda")).to(dtype)
