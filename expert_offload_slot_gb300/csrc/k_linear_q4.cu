@@ -395,7 +395,7 @@ bool rows_are_faster(const LinearArgs& a) {
 cudaError_t linear_q4_rows_status(int32_t* st) { return take_status(g_status, st); }
 
 cudaError_t launch_linear_q4(const LinearArgs& a, int group, cudaStream_t s) {
-  const bool tiles = a.K >= 256 && a.N >= 128, aligned = (reinterpret_cast<uintptr_t>(a.x) & 15) == 0 && a.x_stride % 8 == 0;
+  const bool tiles = a.K >= 256, aligned = (reinterpret_cast<uintptr_t>(a.x) & 15) == 0 && a.x_stride % 8 == 0;
   if (tiles && !a.x_f32 && aligned && !rows_are_faster(a)) return launch_linear_q4_tiles(a, group, s);
   if (tiles && (a.x_f32 ? a.rows > 5 : a.rows > 32 && !aligned)) return launch_linear_q4_split(a, group, s);
   return group == 32 ? pick<32>(a, s) : group == 64 ? pick<64>(a, s) : pick<128>(a, s);

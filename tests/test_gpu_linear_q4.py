@@ -49,7 +49,8 @@ def check(x, codes, scales, group, bias=None, out_type=None, pad=0):
 @pytest.mark.parametrize("group", [32, 64, 128])
 @pytest.mark.parametrize("rows, n, k", [(1, 1, 32), (1, 16, 128), (1, 17, 160), (2, 100, 96), (3, 333, 1120), (5, 64, 2048), (8, 15, 416),
                                         (9, 129, 512), (10, 31, 4096), (16, 200, 2016), (17, 2000, 256), (31, 48, 64), (33, 260, 544),
-                                        (64, 130, 1056), (100, 257, 800), (129, 384, 1152)])
+                                        (64, 130, 1056), (100, 257, 800), (129, 384, 1152), (40, 1, 256),
+                                        (300, 77, 608), (90, 120, 2048)])
 def test_sizes(dtype, group, rows, n, k):
     rng = np.random.default_rng(rows * n + k)
     for scale_type, out_type, pad in ((F32, None, 0), (BF16, F32, 3)):
