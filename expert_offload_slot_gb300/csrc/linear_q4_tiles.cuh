@@ -24,16 +24,16 @@
 // by many outputs are a stream of codes.
 // Tensor memory (512 columns): two to six steps of expanded codes of 64 columns, then three or four accumulators.
 //
-// What bounds it.  2048 rows by 4096 x 6144 (103 GFLOP): 77 us, 1.33 PFLOP/s or 68 % of cuBLAS's bf16 burst
+// What bounds it.  2048 rows by 4096 x 6144 (103 GFLOP): 77 us, 1.34 PFLOP/s or 68 % of cuBLAS's bf16 burst
 // rate; the products alone take 52, with the drain beside them 69: each accumulator's 64 KB pass
 // through tensor memory's port once more for every 512 cycles of products, and an SM's TMA unit, at some 35
 // bytes a cycle, needs 1170 cycles for the x and codes of a step whose products take 1024.  Groups of 64 and 32
-// have two and four accumulators a step: 124 and 218 us.  One tile of the drain's loop unrolled over four groups
-// made it 83 us.  16 rows by 2048 x 131072 (147 MB): 49 us, 3.0 TB/s: a step's own instructions, barriers and
-// waits, in each role one after another, take 475 cycles in the products' warp alone (28 us) and 850 with all
+// have two and four accumulators a step: 124 and 218 us.  The drain's loop unrolled over four groups cost 6 us.
+// 16 rows by 2048 x 131072 (147 MB): 48 us, 3.1 TB/s: a step's own instructions, barriers and
+// waits, in each role one after another, take 475 cycles in the products' warp alone (28 us) and 830 with all
 // roles beside it; HBM would allow 350.  With x brought in for every step, and two converter
 // warpgroups instead of four, it took 56; with codes by cp.async of two warps 67.  A warp's own instructions
-// being the cost, barriers' phases are kept, not computed, and a wait that need not wait is a test and a branch.
+// being the cost, barriers' phases are kept where that is cheap, and a wait that need not wait is a test and a branch.
 #pragma once
 
 #include <cudaTypedefs.h>
@@ -162,7 +162,7 @@ void linear_q4_tiles_kernel(const __grid_constant__ CUtensorMap mc, const __grid
   if (tid == 0) {
     for (int s = 0; s < C::CODE_STAGES; ++s) {
       bar_init(c_full + s, 1);
-      bar_init(c_empty + s, 8);
+      bar_init(c_empty + s, C::CONVERTERS == 1 ? 4 : 8);
     }
     for (int s = 0; s < kXBars; ++s) bar_init(x_full + s, C::PARTS == 0 ? 2 : 4);
     for (int s = 0; s < C::X_STAGES; ++s) bar_init(x_empty + s, 1);
@@ -355,41 +355,61 @@ void linear_q4_tiles_kernel(const __grid_constant__ CUtensorMap mc, const __grid
   } else if (wid < 4 + 4 * C::CONVERTERS) {
     regs_give<C::CONVERT>();
     // ------------------------------------------------------------- expansion
-    // The warpgroups take turns at the steps of all tiles, in one count: each is CONVERTERS steps after its last one.
-    // That keeps a wait for a buffer apart from the phase before: it holds the step 2 A_BUFS before this one to
-    // have ended, and at its last step the thread saw that the one A_BUFS before that had.
-    static_assert(C::A_BUFS >= C::CONVERTERS, "a warpgroup's waits could meet an older phase of a buffer");
     const int group = (wid >> 2) - 1, row = (wid & 3) * 32 + lane, stages = (steps + 1) / 2;
     const uint32_t lanes = tmem + ((uint32_t)(wid & 3) << 21), lead_full = lead_addr(a_full);
-    uint32_t n = group, nc0 = 0;                         // step, of all tiles; first stage of codes of the tile
-    int s = group;                                       // step of the tile
-    for (int tile = pair; tile < tiles; tile += pairs, s -= steps, nc0 += stages) {
-      for (; s < steps; s += C::CONVERTERS, n += C::CONVERTERS) {
-        const uint32_t nc = nc0 + s / 2, st = nc % C::CODE_STAGES, ab = n % C::A_BUFS;
-        wait(c_full + st, (nc / C::CODE_STAGES) & 1);
-        wait(a_empty + ab, ((n / C::A_BUFS) & 1) ^ 1);
-        tc_fence_after();
-        const uint8_t* src = smem + st * kCodeStage + row * 128;
+    auto expand = [&](uint32_t st, int half, uint32_t ab) {              // half a stage of codes into buffer ab
+      const uint8_t* src = smem + st * kCodeStage + row * 128;
+      tc_fence_after();
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {                    // 64 codes at a time
-          uint32_t w[32];
+      for (int q = 0; q < 2; ++q) {                      // 64 codes at a time
+        uint32_t w[32];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint4 u = *reinterpret_cast<const uint4*>(src + ((((s & 1) * 4 + q * 2 + i) ^ (row & 7)) << 4));
-            widen(u.x, w + i * 16);
-            widen(u.y, w + i * 16 + 4);
-            widen(u.z, w + i * 16 + 8);
-            widen(u.w, w + i * 16 + 12);
-          }
-          tmem_st32(lanes + ab * 64 + q * 32, w);
+        for (int i = 0; i < 2; ++i) {
+          const uint4 u = *reinterpret_cast<const uint4*>(src + (((half * 4 + q * 2 + i) ^ (row & 7)) << 4));
+          widen(u.x, w + i * 16);
+          widen(u.y, w + i * 16 + 4);
+          widen(u.z, w + i * 16 + 8);
+          widen(u.w, w + i * 16 + 12);
         }
-        tc_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          bar_arrive_at(lead_full + ab * 8);
-          bar_arrive(c_empty + st);                      // once for each half of a stage; a tile's last may have one only
-          if (s + 1 == steps && (s & 1) == 0) bar_arrive(c_empty + st);
+        tmem_st32(lanes + ab * 64 + q * 32, w);
+      }
+      tc_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive_at(lead_full + ab * 8);
+    };
+    if constexpr (C::CONVERTERS == 1) {                  // its own loop: 2048 rows by 4096 x 6144 77 us, by the other one 82
+      Ring<C::CODE_STAGES> rc;
+      Ring<C::A_BUFS> ra;
+      ra.phase = 1;
+      for (int tile = pair; tile < tiles; tile += pairs) {
+        for (int s0 = 0; s0 < steps; s0 += 2, rc.next()) {
+          wait(c_full + rc.i, rc.phase);
+#pragma unroll 1
+          for (int half = 0; half < 2 && s0 + half < steps; ++half, ra.next()) {
+            wait(a_empty + ra.i, ra.phase);
+            expand(rc.i, half, ra.i);
+          }
+          if (lane == 0) bar_arrive(c_empty + rc.i);
+        }
+      }
+    } else {
+      // The warpgroups take turns at the steps of all tiles, in one count: each is CONVERTERS steps after its last
+      // one.  That keeps a wait for a buffer apart from the phase before: it holds the step 2 A_BUFS before this one
+      // to have ended, and at its last step the thread saw that the one A_BUFS before that had.
+      static_assert(C::A_BUFS >= C::CONVERTERS, "a warpgroup's waits could meet an older phase of a buffer");
+      uint32_t n = group, nc0 = 0;                       // step, of all tiles; first stage of codes of the tile
+      int s = group;                                     // step of the tile
+      for (int tile = pair; tile < tiles; tile += pairs, s -= steps, nc0 += stages) {
+        for (; s < steps; s += C::CONVERTERS, n += C::CONVERTERS) {
+          const uint32_t nc = nc0 + s / 2, st = nc % C::CODE_STAGES, ab = n % C::A_BUFS;
+          wait(c_full + st, (nc / C::CODE_STAGES) & 1);
+          wait(a_empty + ab, ((n / C::A_BUFS) & 1) ^ 1);
+          expand(st, s & 1, ab);
+          if (lane == 0) {
+            bar_arrive(c_empty + st);                    // once for each half of a stage; a tile's last may have one only
+            if (s + 1 == steps && (s & 1) == 0) bar_arrive(c_empty + st);
+          }
         }
       }
     }
