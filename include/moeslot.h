@@ -629,8 +629,8 @@ MOE_API moe_status moe_q4_pack(const float* w, int32_t out_features, int32_t in_
  *            aligned
  *   bias     device [out_features] of dtype, or NULL
  *   out      device [rows] rows of [out_features] of out_dtype (dtype or MOE_F32), out_stride elements apart
- * Products are exact, sums fp32, in the same order in every call with the same sizes; rounded once.
- * out must not overlap an input. */
+ * Products are exact, sums fp32, in the same order in every call with the same sizes, types and alignment of x;
+ * rounded once.  bf16 rows of x that start on 16-byte boundaries are faster.  out must not overlap an input. */
 MOE_API moe_status moe_linear_q4(const void* x, int32_t dtype, int64_t x_stride, int32_t rows, int32_t in_features,
                                  const uint8_t* codes, const void* scales, int32_t scale_dtype, int32_t group,
                                  const void* bias, int32_t out_features, void* out, int32_t out_dtype, int64_t out_stride,
