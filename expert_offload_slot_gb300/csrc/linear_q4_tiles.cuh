@@ -42,6 +42,7 @@
 
 #include <atomic>
 
+#include "linear_q4_turns.cuh"
 #include "sm103.cuh"
 #include "step_internal.cuh"
 
@@ -355,7 +356,7 @@ void linear_q4_tiles_kernel(const __grid_constant__ CUtensorMap mc, const __grid
   } else if (wid < 4 + 4 * C::CONVERTERS) {
     regs_give<C::CONVERT>();
     // ------------------------------------------------------------- expansion
-    const int group = (wid >> 2) - 1, row = (wid & 3) * 32 + lane, stages = (steps + 1) / 2;
+    const int group = (wid >> 2) - 1, row = (wid & 3) * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(wid & 3) << 21), lead_full = lead_addr(a_full);
     auto expand = [&](uint32_t st, int half, uint32_t ab) {              // half a stage of codes into buffer ab
       const uint8_t* src = smem + st * kCodeStage + row * 128;
@@ -394,24 +395,15 @@ void linear_q4_tiles_kernel(const __grid_constant__ CUtensorMap mc, const __grid
         }
       }
     } else {
-      // The warpgroups take turns at the steps of all tiles, in one count: each is CONVERTERS steps after its last
-      // one.  That keeps a wait for a buffer apart from the phase before: it holds the step 2 A_BUFS before this one
-      // to have ended, and at its last step the thread saw that the one A_BUFS before that had.
-      static_assert(C::A_BUFS >= C::CONVERTERS, "a warpgroup's waits could meet an older phase of a buffer");
-      uint32_t n = group, nc0 = 0;                       // step, of all tiles; first stage of codes of the tile
-      int s = group;                                     // step of the tile
-      for (int tile = pair; tile < tiles; tile += pairs, s -= steps, nc0 += stages) {
-        for (; s < steps; s += C::CONVERTERS, n += C::CONVERTERS) {
-          const uint32_t nc = nc0 + s / 2, st = nc % C::CODE_STAGES, ab = n % C::A_BUFS;
-          wait(c_full + st, (nc / C::CODE_STAGES) & 1);
-          wait(a_empty + ab, ((n / C::A_BUFS) & 1) ^ 1);
-          expand(st, s & 1, ab);
-          if (lane == 0) {
-            bar_arrive(c_empty + st);                    // once for each half of a stage; a tile's last may have one only
-            if (s + 1 == steps && (s & 1) == 0) bar_arrive(c_empty + st);
-          }
-        }
-      }
+      converter_turns<C>(
+          group, steps, pair, tiles, pairs, [&](uint32_t ab, uint32_t parity) { wait(a_empty + ab, parity); },
+          [&](uint32_t st, uint32_t parity) { wait(c_full + st, parity); }, expand,
+          [&](uint32_t st, bool twice) {
+            if (lane == 0) {
+              bar_arrive(c_empty + st);
+              if (twice) bar_arrive(c_empty + st);
+            }
+          });
     }
   } else {
     regs_take<C::DRAIN>();
