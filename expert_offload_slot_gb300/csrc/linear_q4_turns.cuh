@@ -1,5 +1,5 @@
-// The turns of the converter warpgroups of linear_q4_tiles.cuh, apart from what a turn does, so that their waits can
-// be walked through on the host, too (tests/q4_turns.cu).
+// The turns of the converter warpgroups of linear_q4_tiles.cuh, apart from what a turn does, and the waits at a kernel's
+// end, so that they can be walked through on the host, too (tests/q4_turns.cu).
 #pragma once
 
 #include <stdint.h>
@@ -42,6 +42,37 @@ __host__ __device__ __forceinline__ void converter_turns(int group, int steps, i
       release(st, s + 1 == steps && (s & 1) == 0);       // once for each half of a stage; a tile's last may have one only
     }
   }
+}
+
+// The end.  Products report that a buffer or a stage of x is free to the barriers of both CTAs of a pair, on their own time:
+// a CTA that left before the last reports have come would have them land in memory that is another's by then.  So whoever
+// waits for a barrier's reports does so to the last use.
+
+// Of a converter warpgroup after `total` steps of all warpgroups.  Step by step, so that each wait knows the phase before
+// to be over; for the first, step total - 2 A_BUFS, the warpgroup's last turn told.
+#pragma nv_exec_check_disable
+template <typename C, typename WaitBuffer>
+__host__ __device__ __forceinline__ void converter_end(uint32_t total, WaitBuffer wait_buffer) {
+  for (uint32_t n = total > C::A_BUFS ? total - C::A_BUFS : 0; n < total; ++n) wait_buffer(n % C::A_BUFS, (n / C::A_BUFS) & 1);
+}
+
+// A ring's place, and the parity of its barriers' phase there.
+template <int N>
+struct Ring {
+  uint32_t i = 0, phase = 0;
+  __host__ __device__ __forceinline__ void next() {
+    if (++i == N) {
+      i = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+// Of who fills a ring's stages, at the place that would be filled next: all N are free again, or never were filled.
+#pragma nv_exec_check_disable
+template <int N, typename WaitEmpty>
+__host__ __device__ __forceinline__ void ring_end(Ring<N> r, WaitEmpty wait_empty) {
+  for (int k = 0; k < N; ++k, r.next()) wait_empty(r.i, r.phase);
 }
 
 }  // namespace moeslot

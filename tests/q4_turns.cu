@@ -1,5 +1,5 @@
 // The converter warpgroups' turns of moe_linear_q4's tile kernels on the host: what each waits for, in its order, as
-// (what, slot, parity, 0), and what it does with it.
+// (what, slot, parity, 0), and what it does with it; and the waits at the end.
 #include "../expert_offload_slot_gb300/csrc/linear_q4_tiles.cuh"
 
 using namespace moeslot;
@@ -25,12 +25,13 @@ int walk(int group, int steps, int tile, int tiles, int pairs, int* out, int roo
   return n;
 }
 
-// f(Tile<columns, ...>) of a kernel whose warpgroups take turns; -1 for others
+// f(Tile<columns, ...>) of a kernel; -1 for others
 template <typename F>
 int with(int columns, int parts, F f) {
   if (parts == 0 && columns == 32) return f(Tile<32, 128, 0>());
   if (parts == 0 && columns == 64) return f(Tile<64, 128, 0>());
   if (parts == 0 && columns == 128) return f(Tile<128, 128, 0>());
+  if (parts == 0 && columns == 256) return f(Tile<256, 128, 0>());       // one warpgroup: no turns
   if (parts == 1 && columns == 64) return f(Tile<64, 128, 1>());
   if (parts == 3 && columns == 64) return f(Tile<64, 128, 3>());
   return -1;
@@ -52,4 +53,29 @@ extern "C" __attribute__((visibility("default"))) int q4_shape(int columns, int 
 extern "C" __attribute__((visibility("default"))) int q4_turns(int columns, int parts, int group, int steps, int tile, int tiles, int pairs,
                                                                int* out, int room) {
   return with(columns, parts, [&](auto shape) { return walk<decltype(shape)>(group, steps, tile, tiles, pairs, out, room); });
+}
+
+// The waits of a converter warpgroup after `total` steps, as (slot, parity).
+extern "C" __attribute__((visibility("default"))) int q4_end(int columns, int parts, int total, int* out) {
+  return with(columns, parts, [&](auto shape) {
+    int n = 0;
+    converter_end<decltype(shape)>(total, [&](uint32_t ab, uint32_t parity) {
+      out[2 * n] = ab;
+      out[2 * n++ + 1] = parity;
+    });
+    return n;
+  });
+}
+
+// Those of a ring of four stages whose first `used` have been filled.
+extern "C" __attribute__((visibility("default"))) int q4_ring_end(int used, int* out) {
+  Ring<4> r;
+  r.phase = 1;
+  for (int k = 0; k < used; ++k) r.next();
+  int n = 0;
+  ring_end(r, [&](uint32_t i, uint32_t parity) {
+    out[2 * n] = i;
+    out[2 * n++ + 1] = parity;
+  });
+  return n;
 }

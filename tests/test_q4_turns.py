@@ -96,3 +96,30 @@ def test_every_step_is_expanded_once_and_every_stage_released(lib, columns, part
                     held.append((what, slot))
         assert sorted(made) == list(range(mine * steps))
         assert set(freed) == set(range(mine * ((steps + 1) // 2))) and all(v == 2 for v in freed.values())
+
+
+@pytest.mark.parametrize("columns, parts", SHAPES + [(256, 0)])
+def test_no_warpgroup_ends_before_its_buffers_have_been_reported_free(lib, columns, parts):
+    converters, buffers, _ = shape_of(lib, columns, parts)
+    for total in range(2, 300):
+        out = np.zeros((buffers, 2), np.int32)
+        n = lib.q4_end(columns, parts, total, out.ctypes.data_as(ctypes.c_void_p))
+        assert n == min(total, buffers)
+        for group in range(converters):
+            last = (total - 1 - group) // converters * converters + group          # its last turn, negative if it had none
+            known = last - buffers
+            for step, (slot, parity) in zip(range(total - n, total), out.tolist()):
+                assert (slot, parity) == (step % buffers, step // buffers % 2)     # the phase that this step's products end
+                assert step < buffers or step - buffers <= known                   # the one before is known to be over
+                known = max(known, step)
+
+
+def test_no_loader_ends_before_its_stages_have_been_reported_free(lib):
+    for used in range(30):
+        out = np.zeros((4, 2), np.int32)
+        assert lib.q4_ring_end(used, out.ctypes.data_as(ctypes.c_void_p)) == 4
+        for k, (slot, parity) in enumerate(out.tolist()):
+            use = used + k                                     # of the ring's stages, from 0; the stage was filled 4 uses before
+            assert slot == use % 4 and parity == (use // 4 + 1) % 2
+            # an unused stage's barrier is in its first phase: parity 1 passes at once, which is that of a first use
+            assert use >= 4 or parity == 1
