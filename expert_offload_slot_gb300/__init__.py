@@ -417,6 +417,39 @@ def _rows(name, t, kind, rows, width, device):
                      f"got {t.dtype}, {tuple(t.shape)}, strides {t.stride()}, on {t.device}")
 
 
+def _splits(shape, width):
+    """Whether the trailing dimensions make up rows of `width` (a flat tensor's layout is the caller's word)."""
+    inner = 1
+    for n in reversed(shape):
+        if inner == width:
+            return True
+        inner *= n
+    return inner == width or len(shape) == 1
+
+
+def _not_rows(name, t, rows, width):
+    return ValueError(f"{name} must hold [{rows}, {width}], got {tuple(t.shape)}")
+
+
+def _matrix(name, t, kind, rows, width, device):
+    """_rows() of a tensor [rows, width], the same count in another order ([width, rows]) refused."""
+    whole = t.shape == (rows, width)
+    if whole and t.dtype is kind and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr(), width
+    at = _rows(name, t, kind, rows, width, device)
+    if not whole and not _splits(t.shape, width):
+        raise _not_rows(name, t, rows, width)
+    return at
+
+
+def _table(name, t, kind, rows, width, device):
+    """_flat() of a tensor [rows, width], the same count in another order refused."""
+    at = _flat(name, t, kind, rows * width, device)
+    if t.shape != (rows, width) and not _splits(t.shape, width):
+        raise _not_rows(name, t, rows, width)
+    return at
+
+
 class Attention:
     """The attention of a step over a paged cache (moe_attn_create ... moe_attn_destroy).
 
@@ -566,10 +599,10 @@ def moe_residual_norm(x, residual, residual_out, y, post_weight=None, pre_weight
             kind, gate_at = MOE_RESIDUAL_GATE_CHANNEL, _flat("gate", gate, dtype, hidden, dev)
         elif gate.size(-1) == 1:
             kind = MOE_RESIDUAL_GATE_ROW
-            gate_at, gate_step = _rows("gate", gate, dtype, rows, 1, dev)
+            gate_at, gate_step = _matrix("gate", gate, dtype, rows, 1, dev)
         else:
             kind = MOE_RESIDUAL_GATE_ELEMENT
-            gate_at, gate_step = _rows("gate", gate, dtype, rows, hidden, dev)
+            gate_at, gate_step = _matrix("gate", gate, dtype, rows, hidden, dev)
     key = (hidden, dtype, stream_type, kind, gate_sigmoid, residual_scale, eps, weight_offset)
     cfg = _norm_configs.get(key)
     if cfg is None:
@@ -578,10 +611,10 @@ def moe_residual_norm(x, residual, residual_out, y, post_weight=None, pre_weight
         cfg = _norm_configs[key] = moe_norm_config(hidden, MOE_F32 if dtype is f32 else MOE_BF16,
                                                    MOE_F32 if stream_type is f32 else MOE_BF16, kind, int(bool(gate_sigmoid)),
                                                    residual_scale, eps, weight_offset)
-    x_at, x_step = (None, 0) if x is None else _rows("x", x, dtype, rows, hidden, dev)
+    x_at, x_step = (None, 0) if x is None else _matrix("x", x, dtype, rows, hidden, dev)
     r_at, r_step = _rows("residual", residual, stream_type, rows, hidden, dev)
-    s_at, s_step = (None, 0) if residual_out is None else _rows("residual_out", residual_out, stream_type, rows, hidden, dev)
-    y_at, y_step = (None, 0) if y is None else _rows("y", y, dtype, rows, hidden, dev)
+    s_at, s_step = (None, 0) if residual_out is None else _matrix("residual_out", residual_out, stream_type, rows, hidden, dev)
+    y_at, y_step = (None, 0) if y is None else _matrix("y", y, dtype, rows, hidden, dev)
     _launch("moe_residual_norm", dev, stream, ctypes.byref(cfg), x_at, x_step, gate_at, gate_step,
             None if post_weight is None else _flat("post_weight", post_weight, dtype, hidden, dev), r_at, r_step, s_at, s_step,
             None if pre_weight is None else _flat("pre_weight", pre_weight, dtype, hidden, dev), y_at, y_step, rows)
@@ -613,10 +646,10 @@ def moe_linear_q4(x, codes, scales, out, group=128, bias=None, stream=None):
     if group not in (32, 64, 128):
         raise ValueError("group must be 32, 64 or 128")
     x_at, x_step = _rows("x", x, dtype, rows, k, dev)
-    out_at, out_step = _rows("out", out, out_type, rows, n, dev)
+    out_at, out_step = _matrix("out", out, out_type, rows, n, dev)
     _launch("moe_linear_q4", dev, stream, x_at, MOE_F32 if dtype is f32 else MOE_BF16, x_step, rows, k,
             _flat("codes", codes, kinds["u8"], n * (k // 2), dev),
-            _flat("scales", scales, scale_type, n * -(-k // group), dev), MOE_F32 if scale_type is f32 else MOE_BF16, group,
+            _table("scales", scales, scale_type, n, -(-k // group), dev), MOE_F32 if scale_type is f32 else MOE_BF16, group,
             None if bias is None else _flat("bias", bias, dtype, n, dev), n, out_at, MOE_F32 if out_type is f32 else MOE_BF16,
             out_step)
 
@@ -637,7 +670,7 @@ def moe_logprobs(logits, targets, logp, entropy=None, rank=None, top_ids=None, t
             _flat("logp", logp, f32, rows, dev), None if entropy is None else _flat("entropy", entropy, f32, rows, dev),
             None if rank is None else _flat("rank", rank, i32, rows, dev),
             None if top_ids is None else _flat("top_ids", top_ids, i32, rows * top, dev),
-            None if top_logp is None else _flat("top_logp", top_logp, f32, rows * top, dev))
+            None if top_logp is None else _table("top_logp", top_logp, f32, rows, top, dev))
 
 
 def moe_step_status():

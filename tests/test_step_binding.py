@@ -1,0 +1,59 @@
+"""Shapes that the binding of moe_residual_norm, moe_linear_q4 and moe_logprobs looks at, without a GPU."""
+import pytest
+import torch
+
+import expert_offload_slot_gb300 as moe
+from tests.test_attn_binding import On, calls  # noqa: F401
+
+F32, BF16, I32, U8 = torch.float32, torch.bfloat16, torch.int32, torch.uint8
+
+
+def linear(**kw):
+    a = dict(x=On((7, 256), BF16, 0), codes=On((50, 128), U8, 0), scales=On((50, 2), F32, 0), out=On((7, 50), F32, 0))
+    moe.moe_linear_q4(**{**a, **kw})
+
+
+def norm(**kw):
+    a = {n: On((7, 64), BF16, 0) for n in ("x", "residual", "residual_out", "y")}
+    moe.moe_residual_norm(**{**a, **kw})
+
+
+def scores(**kw):
+    a = dict(logits=On((7, 50), F32, 0), targets=On((7,), I32, 0), logp=On((7,), F32, 0), top_ids=On((7, 4), I32, 0),
+             top_logp=On((7, 4), F32, 0))
+    moe.moe_logprobs(**{**a, **kw})
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_scales_of_another_order_are_refused(calls, dtype):  # noqa: F811
+    """[groups, out], as several 4-bit formats store them, has the right count of elements."""
+    with pytest.raises(ValueError, match="^scales must"):
+        linear(scales=On((2, 50), dtype, 0))
+    with pytest.raises(ValueError, match="^scales must"):
+        linear(scales=On((2, 5, 10), dtype, 0))
+    assert not calls.seen
+    linear(scales=On((50, 2), dtype, 0))
+    linear(scales=On((50, 2, 1), dtype, 0))
+    linear(scales=On((100,), dtype, 0))
+    assert len(calls.seen) == 3
+
+
+def test_outputs_and_inputs_of_another_order_are_refused(calls):  # noqa: F811
+    for call, name, shape, dtype in [(linear, "out", (50, 7), F32), (norm, "x", (64, 7), BF16), (norm, "residual_out", (64, 7), BF16),
+                                     (norm, "y", (64, 7), BF16), (norm, "y", (8, 7, 8), BF16), (scores, "top_logp", (4, 7), F32)]:
+        with pytest.raises(ValueError, match=f"^{name} must"):
+            call(**{name: On(shape, dtype, 0)})
+    assert not calls.seen
+
+
+def test_rows_in_several_dimensions_are_taken(calls):  # noqa: F811
+    linear(out=On((7, 5, 10), F32, 0))
+    linear(out=On((7, 50, 1), F32, 0))
+    linear(x=On((8, 256), BF16, 0), out=On((2, 4, 50), F32, 0))
+    linear(x=On((1, 256), BF16, 0), out=On((50,), F32, 0))
+    norm(y=On((7, 4, 16), BF16, 0), x=On((7, 1, 64), BF16, 0))
+    norm(residual=On((0, 64), BF16, 0), x=On((0, 64), BF16, 0), y=On((0, 64), BF16, 0), residual_out=On((0, 64), BF16, 0))
+    scores(top_logp=On((28,), F32, 0))
+    scores(logits=On((1, 50), F32, 0), targets=On((1,), I32, 0), logp=On((1,), F32, 0), top_ids=On((1, 4), I32, 0),
+           top_logp=On((4,), F32, 0))
+    assert len(calls.seen) == 8
