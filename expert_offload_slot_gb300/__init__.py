@@ -603,14 +603,14 @@ def moe_residual_norm(x, residual, residual_out, y, post_weight=None, pre_weight
         else:
             kind = MOE_RESIDUAL_GATE_ELEMENT
             gate_at, gate_step = _matrix("gate", gate, dtype, rows, hidden, dev)
-    key = (hidden, dtype, stream_type, kind, gate_sigmoid, residual_scale, eps, weight_offset)
+    # by value: a number held in a tensor may change, and its hash is the tensor's identity
+    key = (hidden, dtype, stream_type, kind, bool(gate_sigmoid), float(residual_scale), float(eps), float(weight_offset))
     cfg = _norm_configs.get(key)
     if cfg is None:
         if len(_norm_configs) > 256:
             _norm_configs.clear()
         cfg = _norm_configs[key] = moe_norm_config(hidden, MOE_F32 if dtype is f32 else MOE_BF16,
-                                                   MOE_F32 if stream_type is f32 else MOE_BF16, kind, int(bool(gate_sigmoid)),
-                                                   residual_scale, eps, weight_offset)
+                                                   MOE_F32 if stream_type is f32 else MOE_BF16, kind, *key[4:])
     x_at, x_step = (None, 0) if x is None else _matrix("x", x, dtype, rows, hidden, dev)
     r_at, r_step = _rows("residual", residual, stream_type, rows, hidden, dev)
     s_at, s_step = (None, 0) if residual_out is None else _matrix("residual_out", residual_out, stream_type, rows, hidden, dev)

@@ -1,4 +1,7 @@
 """Shapes that the binding of moe_residual_norm, moe_linear_q4 and moe_logprobs looks at, without a GPU."""
+import ctypes
+import types
+
 import pytest
 import torch
 
@@ -57,3 +60,23 @@ def test_rows_in_several_dimensions_are_taken(calls):  # noqa: F811
     scores(logits=On((1, 50), F32, 0), targets=On((1,), I32, 0), logp=On((1,), F32, 0), top_ids=On((1, 4), I32, 0),
            top_logp=On((4,), F32, 0))
     assert len(calls.seen) == 8
+
+
+def test_norm_numbers_are_taken_anew_in_every_call(monkeypatch):
+    """Numbers held in tensors that change between calls, as a learned scale does: none is kept by its identity."""
+    seen = []
+
+    def call(cfg, *args):
+        c = ctypes.cast(cfg, ctypes.POINTER(moe.moe_norm_config)).contents
+        seen.append((c.gate_sigmoid, c.residual_scale, c.norm_eps, c.weight_offset))
+        return moe.MOE_OK
+    monkeypatch.setattr(moe, "_lib", types.SimpleNamespace(moe_residual_norm=call))
+    monkeypatch.setattr(moe, "_kinds", {**moe._torch_kinds(), "stream": lambda d: 5, "device": lambda: 0})
+    sigmoid, scale, eps, offset = torch.tensor(False), torch.tensor(2.0), torch.tensor(0.5), torch.tensor(1.0)
+    for k in range(3):
+        norm(gate_sigmoid=sigmoid, residual_scale=scale, eps=eps, weight_offset=offset)
+        norm(gate_sigmoid=k % 2, residual_scale=2 + k, eps=0.5 + k, weight_offset=True)
+        assert seen[-2] == (k % 2, 2.0 + k, 0.5 + k, 1.0 + k) and seen[-1] == (k % 2, 2.0 + k, 0.5 + k, 1.0)
+        for t in (scale, eps, offset):
+            t += 1
+        sigmoid.logical_not_()
