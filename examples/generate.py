@@ -131,6 +131,15 @@ class Server:
         self.host.free()
 
 
+def check(server):
+    """Raise where a kernel of the steps so far gave up: its output, and the tokens made of it, are undefined."""
+    status = {"attention": server.attn.status(), "experts": server.pool.status()}
+    if server.unembed.q4:
+        status["projections"] = moe.moe_step_status()          # of the device, and reset by this
+    if any(status.values()):
+        raise RuntimeError("device status " + ", ".join(f"{v} ({n})" for n, v in status.items()))
+
+
 def generate(server, prompts, count, temperature=0.8, top_k=50, top_p=0.95, min_p=0.0, seed=0, scores=None, top=0):
     """Token ids [R, count] that follow the prompts (lists of ids, none empty: a first token follows its prompt's last).
 
@@ -156,8 +165,7 @@ def generate(server, prompts, count, temperature=0.8, top_k=50, top_p=0.95, min_
             moe.moe_logprobs(logits, ids, **row)
             scores.append(row)
         tokens, new = ids.long(), [1] * R
-    if server.attn.status() or server.pool.status():
-        raise RuntimeError(f"device status {server.attn.status()} (attention), {server.pool.status()} (experts)")
+    check(server)
     return torch.stack(made, 1)
 
 

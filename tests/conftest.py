@@ -24,3 +24,13 @@ def pytest_collection_modifyitems(config, items):
     for item in items:
         if "gpu" in item.keywords:
             item.add_marker(skip)
+
+
+@pytest.fixture(autouse=True)
+def projections_end(request):
+    """4-bit projections report a wait that ran out in a status of the device alone: read after each test that makes them."""
+    yield
+    if "gpu" in request.node.keywords and request.module.__name__.split(".")[-1] in (
+            "test_gpu_linear_q4", "test_gpu_linear_q4_turns", "test_gpu_generate_q4", "test_gpu_step"):
+        import expert_offload_slot_gb300 as moe
+        assert moe.moe_step_status() == moe.MOE_OK

@@ -16,3 +16,21 @@ def test_prompts_that_do_not_fit_the_server_are_refused(prompts):
     # an empty prompt has no last row: the row before it, of another request, would be taken for it
     with pytest.raises(ValueError, match="prompts of one token or more"):
         example.generate(types.SimpleNamespace(R=2), prompts, 3)
+
+
+@pytest.mark.parametrize("q4", [False, True])
+@pytest.mark.parametrize("attention, experts, projections", [(0, 0, 0), (3, 0, 0), (0, 3, 0), (0, 0, 3)])
+def test_a_kernel_that_gave_up_is_reported(monkeypatch, q4, attention, experts, projections):
+    spec = importlib.util.spec_from_file_location("generate_example_host", PATH)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    reads = []
+    monkeypatch.setattr(example.moe, "moe_step_status", lambda: reads.append(1) or projections)
+    server = types.SimpleNamespace(attn=types.SimpleNamespace(status=lambda: attention), pool=types.SimpleNamespace(status=lambda: experts),
+                                   unembed=types.SimpleNamespace(q4=q4))
+    if attention or experts or (q4 and projections):
+        with pytest.raises(RuntimeError, match=r"3 \((attention|experts|projections)\)"):
+            example.check(server)
+    else:
+        example.check(server)
+    assert len(reads) == q4                                    # it resets what it reads, and plain projections do not use it
