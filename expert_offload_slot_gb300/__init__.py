@@ -581,7 +581,7 @@ def moe_residual_norm(x, residual, residual_out, y, post_weight=None, pre_weight
 
     x, residual, residual_out and y are [rows, hidden] with contiguous rows; x (then residual_out, too) or y may be
     None.  The block's output is normed only where post_weight [hidden] is given.  gate is [rows, 1], [hidden] or
-    [rows, hidden].
+    [rows, hidden].  residual_out may be residual, and y may be x or, without x, residual.
     """
     kinds = _torch_kinds()
     f32, bf16 = kinds[MOE_F32], kinds[MOE_BF16]

@@ -605,8 +605,8 @@ typedef struct {
  *   x NULL     nothing is added: y is the norm of residual; residual_out and post_weight must be
  *              NULL and the config without a gate
  *   y NULL     only residual_out is wanted
- * Computed in fp32, rounded once.  residual_out may be residual and y may be x (the same address,
- * stride and type); other overlaps of an output with an input are not allowed.  Rows that lie on
+ * Computed in fp32, rounded once.  residual_out may be residual, and y may be x or, where x is NULL, residual (the
+ * same address, stride and type); other overlaps of an output with an input are not allowed.  Rows that lie on
  * 16-byte boundaries with a hidden that is a multiple of 8 are faster. */
 MOE_API moe_status moe_residual_norm(const moe_norm_config* cfg, const void* x, int64_t x_stride, const void* gate,
                                      int64_t gate_stride, const void* post_weight, const void* residual,
