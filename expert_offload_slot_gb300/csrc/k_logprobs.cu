@@ -35,7 +35,7 @@ namespace cg = cooperative_groups;
 typedef __nv_bfloat16 bf16;
 typedef unsigned long long u64;
 
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 8, kMaxThreads = 512;
 constexpr int kTop = MOE_LOGPROBS_MAX_TOP;
 constexpr int kGroups = 64;                    // whose maxima bound the best tokens; twice kTop
 constexpr int kFew = 20;                       // of 32 groups' maxima: some 32 ln(32 / 12) = 31 logits reach the 20th
@@ -60,14 +60,13 @@ __device__ __forceinline__ void join(Soft& a, const Soft& b) {
 }
 
 struct Shared {                                // of a CTA; the cluster reads the second part
-  Soft warp[32];
-  int32_t count[32];
-  float best[1024];
+  Soft warp[kMaxThreads / 32];
+  int32_t count[kMaxThreads / 32];
+  float best[kMaxThreads];
   u64 list[kList];
   float bound;
   int32_t found, owners;
-  int16_t owner[1024];
-  u64 bits[32];
+  int16_t owner[kMaxThreads];
   // shown to the cluster
   Soft soft;
   float most;
@@ -193,6 +192,7 @@ struct Share {
 template <typename T, int NT>
 __global__ void __launch_bounds__(NT, NT == 256 ? 5 : 2) logprobs_kernel(const LogprobArgs a) {
   constexpr int W = Vec<T>::W, NW = NT / 32, U = 4;
+  static_assert(NT <= kMaxThreads, "room for every thread");
   __shared__ Shared sm;
   cg::cluster_group cluster = cg::this_cluster();
   const int cs = (int)cluster.num_blocks(), rank = (int)cluster.block_rank(), row = blockIdx.x / cs;

@@ -1,6 +1,7 @@
-// Thin wrappers over the PTX that the attention and sampling kernels use:
-// mbarriers with bounded waits, TMA tile loads, ldmatrix, warp-level matrix
-// products.  No arithmetic of an operator lives here.
+// Thin wrappers over the PTX that the kernels of a step use (attention, sampling,
+// norms, 4-bit projections, token scores): mbarriers with bounded waits, TMA tile
+// loads, ldmatrix, warp-level and tcgen05 matrix products, asynchronous copies.  No
+// arithmetic of an operator lives here.
 #pragma once
 
 #include <cuda.h>
