@@ -7,6 +7,7 @@ as ``torch.cuda.Stream.cuda_stream``.  There is no fallback: if the library has
 not been built, importing this package raises.
 """
 import ctypes
+import numbers
 import os
 
 import numpy as np
@@ -433,19 +434,24 @@ def _not_rows(name, t, rows, width):
 
 def _matrix(name, t, kind, rows, width, device):
     """_rows() of a tensor [rows, width], the same count in another order ([width, rows]) refused."""
-    whole = t.shape == (rows, width)
-    if whole and t.dtype is kind and t.get_device() == device and t.is_contiguous():
-        return t.data_ptr(), width
+    if t.dtype is kind and t.shape == (rows, width) and t.get_device() == device:
+        if t.is_contiguous():
+            return t.data_ptr(), width
+        step, inner = t.stride()
+        if inner == 1 or width == 1:
+            return t.data_ptr(), (step if rows > 1 else width)
     at = _rows(name, t, kind, rows, width, device)
-    if not whole and not _splits(t.shape, width):
+    if not _splits(t.shape, width):
         raise _not_rows(name, t, rows, width)
     return at
 
 
 def _table(name, t, kind, rows, width, device):
     """_flat() of a tensor [rows, width], the same count in another order refused."""
+    if t.dtype is kind and t.shape == (rows, width) and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
     at = _flat(name, t, kind, rows * width, device)
-    if t.shape != (rows, width) and not _splits(t.shape, width):
+    if not _splits(t.shape, width):
         raise _not_rows(name, t, rows, width)
     return at
 
@@ -586,7 +592,9 @@ def moe_residual_norm(x, residual, residual_out, y, post_weight=None, pre_weight
     kinds = _torch_kinds()
     f32, bf16 = kinds[MOE_F32], kinds[MOE_BF16]
     rows, hidden = residual.shape
-    dev = max(residual.get_device(), 0)        # a host tensor (-1) is refused below
+    dev = residual.get_device()
+    if dev < 0:                                # a host tensor is refused below
+        dev = 0
     first = y if x is None else x
     if first is None:
         raise ValueError("x and y must not both be None")
@@ -597,20 +605,22 @@ def moe_residual_norm(x, residual, residual_out, y, post_weight=None, pre_weight
     if gate is not None:
         if gate.dim() == 1:
             kind, gate_at = MOE_RESIDUAL_GATE_CHANNEL, _flat("gate", gate, dtype, hidden, dev)
-        elif gate.size(-1) == 1:
+        elif gate.shape[-1] == 1:
             kind = MOE_RESIDUAL_GATE_ROW
             gate_at, gate_step = _matrix("gate", gate, dtype, rows, 1, dev)
         else:
             kind = MOE_RESIDUAL_GATE_ELEMENT
             gate_at, gate_step = _matrix("gate", gate, dtype, rows, hidden, dev)
-    # by value: a number held in a tensor may change, and its hash is the tensor's identity
-    key = (hidden, dtype, stream_type, kind, bool(gate_sigmoid), float(residual_scale), float(eps), float(weight_offset))
+    key = (hidden, dtype, stream_type, kind, gate_sigmoid, residual_scale, eps, weight_offset)
     cfg = _norm_configs.get(key)
     if cfg is None:
-        if len(_norm_configs) > 256:
-            _norm_configs.clear()
-        cfg = _norm_configs[key] = moe_norm_config(hidden, MOE_F32 if dtype is f32 else MOE_BF16,
-                                                   MOE_F32 if stream_type is f32 else MOE_BF16, kind, *key[4:])
+        cfg = moe_norm_config(hidden, MOE_F32 if dtype is f32 else MOE_BF16, MOE_F32 if stream_type is f32 else MOE_BF16, kind,
+                              int(bool(gate_sigmoid)), residual_scale, eps, weight_offset)
+        # plain numbers alone are kept: a tensor's number may change, and its hash is the tensor's identity
+        if all(isinstance(v, numbers.Real) for v in key[4:]):
+            if len(_norm_configs) > 256:
+                _norm_configs.clear()
+            _norm_configs[key] = cfg
     x_at, x_step = (None, 0) if x is None else _matrix("x", x, dtype, rows, hidden, dev)
     r_at, r_step = _rows("residual", residual, stream_type, rows, hidden, dev)
     s_at, s_step = (None, 0) if residual_out is None else _matrix("residual_out", residual_out, stream_type, rows, hidden, dev)
@@ -638,8 +648,10 @@ def moe_linear_q4(x, codes, scales, out, group=128, bias=None, stream=None):
     kinds = _torch_kinds()
     f32, bf16 = kinds[MOE_F32], kinds[MOE_BF16]
     rows, k = x.shape
-    n = codes.size(0)
-    dev = max(x.get_device(), 0)               # a host tensor (-1) is refused below
+    n = codes.shape[0]
+    dev = x.get_device()
+    if dev < 0:                                # a host tensor is refused below
+        dev = 0
     dtype = f32 if x.dtype is f32 else bf16
     out_type = f32 if out.dtype is f32 else dtype
     scale_type = f32 if scales.dtype is f32 else bf16
@@ -661,11 +673,13 @@ def moe_logprobs(logits, targets, logp, entropy=None, rank=None, top_ids=None, t
     f32, i32 = kinds[MOE_F32], kinds["i32"]
     rows, vocab = logits.shape
     dtype = MOE_F32 if logits.dtype is f32 else MOE_BF16
-    dev = max(logits.get_device(), 0)          # a host tensor (-1) is refused below
+    dev = logits.get_device()
+    if dev < 0:                                # a host tensor is refused below
+        dev = 0
     at, step = _rows("logits", logits, f32 if dtype == MOE_F32 else kinds[MOE_BF16], rows, vocab, dev)
     if (top_ids is None) != (top_logp is None):
         raise ValueError("top_ids and top_logp go together")
-    top = 0 if top_ids is None else top_ids.size(1)
+    top = 0 if top_ids is None else top_ids.shape[1]
     _launch("moe_logprobs", dev, stream, at, dtype, rows, vocab, step, _flat("targets", targets, i32, rows, dev), top,
             _flat("logp", logp, f32, rows, dev), None if entropy is None else _flat("entropy", entropy, f32, rows, dev),
             None if rank is None else _flat("rank", rank, i32, rows, dev),

@@ -80,3 +80,19 @@ def test_norm_numbers_are_taken_anew_in_every_call(monkeypatch):
         for t in (scale, eps, offset):
             t += 1
         sigmoid.logical_not_()
+
+
+def test_strides_of_padded_rows(monkeypatch):
+    """The address and row stride that each form of rows gives; a column that is not contiguous is refused."""
+    kind = torch.float32
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 0)
+    wide = torch.zeros(6, 20)
+    for t, want in [(wide, 20), (wide[:, :7], 20), (wide[::2, :7], 40), (wide[:1, :7], 7), (wide[:, 3:4], 20), (wide.T[:4].T, 20),
+                    (wide[:, :8].unflatten(1, (2, 4)), 20), (wide[:0, :7], 7)]:
+        rows, width = t.shape[0], t[0].numel() if t.shape[0] else 7
+        assert moe._matrix("t", t, kind, rows, width, 0) == (t.data_ptr(), want) == moe._rows("t", t, kind, rows, width, 0)
+    for t in (wide.T[:4], wide[:, ::2], wide[:1, ::2], wide[:, :8].unflatten(1, (2, 4)).transpose(1, 2)):
+        for f in (moe._matrix, moe._rows):
+            with pytest.raises(ValueError, match="^t must"):
+                f("t", t, kind, t.shape[0], t[0].numel(), 0)
+    assert moe._matrix("t", wide[:, 3:4].expand(6, 1), kind, 6, 1, 0)[1] == 20
