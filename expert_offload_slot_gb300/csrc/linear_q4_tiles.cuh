@@ -131,6 +131,18 @@ struct Eight {
   }
 };
 
+// A ring's place, and the parity of its barriers' phase there.
+template <int N>
+struct Ring {
+  uint32_t i = 0, phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++i == N) {
+      i = 0;
+      phase ^= 1;
+    }
+  }
+};
+
 template <int N>
 __device__ __forceinline__ void tmem_load(uint32_t addr, float* v) {
   if constexpr (N == 16) tmem_ld16(addr, v);
@@ -177,6 +189,7 @@ void linear_q4_tiles_kernel(const __grid_constant__ CUtensorMap mc, const __grid
   const int steps = (a.K + 127) / 128, n_tiles = (a.rows + C::ROWS - 1) / C::ROWS, tiles = (a.N + 255) / 256 * n_tiles;
   const int pair = (int)blockIdx.x / 2, pairs = (int)gridDim.x / 2;
   const int eighth = (steps + kXBars - 1) / kXBars;      // steps behind one barrier of a resident x
+  const uint32_t mine = (uint32_t)((tiles - pair + pairs - 1) / pairs);  // tiles of this pair
   bool alive = true;
   auto wait = [&](uint64_t* b, uint32_t parity) {        // bounded; after a timeout nothing waits any more
     if (!bar_test(b, parity) && alive && !bar_wait(b, parity)) {
@@ -227,7 +240,6 @@ void linear_q4_tiles_kernel(const __grid_constant__ CUtensorMap mc, const __grid
           rx.next();
         }
       }
-      if (wid == 0) ring_end(rx, [&](uint32_t i, uint32_t parity) { wait(x_empty + i, parity); });
     } else if (wid == 0) {
       // ------------------------------------------------------------ x, by TMA
       uint32_t st = 0, phase = 1;
@@ -251,6 +263,8 @@ void linear_q4_tiles_kernel(const __grid_constant__ CUtensorMap mc, const __grid
           if (s % eighth == 0) announce(bar, min(eighth, steps - s) * C::X_STAGE);
           load(xs + s * C::X_STAGE, lead_addr(bar), s, rank * (C::HN / 2));
         }
+        if (rank == 0)
+          for (int s = 0; s < steps; s += eighth) wait(x_full + s / eighth, 0);
       } else {
         for (int tile = pair; tile < tiles; tile += pairs) {
           const int t0 = tile % n_tiles * C::BN + rank * (C::HN / 2);
@@ -264,10 +278,10 @@ void linear_q4_tiles_kernel(const __grid_constant__ CUtensorMap mc, const __grid
             }
           }
         }
-        ring_end(Ring<C::X_STAGES>{st, phase}, [&](uint32_t i, uint32_t parity) { wait(x_empty + i, parity); });
+        if (rank == 0) last_uses<C::X_STAGES>(mine * steps, [&](uint32_t i, uint32_t parity) { wait(x_full + i, parity); });
       }
-      if (!alive) {                                      // bounded: copies in flight land (on the first CTA's barriers,
-        const uint64_t t = now_ns();                     // which this one cannot test) before the memory is given up
+      if (!alive) {                                      // bounded: copies in flight land before the memory is given up
+        const uint64_t t = now_ns();
         while (now_ns() - t < 1000000ull) __nanosleep(1000);
       }
     } else if (wid == 2) {
@@ -287,6 +301,7 @@ void linear_q4_tiles_kernel(const __grid_constant__ CUtensorMap mc, const __grid
           }
         }
       }
+      last_uses<C::CODE_STAGES>(mine * ((steps + 1) / 2), [&](uint32_t i, uint32_t parity) { wait(c_full + i, parity); });
       if (!alive) {
         const uint64_t t = now_ns();
         while (now_ns() - t < 1000000ull) __nanosleep(1000);
@@ -338,10 +353,9 @@ void linear_q4_tiles_kernel(const __grid_constant__ CUtensorMap mc, const __grid
           }
         }
       }
-      if (!alive) {                                      // bounded: products in flight end before the memory is given up
-        tc_commit(lead, &drained);
-        bar_wait(&drained, 0);
-      }
+      // products in flight end before the memory is given up, also where the drain has given up waiting for them
+      tc_commit(lead, &drained, 1);
+      if (!bar_wait(&drained, 0)) atomicCAS(&g_status, 0, MOE_ERR_TIMEOUT);
     }
   } else if (wid < 4 + 4 * C::CONVERTERS) {
     regs_give<C::CONVERT>();
@@ -396,7 +410,7 @@ void linear_q4_tiles_kernel(const __grid_constant__ CUtensorMap mc, const __grid
           });
     }
     // one warp: waits of all of them slow the drain of the last products (32 rows by 2048 x 2048 10.0 instead of 9.7 us)
-    if (wid == 4) converter_end<C>((uint32_t)((tiles - pair + pairs - 1) / pairs) * steps, wait_buffer);
+    if (wid == 4) converter_end<C>(mine * steps, !a.resident, wait_buffer, [&](uint32_t i, uint32_t parity) { wait(x_empty + i, parity); });
   } else {
     regs_take<C::DRAIN>();
     // ----------------------------------------------- scaling, sums and output

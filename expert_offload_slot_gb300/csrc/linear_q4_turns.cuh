@@ -44,35 +44,26 @@ __host__ __device__ __forceinline__ void converter_turns(int group, int steps, i
   }
 }
 
-// The end.  Products report that a buffer or a stage of x is free to the barriers of both CTAs of a pair, on their own time:
-// a CTA that left before the last reports have come would have them land in memory that is another's by then.  So whoever
-// waits for a barrier's reports does so to the last use.
+// The end.  Products report that a buffer or a stage of x is free to the barriers of both CTAs of a pair, and copies land, on
+// their own time: a CTA that left before would have them come to memory that is another's by then.  So every barrier's
+// last use is waited for, by a converter warp (reports) and by who brings data in, where another warp has given up waiting, too.
 
-// Of a converter warpgroup after `total` steps of all warpgroups.  Step by step, so that each wait knows the phase before
-// to be over; for the first, step total - 2 A_BUFS, the warpgroup's last turn told.
+// The last N of `total` uses of N barriers in turn, one after another: each wait knows the phase before to be over if that
+// holds for the first.
 #pragma nv_exec_check_disable
-template <typename C, typename WaitBuffer>
-__host__ __device__ __forceinline__ void converter_end(uint32_t total, WaitBuffer wait_buffer) {
-  for (uint32_t n = total > C::A_BUFS ? total - C::A_BUFS : 0; n < total; ++n) wait_buffer(n % C::A_BUFS, (n / C::A_BUFS) & 1);
+template <uint32_t N, typename Wait>
+__host__ __device__ __forceinline__ void last_uses(uint32_t total, Wait wait) {
+  for (uint32_t n = total > N ? total - N : 0; n < total; ++n) wait(n % N, (n / N) & 1);
 }
 
-// A ring's place, and the parity of its barriers' phase there.
-template <int N>
-struct Ring {
-  uint32_t i = 0, phase = 0;
-  __host__ __device__ __forceinline__ void next() {
-    if (++i == N) {
-      i = 0;
-      phase ^= 1;
-    }
-  }
-};
-
-// Of who fills a ring's stages, at the place that would be filled next: all N are free again, or never were filled.
+// Of a converter warpgroup after `total` steps of all warpgroups.  The first step waited for is total - A_BUFS, and that
+// total - 2 A_BUFS is over the warpgroup's last turn told.  After that all steps are known to be multiplied, so each one's
+// x had come, which its loader brought once the stage's use before had been reported free.
 #pragma nv_exec_check_disable
-template <int N, typename WaitEmpty>
-__host__ __device__ __forceinline__ void ring_end(Ring<N> r, WaitEmpty wait_empty) {
-  for (int k = 0; k < N; ++k, r.next()) wait_empty(r.i, r.phase);
+template <typename C, typename WaitBuffer, typename WaitX>
+__host__ __device__ __forceinline__ void converter_end(uint32_t total, bool x_ring, WaitBuffer wait_buffer, WaitX wait_x) {
+  last_uses<C::A_BUFS>(total, wait_buffer);
+  if (x_ring) last_uses<C::X_STAGES>(total, wait_x);
 }
 
 }  // namespace moeslot

@@ -191,13 +191,13 @@ __device__ __forceinline__ uint32_t elect_lead() {
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
   return r;
 }
-// Arrive on `bar` in both CTAs once every MMA this thread has issued so far has completed.
-__device__ __forceinline__ void tc_commit(uint32_t lead, uint64_t* bar) {
+// Arrive on `bar` in both CTAs (or those of the mask) once every MMA this thread has issued so far has completed.
+__device__ __forceinline__ void tc_commit(uint32_t lead, uint64_t* bar, uint16_t ctas = 3) {
   asm volatile(
       "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
       " @q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;\n}\n" ::"r"(
           smem_addr(bar)),
-      "r"(lead), "h"((uint16_t)3)
+      "r"(lead), "h"(ctas)
       : "memory");
 }
 // D[tmem] (+)= A B, bf16 in, fp32 out; A and B by shared-memory descriptors.

@@ -55,27 +55,30 @@ extern "C" __attribute__((visibility("default"))) int q4_turns(int columns, int 
   return with(columns, parts, [&](auto shape) { return walk<decltype(shape)>(group, steps, tile, tiles, pairs, out, room); });
 }
 
-// The waits of a converter warpgroup after `total` steps, as (slot, parity).
-extern "C" __attribute__((visibility("default"))) int q4_end(int columns, int parts, int total, int* out) {
+// The waits of a converter warpgroup after `total` steps, as (what, slot, parity); the stages of x in *stages.
+extern "C" __attribute__((visibility("default"))) int q4_end(int columns, int parts, int total, int x_ring, int* out, int* stages) {
   return with(columns, parts, [&](auto shape) {
     int n = 0;
-    converter_end<decltype(shape)>(total, [&](uint32_t ab, uint32_t parity) {
-      out[2 * n] = ab;
-      out[2 * n++ + 1] = parity;
-    });
+    auto note = [&](int what, int slot, int parity) {
+      out[3 * n] = what;
+      out[3 * n + 1] = slot;
+      out[3 * n++ + 2] = parity;
+    };
+    *stages = decltype(shape)::X_STAGES;
+    converter_end<decltype(shape)>(total, x_ring != 0, [&](uint32_t ab, uint32_t parity) { note(0, ab, parity); },
+                                   [&](uint32_t st, uint32_t parity) { note(1, st, parity); });
     return n;
   });
 }
 
-// Those of a ring of four stages whose first `used` have been filled.
-extern "C" __attribute__((visibility("default"))) int q4_ring_end(int used, int* out) {
-  Ring<4> r;
-  r.phase = 1;
-  for (int k = 0; k < used; ++k) r.next();
-  int n = 0;
-  ring_end(r, [&](uint32_t i, uint32_t parity) {
-    out[2 * n] = i;
-    out[2 * n++ + 1] = parity;
+// Those of who loads the codes, after `total` loads.
+extern "C" __attribute__((visibility("default"))) int q4_codes_end(int columns, int parts, int total, int* out) {
+  return with(columns, parts, [&](auto shape) {
+    int n = 0;
+    last_uses<decltype(shape)::CODE_STAGES>(total, [&](uint32_t st, uint32_t parity) {
+      out[2 * n] = st;
+      out[2 * n++ + 1] = parity;
+    });
+    return n;
   });
-  return n;
 }

@@ -98,28 +98,35 @@ def test_every_step_is_expanded_once_and_every_stage_released(lib, columns, part
         assert set(freed) == set(range(mine * ((steps + 1) // 2))) and all(v == 2 for v in freed.values())
 
 
+@pytest.mark.parametrize("x_ring", [0, 1])
 @pytest.mark.parametrize("columns, parts", SHAPES + [(256, 0)])
-def test_no_warpgroup_ends_before_its_buffers_have_been_reported_free(lib, columns, parts):
+def test_no_warpgroup_ends_before_buffers_and_stages_have_been_reported_free(lib, columns, parts, x_ring):
     converters, buffers, _ = shape_of(lib, columns, parts)
     for total in range(2, 300):
-        out = np.zeros((buffers, 2), np.int32)
-        n = lib.q4_end(columns, parts, total, out.ctypes.data_as(ctypes.c_void_p))
-        assert n == min(total, buffers)
+        out, rings = np.zeros((32, 3), np.int32), ctypes.c_int()
+        n = lib.q4_end(columns, parts, total, x_ring, out.ctypes.data_as(ctypes.c_void_p), ctypes.byref(rings))
+        x_stages = rings.value
+        assert n == min(total, buffers) + x_ring * min(total, x_stages)
+        waits = out[:n].tolist()
         for group in range(converters):
             last = (total - 1 - group) // converters * converters + group          # its last turn, negative if it had none
-            known = last - buffers
-            for step, (slot, parity) in zip(range(total - n, total), out.tolist()):
-                assert (slot, parity) == (step % buffers, step // buffers % 2)     # the phase that this step's products end
+            known = last - buffers                                                 # multiplied
+            for step, (what, slot, parity) in zip(range(total - min(total, buffers), total), waits):
+                assert (what, slot, parity) == (0, step % buffers, step // buffers % 2)    # the phase that this step's products end
                 assert step < buffers or step - buffers <= known                   # the one before is known to be over
                 known = max(known, step)
+            assert known == total - 1          # all are: the x of each had come, once its stage's use before was reported
+            for step, wait in zip(range(total - min(total, x_stages), total), waits[min(total, buffers):]):
+                assert wait == [1, step % x_stages, step // x_stages % 2]
 
 
-def test_no_loader_ends_before_its_stages_have_been_reported_free(lib):
-    for used in range(30):
-        out = np.zeros((4, 2), np.int32)
-        assert lib.q4_ring_end(used, out.ctypes.data_as(ctypes.c_void_p)) == 4
-        for k, (slot, parity) in enumerate(out.tolist()):
-            use = used + k                                     # of the ring's stages, from 0; the stage was filled 4 uses before
-            assert slot == use % 4 and parity == (use // 4 + 1) % 2
-            # an unused stage's barrier is in its first phase: parity 1 passes at once, which is that of a first use
-            assert use >= 4 or parity == 1
+@pytest.mark.parametrize("columns, parts", SHAPES + [(256, 0)])
+def test_no_loader_of_codes_ends_before_its_loads_have_landed(lib, columns, parts):
+    _, _, stages = shape_of(lib, columns, parts)
+    for total in range(1, 200):
+        out = np.zeros((stages, 2), np.int32)
+        n = lib.q4_codes_end(columns, parts, total, out.ctypes.data_as(ctypes.c_void_p))
+        assert n == min(total, stages)
+        known = total - 1 - stages                             # the load whose stage was free for the last one
+        for load, (slot, parity) in zip(range(total - n, total), out.tolist()):
+            assert (slot, parity) == (load % stages, load // stages % 2) and load - stages <= known
