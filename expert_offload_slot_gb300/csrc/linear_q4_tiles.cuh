@@ -28,7 +28,7 @@
 // rate; the products alone take 52, with the drain beside them 69: each accumulator's 64 KB pass
 // through tensor memory's port once more for every 512 cycles of products, and an SM's TMA unit, at some 35
 // bytes a cycle, needs 1170 cycles for the x and codes of a step whose products take 1024.  Groups of 64 and 32
-// have two and four accumulators a step: 124 and 218 us.  The drain's loop unrolled over four groups cost 6 us.
+// have two and four accumulators a step: 116 and 206 us.  The drain's loop unrolled over four groups cost 6 us.
 // 16 rows by 2048 x 131072 (147 MB): 48 us, 3.1 TB/s: a step's own instructions, barriers and
 // waits, in each role one after another, take 475 cycles in the products' warp alone (28 us) and 830 with all
 // roles beside it; HBM would allow 350.  With x brought in for every step, and two converter
